@@ -61,7 +61,7 @@ TRAFFIC = {"decode_int8": (270069760 + 736256 + 5003008, "4d213eb79d7e8572")}  #
 def _src_hash():
     """Hash of the decode kernel's source code, comments and blank lines left
     out (a comment edit does not change the counters)."""
-    p = os.path.join(ROOT, "paged_kv_cache_234_gb300", "csrc", "pkv_decode.cu")
+    p = os.path.join(ROOT, "paged_kv_cache_234_gb300", "csrc", "pkv_decode.cuh")
     code = []
     for line in open(p):
         line = line.split("//", 1)[0].rstrip()

@@ -81,6 +81,7 @@ typedef enum pkv_status {
 #define PKV_DEV_BAD_CTX 2u   /* context_lens[s] outside [0, max_context_len] or
                                 beyond max_blocks_per_seq * block_size */
 #define PKV_DEV_TIMEOUT 4u   /* a bounded wait for an asynchronous copy ran out */
+#define PKV_DEV_BAD_POS 8u   /* a rotary position outside [0, max_position) */
 
 /*
  * pkv_quantize_blocks -- symmetric per-(block, kv head) INT8 quantization
@@ -312,6 +313,135 @@ PKV_API pkv_status pkv_append_fp8(void *k_cache, void *v_cache, uint8_t *k_codes
                                   const int32_t *positions, int num_seqs, int num_kv_heads,
                                   int head_dim, int block_size, int32_t *dev_status,
                                   void *stream);
+
+/*
+ * pkv_paged_decode_scored_fp16 / _int8 / _fp8 -- the decode step with other
+ * scores, over the same caches.  With the new token at position i = ctx - 1
+ * (ctx = context_lens[s]) and a cached token t:
+ *   z   = softmax_scale * <query[s][h], K_t>
+ *   z'  = logit_cap * tanh(z / logit_cap)   if logit_cap > 0, else z
+ *   z'' = z' - slopes[h] * (i - t)          if slopes is given, else z'
+ *   t is seen if  i - t < window  or  t < prefix_lens[s]
+ *   out[s][h] = sum over seen t of softmax(z'')_t * V_t   (FP32 accumulation)
+ * A token that is not seen has no effect, whatever its slot holds, and table
+ * entries of blocks without a seen token are not read (their blocks may have
+ * been freed).  ctx == 0 gives zeros.
+ *
+ *   out         fp16 [num_seqs][num_heads][head_dim], 16-byte aligned (the
+ *               type of the query and of the projection that follows; the
+ *               fp32 result is rounded once)
+ *   logit_cap   0: no cap; finite, >= 0
+ *   window      0: no window (every t <= i is seen); else tokens at a
+ *               distance below it are seen
+ *   slopes      fp32 [num_heads] in device memory, or NULL: no bias
+ *   prefix_lens int32 [num_seqs] in device memory, or NULL: no prefix (a
+ *               negative length counts as 0, one beyond ctx as ctx)
+ * Everything else, the workspace and its size included, is as for
+ * pkv_paged_decode_fp16 / _int8 / _fp8.
+ */
+PKV_API pkv_status pkv_paged_decode_scored_fp16(
+    void *out, const void *query, const void *k_cache, const void *v_cache,
+    int num_blocks, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *context_lens, int max_context_len, int num_seqs, int num_heads,
+    int num_kv_heads, int head_dim, int block_size, float softmax_scale, float logit_cap,
+    int window, const float *slopes, const int32_t *prefix_lens, void *workspace,
+    size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+PKV_API pkv_status pkv_paged_decode_scored_int8(
+    void *out, const void *query, const int8_t *k_codes, const int8_t *v_codes,
+    const float *k_scales, const float *v_scales,
+    int num_blocks, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *context_lens, int max_context_len, int num_seqs, int num_heads,
+    int num_kv_heads, int head_dim, int block_size, float softmax_scale, float logit_cap,
+    int window, const float *slopes, const int32_t *prefix_lens, void *workspace,
+    size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+PKV_API pkv_status pkv_paged_decode_scored_fp8(
+    void *out, const void *query, const uint8_t *k_codes, const uint8_t *v_codes,
+    const float *k_scales, const float *v_scales,
+    int num_blocks, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *context_lens, int max_context_len, int num_seqs, int num_heads,
+    int num_kv_heads, int head_dim, int block_size, float softmax_scale, float logit_cap,
+    int window, const float *slopes, const int32_t *prefix_lens, void *workspace,
+    size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
+ * A ragged batch of new tokens, as pkv_rope_append_* and pkv_paged_prefill_*
+ * take it: sequence s owns the rows query_starts[s] .. query_starts[s + 1) of
+ * the [num_tokens] arrays (int32 [num_seqs + 1], not decreasing, starting at
+ * 0).  With n rows, its tokens are the last n of its context_lens[s] cached
+ * tokens, positions ctx - n .. ctx - 1.  n == 0 means no token.  Rows from
+ * query_starts[num_seqs] on belong to nobody: nothing is done for them, and
+ * their outputs are left as they were.  A sequence whose rows do not lie in
+ * [0, num_tokens], or with n > ctx or ctx beyond the block table (for the
+ * prefill: beyond max_context_len), sets PKV_DEV_BAD_CTX; its outputs become
+ * zeros and nothing is written for it.
+ */
+
+/*
+ * pkv_rope_append_fp16 / _int8 / _fp8 -- rotary positions applied to the
+ * queries and keys of a ragged batch of new tokens, and the append of keys
+ * and values to the paged cache, in one launch ([GLO] section 2.1: block =
+ * table[t / 16], slot = t % 16; 3.3.2).  For a token with cache position t
+ * and pair i < rot_dim / 2 of every query and key head, with a = x[lo], b =
+ * x[hi] (lo, hi = i, i + rot_dim / 2, or 2 i, 2 i + 1 if interleaved):
+ *   p  = rope_positions[axis_of_pair[i]][token], or t without rope_positions
+ *   c  = cos_sin[p][i],  s = cos_sin[p][rot_dim / 2 + i]
+ *   a' = a * c - b * s,  b' = b * c + a * s
+ * in fp32 (each product and each sum rounded; no fused multiply-add), rounded
+ * once to fp16.  Values past rot_dim are unchanged.  Rotated queries go to
+ * q_out, rotated keys and the values to slot t % 16 of block table[t / 16].
+ * _int8 / _fp8 then quantize every (block, kv head) tile that got a row, all
+ * 16 slots, bit-identical to pkv_quantize_blocks[_fp8] on the block.
+ *
+ *   q_out       fp16 [num_tokens][num_heads][head_dim], 16-byte aligned; may
+ *               be q itself when q_stride == num_heads * head_dim
+ *   k_cache ..  pools as for pkv_append_fp16 / _int8 / _fp8
+ *   q, k, v     fp16 [num_tokens][heads][head_dim], heads and values
+ *               contiguous, tokens q_stride / k_stride / v_stride values
+ *               apart (multiples of 8: slices of one fused projection will
+ *               do), 16-byte aligned
+ *   cos_sin     fp32 [max_position][rot_dim] in device memory: the cosines
+ *               of all pairs, then their sines; 16-byte aligned
+ *   rot_dim     a multiple of 16, at most head_dim
+ *   rope_positions  int32 [num_axes][num_tokens] in device memory, or NULL
+ *               (num_axes 1: the cache positions)
+ *   axis_of_pair  HOST array of rot_dim / 2 axis numbers < num_axes, read
+ *               during the call; may be NULL with one axis
+ *   query_starts, context_lens, num_tokens  the ragged batch (above)
+ * A position outside [0, max_position) sets PKV_DEV_BAD_POS: the token's
+ * query becomes zeros and it is not appended.  A block id outside
+ * [0, num_blocks) sets PKV_DEV_BAD_BLOCK: the token is not appended.  As for
+ * pkv_append_*, no block may receive tokens of two sequences.
+ */
+PKV_API pkv_status pkv_rope_append_fp16(
+    void *q_out, void *k_cache, void *v_cache, int num_blocks,
+    const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+    int64_t v_stride, const float *cos_sin, int max_position, int rot_dim, int interleaved,
+    const int32_t *rope_positions, int num_axes, const uint8_t *axis_of_pair,
+    const int32_t *query_starts, const int32_t *context_lens, const int32_t *block_tables,
+    int max_blocks_per_seq, int num_tokens, int num_seqs, int num_heads, int num_kv_heads,
+    int head_dim, int block_size, int32_t *dev_status, void *stream);
+
+PKV_API pkv_status pkv_rope_append_int8(
+    void *q_out, void *k_cache, void *v_cache, int8_t *k_codes, int8_t *v_codes,
+    float *k_scales, float *v_scales, int num_blocks,
+    const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+    int64_t v_stride, const float *cos_sin, int max_position, int rot_dim, int interleaved,
+    const int32_t *rope_positions, int num_axes, const uint8_t *axis_of_pair,
+    const int32_t *query_starts, const int32_t *context_lens, const int32_t *block_tables,
+    int max_blocks_per_seq, int num_tokens, int num_seqs, int num_heads, int num_kv_heads,
+    int head_dim, int block_size, int32_t *dev_status, void *stream);
+
+PKV_API pkv_status pkv_rope_append_fp8(
+    void *q_out, void *k_cache, void *v_cache, uint8_t *k_codes, uint8_t *v_codes,
+    float *k_scales, float *v_scales, int num_blocks,
+    const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+    int64_t v_stride, const float *cos_sin, int max_position, int rot_dim, int interleaved,
+    const int32_t *rope_positions, int num_axes, const uint8_t *axis_of_pair,
+    const int32_t *query_starts, const int32_t *context_lens, const int32_t *block_tables,
+    int max_blocks_per_seq, int num_tokens, int num_seqs, int num_heads, int num_kv_heads,
+    int head_dim, int block_size, int32_t *dev_status, void *stream);
 
 /*
  * pkv_evict_select -- score every physical block for eviction and choose

@@ -13,6 +13,10 @@ The functions carry the C names and take torch tensors:
 * ``pkv_paged_decode_int8``   decode-step attention over INT8 K/V pools
 * ``pkv_quantize_blocks_fp8`` fp16 K/V tiles -> FP8 (E4M3) codes + fp32 scales
 * ``pkv_paged_decode_fp8``    decode-step attention over FP8 K/V pools
+* ``pkv_paged_decode_scored_fp16`` / ``_int8`` / ``_fp8``  decode-step attention
+                              with capped or biased scores, a window, a prefix
+* ``pkv_rope_append_fp16`` / ``_int8`` / ``_fp8``  rotate the queries and keys of
+                              a ragged batch of new tokens, append keys and values
 * ``pkv_append_fp16``         write one new token per sequence into fp16 pools
 * ``pkv_append_int8``         the same, re-quantizing every tile it writes
 * ``pkv_evict_select``        eviction scores of every block + the k to evict
@@ -22,7 +26,8 @@ The functions carry the C names and take torch tensors:
 * ``pkv_decode_workspace_size``, ``pkv_set_decode_workers``,
   ``pkv_status_string``
 
-``prepare_paged_decode_fp16`` / ``_int8`` / ``_fp8`` and
+``prepare_paged_decode_fp16`` / ``_int8`` / ``_fp8``,
+``prepare_paged_decode_scored_*``, ``prepare_rope_append_*`` and
 ``prepare_quantize_blocks`` / ``_fp8`` take the same arguments as the calls
 above and return a ``PreparedCall``: the arguments checked and marshalled
 once, each call of the object issuing the same C call again (for serving
@@ -49,11 +54,14 @@ PKV_ERR_EXHAUSTED = 6
 PKV_DEV_BAD_BLOCK = 1
 PKV_DEV_BAD_CTX = 2
 PKV_DEV_TIMEOUT = 4
+PKV_DEV_BAD_POS = 8
 
 EXPORTED = ("pkv_quantize_blocks", "pkv_paged_decode_fp16", "pkv_paged_decode_int8",
             "pkv_quantize_blocks_fp8", "pkv_paged_decode_fp8",
             "pkv_paged_decode_int8_static_workspace", "pkv_append_fp16", "pkv_append_int8",
-            "pkv_append_fp8",
+            "pkv_append_fp8", "pkv_paged_decode_scored_fp16", "pkv_paged_decode_scored_int8",
+            "pkv_paged_decode_scored_fp8", "pkv_rope_append_fp16", "pkv_rope_append_int8",
+            "pkv_rope_append_fp8",
             "pkv_evict_select", "pkv_bm_create", "pkv_bm_destroy", "pkv_bm_allocate",
             "pkv_bm_free", "pkv_bm_fork", "pkv_bm_cow", "pkv_bm_set_fill", "pkv_bm_stats",
             "pkv_bm_refcounts", "pkv_copy_blocks", "pkv_decode_workspace_size",
@@ -139,6 +147,15 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.pkv_append_int8.argtypes = app[:2] + [P, P, P, P] + app[2:]
     L.pkv_append_fp8.restype = I
     L.pkv_append_fp8.argtypes = app[:2] + [P, P, P, P] + app[2:]
+    scored = dec[:15] + [F, I, P, P] + dec[15:]
+    rope = [P, P, P, I] + [P, ctypes.c_int64] * 3 + [P, I, I, I, P, I, P, P, P, P, I, I, I, I, I, I,
+                                                    I, P, P]
+    for kind in ("fp16", "int8", "fp8"):
+        codes = [] if kind == "fp16" else [P, P]
+        fn = getattr(L, "pkv_paged_decode_scored_" + kind)
+        fn.restype, fn.argtypes = I, scored[:4] + codes + scored[4:]
+        fn = getattr(L, "pkv_rope_append_" + kind)
+        fn.restype, fn.argtypes = I, rope[:3] + 2 * codes + rope[3:]
     L.pkv_evict_select.restype = I
     L.pkv_evict_select.argtypes = [P, P, I, ctypes.c_int64, F, F, I, P, P, P, P]
     L.pkv_bm_create.restype = I
@@ -472,6 +489,311 @@ def pkv_append_fp8(k_cache, v_cache, k_codes, v_codes, k_scales, v_scales, k_new
     """pkv_append_fp16, then re-quantize every written tile to FP8 (E4M3)."""
     _append("pkv_append_fp8", k_cache, v_cache, (k_codes, v_codes, k_scales, v_scales), k_new,
             v_new, block_tables, positions, dev_status, stream)
+
+
+
+# ------------------------------------------- scored decode, rotation + append
+def _same_device(*named):
+    """The calls run on the current device: every tensor has to live there
+    (pinned host tensors aside)."""
+    import torch
+    dev = torch.cuda.current_device()
+    for name, t in named:
+        if t is not None and t.is_cuda and t.device.index != dev:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _shape(name, t, *want):
+    if t is not None and tuple(t.shape) != want:
+        raise ValueError(f"{name} must have the shape {want}, got {tuple(t.shape)}")
+
+
+def _scored(fn_name, out, query, kp, vp, ks, vs, block_tables, context_lens, max_context_len,
+            softmax_scale, workspace, logit_cap, window, slopes, prefix_lens, dev_status, stream):
+    """Checks and marshals a scored decode call: (C function name, arguments)."""
+    import torch
+    _check(out, "out", torch.float16, host_ok=True)
+    _check(query, "query", torch.float16, host_ok=True)
+    _check(block_tables, "block_tables", torch.int32, host_ok=True)
+    _check(context_lens, "context_lens", torch.int32, host_ok=True)
+    _check(workspace, "workspace")
+    _check(dev_status, "dev_status", torch.int32)
+    _check_pools(fn_name, kp, vp, ks, vs)
+    _check(slopes, "slopes", torch.float32)
+    _check(prefix_lens, "prefix_lens", torch.int32)
+    n, hq, d = query.shape
+    nb, hkv, bs, _ = kp.shape
+    _shape("out", out, n, hq, d)
+    _shape("context_lens", context_lens, n)
+    _shape("slopes", slopes, hq)
+    _shape("prefix_lens", prefix_lens, n)
+    _same_device(("out", out), ("query", query), ("k", kp), ("v", vp), ("k_scales", ks),
+                 ("v_scales", vs), ("block_tables", block_tables), ("context_lens", context_lens),
+                 ("workspace", workspace), ("slopes", slopes), ("prefix_lens", prefix_lens),
+                 ("dev_status", dev_status))
+    mb = block_tables.shape[1] if block_tables.dim() == 2 else 0
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    args = [_ptr(out), _ptr(query), _ptr(kp), _ptr(vp)]
+    if ks is not None:
+        args += [_ptr(ks), _ptr(vs)]
+    args += [nb, _ptr(block_tables), mb, _ptr(context_lens), int(max_context_len), n, hq, hkv,
+             d, bs, float(softmax_scale), float(logit_cap), int(window), _ptr(slopes),
+             _ptr(prefix_lens), _ptr(workspace), ws_bytes, _ptr(dev_status), _stream(stream)]
+    return fn_name, args
+
+
+def _check_pools(fn_name, kp, vp, ks, vs):
+    import torch
+    if fn_name.endswith("fp16"):
+        _check(kp, "k_cache", torch.float16)
+        _check(vp, "v_cache", torch.float16)
+    else:
+        code_t = torch.uint8 if fn_name.endswith("fp8") else torch.int8
+        _check(kp, "k_codes", code_t)
+        _check(vp, "v_codes", code_t)
+        _check(ks, "k_scales", torch.float32)
+        _check(vs, "v_scales", torch.float32)
+        _shape("k_scales", ks, *kp.shape[:2])
+        _shape("v_scales", vs, *kp.shape[:2])
+    _shape("v pool", vp, *kp.shape)
+
+
+def _rope(fn_name, q_out, k_cache, v_cache, codes, q, k, v, cos_sin, query_starts, context_lens,
+          block_tables, rope_positions, axis_of_pair, interleaved, dev_status, stream):
+    """Checks and marshals a rotate-and-append call: (C function name,
+    arguments, the host array of axes, which has to live as long)."""
+    import numpy as np
+    import torch
+    _check(q_out, "q_out", torch.float16)
+    _check(k_cache, "k_cache", torch.float16)
+    _check(v_cache, "v_cache", torch.float16)
+    _check(cos_sin, "cos_sin", torch.float32)
+    _check(query_starts, "query_starts", torch.int32)
+    _check(context_lens, "context_lens", torch.int32)
+    _check(block_tables, "block_tables", torch.int32)
+    _check(rope_positions, "rope_positions", torch.int32)
+    _check(dev_status, "dev_status", torch.int32)
+    nb, hkv, bs, d = k_cache.shape
+    t, hq, _ = q.shape
+    n = context_lens.numel()
+    strides = []
+    for name, x, heads in (("q", q, hq), ("k", k, hkv), ("v", v, hkv)):
+        if not x.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if x.dtype != torch.float16:
+            raise ValueError(f"{name} must be {torch.float16}, got {x.dtype}")
+        _shape(name, x, t, heads, d)
+        if x.stride(2) != 1 or (heads > 1 and x.stride(1) != d):
+            raise ValueError(f"{name} must be contiguous within a token")
+        # one token has no next one: any stride will do
+        strides.append(x.stride(0) if t > 1 else heads * d)
+    _shape("q_out", q_out, t, hq, d)
+    _shape("v_cache", v_cache, *k_cache.shape)
+    _shape("query_starts", query_starts, n + 1)
+    if cos_sin.dim() != 2 or block_tables.dim() != 2 or block_tables.shape[0] != n:
+        raise ValueError("cos_sin must be [max_position][rot_dim], block_tables [num_seqs][...]")
+    axes, axis = 1, None
+    if rope_positions is not None:
+        if rope_positions.dim() == 2:
+            axes = rope_positions.shape[0]
+        _shape("rope_positions", rope_positions,
+               *((axes, t) if rope_positions.dim() == 2 else (t,)))
+    if axis_of_pair is not None:
+        axis = np.asarray(axis_of_pair)
+        if axis.shape != (cos_sin.shape[1] // 2,) or (axis.size and not
+                                                      0 <= axis.min() <= axis.max() < axes):
+            raise ValueError("axis_of_pair must hold an axis for each of the rot_dim / 2 pairs")
+        axis = np.ascontiguousarray(axis, dtype=np.uint8)
+    args = [_ptr(q_out), _ptr(k_cache), _ptr(v_cache)]
+    if codes is not None:
+        kc, vc, ks, vs = codes
+        _check_pools(fn_name, kc, vc, ks, vs)
+        _shape("k_codes", kc, *k_cache.shape)
+        args += [_ptr(kc), _ptr(vc), _ptr(ks), _ptr(vs)]
+    _same_device(("q_out", q_out), ("k_cache", k_cache), ("v_cache", v_cache), ("q", q), ("k", k),
+                 ("v", v), ("cos_sin", cos_sin), ("query_starts", query_starts),
+                 ("context_lens", context_lens), ("block_tables", block_tables),
+                 ("rope_positions", rope_positions), ("dev_status", dev_status),
+                 *(("codes", x) for x in codes or ()))
+    args += [nb, _ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2], _ptr(cos_sin),
+             cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)), _ptr(rope_positions),
+             axes, None if axis is None else axis.ctypes.data, _ptr(query_starts),
+             _ptr(context_lens), _ptr(block_tables), block_tables.shape[1], t, n, hq, hkv, d, bs,
+             _ptr(dev_status), _stream(stream)]
+    return fn_name, args, axis
+
+
+def rope_table(max_position, rot_dim, base=10000.0, inv_freq=None, device=None):
+    """fp32 [max_position][rot_dim] for the rotation: the cosines of p * f_i of
+    every position p and pair i, then the sines, computed in fp64 and rounded
+    once.  f_i = base ** (-2 i / rot_dim) unless ``inv_freq`` gives the
+    rot_dim / 2 frequencies."""
+    import torch
+    dev = device or "cuda"
+    if inv_freq is None:
+        f = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=dev) / rot_dim)
+    else:
+        f = torch.as_tensor(inv_freq, dtype=torch.float64, device=dev)
+        _shape("inv_freq", f, rot_dim // 2)
+    a = torch.arange(max_position, dtype=torch.float64, device=dev)[:, None] * f
+    return torch.cat([a.cos(), a.sin()], dim=1).float()
+
+
+def pkv_paged_decode_scored_fp16(out, query, k_cache, v_cache, block_tables,
+                                  context_lens, max_context_len, softmax_scale, workspace,
+                                  logit_cap=0.0, window=0, slopes=None, prefix_lens=None,
+                                  dev_status=None, stream=None) -> None:
+    """out[N][Hq][d] fp16 = decode attention over fp16 pools with
+    capped (logit_cap), biased (slopes) or masked (window, prefix_lens) scores."""
+    _invoke(*_scored("pkv_paged_decode_scored_fp16", out, query, k_cache, v_cache, None, None,
+                     block_tables, context_lens, max_context_len, softmax_scale, workspace,
+                     logit_cap, window, slopes, prefix_lens, dev_status, stream))
+
+
+def prepare_paged_decode_scored_fp16(out, query, k_cache, v_cache, block_tables,
+                                      context_lens, max_context_len, softmax_scale, workspace,
+                                      logit_cap=0.0, window=0, slopes=None, prefix_lens=None,
+                                      dev_status=None, stream=None) -> PreparedCall:
+    """``pkv_paged_decode_scored_fp16`` with its arguments marshalled once."""
+    return PreparedCall(*_scored("pkv_paged_decode_scored_fp16", out, query, k_cache, v_cache, None, None,
+                                 block_tables, context_lens, max_context_len, softmax_scale,
+                                 workspace, logit_cap, window, slopes, prefix_lens, dev_status,
+                                 stream),
+                        keep=(out, query, k_cache, v_cache, block_tables,
+                              context_lens, workspace, slopes, prefix_lens, dev_status))
+
+
+def pkv_rope_append_fp16(q_out, k_cache, v_cache, q, k, v,
+                         cos_sin, query_starts, context_lens, block_tables, rope_positions=None,
+                         axis_of_pair=None, interleaved=False, dev_status=None,
+                         stream=None) -> None:
+    """Rotate the queries ([T][Hq][d], into q_out) and keys ([T][Hkv][d]) of a ragged
+    batch of new tokens and append keys and values to the fp16 pools.
+    Sequence s owns rows query_starts[s] .. query_starts[s + 1), its last
+    tokens of context_lens[s].  q, k and v may be slices of one fused
+    projection.  rope_positions ([T], or [axes][T] with an axis for each pair
+    in axis_of_pair) default to the cache positions."""
+    fn, args, _axis = _rope("pkv_rope_append_fp16", q_out, k_cache, v_cache,
+                            None, q, k, v, cos_sin,
+                            query_starts, context_lens, block_tables, rope_positions,
+                            axis_of_pair, interleaved, dev_status, stream)
+    _invoke(fn, args)
+
+
+def prepare_rope_append_fp16(q_out, k_cache, v_cache, q, k,
+                             v, cos_sin, query_starts, context_lens, block_tables,
+                             rope_positions=None, axis_of_pair=None, interleaved=False,
+                             dev_status=None, stream=None) -> PreparedCall:
+    """``pkv_rope_append_fp16`` with its arguments marshalled once."""
+    fn, args, axis = _rope("pkv_rope_append_fp16", q_out, k_cache, v_cache,
+                           None, q, k, v, cos_sin,
+                           query_starts, context_lens, block_tables, rope_positions,
+                           axis_of_pair, interleaved, dev_status, stream)
+    return PreparedCall(fn, args, keep=(q_out, k_cache, v_cache, q, k, v,
+                                        cos_sin, query_starts, context_lens, block_tables,
+                                        rope_positions, axis, dev_status))
+
+
+def pkv_paged_decode_scored_int8(out, query, k_codes, v_codes, k_scales, v_scales, block_tables,
+                                  context_lens, max_context_len, softmax_scale, workspace,
+                                  logit_cap=0.0, window=0, slopes=None, prefix_lens=None,
+                                  dev_status=None, stream=None) -> None:
+    """out[N][Hq][d] fp16 = decode attention over INT8 pools with
+    capped (logit_cap), biased (slopes) or masked (window, prefix_lens) scores."""
+    _invoke(*_scored("pkv_paged_decode_scored_int8", out, query, k_codes, v_codes, k_scales, v_scales,
+                     block_tables, context_lens, max_context_len, softmax_scale, workspace,
+                     logit_cap, window, slopes, prefix_lens, dev_status, stream))
+
+
+def prepare_paged_decode_scored_int8(out, query, k_codes, v_codes, k_scales, v_scales, block_tables,
+                                      context_lens, max_context_len, softmax_scale, workspace,
+                                      logit_cap=0.0, window=0, slopes=None, prefix_lens=None,
+                                      dev_status=None, stream=None) -> PreparedCall:
+    """``pkv_paged_decode_scored_int8`` with its arguments marshalled once."""
+    return PreparedCall(*_scored("pkv_paged_decode_scored_int8", out, query, k_codes, v_codes, k_scales, v_scales,
+                                 block_tables, context_lens, max_context_len, softmax_scale,
+                                 workspace, logit_cap, window, slopes, prefix_lens, dev_status,
+                                 stream),
+                        keep=(out, query, k_codes, v_codes, k_scales, v_scales, block_tables,
+                              context_lens, workspace, slopes, prefix_lens, dev_status))
+
+
+def pkv_rope_append_int8(q_out, k_cache, v_cache, k_codes, v_codes, k_scales, v_scales, q, k, v,
+                         cos_sin, query_starts, context_lens, block_tables, rope_positions=None,
+                         axis_of_pair=None, interleaved=False, dev_status=None,
+                         stream=None) -> None:
+    """Rotate the queries and keys of a ragged batch of new tokens, append keys and
+    values to the fp16 pools and re-quantize every written tile."""
+    fn, args, _axis = _rope("pkv_rope_append_int8", q_out, k_cache, v_cache,
+                            (k_codes, v_codes, k_scales, v_scales), q, k, v, cos_sin,
+                            query_starts, context_lens, block_tables, rope_positions,
+                            axis_of_pair, interleaved, dev_status, stream)
+    _invoke(fn, args)
+
+
+def prepare_rope_append_int8(q_out, k_cache, v_cache, k_codes, v_codes, k_scales, v_scales, q, k,
+                             v, cos_sin, query_starts, context_lens, block_tables,
+                             rope_positions=None, axis_of_pair=None, interleaved=False,
+                             dev_status=None, stream=None) -> PreparedCall:
+    """``pkv_rope_append_int8`` with its arguments marshalled once."""
+    fn, args, axis = _rope("pkv_rope_append_int8", q_out, k_cache, v_cache,
+                           (k_codes, v_codes, k_scales, v_scales), q, k, v, cos_sin,
+                           query_starts, context_lens, block_tables, rope_positions,
+                           axis_of_pair, interleaved, dev_status, stream)
+    return PreparedCall(fn, args, keep=(q_out, k_cache, v_cache, k_codes, v_codes, k_scales, v_scales, q, k, v,
+                                        cos_sin, query_starts, context_lens, block_tables,
+                                        rope_positions, axis, dev_status))
+
+
+def pkv_paged_decode_scored_fp8(out, query, k_codes, v_codes, k_scales, v_scales, block_tables,
+                                  context_lens, max_context_len, softmax_scale, workspace,
+                                  logit_cap=0.0, window=0, slopes=None, prefix_lens=None,
+                                  dev_status=None, stream=None) -> None:
+    """out[N][Hq][d] fp16 = decode attention over FP8 pools with
+    capped (logit_cap), biased (slopes) or masked (window, prefix_lens) scores."""
+    _invoke(*_scored("pkv_paged_decode_scored_fp8", out, query, k_codes, v_codes, k_scales, v_scales,
+                     block_tables, context_lens, max_context_len, softmax_scale, workspace,
+                     logit_cap, window, slopes, prefix_lens, dev_status, stream))
+
+
+def prepare_paged_decode_scored_fp8(out, query, k_codes, v_codes, k_scales, v_scales, block_tables,
+                                      context_lens, max_context_len, softmax_scale, workspace,
+                                      logit_cap=0.0, window=0, slopes=None, prefix_lens=None,
+                                      dev_status=None, stream=None) -> PreparedCall:
+    """``pkv_paged_decode_scored_fp8`` with its arguments marshalled once."""
+    return PreparedCall(*_scored("pkv_paged_decode_scored_fp8", out, query, k_codes, v_codes, k_scales, v_scales,
+                                 block_tables, context_lens, max_context_len, softmax_scale,
+                                 workspace, logit_cap, window, slopes, prefix_lens, dev_status,
+                                 stream),
+                        keep=(out, query, k_codes, v_codes, k_scales, v_scales, block_tables,
+                              context_lens, workspace, slopes, prefix_lens, dev_status))
+
+
+def pkv_rope_append_fp8(q_out, k_cache, v_cache, k_codes, v_codes, k_scales, v_scales, q, k, v,
+                         cos_sin, query_starts, context_lens, block_tables, rope_positions=None,
+                         axis_of_pair=None, interleaved=False, dev_status=None,
+                         stream=None) -> None:
+    """Rotate the queries and keys of a ragged batch of new tokens, append keys and
+    values to the fp16 pools and re-quantize every written tile."""
+    fn, args, _axis = _rope("pkv_rope_append_fp8", q_out, k_cache, v_cache,
+                            (k_codes, v_codes, k_scales, v_scales), q, k, v, cos_sin,
+                            query_starts, context_lens, block_tables, rope_positions,
+                            axis_of_pair, interleaved, dev_status, stream)
+    _invoke(fn, args)
+
+
+def prepare_rope_append_fp8(q_out, k_cache, v_cache, k_codes, v_codes, k_scales, v_scales, q, k,
+                             v, cos_sin, query_starts, context_lens, block_tables,
+                             rope_positions=None, axis_of_pair=None, interleaved=False,
+                             dev_status=None, stream=None) -> PreparedCall:
+    """``pkv_rope_append_fp8`` with its arguments marshalled once."""
+    fn, args, axis = _rope("pkv_rope_append_fp8", q_out, k_cache, v_cache,
+                           (k_codes, v_codes, k_scales, v_scales), q, k, v, cos_sin,
+                           query_starts, context_lens, block_tables, rope_positions,
+                           axis_of_pair, interleaved, dev_status, stream)
+    return PreparedCall(fn, args, keep=(q_out, k_cache, v_cache, k_codes, v_codes, k_scales, v_scales, q, k, v,
+                                        cos_sin, query_starts, context_lens, block_tables,
+                                        rope_positions, axis, dev_status))
 
 
 def pkv_evict_select(refcnt, last_used, current_tick, k, evict_ids, num_evicted, scores=None,

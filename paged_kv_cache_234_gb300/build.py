@@ -18,8 +18,8 @@ BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libpkv.so")
 DEBUG_LIB_PATH = os.path.join(BUILD_DIR, "libpkv_debug.so")
 INCLUDE = os.path.join(os.path.dirname(PKG_DIR), "include")
-SOURCES = ("pkv_host.cu", "pkv_quantize.cu", "pkv_decode.cu", "pkv_append.cu", "pkv_evict.cu",
-           "pkv_copy.cu", "pkv_block_manager.cpp")
+SOURCES = ("pkv_host.cu", "pkv_quantize.cu", "pkv_decode.cu", "pkv_decode_scored.cu",
+           "pkv_append.cu", "pkv_rope.cu", "pkv_evict.cu", "pkv_copy.cu", "pkv_block_manager.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -74,7 +74,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     return LIB_PATH
 
 
-DEBUG_SOURCES = ("pkv_decode.cu", "pkv_evict.cu")  # the kernels with PKV_DEBUG checks
+DEBUG_SOURCES = ("pkv_decode.cu", "pkv_decode_scored.cu", "pkv_evict.cu")  # the kernels with PKV_DEBUG checks
 
 
 def build_debug() -> str:

@@ -6,6 +6,9 @@
 
 namespace pkv {
 
+int g_worker_cap = 0;
+std::mutex g_cfg_mu;
+
 namespace {
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "../../include/pkv.h"
 
 namespace pkv {
@@ -27,6 +29,11 @@ bool current_device_info(DeviceInfo *out);
 // encoded are kept and handed out again for the same description.
 bool encode_tmap_2d(CUtensorMap *map, const void *base, int elem_bytes, uint64_t inner_elems,
                     uint64_t rows, uint32_t box_inner, uint32_t box_rows, int swizzle_bytes);
+
+// Decode workers at most (pkv_set_decode_workers; 0: automatic), and the lock
+// of it and of the launches' per-device caches.
+extern int g_worker_cap;
+extern std::mutex g_cfg_mu;
 
 inline bool aligned(const void *p, uintptr_t a)
 {
