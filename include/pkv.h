@@ -444,6 +444,71 @@ PKV_API pkv_status pkv_rope_append_fp8(
     int head_dim, int block_size, int32_t *dev_status, void *stream);
 
 /*
+ * pkv_paged_prefill_fp16 / _int8 / _fp8 -- attention of a ragged batch of new
+ * tokens over the paged cache, which already holds them (prompts, chunks of
+ * prompts, drafted tokens to verify, and single tokens among them; [GLO]
+ * section 2.1, Kernel Mechanics).  For the token at position i of sequence s
+ * and a cached token t < ctx = context_lens[s]:
+ *   z   = softmax_scale * <query[row][h], K_t>
+ *   z'  = logit_cap * tanh(z / logit_cap)   if logit_cap > 0, else z
+ *   z'' = z' - slopes[h] * |i - t|          if slopes is given, else z'
+ *   t is seen if  (t <= i and i - t < window)  or  t < prefix_lens[s]
+ *   out[row][h] = sum over seen t of softmax(z'')_t * V_t
+ * with FP32 sums, maxima and accumulators; the probabilities enter the second
+ * product rounded to fp16.  A key that no query row of the same work item (256
+ * rows: tokens times heads of a kv head) sees has no effect, whatever its slot
+ * holds, and the blocks that only hold such keys are not read.  Keys and
+ * values that a query of the call sees must be finite.
+ *
+ *   out, query  fp16 [num_tokens][num_heads][head_dim], 16-byte aligned
+ *   query_starts, context_lens, num_tokens  the ragged batch (above);
+ *               max_context_len bounds context_lens and sizes the launch
+ *   logit_cap, window, slopes, prefix_lens  as for the scored decode (the
+ *               prefix is seen by every token, also ahead of it)
+ *   workspace   device scratch of at least pkv_prefill_workspace_size()
+ *               bytes, 16-byte aligned (NULL will do where that is 0); needs
+ *               no initialisation
+ * A block id outside [0, num_blocks) sets PKV_DEV_BAD_BLOCK; the outputs of
+ * every work item that needs the block become zeros.  Two calls sharing a
+ * workspace must not overlap on the GPU.
+ */
+PKV_API pkv_status pkv_paged_prefill_fp16(
+    void *out, const void *query, const void *k_cache, const void *v_cache,
+    int num_blocks, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *query_starts, const int32_t *context_lens, int max_context_len,
+    int num_tokens, int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+    float softmax_scale, float logit_cap, int window, const float *slopes,
+    const int32_t *prefix_lens, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+    void *stream);
+
+PKV_API pkv_status pkv_paged_prefill_int8(
+    void *out, const void *query, const int8_t *k_codes, const int8_t *v_codes,
+    const float *k_scales, const float *v_scales,
+    int num_blocks, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *query_starts, const int32_t *context_lens, int max_context_len,
+    int num_tokens, int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+    float softmax_scale, float logit_cap, int window, const float *slopes,
+    const int32_t *prefix_lens, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+    void *stream);
+
+PKV_API pkv_status pkv_paged_prefill_fp8(
+    void *out, const void *query, const uint8_t *k_codes, const uint8_t *v_codes,
+    const float *k_scales, const float *v_scales,
+    int num_blocks, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *query_starts, const int32_t *context_lens, int max_context_len,
+    int num_tokens, int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+    float softmax_scale, float logit_cap, int window, const float *slopes,
+    const int32_t *prefix_lens, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+    void *stream);
+
+/*
+ * Bytes of workspace a prefill call with these sizes needs (any KV variant);
+ * 0 for most large batches, and for invalid sizes.  Pure host arithmetic.
+ */
+PKV_API size_t pkv_prefill_workspace_size(int num_tokens, int num_seqs, int num_heads,
+                                          int num_kv_heads, int head_dim, int max_context_len);
+
+/*
  * pkv_evict_select -- score every physical block for eviction and choose
  * the k most evictable ones, in one launch ([PKF] Overview, component A:
  * eviction scoring of the paged KV blocks fused with the top-k choice;

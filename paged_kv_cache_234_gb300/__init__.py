@@ -15,6 +15,8 @@ The functions carry the C names and take torch tensors:
 * ``pkv_paged_decode_fp8``    decode-step attention over FP8 K/V pools
 * ``pkv_paged_decode_scored_fp16`` / ``_int8`` / ``_fp8``  decode-step attention
                               with capped or biased scores, a window, a prefix
+* ``pkv_paged_prefill_fp16`` / ``_int8`` / ``_fp8``  the same attention for a ragged
+                              batch of new tokens (``pkv_prefill_workspace_size``)
 * ``pkv_rope_append_fp16`` / ``_int8`` / ``_fp8``  rotate the queries and keys of
                               a ragged batch of new tokens, append keys and values
 * ``pkv_append_fp16``         write one new token per sequence into fp16 pools
@@ -27,7 +29,8 @@ The functions carry the C names and take torch tensors:
   ``pkv_status_string``
 
 ``prepare_paged_decode_fp16`` / ``_int8`` / ``_fp8``,
-``prepare_paged_decode_scored_*``, ``prepare_rope_append_*`` and
+``prepare_paged_decode_scored_*``, ``prepare_paged_prefill_*``,
+``prepare_rope_append_*`` and
 ``prepare_quantize_blocks`` / ``_fp8`` take the same arguments as the calls
 above and return a ``PreparedCall``: the arguments checked and marshalled
 once, each call of the object issuing the same C call again (for serving
@@ -61,7 +64,8 @@ EXPORTED = ("pkv_quantize_blocks", "pkv_paged_decode_fp16", "pkv_paged_decode_in
             "pkv_paged_decode_int8_static_workspace", "pkv_append_fp16", "pkv_append_int8",
             "pkv_append_fp8", "pkv_paged_decode_scored_fp16", "pkv_paged_decode_scored_int8",
             "pkv_paged_decode_scored_fp8", "pkv_rope_append_fp16", "pkv_rope_append_int8",
-            "pkv_rope_append_fp8",
+            "pkv_rope_append_fp8", "pkv_paged_prefill_fp16", "pkv_paged_prefill_int8",
+            "pkv_paged_prefill_fp8", "pkv_prefill_workspace_size",
             "pkv_evict_select", "pkv_bm_create", "pkv_bm_destroy", "pkv_bm_allocate",
             "pkv_bm_free", "pkv_bm_fork", "pkv_bm_cow", "pkv_bm_set_fill", "pkv_bm_stats",
             "pkv_bm_refcounts", "pkv_copy_blocks", "pkv_decode_workspace_size",
@@ -150,10 +154,15 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     scored = dec[:15] + [F, I, P, P] + dec[15:]
     rope = [P, P, P, I] + [P, ctypes.c_int64] * 3 + [P, I, I, I, P, I, P, P, P, P, I, I, I, I, I, I,
                                                     I, P, P]
+    prefill = [P, P, P, P, I, P, I, P, P, I, I, I, I, I, I, I, F, F, I, P, P, P, Z, P, P]
+    L.pkv_prefill_workspace_size.restype = Z
+    L.pkv_prefill_workspace_size.argtypes = [I] * 6
     for kind in ("fp16", "int8", "fp8"):
         codes = [] if kind == "fp16" else [P, P]
         fn = getattr(L, "pkv_paged_decode_scored_" + kind)
         fn.restype, fn.argtypes = I, scored[:4] + codes + scored[4:]
+        fn = getattr(L, "pkv_paged_prefill_" + kind)
+        fn.restype, fn.argtypes = I, prefill[:4] + codes + prefill[4:]
         fn = getattr(L, "pkv_rope_append_" + kind)
         fn.restype, fn.argtypes = I, rope[:3] + 2 * codes + rope[3:]
     L.pkv_evict_select.restype = I
@@ -621,6 +630,139 @@ def _rope(fn_name, q_out, k_cache, v_cache, codes, q, k, v, cos_sin, query_start
              _ptr(context_lens), _ptr(block_tables), block_tables.shape[1], t, n, hq, hkv, d, bs,
              _ptr(dev_status), _stream(stream)]
     return fn_name, args, axis
+
+
+def _prefill(fn_name, out, query, kp, vp, ks, vs, block_tables, query_starts, context_lens,
+             max_context_len, softmax_scale, workspace, logit_cap, window, slopes, prefix_lens,
+             dev_status, stream):
+    """Checks and marshals a prefill call: (C function name, arguments)."""
+    import torch
+    _check(out, "out", torch.float16)
+    _check(query, "query", torch.float16)
+    _check(block_tables, "block_tables", torch.int32)
+    _check(query_starts, "query_starts", torch.int32)
+    _check(context_lens, "context_lens", torch.int32)
+    _check(workspace, "workspace")
+    _check(dev_status, "dev_status", torch.int32)
+    _check_pools(fn_name, kp, vp, ks, vs)
+    _check(slopes, "slopes", torch.float32)
+    _check(prefix_lens, "prefix_lens", torch.int32)
+    t, hq, d = query.shape
+    nb, hkv, bs, _ = kp.shape
+    n = context_lens.numel()
+    _shape("out", out, t, hq, d)
+    _shape("pool", kp, nb, hkv, bs, d)
+    _shape("query_starts", query_starts, n + 1)
+    _shape("slopes", slopes, hq)
+    _shape("prefix_lens", prefix_lens, n)
+    if block_tables.dim() != 2 or block_tables.shape[0] != n:
+        raise ValueError("block_tables must be [num_seqs][max_blocks_per_seq]")
+    _same_device(("out", out), ("query", query), ("k", kp), ("v", vp), ("k_scales", ks),
+                 ("v_scales", vs), ("block_tables", block_tables), ("query_starts", query_starts),
+                 ("context_lens", context_lens), ("workspace", workspace), ("slopes", slopes),
+                 ("prefix_lens", prefix_lens), ("dev_status", dev_status))
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    args = [_ptr(out), _ptr(query), _ptr(kp), _ptr(vp)]
+    if ks is not None:
+        args += [_ptr(ks), _ptr(vs)]
+    args += [nb, _ptr(block_tables), block_tables.shape[1], _ptr(query_starts),
+             _ptr(context_lens), int(max_context_len), t, n, hq, hkv, d, bs, float(softmax_scale),
+             float(logit_cap), int(window), _ptr(slopes), _ptr(prefix_lens), _ptr(workspace),
+             ws_bytes, _ptr(dev_status), _stream(stream)]
+    return fn_name, args
+
+
+def pkv_prefill_workspace_size(num_tokens, num_seqs, num_heads, num_kv_heads, head_dim,
+                               max_context_len) -> int:
+    return int(lib().pkv_prefill_workspace_size(num_tokens, num_seqs, num_heads, num_kv_heads,
+                                                head_dim, max_context_len))
+
+
+def prefill_workspace(num_tokens, num_seqs, num_heads, num_kv_heads, head_dim, max_context_len,
+                      device=None):
+    """A uint8 CUDA tensor big enough to serve as a prefill workspace."""
+    import torch
+    nbytes = pkv_prefill_workspace_size(num_tokens, num_seqs, num_heads, num_kv_heads, head_dim,
+                                        max_context_len)
+    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def pkv_paged_prefill_fp16(out, query, k_cache, v_cache, block_tables, query_starts,
+                           context_lens, max_context_len, softmax_scale, workspace,
+                           logit_cap=0.0, window=0, slopes=None, prefix_lens=None,
+                           dev_status=None, stream=None) -> None:
+    """out[T][Hq][d] fp16 = causal attention of a ragged batch of new tokens over
+    fp16 pools; sequence s owns rows query_starts[s] .. query_starts[s + 1),
+    its last tokens of context_lens[s]."""
+    _invoke(*_prefill("pkv_paged_prefill_fp16", out, query, k_cache, v_cache, None, None,
+                      block_tables, query_starts, context_lens, max_context_len, softmax_scale,
+                      workspace, logit_cap, window, slopes, prefix_lens, dev_status, stream))
+
+
+def prepare_paged_prefill_fp16(out, query, k_cache, v_cache, block_tables,
+                               query_starts, context_lens, max_context_len, softmax_scale,
+                               workspace, logit_cap=0.0, window=0, slopes=None, prefix_lens=None,
+                               dev_status=None, stream=None) -> PreparedCall:
+    """``pkv_paged_prefill_fp16`` with its arguments marshalled once."""
+    return PreparedCall(*_prefill("pkv_paged_prefill_fp16", out, query, k_cache, v_cache, None, None,
+                                  block_tables, query_starts, context_lens, max_context_len,
+                                  softmax_scale, workspace, logit_cap, window, slopes,
+                                  prefix_lens, dev_status, stream),
+                        keep=(out, query, k_cache, v_cache, block_tables,
+                              query_starts, context_lens, workspace, slopes, prefix_lens,
+                              dev_status))
+
+
+def pkv_paged_prefill_int8(out, query, k_codes, v_codes, k_scales, v_scales, block_tables, query_starts,
+                           context_lens, max_context_len, softmax_scale, workspace,
+                           logit_cap=0.0, window=0, slopes=None, prefix_lens=None,
+                           dev_status=None, stream=None) -> None:
+    """out[T][Hq][d] fp16 = causal attention of a ragged batch of new tokens over
+    INT8 pools; sequence s owns rows query_starts[s] .. query_starts[s + 1),
+    its last tokens of context_lens[s]."""
+    _invoke(*_prefill("pkv_paged_prefill_int8", out, query, k_codes, v_codes, k_scales, v_scales,
+                      block_tables, query_starts, context_lens, max_context_len, softmax_scale,
+                      workspace, logit_cap, window, slopes, prefix_lens, dev_status, stream))
+
+
+def prepare_paged_prefill_int8(out, query, k_codes, v_codes, k_scales, v_scales, block_tables,
+                               query_starts, context_lens, max_context_len, softmax_scale,
+                               workspace, logit_cap=0.0, window=0, slopes=None, prefix_lens=None,
+                               dev_status=None, stream=None) -> PreparedCall:
+    """``pkv_paged_prefill_int8`` with its arguments marshalled once."""
+    return PreparedCall(*_prefill("pkv_paged_prefill_int8", out, query, k_codes, v_codes, k_scales, v_scales,
+                                  block_tables, query_starts, context_lens, max_context_len,
+                                  softmax_scale, workspace, logit_cap, window, slopes,
+                                  prefix_lens, dev_status, stream),
+                        keep=(out, query, k_codes, v_codes, k_scales, v_scales, block_tables,
+                              query_starts, context_lens, workspace, slopes, prefix_lens,
+                              dev_status))
+
+
+def pkv_paged_prefill_fp8(out, query, k_codes, v_codes, k_scales, v_scales, block_tables, query_starts,
+                           context_lens, max_context_len, softmax_scale, workspace,
+                           logit_cap=0.0, window=0, slopes=None, prefix_lens=None,
+                           dev_status=None, stream=None) -> None:
+    """out[T][Hq][d] fp16 = causal attention of a ragged batch of new tokens over
+    FP8 pools; sequence s owns rows query_starts[s] .. query_starts[s + 1),
+    its last tokens of context_lens[s]."""
+    _invoke(*_prefill("pkv_paged_prefill_fp8", out, query, k_codes, v_codes, k_scales, v_scales,
+                      block_tables, query_starts, context_lens, max_context_len, softmax_scale,
+                      workspace, logit_cap, window, slopes, prefix_lens, dev_status, stream))
+
+
+def prepare_paged_prefill_fp8(out, query, k_codes, v_codes, k_scales, v_scales, block_tables,
+                               query_starts, context_lens, max_context_len, softmax_scale,
+                               workspace, logit_cap=0.0, window=0, slopes=None, prefix_lens=None,
+                               dev_status=None, stream=None) -> PreparedCall:
+    """``pkv_paged_prefill_fp8`` with its arguments marshalled once."""
+    return PreparedCall(*_prefill("pkv_paged_prefill_fp8", out, query, k_codes, v_codes, k_scales, v_scales,
+                                  block_tables, query_starts, context_lens, max_context_len,
+                                  softmax_scale, workspace, logit_cap, window, slopes,
+                                  prefix_lens, dev_status, stream),
+                        keep=(out, query, k_codes, v_codes, k_scales, v_scales, block_tables,
+                              query_starts, context_lens, workspace, slopes, prefix_lens,
+                              dev_status))
 
 
 def rope_table(max_position, rot_dim, base=10000.0, inv_freq=None, device=None):

@@ -19,7 +19,8 @@ LIB_PATH = os.path.join(BUILD_DIR, "libpkv.so")
 DEBUG_LIB_PATH = os.path.join(BUILD_DIR, "libpkv_debug.so")
 INCLUDE = os.path.join(os.path.dirname(PKG_DIR), "include")
 SOURCES = ("pkv_host.cu", "pkv_quantize.cu", "pkv_decode.cu", "pkv_decode_scored.cu",
-           "pkv_append.cu", "pkv_rope.cu", "pkv_evict.cu", "pkv_copy.cu", "pkv_block_manager.cpp")
+           "pkv_prefill.cu", "pkv_append.cu", "pkv_rope.cu", "pkv_evict.cu", "pkv_copy.cu",
+           "pkv_block_manager.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

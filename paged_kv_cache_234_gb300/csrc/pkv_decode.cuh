@@ -68,6 +68,7 @@
 
 #include "pkv_host.cuh"
 #include "pkv_ptx.cuh"
+#include "pkv_score.cuh"
 
 namespace pkv {
 namespace {
@@ -138,32 +139,6 @@ struct PageSpan {
         visited = pages - gap;
     }
 };
-
-// The 16-bit mask of a page's tokens (its first is t0) that the decode at
-// position ctx - 1 sees.
-__device__ __forceinline__ uint32_t below(int n)
-{
-    return n >= kPage ? 0xffffu : n <= 0 ? 0u : (1u << n) - 1u;
-}
-
-__device__ __forceinline__ uint32_t seen_mask(int t0, int ctx, int lo, int pre)
-{
-    return below(ctx - t0) & (~below(lo - t0) | below(pre - t0));
-}
-
-// cap * tanh(x / cap) of a score in log2 units.  Away from zero 1 - 2 / (1 +
-// e^2u) has an absolute error of some 2^-23; near zero it would lose the
-// score's relative precision, so |u| < 1/4 takes the series of tanh up to
-// u^9, whose first omitted term, 1382/155925 u^11, is 1e-8 of u there.
-__device__ __forceinline__ float cap_score(float x, float cap, float cap_inv)
-{
-    const float u = x * cap_inv, w = u * u;
-    const float poly = x + x * w *
-        fmaf(w, fmaf(w, fmaf(w, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f);
-    const float e = ptx::ex2(u * 2.885390081777927f);
-    const float far = fmaf(-2.f * cap, __fdividef(1.f, 1.f + e), cap);
-    return w < 0.0625f ? poly : far;
-}
 
 // ------------------------------------------------------ debug build checks
 // Built with PKV_DEBUG, the decode kernel checks every shared-memory address
@@ -497,21 +472,6 @@ __device__ __forceinline__ float2 unpack_half2(uint32_t w)
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
-// two int8 codes (bytes picked by sel from a word already XOR-ed with 0x80)
-// as an f16 pair 1152 + c, exact
-__device__ __forceinline__ uint32_t i8pair_biased(uint32_t xw, uint32_t sel)
-{
-    return ptx::prmt(xw, 0x64646464u, sel);
-}
-
-// the same pair with the bias removed: exactly c
-__device__ __forceinline__ uint32_t i8pair_exact(uint32_t xw, uint32_t sel)
-{
-    uint32_t r;
-    asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(i8pair_biased(xw, sel)), "r"(0x64806480u));
-    return r;
-}
-
 // Which worker's page range holds stream page x (largest w with a_w <= x).
 __device__ __forceinline__ int64_t worker_of(int64_t x, int64_t total, int workers)
 {
@@ -575,10 +535,10 @@ __device__ __forceinline__ void page_scores(uint32_t kt, const uint32_t (&qf)[kG
         for (int ks = 0; ks < KS; ++ks) {
             uint32_t a0, a1, a2, a3;
             if constexpr (kKv == kKvI8) {
-                a0 = i8pair_biased(kw[0][ks], 0x4140u);
-                a2 = i8pair_biased(kw[0][ks], 0x4342u);
-                a1 = i8pair_biased(kw[1][ks], 0x4140u);
-                a3 = i8pair_biased(kw[1][ks], 0x4342u);
+                a0 = ptx::i8pair_biased(kw[0][ks], 0x4140u);
+                a2 = ptx::i8pair_biased(kw[0][ks], 0x4342u);
+                a1 = ptx::i8pair_biased(kw[1][ks], 0x4140u);
+                a3 = ptx::i8pair_biased(kw[1][ks], 0x4342u);
             } else {
                 a0 = ptx::e4m3x2_to_f16x2(kw[0][ks]);
                 a2 = ptx::e4m3x2_to_f16x2(kw[0][ks] >> 16);
@@ -688,10 +648,10 @@ __device__ __forceinline__ void page_pv(uint32_t vt, const uint32_t (&pb0)[kG],
             const uint32_t il23 = ptx::prmt(vw[2][i >> 1], vw[3][i >> 1], sel);
             uint32_t a0, a1, a2, a3;
             if constexpr (kKv == kKvI8) {
-                a0 = i8pair_exact(il01, 0x4140u);
-                a1 = i8pair_exact(il01, 0x4342u);
-                a2 = i8pair_exact(il23, 0x4140u);
-                a3 = i8pair_exact(il23, 0x4342u);
+                a0 = ptx::i8pair_exact(il01, 0x4140u);
+                a1 = ptx::i8pair_exact(il01, 0x4342u);
+                a2 = ptx::i8pair_exact(il23, 0x4140u);
+                a3 = ptx::i8pair_exact(il23, 0x4342u);
             } else {
                 a0 = ptx::e4m3x2_to_f16x2(il01) & mlo;
                 a1 = ptx::e4m3x2_to_f16x2(il01 >> 16) & mlo;

@@ -87,6 +87,17 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void *tmap, int 
         : "memory");
 }
 
+// The same without a cache hint (data that other CTAs read again).
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void *tmap, int x, int y,
+                                            uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
 __device__ __forceinline__ uint64_t policy_evict_first()
 {
     uint64_t p;
@@ -196,6 +207,21 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel)
     uint32_t d;
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
     return d;
+}
+
+// two int8 codes (bytes picked by sel from a word already XOR-ed with 0x80)
+// as an f16 pair 1152 + c, exact
+__device__ __forceinline__ uint32_t i8pair_biased(uint32_t xw, uint32_t sel)
+{
+    return prmt(xw, 0x64646464u, sel);
+}
+
+// the same pair with the bias removed: exactly c
+__device__ __forceinline__ uint32_t i8pair_exact(uint32_t xw, uint32_t sel)
+{
+    uint32_t r;
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(i8pair_biased(xw, sel)), "r"(0x64806480u));
+    return r;
 }
 
 // Two OCP E4M3 values (the low 16 bits of w, low byte first) to an f16 pair

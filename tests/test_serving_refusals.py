@@ -82,6 +82,48 @@ def test_rope_append(kind):
         assert c(vc=FAKE + 8) == c(ks=FAKE + 2) == MISALIGNED
 
 
+PREFILL = dict(out=FAKE, query=FAKE, k=FAKE, v=FAKE, ks=FAKE, vs=FAKE, num_blocks=16, tables=FAKE,
+               mb=4, starts=FAKE, lens=FAKE, max_ctx=64, t=10, n=2, hq=8, hkv=2, d=64, bs=16,
+               scale=0.125, cap=0.0, window=0, slopes=None, prefix=None, ws=FAKE,
+               ws_bytes=1 << 30, status=None, stream=None)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_prefill(kind):
+    order = [n for n in PREFILL if kind != "fp16" or n not in ("ks", "vs")]
+
+    def c(**kw):
+        return call(order, PREFILL, "pkv_paged_prefill_" + kind, **kw)
+    for name in ("out", "query", "k", "v", "tables", "starts", "lens"):
+        assert c(**{name: None}) == INVALID
+    assert c(cap=-1.0) == c(cap=float("nan")) == c(cap=float("inf")) == INVALID
+    assert c(window=-1) == c(t=-1) == c(n=-1) == c(hq=7) == c(mb=-1) == c(max_ctx=-1) == INVALID
+    assert c(scale=float("nan")) == c(scale=float("-inf")) == INVALID
+    assert c(d=96) == c(bs=32) == c(num_blocks=1 << 27) == c(t=1 << 30) == UNSUPPORTED
+    assert c(max_ctx=(1 << 31) - 1, ws_bytes=1 << 40) == UNSUPPORTED
+    for name in ("slopes", "prefix", "lens", "starts", "tables", "status"):
+        assert c(**{name: FAKE + 2}) == MISALIGNED
+    assert c(out=FAKE + 8) == c(k=FAKE + 4) == c(query=FAKE + 2) == MISALIGNED
+    need = pkv.pkv_prefill_workspace_size(10, 2, 8, 2, 64, 6400)
+    assert need > 0
+    assert c(max_ctx=6400, ws=None) == c(max_ctx=6400, ws_bytes=need - 1) == WORKSPACE
+    assert c(max_ctx=6400, ws=FAKE + 4) == MISALIGNED
+    assert c(t=0) == c(n=0) == pkv.PKV_OK
+    if kind != "fp16":
+        assert c(ks=None) == INVALID and c(vs=FAKE + 1) == MISALIGNED
+
+
+def test_prefill_workspace_size():
+    # splits * rows * (head_dim + 2) floats; none where the items fill the GPU
+    one = 8 * 4 * (128 + 2) * 4
+    size = pkv.pkv_prefill_workspace_size(8, 1, 4, 1, 128, 20000)
+    assert size % one == 0 and 2 <= size // one <= 64
+    assert pkv.pkv_prefill_workspace_size(65536, 16, 32, 8, 128, 4096) == 0
+    assert pkv.pkv_prefill_workspace_size(8, 1, 4, 3, 128, 20000) == 0
+    assert pkv.pkv_prefill_workspace_size(8, 1, 4, 1, 96, 20000) == 0
+    assert pkv.pkv_prefill_workspace_size(0, 0, 4, 1, 64, 20000) == 0
+
+
 def tensors():
     return dict(out=torch.zeros(2, 8, 64, dtype=torch.float16),
                 q=torch.zeros(2, 8, 64, dtype=torch.float16),
@@ -101,6 +143,10 @@ CPU_CALLS = [
                                        a["tab"], a["starts"], a["cl"], a["bt"]),
     lambda a: pkv.prepare_rope_append_fp16(a["out"], a["pool"], a["pool"], a["q"], a["kv"],
                                            a["kv"], a["tab"], a["starts"], a["cl"], a["bt"]),
+    lambda a: pkv.pkv_paged_prefill_fp16(a["out"], a["q"], a["pool"], a["pool"], a["bt"],
+                                         a["starts"], a["cl"], 32, 0.125, a["ws"]),
+    lambda a: pkv.prepare_paged_prefill_fp16(a["out"], a["q"], a["pool"], a["pool"], a["bt"],
+                                             a["starts"], a["cl"], 32, 0.125, a["ws"]),
 ]
 
 
