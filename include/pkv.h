@@ -392,7 +392,11 @@ PKV_API pkv_status pkv_paged_decode_scored_fp8(
  * once to fp16.  Values past rot_dim are unchanged.  Rotated queries go to
  * q_out, rotated keys and the values to slot t % 16 of block table[t / 16].
  * _int8 / _fp8 then quantize every (block, kv head) tile that got a row, all
- * 16 slots, bit-identical to pkv_quantize_blocks[_fp8] on the block.
+ * 16 slots, as pkv_quantize_blocks[_fp8] does but for the scale's rounding:
+ *   scale = amax * fl(1 / 127)  (fl(1 / 448) for FP8), rounded to fp32
+ * which is within 2^-23 of the quotient that pkv_quantize_blocks rounds; a
+ * code whose x / scale lies that close to a rounding border may differ by one
+ * step.  Either pair of codes and scale stands for the tile.
  *
  *   q_out       fp16 [num_tokens][num_heads][head_dim], 16-byte aligned; may
  *               be q itself when q_stride == num_heads * head_dim

@@ -13,8 +13,8 @@
 // shares every key and value that is read -- as two tiles of 128 rows, the M of
 // one tcgen05.mma.  Per 128 keys (eight pages) a tile does
 //   S = Q K^T   (128 x 128 fp32 in TMEM; Q, K in shared memory)
-//   P = 2^(S' - m)  (registers: one thread per row, so maxima and sums need no
-//                    exchange between threads; back to TMEM as fp16)
+//   P = 2^(S' - m)  (registers: two threads per row, which exchange their
+//                    maxima through shared memory; back to TMEM as fp16)
 //   O += P V    (128 x d fp32 in TMEM; P from TMEM, V in shared memory as it
 //                lies in the page, rows of keys)
 // and the two tiles take turns: while one is in its softmax, the tensor core
@@ -25,10 +25,11 @@
 // out over the keys and stays below the rounding of the fp16 output.  Sums,
 // maxima and accumulators are fp32.
 //
-// Roles of the warps: 0-3 and 4-7 the rows of the two tiles, 8 issues the
-// products, 9 the TMA loads of the pages (a ring of tiles of 128 keys, K and V
-// in turn).  INT8 / FP8 pages land in a second ring, and warps 12-15 widen
-// them exactly to fp16; the K scales multiply the scores, the V scales enter
+// Roles of the warps: 0-15 the rows of the two tiles (two threads per row, 64
+// columns of S each), 16 issues the products, 17 and 19 the TMA loads of K and
+// V (a ring of tiles of 128 keys, K and V in turn), 18 zeroes rows of V that
+// must not count.  INT8 / FP8 pages land in a second ring, and warps 20-23
+// widen them exactly to fp16; the K scales multiply the scores, the V scales enter
 // the probabilities as a ratio to the largest one so far.
 //
 // Items are numbered by bounds that the host knows (pkv_ragged.cuh), the ones
@@ -53,6 +54,8 @@ constexpr int kRows = 256;      // query rows per item: two tiles
 constexpr int kTile = 128;      // rows per tile, keys per step
 constexpr int kPage = 16;
 constexpr int kPagesPerTile = kTile / kPage;
+constexpr int kCols = kTile / 2;    // columns of S per softmax thread
+constexpr int kSoftWarps = 16;      // two halves of two tiles of four warps
 constexpr int kSms = 152;       // GB300: what the split over the keys aims to fill
 constexpr int kMaxSplits = 64;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // bounded waits: 1 s
@@ -90,38 +93,48 @@ struct Smem {
     static constexpr int kRing = 2 * kTileBytes;
     static constexpr int kCodeRing = kRing + kStages * kTileBytes;
     static constexpr int kCtl = kCodeRing + kCodeStages * kCodeBytes;
-    static constexpr int kBars = 2 * kStages + 2 * kCodeStages + 8;
+    static constexpr int kBars = 2 * kStages + 2 * kCodeStages + 9;
     // scales [kScaleTiles][K, V][8 pages]: the loads run at most five tiles
     // ahead of the softmax (the code ring, the ring and the tile at work)
     static constexpr int kScaleTiles = 8;
     static constexpr int kScales = kCtl + 8 * kBars;
     static constexpr int kFlags =
         kScales + (kCodes ? kScaleTiles * 2 * kPagesPerTile * 4 : 0);
-    static constexpr int kBytes = kFlags + 16;
+    static constexpr int kSwap = kFlags + 16;                  // [2 tiles][2 halves][128 rows]
+    static constexpr int kBytes = kSwap + 2 * 2 * kTile * 4;
     // a second CTA on the SM would wait for TMEM: ask for more than half
-    static constexpr int kAsk = 1024 + (kBytes > 120 * 1024 ? kBytes : 120 * 1024);
+    static constexpr int kAsk = kBytes > 120 * 1024 ? kBytes : 120 * 1024;
+    static_assert(kAsk <= 227 * 1024, "shared memory of one CTA");
 };
 
 struct Waiter {
     volatile int *abort;
     int32_t *dev_status;
-    // Bounded wait of a whole warp; false once any wait of the CTA ran out.
+    // Bounded waits; false once any wait of the CTA ran out.  By one thread:
+    __device__ __forceinline__ bool one(uint32_t bar, uint32_t parity) const
+    {
+        return ptx::mbar_try_wait(bar, parity) || slow(bar, parity);
+    }
+    // by a whole warp, all lanes with the same outcome:
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const
     {
-        bool ok = ptx::mbar_try_wait(bar, parity);
-        if (!__all_sync(0xffffffffu, ok)) {
-            const uint64_t t0 = ptx::globaltimer_ns();
-            while (!ok) {
-                for (int i = 0; i < 64 && !ok; ++i) ok = ptx::mbar_try_wait(bar, parity);
-                if (ok || *abort) break;
-                if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
-                    *abort = 1;
-                    if (dev_status) atomicOr(dev_status, PKV_DEV_TIMEOUT);
-                }
+        if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+        return __all_sync(0xffffffffu, slow(bar, parity));
+    }
+    __device__ __forceinline__ bool slow(uint32_t bar, uint32_t parity) const
+    {
+        uint64_t t0 = 0;  // the timer is slow to read: only after many tries
+        for (;;) {
+            for (int i = 0; i < 4096; ++i)
+                if (ptx::mbar_try_wait(bar, parity)) return true;
+            if (*abort) return false;
+            const uint64_t now = ptx::globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kWaitLimitNs) {
+                *abort = 1;
+                if (dev_status) atomicOr(dev_status, PKV_DEV_TIMEOUT);
             }
-            ok = __all_sync(0xffffffffu, ok);
         }
-        return ok;
     }
 };
 
@@ -136,6 +149,14 @@ struct Item {
     bool ok;
 
     __device__ __forceinline__ int real(int v) const { return v + (v >= np1 ? gap : 0); }
+
+    // whether a tile of keys holds some that no row sees
+    __device__ __forceinline__ bool dirty(int tile) const
+    {
+        const int tmin = real(tile * kPagesPerTile) * kPage;
+        const int tmax = real(tile * kPagesPerTile + kPagesPerTile - 1) * kPage + kPage - 1;
+        return !((tmax <= hi && tmin >= lo) || tmax < pre);
+    }
 
     // bits of a page's tokens (its first is t0) that some row may see
     __device__ __forceinline__ uint32_t live(int t0) const
@@ -191,27 +212,27 @@ __device__ __forceinline__ int64_t row_at(const PrefillArgs &p, const Item &it, 
 template <int kKv>
 __host__ __device__ constexpr int prefill_threads()
 {
-    return kKv == kKvF16 ? 384 : 512;
+    return kKv == kKvF16 ? 640 : 768;
 }
 
-// Registers: launched with 168 (128 with the widening warps) per thread; the
-// softmax warpgroups take what the others give back.
+// Registers: launched with 96 (80 with the widening warps) per thread; the
+// softmax warps take what the others give back.
 template <int kKv>
 __device__ __forceinline__ void more_registers()
 {
     if constexpr (kKv == kKvF16)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     else
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
 }
 
 template <int kKv>
 __device__ __forceinline__ void fewer_registers()
 {
     if constexpr (kKv == kKvF16)
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    else
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
 }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
@@ -227,6 +248,67 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint4 v)
                  : "memory");
 }
 
+// Exchange between the two halves of a tile's columns (256 threads).  A warp
+// whose wait ran out arrives without waiting, so that the others get through:
+// they then find no further product coming, and give up at their own wait.
+__device__ __forceinline__ void swap_sync(int tile)
+{
+    asm volatile("bar.sync %0, 256;" ::"r"(tile + 1) : "memory");
+}
+
+__device__ __forceinline__ void swap_arrive(int tile)
+{
+    asm volatile("bar.arrive %0, 256;" ::"r"(tile + 1) : "memory");
+}
+
+// The largest of a thread's scores.
+__device__ __forceinline__ float row_max(const float (&x)[kCols])
+{
+    float m[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+    for (int c = 4; c < kCols; c += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            m[e] = c + 4 + e < kCols ? fmaxf(fmaxf(m[e], x[c + e]), x[c + 4 + e])
+                                     : fmaxf(m[e], x[c + e]);
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// cap_score of a thread's scores, two at a time.  The polynomial alone while no
+// score of the warp's rows passes the cap.
+__device__ __forceinline__ void cap_scores(float (&x)[kCols], float cap, float cap_inv)
+{
+    float top = 0.f;
+#pragma unroll
+    for (int c = 0; c < kCols; c += 2) top = fmaxf(fmaxf(top, fabsf(x[c])), fabsf(x[c + 1]));
+    const uint64_t ci = ptx::f32x2(cap_inv, cap_inv);
+    auto poly = [&](int c, uint64_t &u) {
+        const uint64_t x2 = ptx::f32x2(x[c], x[c + 1]);
+        u = ptx::mul2(x2, ci);
+        const uint64_t w = ptx::mul2(u, u);
+        uint64_t q = ptx::f32x2(tanh_coef(6), tanh_coef(6));
+#pragma unroll
+        for (int k = 5; k >= 0; --k) q = ptx::fma2(q, w, ptx::f32x2(tanh_coef(k), tanh_coef(k)));
+        return ptx::f32x2_parts(ptx::mul2(x2, q));
+    };
+    uint64_t u;
+    if (__all_sync(0xffffffffu, top * cap_inv <= 1.f)) {
+#pragma unroll
+        for (int c = 0; c < kCols; c += 2) {
+            const float2 y = poly(c, u);
+            x[c] = y.x;
+            x[c + 1] = y.y;
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < kCols; c += 2) {
+            const float2 y = poly(c, u), v = ptx::f32x2_parts(u);
+            x[c] = fabsf(v.x) <= 1.f ? y.x : cap_far(v.x, cap);
+            x[c + 1] = fabsf(v.y) <= 1.f ? y.y : cap_far(v.y, cap);
+        }
+    }
+}
+
 // kMod: any of cap, bias or scales, or a scale that is not positive -- the scores are
 // worked out before their maximum is taken.  Without it the scale is folded
 // into the exponent.
@@ -239,11 +321,9 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
     constexpr bool kCodes = M::kCodes;
     constexpr int S = M::kStages;
     constexpr int kRowChunks = kD / 8;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = ptx::smem_addr(smem);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     // barriers: ring full / empty, code ring full / empty, then single ones
     auto full = [&](int s) { return base + M::kCtl + 8 * s; };
@@ -257,6 +337,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
     auto s_full = [&](int i) { return one + 16 + 8 * i; };
     auto p_full = [&](int i) { return one + 32 + 8 * i; };
     auto o_full = [&](int i) { return one + 48 + 8 * i; };
+    [[maybe_unused]] const uint32_t fixed = one + 64;
     volatile int *flags = reinterpret_cast<volatile int *>(smem + M::kFlags);  // abort, bad, tmem
     const Waiter wait{flags, p.dev_status};
 
@@ -298,36 +379,38 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
             ptx::mbar_init(cfull(s), 1);
             ptx::mbar_init(cempty(s), 128);
         }
-        ptx::mbar_init(q_full, kRows);
+        ptx::mbar_init(q_full, kSoftWarps);
         ptx::mbar_init(drain, 1);
+        ptx::mbar_init(fixed, 1);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(s_full(i), 1);
-            ptx::mbar_init(p_full(i), kTile);
+            ptx::mbar_init(p_full(i), kSoftWarps / 2);
             ptx::mbar_init(o_full(i), 1);
         }
         ptx::fence_mbar_init();
         flags[0] = flags[1] = 0;
     }
-    if (warp == 8) umma::alloc(base + M::kFlags + 8, 512);
+    if (warp == kSoftWarps) umma::alloc(base + M::kFlags + 8, 512);
     umma::fence_before();
     __syncthreads();
     umma::fence_after();
-    const uint32_t tmem = static_cast<uint32_t>(flags[2]);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, static_cast<uint32_t>(flags[2]), 0);
     auto t_s = [&](int i) { return tmem + kTile * i; };            // S, then P, of tile i
     auto t_o = [&](int i) { return tmem + 2 * kTile + kD * i; };   // O of tile i
 
-    if (warp < 8) {
+    if (warp < kSoftWarps) {
         // ------------------------------------------------ rows of the tiles
         more_registers<kKv>();
-        const int i = warp >> 2;                        // tile
-        const int tid = threadIdx.x & (kTile - 1);
-        const int r = kTile * i + tid;                  // row of the item
+        const int i = warp >> 3, half = warp >> 2 & 1;  // tile, half of its columns
+        const int tid = threadIdx.x & (2 * kTile - 1);
+        const int rt = threadIdx.x & (kTile - 1);       // row of the tile
+        const int r = kTile * i + rt;                   // row of the item
         {
             // the tile's queries, K-major with the 128-byte swizzle; 16 bytes
             // a thread, neighbouring threads along a row
             const uint32_t dst = base + i * M::kTileBytes;
 #pragma unroll 4
-            for (int e = tid; e < kTile * kRowChunks; e += kTile) {
+            for (int e = tid; e < kTile * kRowChunks; e += 2 * kTile) {
                 const int row = e / kRowChunks, ch = e % kRowChunks;
                 uint4 v = make_uint4(0, 0, 0, 0);
                 if (kTile * i + row < it.rows)
@@ -337,7 +420,8 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                                 (((ch & 7) ^ (row & 7)) << 4), v);
             }
             ptx::fence_proxy_async_smem();
-            ptx::mbar_arrive(q_full);
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(q_full);
         }
         if (i == 0 || two) {
             const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 (w mod 4)
@@ -355,85 +439,83 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
             float m = -INFINITY, l = 0.f;
             float vref = 0.f, vinv = 0.f;
             bool ok = true;
+            // log2 units throughout; without kMod x stays as the product left
+            // it and the scale enters with the exponent
+            const float sl = kMod ? 1.f : p.scale_log2;
             for (int j = 0; j < nt && ok; ++j) {
-                int t0[kPagesPerTile];
-#pragma unroll
-                for (int g = 0; g < kPagesPerTile; ++g)
-                    t0[g] = it.real((it.ta + j) * kPagesPerTile + g) * kPage;
                 ok = wait(s_full(i), j & 1);
-                if (!ok) break;
+                if (!ok) {
+                    swap_arrive(i);
+                    break;
+                }
                 umma::fence_after();
-                float x[kTile];
+                // first page of the thread's columns
+                const int v0 = (it.ta + j) * kPagesPerTile + half * (kPagesPerTile / 2);
+                float x[kCols];
 #pragma unroll
-                for (int c = 0; c < kTile; c += 32) umma::ld32(t_s(i) + lanes + c, x + c);
-                [[maybe_unused]] float vr[kPagesPerTile];
+                for (int c = 0; c < kCols; c += 32)
+                    umma::ld32(t_s(i) + lanes + half * kCols + c, x + c);
+                [[maybe_unused]] const float *vs =
+                    reinterpret_cast<const float *>(smem + M::kScales) +
+                    ((it.ta + j) & (M::kScaleTiles - 1)) * 2 * kPagesPerTile + kPagesPerTile;
+                [[maybe_unused]] const float *ks = vs - kPagesPerTile + half * (kPagesPerTile / 2);
                 float ov = 1.f;  // change of the V reference
                 if constexpr (kCodes) {
-                    const float *ks = reinterpret_cast<const float *>(smem + M::kScales) +
-                                      ((it.ta + j) & (M::kScaleTiles - 1)) * 2 * kPagesPerTile;
-                    const float *vs = ks + kPagesPerTile;
-                    umma::wait_ld();
                     float most = 0.f;
 #pragma unroll
-                    for (int g = 0; g < kPagesPerTile; ++g) {
-                        const float f = ks[g] * p.scale_log2;
-                        vr[g] = vs[g];
-                        most = fmaxf(most, vr[g]);
-#pragma unroll
-                        for (int c = 0; c < kPage; ++c) x[kPage * g + c] *= f;
-                    }
+                    for (int g = 0; g < kPagesPerTile; ++g)
+                        most = fmaxf(most, vs[g]);
                     if (most > kVLazy * vref) {
                         vinv = __frcp_rn(most);
                         ov = vref * vinv;
                         vref = most;
                     }
-#pragma unroll
-                    for (int g = 0; g < kPagesPerTile; ++g) vr[g] *= vinv;
-                } else {
-                    umma::wait_ld();
-                    if constexpr (kMod) {
-#pragma unroll
-                        for (int c = 0; c < kTile; ++c) x[c] *= p.scale_log2;
-                    }
+                    vs += half * (kPagesPerTile / 2);
                 }
+                umma::wait_ld();
                 if constexpr (kMod) {
-                    if (p.cap > 0.f) {
+                    float f = p.scale_log2;
 #pragma unroll
-                        for (int c = 0; c < kTile; ++c) x[c] = cap_score(x[c], p.cap, p.cap_inv);
+                    for (int c = 0; c < kCols; c += 2) {
+                        if (kCodes && c % kPage == 0) f = ks[c / kPage] * p.scale_log2;
+                        const float2 y =
+                            ptx::f32x2_parts(ptx::mul2(ptx::f32x2(x[c], x[c + 1]), ptx::f32x2(f, f)));
+                        x[c] = y.x;
+                        x[c + 1] = y.y;
                     }
+                    if (p.cap > 0.f) cap_scores(x, p.cap, p.cap_inv);
                     if (p.slopes) {
 #pragma unroll
-                        for (int g = 0; g < kPagesPerTile; ++g) {
-                            const float f = static_cast<float>(pos - t0[g]);
+                        for (int g = 0; g < kPagesPerTile / 2; ++g) {
+                            const float f = static_cast<float>(pos - it.real(v0 + g) * kPage);
 #pragma unroll
                             for (int c = 0; c < kPage; ++c)
                                 x[kPage * g + c] = fmaf(-slope, fabsf(f - c), x[kPage * g + c]);
                         }
                     }
                 }
-                const int tmin = t0[0], tmax = t0[kPagesPerTile - 1] + kPage - 1;
+                const int tmin = it.real(v0) * kPage, tmax = it.real(v0 + kPagesPerTile / 2 - 1) * kPage + kPage - 1;
                 if (!((tmax <= pos_a && (p.window <= 0 || tmin > pos_b - p.window)) ||
                       tmax < it.pre)) {
+                    // some row of the tile does not see some key
 #pragma unroll
-                    for (int g = 0; g < kPagesPerTile; ++g)
+                    for (int g = 0; g < kPagesPerTile / 2; ++g) {
+                        const int t0 = it.real(v0 + g) * kPage;
+                        const uint32_t seen =
+                            (below(pos + 1 - t0) & ~below(lo - t0)) | below(it.pre - t0);
 #pragma unroll
-                        for (int c = 0; c < kPage; ++c) {
-                            const int t = t0[g] + c;
-                            const bool seen = (t <= pos && t >= lo) || t < it.pre;
-                            if (!seen) x[kPage * g + c] = -INFINITY;
-                        }
+                        for (int c = 0; c < kPage; ++c)
+                            if (!(seen >> c & 1u)) x[kPage * g + c] = -INFINITY;
+                    }
                 }
-                float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                for (int c = 4; c < kTile; c += 4) {
-                    mx[0] = fmaxf(mx[0], x[c]);
-                    mx[1] = fmaxf(mx[1], x[c + 1]);
-                    mx[2] = fmaxf(mx[2], x[c + 2]);
-                    mx[3] = fmaxf(mx[3], x[c + 3]);
-                }
-                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                const float sl = kMod ? 1.f : p.scale_log2;
-                top *= sl;
+                // the row's maximum: the other half of its columns has the
+                // other one (the buffer is free again: S of this tile was not
+                // started before both halves of the last one were through)
+                float top = row_max(x) * sl;
+                float *sw = reinterpret_cast<float *>(smem + M::kSwap) + i * 2 * kTile;
+                sw[half * kTile + rt] = top;
+                swap_sync(i);
+                top = fmaxf(top, sw[(half ^ 1) * kTile + rt]);
                 if (__any_sync(0xffffffffu, top > m + kLazy || ov != 1.f)) {
                     const float mn = fmaxf(m, top);
                     const float f = m == -INFINITY ? 0.f : ptx::ex2(m - mn);
@@ -441,45 +523,58 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                     m = mn;
                     if (j > 0) {
                         const float fo = f * ov;
-#pragma unroll
-                        for (int c = 0; c < kD; c += 32) {
-                            float o[32];
-                            umma::ld32(t_o(i) + lanes + c, o);
+#pragma unroll 1
+                        for (int c = half * (kD / 2); c < (half + 1) * (kD / 2); c += 16) {
+                            float o[16];
+                            umma::ld16(t_o(i) + lanes + c, o);
                             umma::wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] *= fo;
-                            umma::st32(t_o(i) + lanes + c, reinterpret_cast<const uint32_t *>(o));
+                            for (int e = 0; e < 16; ++e) o[e] *= fo;
+                            umma::st16(t_o(i) + lanes + c, reinterpret_cast<const uint32_t *>(o));
                         }
                     }
                 }
                 // a row that has seen nothing yet: every exponent is -inf
                 const float off = kLift - (m == -INFINITY ? 0.f : m);
-                float ls[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t sl2 = ptx::f32x2(sl, sl), off2 = ptx::f32x2(off, off);
+                uint64_t sum[2] = {0, 0};
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t pk[32];
+                for (int h = 0; h < kCols; h += 32) {
+                    uint32_t pk[16];
+                    [[maybe_unused]] float vr = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const int c = 64 * h + 2 * e;
-                        float a = ptx::ex2(fmaf(x[c], sl, off));
-                        float b = ptx::ex2(fmaf(x[c + 1], sl, off));
-                        ls[(2 * e) & 3] += a;
-                        ls[(2 * e + 1) & 3] += b;
+                    for (int e = 0; e < 16; ++e) {
+                        const int c = h + 2 * e;
+                        uint64_t y = ptx::f32x2(x[c], x[c + 1]);
+                        y = kMod ? ptx::add2(y, off2) : ptx::fma2(y, sl2, off2);
+                        const float2 z2 = ptx::f32x2_parts(y);
+                        y = ptx::f32x2(ptx::ex2(z2.x), ptx::ex2(z2.y));
+                        sum[e & 1] = ptx::add2(sum[e & 1], y);
                         if constexpr (kCodes) {
-                            a *= vr[c / kPage];
-                            b *= vr[c / kPage];
+                            if (c % kPage == 0) vr = vs[c / kPage] * vinv;
+                            y = ptx::mul2(y, ptx::f32x2(vr, vr));
                         }
-                        pk[e] = pack2(a, b);
+                        const float2 pr = ptx::f32x2_parts(y);
+                        pk[e] = pack2(pr.x, pr.y);
                     }
-                    umma::st32(t_s(i) + lanes + 32 * h, pk);
+                    umma::st16(t_s(i) + lanes + half * (kCols / 2) + h / 2, pk);
                 }
-                l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                const float2 both = ptx::f32x2_parts(ptx::add2(sum[0], sum[1]));
+                l += both.x + both.y;
                 umma::wait_st();
                 umma::fence_before();
-                ptx::mbar_arrive(p_full(i));
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(p_full(i));
             }
-            if (ok && wait(o_full(i), 0)) {
+            ok = ok && wait(o_full(i), 0);
+            if (!ok) swap_arrive(i);
+            if (ok) {
                 umma::fence_after();
+                // the sums of the two halves, in their order
+                float *sw = reinterpret_cast<float *>(smem + M::kSwap) + i * 2 * kTile;
+                sw[half * kTile + rt] = l;
+                swap_sync(i);
+                l = sw[rt] + sw[kTile + rt];
                 const bool bad = flags[1] != 0;
                 const bool mine = r < it.rows;
                 const int64_t row = row_at(p, it, rr);
@@ -489,7 +584,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                     const float f = l > 0.f ? vs / l : l;  // an empty row: zeros; NaN stays
                     uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * kD);
 #pragma unroll
-                    for (int c = 0; c < kD; c += 32) {
+                    for (int c = half * (kD / 2); c < (half + 1) * (kD / 2); c += 32) {
                         float o[32];
                         umma::ld32(t_o(i) + lanes + c, o);
                         umma::wait_ld();
@@ -505,9 +600,9 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                     }
                 } else {
                     float4 *dst = reinterpret_cast<float4 *>(p.part_acc + (z * all + row) * kD);
-                    if (mine) p.part_ml[z * all + row] = make_float2(m, bad ? -1.f : l);
+                    if (mine && half == 0) p.part_ml[z * all + row] = make_float2(m, bad ? -1.f : l);
 #pragma unroll
-                    for (int c = 0; c < kD; c += 32) {
+                    for (int c = half * (kD / 2); c < (half + 1) * (kD / 2); c += 32) {
                         float o[32];
                         umma::ld32(t_o(i) + lanes + c, o);
                         umma::wait_ld();
@@ -522,164 +617,177 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                 umma::fence_before();
             }
         }
-    } else if (warp < 12) {
+    } else if (warp < kSoftWarps + 4) {
         fewer_registers<kKv>();
-        if (warp == 8) {
+        if (warp == kSoftWarps) {
             // ------------------------------------------------ products
-            constexpr uint32_t kQk = umma::f16_idesc(kTile, kTile, false);
-            constexpr uint32_t kPv = umma::f16_idesc(kTile, kD, true);
-            auto stage = [&](int n) { return base + M::kRing + (n % S) * M::kTileBytes; };
-            auto qk = [&](int i, int n) {  // S_i = Q_i K^T
-                if (lane == 0) {
+            if (umma::elect_one()) {
+                constexpr uint32_t kQk = umma::f16_idesc(kTile, kTile, false);
+                constexpr uint32_t kPv = umma::f16_idesc(kTile, kD, true);
+                // low descriptor words; the ring advances by whole tiles
+                const uint32_t q_lo = umma::desc_lo(base, 16);
+                const uint32_t k_lo = umma::desc_lo(base + M::kRing, 16);
+                const uint32_t v_lo = umma::desc_lo(base + M::kRing, M::kHalfBytes);
+                auto qk = [&](int i, int s) {  // S_i = Q_i K^T
+                    const uint32_t a = q_lo + i * (M::kTileBytes >> 4);
+                    const uint32_t b = k_lo + s * (M::kTileBytes >> 4);
 #pragma unroll
                     for (int k = 0; k < kD / 16; ++k) {
-                        const uint32_t at = (k >> 2) * M::kHalfBytes + (k & 3) * 32;
-                        umma::mma_ss(t_s(i), umma::smem_desc(base + i * M::kTileBytes + at, 16),
-                                     umma::smem_desc(stage(n) + at, 16), kQk, k > 0);
+                        const uint32_t at = ((k >> 2) * M::kHalfBytes + (k & 3) * 32) >> 4;
+                        umma::mma_ss(t_s(i), umma::desc(a + at), umma::desc(b + at), kQk, k > 0);
                     }
                     umma::commit(s_full(i));
-                }
-                __syncwarp();
-            };
-            auto pv = [&](int i, int n, bool more) {  // O_i += P_i V
-                if (lane == 0) {
+                };
+                auto pv = [&](int i, int s, bool more) {  // O_i += P_i V
+                    const uint32_t b = v_lo + s * (M::kTileBytes >> 4);
 #pragma unroll
                     for (int k = 0; k < kTile / 16; ++k)
-                        umma::mma_ts(t_o(i), t_s(i) + 8 * k,
-                                     umma::smem_desc(stage(n) + k * 2048, M::kHalfBytes), kPv,
+                        umma::mma_ts(t_o(i), t_s(i) + 8 * k, umma::desc(b + k * (2048 >> 4)), kPv,
                                      more || k > 0);
-                }
-                __syncwarp();
-            };
-            auto free_stage = [&](int n) {
-                if (lane == 0) umma::commit(empty(n % S));
-                __syncwarp();
-            };
-            const int last = two ? 1 : 0;
-            bool ok = wait(q_full, 0) && wait(full(0), 0);
-            if (ok) {
-                umma::fence_after();
-                for (int i = 0; i <= last; ++i) qk(i, 0);
-                free_stage(0);
-            }
-            for (int j = 0; j < nt && ok; ++j) {
-                const int nv = 2 * j + 1, nk = 2 * j + 2;
-                ok = wait(full(nv % S), (nv / S) & 1);
-                if (!ok) break;
-                if constexpr (!kCodes) {
-                    // rows of V that no row of the item sees (they may hold
-                    // anything, NaN included, and are not loaded for pages
-                    // past the last) become zeros
-                    const int v = (it.ta + j) * kPagesPerTile + lane;
-                    uint32_t lv = 0xffffu;
-                    if (lane < kPagesPerTile)
-                        lv = v < it.visited ? it.live(it.real(v) * kPage) : 0u;
-                    unsigned todo = __ballot_sync(0xffffffffu, lv != 0xffffu);
-                    if (todo) {
-                        while (todo) {
-                            const int g = __ffs(todo) - 1;
-                            todo &= todo - 1;
-                            const uint32_t keep = __shfl_sync(0xffffffffu, lv, g);
-                            for (int e = lane; e < kPage * kRowChunks; e += 32) {
-                                const int row = e / kRowChunks, ch = e % kRowChunks;
-                                if (!(keep >> row & 1u))
-                                    st_shared16(stage(nv) + (ch >> 3) * M::kHalfBytes +
-                                                    (g * kPage + row) * 128 + ((ch & 7) << 4),
-                                                make_uint4(0, 0, 0, 0));
-                            }
-                        }
-                        ptx::fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                }
-                for (int i = 0; i <= last && ok; ++i) {
-                    ok = wait(p_full(i), j & 1);
-                    if (!ok) break;
+                };
+                const int last = two ? 1 : 0;
+                bool ok = wait.one(q_full, 0) && wait.one(full(0), 0);
+                if (ok) {
                     umma::fence_after();
-                    pv(i, nv, j > 0);
-                    if (i == last) free_stage(nv);
-                    if (j + 1 < nt) {
-                        if (i == 0) {
-                            ok = wait(full(nk % S), (nk / S) & 1);
-                            if (!ok) break;
-                            umma::fence_after();
-                        }
-                        qk(i, nk);
-                        if (i == last) free_stage(nk);
-                    } else {
-                        if (lane == 0) umma::commit(o_full(i));
-                        __syncwarp();
-                    }
+                    qk(0, 0);
+                    if (two) qk(1, 0);
+                    umma::commit(empty(0));
                 }
+                int sv = 0;                  // stage of the last element taken
+                uint32_t phase = 0;          // its parity
+                [[maybe_unused]] int fixes = 0;
+                for (int j = 0; j < nt && ok; ++j) {
+                    if (++sv == S) {
+                        sv = 0;
+                        phase ^= 1;
+                    }
+                    const int sk = sv + 1 == S ? 0 : sv + 1;
+                    const uint32_t kphase = sv + 1 == S ? phase ^ 1 : phase;
+                    ok = wait.one(full(sv), phase);
+                    if (!kCodes && ok && it.dirty(it.ta + j)) ok = wait.one(fixed, fixes++ & 1);
+                    for (int i = 0; i <= last && ok; ++i) {
+                        ok = wait.one(p_full(i), j & 1);
+                        if (!ok) break;
+                        umma::fence_after();
+                        pv(i, sv, j > 0);
+                        if (i == last) umma::commit(empty(sv));
+                        if (j + 1 < nt) {
+                            if (i == 0) {
+                                ok = wait.one(full(sk), kphase);
+                                if (!ok) break;
+                                umma::fence_after();
+                            }
+                            qk(i, sk);
+                            if (i == last) umma::commit(empty(sk));
+                        } else {
+                            umma::commit(o_full(i));
+                        }
+                    }
+                    sv = sk;
+                    phase = kphase;
+                }
+                // nothing of this thread's is in flight after this
+                umma::commit(drain);
+                ptx::mbar_wait_bounded(drain, 0, kWaitLimitNs);
             }
-            // nothing of this thread's is in flight after this
-            if (lane == 0) umma::commit(drain);
             __syncwarp();
-            ptx::mbar_wait_bounded(drain, 0, kWaitLimitNs);
-        } else if (warp == 9) {
+        } else if (warp == kSoftWarps + 1 || warp == kSoftWarps + 3) {
             // ------------------------------------------------ loads of the pages
+            // One warp for K, one for V.  A lane per page looks its block up;
+            // one thread issues the copies, 2 KB of a page each (a copy that
+            // every lane issued for itself took 100 cycles of the warp's time).
             constexpr int R = kCodes ? M::kCodeStages : S;
             constexpr int kBox = kCodes ? kD : 64;                       // values per box
             constexpr int kBoxes = kCodes ? 1 : M::kHalves;
-            constexpr int kPageBytes = kPage * kD * (kCodes ? 1 : 2);
-            const uint32_t ring = base + (kCodes ? M::kCodeRing : M::kRing);
+            constexpr int kBoxBytes = kPage * kBox * (kCodes ? 1 : 2);
             constexpr int kStageBytes = kCodes ? M::kCodeBytes : M::kTileBytes;
+            const uint32_t ring = base + (kCodes ? M::kCodeRing : M::kRing);
+            const bool is_v = warp == kSoftWarps + 3;
+            const void *tm = is_v ? static_cast<const void *>(&tmv) : &tmk;
             const int32_t *table =
                 p.block_tables + static_cast<int64_t>(it.seq) * p.max_blocks_per_seq;
-            int issued = 0;
-            int32_t blk = -1;
-            bool want = false, have = false;
-            for (int n = 0; n < 2 * nt; ++n) {
-                const int s = n % R;
-                if ((n & 1) == 0) {
-                    const int v = (it.ta + n / 2) * kPagesPerTile + lane;
-                    want = lane < kPagesPerTile && v < it.visited;
-                    blk = want ? __ldg(table + it.real(v)) : -1;
-                    have = want && blk >= 0 && blk < p.num_blocks;
-                    if (want && !have) {
-                        flags[1] = 1;
-                        if (p.dev_status) atomicOr(p.dev_status, PKV_DEV_BAD_BLOCK);
-                    }
+            auto lookup = [&](int j) -> int32_t {  // block of the lane's page, -2: none
+                const int v = (it.ta + j) * kPagesPerTile + lane;
+                return lane < kPagesPerTile && v < it.visited ? __ldg(table + it.real(v)) : -2;
+            };
+            int32_t blk = lookup(0);
+            int j = 0;
+            for (; j < nt; ++j) {
+                const int n = 2 * j + (is_v ? 1 : 0), s = n % R;
+                const bool have = blk >= 0 && blk < p.num_blocks;
+                if (blk != -2 && !have) {
+                    flags[1] = 1;
+                    if (p.dev_status) atomicOr(p.dev_status, PKV_DEV_BAD_BLOCK);
                 }
+                [[maybe_unused]] float scale = 0.f;
+                if constexpr (kCodes)
+                    if (have)
+                        scale = __ldg((is_v ? p.v_scales : p.k_scales) +
+                                      static_cast<int64_t>(blk) * p.num_kv_heads + it.kvh);
+                const int row = (blk * p.num_kv_heads + it.kvh) * kPage;
+                const unsigned pages = __ballot_sync(0xffffffffu, have);
                 const uint32_t fb = kCodes ? cfull(s) : full(s);
                 const uint32_t eb = kCodes ? cempty(s) : empty(s);
-                [[maybe_unused]] float ks = 0.f, vs = 0.f;
-                if constexpr (kCodes) {
-                    if ((n & 1) == 0 && have) {
-                        const int64_t at = static_cast<int64_t>(blk) * p.num_kv_heads + it.kvh;
-                        ks = __ldg(p.k_scales + at);
-                        vs = __ldg(p.v_scales + at);
-                    }
-                }
                 if (!wait(eb, ((n / R) & 1) ^ 1)) break;
+                if (j + 1 < nt) blk = lookup(j + 1);
                 if constexpr (kCodes) {
-                    if ((n & 1) == 0 && lane < kPagesPerTile) {
-                        float *sc = reinterpret_cast<float *>(smem + M::kScales) +
-                                    ((it.ta + n / 2) & (M::kScaleTiles - 1)) * 2 * kPagesPerTile;
-                        sc[lane] = ks;
-                        sc[kPagesPerTile + lane] = vs;
-                    }
+                    if (lane < kPagesPerTile)
+                        (reinterpret_cast<float *>(smem + M::kScales) +
+                         ((it.ta + j) & (M::kScaleTiles - 1)) * 2 * kPagesPerTile +
+                         (is_v ? kPagesPerTile : 0))[lane] = scale;
                     __syncwarp();
                 }
-                const int pages = __popc(__ballot_sync(0xffffffffu, have));
-                if (lane == 0) ptx::mbar_arrive_expect_tx(fb, pages * kPageBytes);
+                if (umma::elect_one())
+                    ptx::mbar_arrive_expect_tx(fb, __popc(pages) * kBoxes * kBoxBytes);
                 __syncwarp();
-                if (have) {
-                    const int row = (blk * p.num_kv_heads + it.kvh) * kPage;
-                    const void *tm = n & 1 ? static_cast<const void *>(&tmv) : &tmk;
+                const uint32_t dst = ring + s * kStageBytes;
 #pragma unroll
-                    for (int b = 0; b < kBoxes; ++b)
-                        ptx::tma_load_2d(ring + s * kStageBytes + b * M::kHalfBytes +
-                                             lane * (kPage * kBox * (kCodes ? 1 : 2)),
-                                         tm, b * kBox, row, fb);
+                for (int g = 0; g < kPagesPerTile; ++g) {
+                    const int y = __shfl_sync(0xffffffffu, row, g);
+                    if ((pages >> g & 1u) && umma::elect_one()) {
+#pragma unroll
+                        for (int b = 0; b < kBoxes; ++b)
+                            ptx::tma_load_2d(dst + b * M::kHalfBytes + g * kBoxBytes, tm, b * kBox,
+                                             y, fb);
+                    }
                 }
                 __syncwarp();
-                issued = n + 1;
             }
             // leave no copy in flight: every stage that was issued has landed
-            for (int n = max(0, issued - R); n < issued; ++n)
+            for (int e = max(0, j - R); e < j; ++e) {
+                const int n = 2 * e + (is_v ? 1 : 0);
                 ptx::mbar_wait_bounded(kCodes ? cfull(n % R) : full(n % R), (n / R) & 1,
                                        kWaitLimitNs);
+            }
+        } else if (!kCodes && warp == kSoftWarps + 2) {
+            // ------------------------------------------------ stale rows of V
+            // Rows that no row of the item sees may hold anything, NaN
+            // included (and are not loaded for pages past the last): zeros.
+            for (int j = 0; j < nt; ++j) {
+                if (!it.dirty(it.ta + j)) continue;
+                const int n = 2 * j + 1;
+                if (!wait(full(n % S), (n / S) & 1)) break;
+                const uint32_t stage = base + M::kRing + (n % S) * M::kTileBytes;
+                const int v = (it.ta + j) * kPagesPerTile + lane;
+                uint32_t lv = 0xffffu;
+                if (lane < kPagesPerTile) lv = v < it.visited ? it.live(it.real(v) * kPage) : 0u;
+                unsigned todo = __ballot_sync(0xffffffffu, lv != 0xffffu);
+                while (todo) {
+                    const int g = __ffs(todo) - 1;
+                    todo &= todo - 1;
+                    const uint32_t keep = __shfl_sync(0xffffffffu, lv, g);
+                    for (int e = lane; e < kPage * kRowChunks; e += 32) {
+                        const int row = e / kRowChunks, ch = e % kRowChunks;
+                        if (!(keep >> row & 1u))
+                            st_shared16(stage + (ch >> 3) * M::kHalfBytes +
+                                            (g * kPage + row) * 128 + ((ch & 7) << 4),
+                                        make_uint4(0, 0, 0, 0));
+                    }
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(fixed);
+            }
         }
     } else {
         if constexpr (kCodes) {
@@ -687,7 +795,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
             fewer_registers<kKv>();
             constexpr int R = M::kCodeStages;
             constexpr int kCh = kD / 16;  // 16-byte chunks of codes per row
-            const int tid = threadIdx.x - 384;
+            const int tid = threadIdx.x - 32 * (kSoftWarps + 4);
             for (int n = 0; n < 2 * nt; ++n) {
                 if (!wait(cfull(n % R), (n / R) & 1) || !wait(empty(n % S), ((n / S) & 1) ^ 1))
                     break;
@@ -733,7 +841,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
         }
     }
     __syncthreads();
-    if (warp == 8) umma::dealloc(tmem, 512);
+    if (warp == kSoftWarps) umma::dealloc(tmem, 512);
 }
 
 // Joins the key splits of every row: a warp per row, lanes along head_dim, the

@@ -9,7 +9,11 @@
 //   a' = a cos(p, i) - b sin(p, i),   b' = b cos(p, i) + a sin(p, i)
 // in fp32, each product and each sum rounded, then once to fp16.  No fused
 // multiply-add: the result does not depend on how a compiler contracts the
-// expression, so the codes of a quantized cache can be reproduced bit for bit.
+// expression, so the codes of a quantized cache can be reproduced bit for bit
+// from elementary array operations.  For the same reason a tile's scale is
+// amax times the fp32 reciprocal of the largest code: that is what an array
+// library's division by a constant computes on a GPU.  (The other quantizers
+// of this library divide; the two differ by 2^-23 at most.)
 //
 // Bound by memory: (Hq + 2 Hkv) d fp16 values in and out per token, next to
 // which the table row (4 rot bytes, read once per token and head row from L1)
@@ -320,7 +324,7 @@ __global__ void __launch_bounds__(rope_tile_threads<kD>())
         raw[1] = pool[c1];
     }
     const float amax = cta_absmax<kThreads>(chunks_absmax(raw), warp_max);
-    const float scale = __fdiv_rn(amax, kFp8 ? 448.0f : 127.0f);
+    const float scale = __fmul_rn(amax, kFp8 ? 1.0f / 448.0f : 1.0f / 127.0f);
     const float rcp = __frcp_rn(scale);
     uint2 *dst = reinterpret_cast<uint2 *>(is_v ? p.v_codes : p.k_codes) +
                  (tile * 16 + row) * kRowChunks;

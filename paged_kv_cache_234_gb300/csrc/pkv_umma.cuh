@@ -30,11 +30,17 @@ __device__ __forceinline__ void dealloc(uint32_t tmem, uint32_t columns)
 //   K-major (rows are M or N, 64 values of K each): one 64-wide slice of K.
 //   MN-major (rows are K, 64 values of N each): `next` is the distance from
 //   one 64-wide block of N to the next.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t next)
+// The low word holds the address and `next`, the high word is the same for
+// all, so the operands of one product differ by an addition to the low word.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t next)
 {
-    return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) |
-           (static_cast<uint64_t>(next >> 4) << 16) |
-           (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+    return ((addr & 0x3ffffu) >> 4) | (next >> 4 << 16);
+}
+
+__device__ __forceinline__ uint64_t desc(uint32_t lo)
+{
+    constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+    return static_cast<uint64_t>(hi) << 32 | lo;
 }
 
 // fp16 x fp16 -> fp32, M x N per instruction (K = 16); b_mn: B is MN-major.
@@ -42,6 +48,15 @@ __host__ __device__ constexpr uint32_t f16_idesc(int m, int n, bool b_mn)
 {
     return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
            (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok));
+    return ok != 0;
 }
 
 // ---------------------------------------------------------------- products
@@ -114,17 +129,31 @@ __device__ __forceinline__ void ld32(uint32_t tmem, float *v)
         : "memory");
 }
 
-__device__ __forceinline__ void st32(uint32_t tmem, const uint32_t *r)
+// The same, 16 columns.
+__device__ __forceinline__ void ld16(uint32_t tmem, float *v)
+{
+    uint32_t *r = reinterpret_cast<uint32_t *>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]),
+          "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+          "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(tmem)
+        : "memory");
+}
+
+__device__ __forceinline__ void st16(uint32_t tmem, const uint32_t *r)
 {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
-        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-        "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-        "r"(r[30]), "r"(r[31]), "r"(tmem)
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+        "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(tmem)
         : "memory");
 }
 

@@ -76,6 +76,28 @@ def cache(b, kind):
     return (out[0][0], out[1][0], out[0][1], out[1][1]), tuple(vals)
 
 
+def quantize(tiles, kind):
+    """Codes and scales of fp16 tiles [n][Hkv][16][d] as the rotation's append
+    makes them: scale = amax * fl(1 / most) in fp32, then the nearest code of
+    the fp32 quotient."""
+    f = tiles.astype(np.float32)
+    most = np.float32(127 if kind == "int8" else 448)
+    scale = np.nanmax(np.abs(f), axis=(2, 3)) * (np.float32(1) / most)
+    with np.errstate(invalid="ignore", divide="ignore"):
+        y = np.nan_to_num(f / scale[:, :, None, None], nan=0.0, posinf=most, neginf=-most)
+    y = np.clip(y, -most, most)
+    if kind == "int8":
+        return np.rint(y).astype(np.int8), scale
+    # nearest of the 127 finite magnitudes, ties to the even code
+    mags = e4m3(np.arange(127, dtype=np.uint8))
+    a = np.abs(y).astype(np.float64)
+    hi = np.clip(np.searchsorted(mags, a), 1, 126)
+    lo = hi - 1
+    up, down = mags[hi] - a, a - mags[lo]
+    code = np.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo)
+    return (code | np.where(np.signbit(y), 128, 0)).astype(np.uint8), scale
+
+
 def e4m3(codes):
     """Values of OCP E4M3 bytes (1 sign, 4 exponent, 3 mantissa bits, bias 7)."""
     c = codes.astype(np.int64)

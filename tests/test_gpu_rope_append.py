@@ -1,7 +1,9 @@
 """Rotation of a ragged batch on its way into the paged cache, on the GPU: the
 queries, pools, codes and scales equal the fp32 steps of the definition (each
-product and sum rounded, no fused multiply-add) bit for bit, and the rotated
-values are within their roundings of the 64-bit rotation."""
+product and sum rounded, no fused multiply-add; scale = amax times the fp32
+reciprocal of the largest code) bit for bit, the rotated values are within
+their roundings of the 64-bit rotation, and the codes stand next to those of
+the plain quantizer."""
 import numpy as np
 import pytest
 import torch
@@ -68,8 +70,7 @@ class Run:
             quant = oracle.quantize_fp8 if self.kind == "fp8" else oracle.quantize
             for x, pool, old in ((0, k, self.b.k), (1, v, self.b.v)):
                 codes, scales = quant(old)
-                c2, s2 = quant(pool)
-                codes[written], scales[written] = c2[written], s2[written]
+                codes[written], scales[written] = R.quantize(pool[written], self.kind)
                 assert np.array_equal(self.codes[x].cpu().numpy(), codes)
                 assert np.array_equal(self.codes[2 + x].cpu().numpy().view(np.uint32),
                                       scales.view(np.uint32))
@@ -137,6 +138,26 @@ def test_against_the_64_bit_rotation(interleaved):
     # (the fp64 angle itself: positions * f rounded, 200040 * 2^-53, nothing)
     tol = 2.0 ** -11 * np.abs(want) + 2.0 ** -25 + (2.0 ** -25 + 3 * 2.0 ** -24) * 1.001 * size
     assert np.all(np.abs(r.q_out.cpu().numpy() - want) <= tol)
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+def test_codes_next_to_the_plain_quantizers(kind):
+    # the scales differ by 2^-23 at most (a product and its rounded constant
+    # against a quotient, half a step each), so a code differs only where its
+    # quotient lies within 2^-22 of a border, and then by one step
+    b = R.make(65, [200], [200], 4, 2, 128, nan_tail=False)
+    qkv = qkv_of(b, 65, 200)
+    r = Run(b, kind, qkv, table(200, 128))()
+    quant = oracle.quantize_fp8 if kind == "fp8" else oracle.quantize
+    for x, pool in ((0, r.k), (1, r.v)):
+        codes, scales = quant(pool.cpu().numpy())
+        used = b.used
+        got_c, got_s = r.codes[x].cpu().numpy()[used], r.codes[2 + x].cpu().numpy()[used]
+        assert np.all(np.abs(got_s / scales[used].astype(np.float64) - 1) <= 1.01 * 2.0 ** -23)
+        differ = got_c != codes[used]
+        assert np.mean(differ) < 1e-4
+        step = got_c[differ].astype(np.int64) - codes[used][differ].astype(np.int64)
+        assert np.all(np.abs(step) == 1)
 
 
 @pytest.mark.parametrize("kind", ["fp16", "int8"])
