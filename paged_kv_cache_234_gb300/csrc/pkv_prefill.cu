@@ -27,8 +27,7 @@
 //
 // Roles of the warps: 0-15 the rows of the two tiles (two threads per row, 64
 // columns of S each), 16 issues the products, 17 and 19 the TMA loads of K and
-// V (a ring of tiles of 128 keys, K and V in turn), 18 zeroes rows of V that
-// must not count.  INT8 / FP8 pages land in a second ring, and warps 20-23
+// V (a ring of tiles of 128 keys, K and V in turn).  INT8 / FP8 pages land in a second ring, and warps 20-23
 // widen them exactly to fp16; the K scales multiply the scores, the V scales enter
 // the probabilities as a ratio to the largest one so far.
 //
@@ -93,7 +92,7 @@ struct Smem {
     static constexpr int kRing = 2 * kTileBytes;
     static constexpr int kCodeRing = kRing + kStages * kTileBytes;
     static constexpr int kCtl = kCodeRing + kCodeStages * kCodeBytes;
-    static constexpr int kBars = 2 * kStages + 2 * kCodeStages + 9;
+    static constexpr int kBars = 3 * kStages + 2 * kCodeStages + 8;
     // scales [kScaleTiles][K, V][8 pages]: the loads run at most five tiles
     // ahead of the softmax (the code ring, the ring and the tile at work)
     static constexpr int kScaleTiles = 8;
@@ -337,7 +336,8 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
     auto s_full = [&](int i) { return one + 16 + 8 * i; };
     auto p_full = [&](int i) { return one + 32 + 8 * i; };
     auto o_full = [&](int i) { return one + 48 + 8 * i; };
-    [[maybe_unused]] const uint32_t fixed = one + 64;
+    // one per stage: V is fixed tiles ahead of the products
+    [[maybe_unused]] auto fixed = [&](int s) { return one + 64 + 8 * s; };
     volatile int *flags = reinterpret_cast<volatile int *>(smem + M::kFlags);  // abort, bad, tmem
     const Waiter wait{flags, p.dev_status};
 
@@ -374,6 +374,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
         for (int s = 0; s < S; ++s) {
             ptx::mbar_init(full(s), kCodes ? 128 : 1);
             ptx::mbar_init(empty(s), 1);
+            ptx::mbar_init(fixed(s), 1);
         }
         for (int s = 0; s < M::kCodeStages; ++s) {
             ptx::mbar_init(cfull(s), 1);
@@ -381,7 +382,6 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
         }
         ptx::mbar_init(q_full, kSoftWarps);
         ptx::mbar_init(drain, 1);
-        ptx::mbar_init(fixed, 1);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(s_full(i), 1);
             ptx::mbar_init(p_full(i), kSoftWarps / 2);
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                 }
                 int sv = 0;                  // stage of the last element taken
                 uint32_t phase = 0;          // its parity
-                [[maybe_unused]] int fixes = 0;
+                [[maybe_unused]] uint32_t fixes = 0;  // parity of each stage's fixes
                 for (int j = 0; j < nt && ok; ++j) {
                     if (++sv == S) {
                         sv = 0;
@@ -664,7 +664,10 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                     const int sk = sv + 1 == S ? 0 : sv + 1;
                     const uint32_t kphase = sv + 1 == S ? phase ^ 1 : phase;
                     ok = wait.one(full(sv), phase);
-                    if (!kCodes && ok && it.dirty(it.ta + j)) ok = wait.one(fixed, fixes++ & 1);
+                    if (!kCodes && ok && it.dirty(it.ta + j)) {
+                        ok = wait.one(fixed(sv), fixes >> sv & 1u);
+                        fixes ^= 1u << sv;
+                    }
                     for (int i = 0; i <= last && ok; ++i) {
                         ok = wait.one(p_full(i), j & 1);
                         if (!ok) break;
@@ -752,42 +755,46 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                     }
                 }
                 __syncwarp();
-            }
-            // leave no copy in flight: every stage that was issued has landed
-            for (int e = max(0, j - R); e < j; ++e) {
-                const int n = 2 * e + (is_v ? 1 : 0);
-                ptx::mbar_wait_bounded(kCodes ? cfull(n % R) : full(n % R), (n / R) & 1,
-                                       kWaitLimitNs);
-            }
-        } else if (!kCodes && warp == kSoftWarps + 2) {
-            // ------------------------------------------------ stale rows of V
-            // Rows that no row of the item sees may hold anything, NaN
-            // included (and are not loaded for pages past the last): zeros.
-            for (int j = 0; j < nt; ++j) {
-                if (!it.dirty(it.ta + j)) continue;
-                const int n = 2 * j + 1;
-                if (!wait(full(n % S), (n / S) & 1)) break;
-                const uint32_t stage = base + M::kRing + (n % S) * M::kTileBytes;
-                const int v = (it.ta + j) * kPagesPerTile + lane;
-                uint32_t lv = 0xffffu;
-                if (lane < kPagesPerTile) lv = v < it.visited ? it.live(it.real(v) * kPage) : 0u;
-                unsigned todo = __ballot_sync(0xffffffffu, lv != 0xffffu);
-                while (todo) {
-                    const int g = __ffs(todo) - 1;
-                    todo &= todo - 1;
-                    const uint32_t keep = __shfl_sync(0xffffffffu, lv, g);
-                    for (int e = lane; e < kPage * kRowChunks; e += 32) {
-                        const int row = e / kRowChunks, ch = e % kRowChunks;
-                        if (!(keep >> row & 1u))
-                            st_shared16(stage + (ch >> 3) * M::kHalfBytes +
-                                            (g * kPage + row) * 128 + ((ch & 7) << 4),
-                                        make_uint4(0, 0, 0, 0));
+                if constexpr (!kCodes)
+                    if (is_v && it.dirty(it.ta + j)) {
+                        // rows of V that no row of the item sees may hold
+                        // anything, NaN included (and are not loaded for pages
+                        // past the last): zeros.  The products wait for this,
+                        // so the stage is not filled again meanwhile.
+                        if (!wait(fb, (n / R) & 1)) {
+                            ++j;
+                            break;
+                        }
+                        const int v = (it.ta + j) * kPagesPerTile + lane;
+                        uint32_t lv = 0xffffu;
+                        if (lane < kPagesPerTile)
+                            lv = v < it.visited ? it.live(it.real(v) * kPage) : 0u;
+                        unsigned todo = __ballot_sync(0xffffffffu, lv != 0xffffu);
+                        while (todo) {
+                            const int g = __ffs(todo) - 1;
+                            todo &= todo - 1;
+                            const uint32_t keep = __shfl_sync(0xffffffffu, lv, g);
+                            for (int e = lane; e < kPage * kRowChunks; e += 32) {
+                                const int row = e / kRowChunks, ch = e % kRowChunks;
+                                if (!(keep >> row & 1u))
+                                    st_shared16(dst + (ch >> 3) * M::kHalfBytes +
+                                                    (g * kPage + row) * 128 + ((ch & 7) << 4),
+                                                make_uint4(0, 0, 0, 0));
+                            }
+                        }
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(fixed(s));
                     }
-                }
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(fixed);
             }
+            // The products have waited for every copy, unless a wait ran out:
+            // then leave none of this warp's in flight.
+            if (*wait.abort)
+                for (int e = max(0, j - R); e < j; ++e) {
+                    const int n = 2 * e + (is_v ? 1 : 0);
+                    ptx::mbar_wait_bounded(kCodes ? cfull(n % R) : full(n % R), (n / R) & 1,
+                                           kWaitLimitNs);
+                }
         }
     } else {
         if constexpr (kCodes) {

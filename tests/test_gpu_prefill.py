@@ -128,6 +128,28 @@ def test_split_over_the_keys(kind, option):
     check(b, kind, option)
 
 
+@pytest.mark.parametrize("kind", ["fp16", "int8", "fp8"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("option", ["plain", "all", "window_prefix"])
+def test_long_without_a_split(kind, dim, option):
+    # enough items to fill the GPU: every item walks all of its keys, many
+    # times around the ring of tiles
+    b = R.make(17, [9, 1, 30, 4], [2300, 1555, 1900, 800], 76, 76, dim)
+    assert pkv.pkv_prefill_workspace_size(44, 4, 76, 76, dim, 2300) == 0
+    # (the reference of every fourth head)
+    o = expand(b, dict(OPTIONS[option], window=700) if option != "plain" else option)
+    pools, kv64 = R.cache(b, kind)
+    got, status = Run(b, kind, pools, **o)()
+    b.heads = 19
+    pick = lambda x: np.ascontiguousarray(x[:, ::4])  # noqa: E731
+    b.q, b.kv_heads = pick(b.q), 19
+    ref, mass = R.attend(b, tuple(pick(x) for x in kv64), b.dim ** -0.5,
+                         **dict(o, slopes=None if o["slopes"] is None else o["slopes"][::4]))
+    assert status == 0
+    worst = np.max(np.abs(got[:, ::4] - ref) / bound(b, kind, o, ref, mass))
+    assert worst <= 1.0, worst
+
+
 def test_split_with_a_window_and_a_prefix_far_apart():
     # most splits of the second sequence have no keys
     b = R.make(6, [5, 9], [4001, 50], 4, 1, 64)
