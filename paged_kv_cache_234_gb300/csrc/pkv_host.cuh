@@ -30,6 +30,11 @@ bool current_device_info(DeviceInfo *out);
 bool encode_tmap_2d(CUtensorMap *map, const void *base, int elem_bytes, uint64_t inner_elems,
                     uint64_t rows, uint32_t box_inner, uint32_t box_rows, int swizzle_bytes);
 
+// The same for fp16 values [depth][rows][inner] (dense), with a box of
+// box_inner x box_rows x box_depth values and the 128-byte swizzle.
+bool encode_tmap_3d_f16(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows,
+                        uint64_t depth, uint32_t box_inner, uint32_t box_rows, uint32_t box_depth);
+
 // Decode workers at most (pkv_set_decode_workers; 0: automatic), and the lock
 // of it and of the launches' per-device caches.
 extern int g_worker_cap;

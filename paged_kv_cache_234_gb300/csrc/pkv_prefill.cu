@@ -75,6 +75,8 @@ struct PrefillArgs {
     float2 *part_ml;    // [splits][num_tokens * num_heads]: maximum, sum
     int32_t *dev_status;
     int num_tokens, num_seqs, num_heads, num_kv_heads, group;
+    int chunk, chunks;  // heads of a kv head per item (the group, at most 256), chunks of them
+    int tokens;         // tokens per item: 256 / chunk
     int max_blocks_per_seq, num_blocks, ctx_cap, window, splits, units;
     float scale_log2, cap, cap_inv;
 };
@@ -85,20 +87,22 @@ struct Smem {
     static constexpr bool kCodes = kKv != kKvF16;
     static constexpr int kHalves = kD / 64;
     static constexpr int kHalfBytes = kTile * 128;             // 64 values of 128 rows
-    static constexpr int kTileBytes = kHalves * kHalfBytes;    // 128 rows of Q, K or V
+    static constexpr int kTileBytes = kHalves * kHalfBytes;    // 128 rows of K or V
+    static constexpr int kQHalfBytes = kRows * 128;            // 64 values of the item's rows
     static constexpr int kCodeBytes = kTile * kD;
     static constexpr int kStages = kCodes ? (kD == 128 ? 3 : 6) : (kD == 128 ? 5 : 10);
     static constexpr int kCodeStages = kCodes ? 4 : 0;
     static constexpr int kRing = 2 * kTileBytes;
     static constexpr int kCodeRing = kRing + kStages * kTileBytes;
     static constexpr int kCtl = kCodeRing + kCodeStages * kCodeBytes;
-    static constexpr int kBars = 3 * kStages + 2 * kCodeStages + 8;
+    static constexpr int kBars = 3 * kStages + 2 * kCodeStages + 16;
     // scales [kScaleTiles][K, V][8 pages]: the loads run at most five tiles
     // ahead of the softmax (the code ring, the ring and the tile at work)
     static constexpr int kScaleTiles = 8;
-    static constexpr int kScales = kCtl + 8 * kBars;
-    static constexpr int kFlags =
-        kScales + (kCodes ? kScaleTiles * 2 * kPagesPerTile * 4 : 0);
+    static constexpr int kNext = (kCtl + 8 * kBars + 15) & ~15;   // answer of the launch queue
+    static constexpr int kScales = kNext + 16;
+    static constexpr int kItems = kScales + (kCodes ? kScaleTiles * 2 * kPagesPerTile * 4 : 0);
+    static constexpr int kFlags = kItems + 2 * 64;
     static constexpr int kSwap = kFlags + 16;                  // [2 tiles][2 halves][128 rows]
     static constexpr int kBytes = kSwap + 2 * 2 * kTile * 4;
     // a second CTA on the SM would wait for TMEM: ask for more than half
@@ -138,14 +142,16 @@ struct Waiter {
 };
 
 // ------------------------------------------------------------------- items
-struct Item {
-    int seq, kvh, row0, rows;   // first row of the item among the sequence's, rows
-    int start;                  // first token of the sequence
-    int pos0;                   // position of the sequence's first new token
+struct __align__(16) Item {
+    int seq, kvh;
+    int tok, toks;              // first token (of the batch) and tokens of the item
+    int head, heads;            // first query head and heads
+    int pos;                    // position of the first token
+    int z;                      // split
     int lo, hi, pre;            // keys of the item: lo .. hi and below pre
     int np1, gap, visited;      // pages: np1, a gap, the rest (see the decode)
-    int ta, tb;                 // tiles of this split
-    bool ok;
+    int ta;                     // first tile of keys
+    int nt;                     // tiles of keys; 0: no further item
 
     __device__ __forceinline__ int real(int v) const { return v + (v >= np1 ? gap : 0); }
 
@@ -164,47 +170,48 @@ struct Item {
     }
 };
 
-// The item of unit u; false if the unit names none.
-__device__ __forceinline__ bool find_item(const PrefillArgs &p, int u, int kvh, int z, Item &it)
+static_assert(sizeof(Item) == 64, "an item is 64 bytes of shared memory");
+
+// The item of a block number: 1 an item with keys, 0 one without (its rows are
+// then zeros), -1 none.  The units with the most keys (the last ones of a
+// sequence) first; kv heads, chunks of heads and key splits side by side.
+__device__ __forceinline__ int find_item(const PrefillArgs &p, int block, Item &it, bool &bad)
 {
-    auto base_of = [&](int s) -> int64_t {
-        return static_cast<int64_t>(__ldg(p.query_starts + s)) * p.group / kRows + s;
+    const int per_unit = p.num_kv_heads * p.chunks * p.splits;
+    const int u = p.units - 1 - block / per_unit;
+    int sub = block % per_unit;
+    it.z = sub % p.splits;
+    sub /= p.splits;
+    const int c = sub % p.chunks;
+    it.kvh = sub / p.chunks;
+    auto base_of = [&](int s) -> int {
+        return __ldg(p.query_starts + s) / p.tokens + s;
     };
-    const int seq = warp_search(p.num_seqs, u, base_of);
-    if (seq < 0) return false;
+    it.seq = warp_search(p.num_seqs, u, base_of);
+    if (it.seq < 0) return -1;
     SeqRows sr;
-    sr.load(p.query_starts, p.context_lens, seq, p.num_tokens, p.ctx_cap);
-    const int64_t row0 = (u - base_of(seq)) * kRows;
-    const int64_t rows = static_cast<int64_t>(sr.len) * p.group - row0;
-    if (rows <= 0) return false;
-    it.seq = seq;
-    it.kvh = kvh;
-    it.row0 = static_cast<int>(row0);
-    it.rows = static_cast<int>(rows < kRows ? rows : kRows);
-    it.start = sr.start;
-    it.ok = sr.ok;
-    it.pos0 = sr.ctx - sr.len;
-    if (!sr.ok) return true;
-    const int first = it.pos0 + it.row0 / p.group;
-    const int last = it.pos0 + (it.row0 + it.rows - 1) / p.group;
-    it.lo = p.window > 0 && first >= p.window ? first - p.window + 1 : 0;
-    it.hi = last;
-    it.pre = p.prefix_lens ? min(max(__ldg(p.prefix_lens + seq), 0), sr.ctx) : 0;
+    sr.load(p.query_starts, p.context_lens, it.seq, p.num_tokens, p.ctx_cap);
+    const int64_t t0 = static_cast<int64_t>(u - base_of(it.seq)) * p.tokens;
+    if (t0 < 0 || t0 >= sr.len) return -1;
+    it.tok = sr.start + static_cast<int>(t0);
+    it.toks = min(p.tokens, sr.len - static_cast<int>(t0));
+    it.head = it.kvh * p.group + c * p.chunk;
+    it.heads = min(p.chunk, p.group - c * p.chunk);
+    it.ta = it.nt = 0;
+    bad = !sr.ok;
+    if (bad) return 0;
+    it.pos = sr.ctx - sr.len + static_cast<int>(t0);
+    it.hi = it.pos + it.toks - 1;
+    it.lo = p.window > 0 && it.pos >= p.window ? it.pos - p.window + 1 : 0;
+    it.pre = p.prefix_lens ? min(max(__ldg(p.prefix_lens + it.seq), 0), sr.ctx) : 0;
     const int fp = it.lo / kPage;
     it.np1 = min((it.pre + kPage - 1) / kPage, fp);
     it.gap = fp - it.np1;
-    it.visited = max(last, it.pre - 1) / kPage + 1 - it.gap;
+    it.visited = max(it.hi, it.pre - 1) / kPage + 1 - it.gap;
     const int tiles = (it.visited + kPagesPerTile - 1) / kPagesPerTile;
-    it.ta = static_cast<int>(static_cast<int64_t>(tiles) * z / p.splits);
-    it.tb = static_cast<int>(static_cast<int64_t>(tiles) * (z + 1) / p.splits);
-    return true;
-}
-
-// Row r of the item: its index among all (token, head) rows of the batch.
-__device__ __forceinline__ int64_t row_at(const PrefillArgs &p, const Item &it, int r)
-{
-    const int q = it.row0 + r, j = q / p.group;
-    return (static_cast<int64_t>(it.start) + j) * p.num_heads + it.kvh * p.group + (q - j * p.group);
+    it.ta = static_cast<int>(static_cast<int64_t>(tiles) * it.z / p.splits);
+    it.nt = static_cast<int>(static_cast<int64_t>(tiles) * (it.z + 1) / p.splits) - it.ta;
+    return it.nt > 0;
 }
 
 // ------------------------------------------------------------------ kernel
@@ -245,19 +252,6 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint4 v)
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
                  "r"(v.w)
                  : "memory");
-}
-
-// Exchange between the two halves of a tile's columns (256 threads).  A warp
-// whose wait ran out arrives without waiting, so that the others get through:
-// they then find no further product coming, and give up at their own wait.
-__device__ __forceinline__ void swap_sync(int tile)
-{
-    asm volatile("bar.sync %0, 256;" ::"r"(tile + 1) : "memory");
-}
-
-__device__ __forceinline__ void swap_arrive(int tile)
-{
-    asm volatile("bar.arrive %0, 256;" ::"r"(tile + 1) : "memory");
 }
 
 // The largest of a thread's scores.
@@ -308,13 +302,18 @@ __device__ __forceinline__ void cap_scores(float (&x)[kCols], float cap, float c
     }
 }
 
-// kMod: any of cap, bias or scales, or a scale that is not positive -- the scores are
-// worked out before their maximum is taken.  Without it the scale is folded
-// into the exponent.
+// kMod: any of cap, bias or scales, or a scale that is not positive -- the
+// scores are worked out before their maximum is taken.  Without it the scale
+// is folded into the exponent.
+//
+// One CTA per SM, which takes the block numbers of CTAs that have not started
+// (cluster launch control) as long as there are any: a warp asks for the next
+// one, works out its item and hands it to the others, so that loads and
+// products of an item begin while the last one's rows are written.
 template <int kKv, int kD, bool kMod>
 __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
-    prefill_kernel(const __grid_constant__ PrefillArgs p, const __grid_constant__ CUtensorMap tmk,
-                   const __grid_constant__ CUtensorMap tmv)
+    prefill_kernel(const __grid_constant__ PrefillArgs p, const __grid_constant__ CUtensorMap tmq,
+                   const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv)
 {
     using M = Smem<kKv, kD>;
     constexpr bool kCodes = M::kCodes;
@@ -332,43 +331,22 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
         return base + M::kCtl + 8 * (2 * S + M::kCodeStages + s);
     };
     const uint32_t one = base + M::kCtl + 8 * (2 * S + 2 * M::kCodeStages);
-    const uint32_t q_full = one, drain = one + 8;
-    auto s_full = [&](int i) { return one + 16 + 8 * i; };
-    auto p_full = [&](int i) { return one + 32 + 8 * i; };
-    auto o_full = [&](int i) { return one + 48 + 8 * i; };
+    const uint32_t q_full = one, q_empty = one + 8, drain = one + 16, next_full = one + 24;
+    auto s_full = [&](int i) { return one + 32 + 8 * i; };
+    auto p_full = [&](int i) { return one + 48 + 8 * i; };
+    auto o_full = [&](int i) { return one + 64 + 8 * i; };
+    auto swapped = [&](int i) { return one + 80 + 8 * i; };
+    auto i_full = [&](int k) { return one + 96 + 8 * (k & 1); };
+    auto i_empty = [&](int k) { return one + 112 + 8 * (k & 1); };
     // one per stage: V is fixed tiles ahead of the products
-    [[maybe_unused]] auto fixed = [&](int s) { return one + 64 + 8 * s; };
-    volatile int *flags = reinterpret_cast<volatile int *>(smem + M::kFlags);  // abort, bad, tmem
+    [[maybe_unused]] auto fixed = [&](int s) { return one + 128 + 8 * s; };
+    volatile int *flags = reinterpret_cast<volatile int *>(smem + M::kFlags);
+    // flags: abort, bad of item slot 0, of slot 1, TMEM address
     const Waiter wait{flags, p.dev_status};
-
-    ptx::griddep_wait();
-    ptx::griddep_launch_dependents();
-
-    // the units with the most keys (the last ones of a sequence) first; the
-    // kv heads and key splits of a unit side by side
-    const int per_unit = p.num_kv_heads * p.splits;
-    const int u = p.units - 1 - static_cast<int>(blockIdx.x / per_unit);
-    const int sub = static_cast<int>(blockIdx.x % per_unit);
-    const int z = sub % p.splits;
-    Item it;
-    if (!find_item(p, u, sub / p.splits, z, it)) return;
-    const int nt = it.ok ? it.tb - it.ta : 0;
-    if (nt == 0) {
-        // a sequence that does not fit (zeros), or a split without keys
-        if (!it.ok && it.row0 == 0 && sub == 0 && threadIdx.x == 0 && p.dev_status)
-            atomicOr(p.dev_status, PKV_DEV_BAD_CTX);
-        for (int i = threadIdx.x; i < it.rows * kRowChunks; i += blockDim.x) {
-            const int64_t row = row_at(p, it, i / kRowChunks);
-            if (row < 0 || row >= static_cast<int64_t>(p.num_tokens) * p.num_heads) continue;
-            if (p.splits == 1)
-                reinterpret_cast<uint4 *>(p.out + row * kD)[i % kRowChunks] = make_uint4(0, 0, 0, 0);
-            else if (i % kRowChunks == 0)
-                p.part_ml[static_cast<int64_t>(z) * p.num_tokens * p.num_heads + row] =
-                    make_float2(-INFINITY, 0.f);
-        }
-        return;
-    }
-    const bool two = it.rows > kTile;
+    // the k-th item of this CTA
+    auto item = [&](int k) -> Item & {
+        return *reinterpret_cast<Item *>(smem + M::kItems + 64 * (k & 1));
+    };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -380,21 +358,28 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
             ptx::mbar_init(cfull(s), 1);
             ptx::mbar_init(cempty(s), 128);
         }
-        ptx::mbar_init(q_full, kSoftWarps);
+        ptx::mbar_init(q_full, 1);
+        ptx::mbar_init(q_empty, 1);
         ptx::mbar_init(drain, 1);
+        ptx::mbar_init(next_full, 1);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(s_full(i), 1);
             ptx::mbar_init(p_full(i), kSoftWarps / 2);
             ptx::mbar_init(o_full(i), 1);
+            ptx::mbar_init(swapped(i), kSoftWarps / 2);
+            ptx::mbar_init(i_full(i), 1);
+            ptx::mbar_init(i_empty(i), kSoftWarps + 3 + (kCodes ? 4 : 0));
         }
         ptx::fence_mbar_init();
-        flags[0] = flags[1] = 0;
+        flags[0] = flags[1] = flags[2] = 0;
     }
-    if (warp == kSoftWarps) umma::alloc(base + M::kFlags + 8, 512);
+    if (warp == kSoftWarps) umma::alloc(base + M::kFlags + 12, 512);
     umma::fence_before();
     __syncthreads();
     umma::fence_after();
-    const uint32_t tmem = __shfl_sync(0xffffffffu, static_cast<uint32_t>(flags[2]), 0);
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, static_cast<uint32_t>(flags[3]), 0);
     auto t_s = [&](int i) { return tmem + kTile * i; };            // S, then P, of tile i
     auto t_o = [&](int i) { return tmem + 2 * kTile + kD * i; };   // O of tile i
 
@@ -402,52 +387,47 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
         // ------------------------------------------------ rows of the tiles
         more_registers<kKv>();
         const int i = warp >> 3, half = warp >> 2 & 1;  // tile, half of its columns
-        const int tid = threadIdx.x & (2 * kTile - 1);
         const int rt = threadIdx.x & (kTile - 1);       // row of the tile
         const int r = kTile * i + rt;                   // row of the item
-        {
-            // the tile's queries, K-major with the 128-byte swizzle; 16 bytes
-            // a thread, neighbouring threads along a row
-            const uint32_t dst = base + i * M::kTileBytes;
-#pragma unroll 4
-            for (int e = tid; e < kTile * kRowChunks; e += 2 * kTile) {
-                const int row = e / kRowChunks, ch = e % kRowChunks;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (kTile * i + row < it.rows)
-                    v = __ldg(reinterpret_cast<const uint4 *>(
-                                  p.query + row_at(p, it, kTile * i + row) * kD) + ch);
-                st_shared16(dst + (ch >> 3) * M::kHalfBytes + row * 128 +
-                                (((ch & 7) ^ (row & 7)) << 4), v);
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 (w mod 4)
+        float *sw = reinterpret_cast<float *>(smem + M::kSwap) + i * 2 * kTile;
+        const int rj = r / p.chunk, rh = r - rj * p.chunk;  // token and head of the row
+        // log2 units throughout; without kMod x stays as the product left it
+        // and the scale enters with the exponent
+        const float sl = kMod ? 1.f : p.scale_log2;
+        uint32_t steps = 0;   // tiles of keys of this tile of rows so far
+        uint32_t swaps = 0, outs = 0;
+        [[maybe_unused]] uint32_t tiles = 0;  // tiles of keys of the CTA so far
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            ok = wait(i_full(k), k >> 1 & 1);
+            if (!ok) break;
+            const Item &it = item(k);
+            const int nt = it.nt;
+            if (nt == 0) break;
+            const int rows = it.toks * p.chunk;
+            if (i == 1 && rows <= kTile) {
+                tiles += nt;
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(i_empty(k));
+                continue;
             }
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(q_full);
-        }
-        if (i == 0 || two) {
-            const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 (w mod 4)
-            const int rr = min(r, it.rows - 1);
-            const int q = it.row0 + rr;
-            const int pos = it.pos0 + q / p.group;
+            const int pos = it.pos + min(rj, it.toks - 1);
             const int lo = p.window > 0 ? pos - p.window + 1 : 0;
+            const int pre = it.pre;
             // positions of the tile's first and last row: which tiles of keys
             // all of its rows see
-            const int pos_a = it.pos0 + (it.row0 + kTile * i) / p.group;
-            const int pos_b = it.pos0 + (it.row0 + min(kTile * i + kTile, it.rows) - 1) / p.group;
+            const int pos_a = it.pos + kTile * i / p.chunk;
+            const int pos_b = it.pos + (min(kTile * i + kTile, rows) - 1) / p.chunk;
             float slope = 0.f;
-            if (kMod && p.slopes)
-                slope = __ldg(p.slopes + it.kvh * p.group + q % p.group) * 1.4426950408889634f;
+            if (kMod && p.slopes && rh < it.heads)
+                slope = __ldg(p.slopes + it.head + rh) * 1.4426950408889634f;
             float m = -INFINITY, l = 0.f;
-            float vref = 0.f, vinv = 0.f;
-            bool ok = true;
-            // log2 units throughout; without kMod x stays as the product left
-            // it and the scale enters with the exponent
-            const float sl = kMod ? 1.f : p.scale_log2;
-            for (int j = 0; j < nt && ok; ++j) {
-                ok = wait(s_full(i), j & 1);
-                if (!ok) {
-                    swap_arrive(i);
-                    break;
-                }
+            [[maybe_unused]] float vref = 0.f, vinv = 0.f;
+            for (int j = 0; j < nt; ++j) {
+                ok = wait(s_full(i), steps & 1);
+                if (!ok) break;
+                ++steps;
                 umma::fence_after();
                 // first page of the thread's columns
                 const int v0 = (it.ta + j) * kPagesPerTile + half * (kPagesPerTile / 2);
@@ -457,14 +437,14 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                     umma::ld32(t_s(i) + lanes + half * kCols + c, x + c);
                 [[maybe_unused]] const float *vs =
                     reinterpret_cast<const float *>(smem + M::kScales) +
-                    ((it.ta + j) & (M::kScaleTiles - 1)) * 2 * kPagesPerTile + kPagesPerTile;
+                    (tiles & (M::kScaleTiles - 1)) * 2 * kPagesPerTile + kPagesPerTile;
                 [[maybe_unused]] const float *ks = vs - kPagesPerTile + half * (kPagesPerTile / 2);
                 float ov = 1.f;  // change of the V reference
                 if constexpr (kCodes) {
+                    ++tiles;
                     float most = 0.f;
 #pragma unroll
-                    for (int g = 0; g < kPagesPerTile; ++g)
-                        most = fmaxf(most, vs[g]);
+                    for (int g = 0; g < kPagesPerTile; ++g) most = fmaxf(most, vs[g]);
                     if (most > kVLazy * vref) {
                         vinv = __frcp_rn(most);
                         ov = vref * vinv;
@@ -494,15 +474,15 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                         }
                     }
                 }
-                const int tmin = it.real(v0) * kPage, tmax = it.real(v0 + kPagesPerTile / 2 - 1) * kPage + kPage - 1;
-                if (!((tmax <= pos_a && (p.window <= 0 || tmin > pos_b - p.window)) ||
-                      tmax < it.pre)) {
+                const int tmin = it.real(v0) * kPage;
+                const int tmax = it.real(v0 + kPagesPerTile / 2 - 1) * kPage + kPage - 1;
+                if (!((tmax <= pos_a && (p.window <= 0 || tmin > pos_b - p.window)) || tmax < pre)) {
                     // some row of the tile does not see some key
 #pragma unroll
                     for (int g = 0; g < kPagesPerTile / 2; ++g) {
                         const int t0 = it.real(v0 + g) * kPage;
                         const uint32_t seen =
-                            (below(pos + 1 - t0) & ~below(lo - t0)) | below(it.pre - t0);
+                            (below(pos + 1 - t0) & ~below(lo - t0)) | below(pre - t0);
 #pragma unroll
                         for (int c = 0; c < kPage; ++c)
                             if (!(seen >> c & 1u)) x[kPage * g + c] = -INFINITY;
@@ -512,9 +492,12 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                 // other one (the buffer is free again: S of this tile was not
                 // started before both halves of the last one were through)
                 float top = row_max(x) * sl;
-                float *sw = reinterpret_cast<float *>(smem + M::kSwap) + i * 2 * kTile;
                 sw[half * kTile + rt] = top;
-                swap_sync(i);
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(swapped(i));
+                ok = wait(swapped(i), swaps & 1);
+                if (!ok) break;
+                ++swaps;
                 top = fmaxf(top, sw[(half ^ 1) * kTile + rt]);
                 if (__any_sync(0xffffffffu, top > m + kLazy || ov != 1.f)) {
                     const float mn = fmaxf(m, top);
@@ -566,56 +549,64 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(p_full(i));
             }
-            ok = ok && wait(o_full(i), 0);
-            if (!ok) swap_arrive(i);
-            if (ok) {
-                umma::fence_after();
-                // the sums of the two halves, in their order
-                float *sw = reinterpret_cast<float *>(smem + M::kSwap) + i * 2 * kTile;
-                sw[half * kTile + rt] = l;
-                swap_sync(i);
-                l = sw[rt] + sw[kTile + rt];
-                const bool bad = flags[1] != 0;
-                const bool mine = r < it.rows;
-                const int64_t row = row_at(p, it, rr);
-                const int64_t all = static_cast<int64_t>(p.num_tokens) * p.num_heads;
-                const float vs = kCodes ? vref : 1.f;
-                if (p.splits == 1) {
-                    const float f = l > 0.f ? vs / l : l;  // an empty row: zeros; NaN stays
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * kD);
+            ok = ok && wait(o_full(i), outs & 1);
+            if (!ok) break;
+            ++outs;
+            umma::fence_after();
+            // the sums of the two halves, in their order
+            sw[half * kTile + rt] = l;
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(swapped(i));
+            ok = wait(swapped(i), swaps & 1);
+            if (!ok) break;
+            ++swaps;
+            l = sw[rt] + sw[kTile + rt];
+            const bool bad = flags[1 + (k & 1)] != 0;
+            const bool mine = rj < it.toks && rh < it.heads;
+            const int64_t row =
+                static_cast<int64_t>(it.tok + rj) * p.num_heads + it.head + rh;
+            const float vs = kCodes ? vref : 1.f;
+            if (p.splits == 1) {
+                const float f = l > 0.f ? vs / l : l;  // an empty row: zeros; NaN stays
+                uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * kD);
 #pragma unroll
-                    for (int c = half * (kD / 2); c < (half + 1) * (kD / 2); c += 32) {
-                        float o[32];
-                        umma::ld32(t_o(i) + lanes + c, o);
-                        umma::wait_ld();
+                for (int c = half * (kD / 2); c < (half + 1) * (kD / 2); c += 32) {
+                    float o[32];
+                    umma::ld32(t_o(i) + lanes + c, o);
+                    umma::wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = bad ? 0.f : o[e] * f;
-                        if (mine) {
+                    for (int e = 0; e < 32; ++e) o[e] = bad ? 0.f : o[e] * f;
+                    if (mine) {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 8)
-                                dst[(c + e) / 8] = make_uint4(
-                                    pack2(o[e], o[e + 1]), pack2(o[e + 2], o[e + 3]),
-                                    pack2(o[e + 4], o[e + 5]), pack2(o[e + 6], o[e + 7]));
-                        }
-                    }
-                } else {
-                    float4 *dst = reinterpret_cast<float4 *>(p.part_acc + (z * all + row) * kD);
-                    if (mine && half == 0) p.part_ml[z * all + row] = make_float2(m, bad ? -1.f : l);
-#pragma unroll
-                    for (int c = half * (kD / 2); c < (half + 1) * (kD / 2); c += 32) {
-                        float o[32];
-                        umma::ld32(t_o(i) + lanes + c, o);
-                        umma::wait_ld();
-                        if (mine) {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                dst[(c + e) / 4] = make_float4(o[e] * vs, o[e + 1] * vs,
-                                                               o[e + 2] * vs, o[e + 3] * vs);
-                        }
+                        for (int e = 0; e < 32; e += 8)
+                            dst[(c + e) / 8] = make_uint4(
+                                pack2(o[e], o[e + 1]), pack2(o[e + 2], o[e + 3]),
+                                pack2(o[e + 4], o[e + 5]), pack2(o[e + 6], o[e + 7]));
                     }
                 }
-                umma::fence_before();
+            } else {
+                const int64_t at =
+                    static_cast<int64_t>(it.z) * p.num_tokens * p.num_heads + row;
+                float4 *dst = reinterpret_cast<float4 *>(p.part_acc + at * kD);
+                if (mine && half == 0) p.part_ml[at] = make_float2(m, bad ? -1.f : l);
+#pragma unroll
+                for (int c = half * (kD / 2); c < (half + 1) * (kD / 2); c += 32) {
+                    float o[32];
+                    umma::ld32(t_o(i) + lanes + c, o);
+                    umma::wait_ld();
+                    if (mine) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            dst[(c + e) / 4] = make_float4(o[e] * vs, o[e + 1] * vs,
+                                                           o[e + 2] * vs, o[e + 3] * vs);
+                    }
+                }
             }
+            // (the next item's first product into O waits for this tile's next
+            // probabilities, which come after this)
+            umma::fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(i_empty(k));
         }
     } else if (warp < kSoftWarps + 4) {
         fewer_registers<kKv>();
@@ -629,13 +620,15 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                 const uint32_t k_lo = umma::desc_lo(base + M::kRing, 16);
                 const uint32_t v_lo = umma::desc_lo(base + M::kRing, M::kHalfBytes);
                 auto qk = [&](int i, int s) {  // S_i = Q_i K^T
-                    const uint32_t a = q_lo + i * (M::kTileBytes >> 4);
+                    const uint32_t a = q_lo + i * (M::kHalfBytes >> 4);
                     const uint32_t b = k_lo + s * (M::kTileBytes >> 4);
 #pragma unroll
-                    for (int k = 0; k < kD / 16; ++k) {
-                        const uint32_t at = ((k >> 2) * M::kHalfBytes + (k & 3) * 32) >> 4;
-                        umma::mma_ss(t_s(i), umma::desc(a + at), umma::desc(b + at), kQk, k > 0);
-                    }
+                    for (int k = 0; k < kD / 16; ++k)
+                        umma::mma_ss(
+                            t_s(i),
+                            umma::desc(a + (((k >> 2) * M::kQHalfBytes + (k & 3) * 32) >> 4)),
+                            umma::desc(b + (((k >> 2) * M::kHalfBytes + (k & 3) * 32) >> 4)), kQk,
+                            k > 0);
                     umma::commit(s_full(i));
                 };
                 auto pv = [&](int i, int s, bool more) {  // O_i += P_i V
@@ -645,49 +638,66 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                         umma::mma_ts(t_o(i), t_s(i) + 8 * k, umma::desc(b + k * (2048 >> 4)), kPv,
                                      more || k > 0);
                 };
-                const int last = two ? 1 : 0;
-                bool ok = wait.one(q_full, 0) && wait.one(full(0), 0);
-                if (ok) {
-                    umma::fence_after();
-                    qk(0, 0);
-                    if (two) qk(1, 0);
-                    umma::commit(empty(0));
-                }
-                int sv = 0;                  // stage of the last element taken
+                int s = 0;                   // next stage of the ring
                 uint32_t phase = 0;          // its parity
-                [[maybe_unused]] uint32_t fixes = 0;  // parity of each stage's fixes
-                for (int j = 0; j < nt && ok; ++j) {
-                    if (++sv == S) {
-                        sv = 0;
+                auto advance = [&]() {
+                    if (++s == S) {
+                        s = 0;
                         phase ^= 1;
                     }
-                    const int sk = sv + 1 == S ? 0 : sv + 1;
-                    const uint32_t kphase = sv + 1 == S ? phase ^ 1 : phase;
-                    ok = wait.one(full(sv), phase);
-                    if (!kCodes && ok && it.dirty(it.ta + j)) {
-                        ok = wait.one(fixed(sv), fixes >> sv & 1u);
-                        fixes ^= 1u << sv;
-                    }
-                    for (int i = 0; i <= last && ok; ++i) {
-                        ok = wait.one(p_full(i), j & 1);
-                        if (!ok) break;
-                        umma::fence_after();
-                        pv(i, sv, j > 0);
-                        if (i == last) umma::commit(empty(sv));
-                        if (j + 1 < nt) {
-                            if (i == 0) {
-                                ok = wait.one(full(sk), kphase);
-                                if (!ok) break;
-                                umma::fence_after();
-                            }
-                            qk(i, sk);
-                            if (i == last) umma::commit(empty(sk));
-                        } else {
-                            umma::commit(o_full(i));
+                };
+                [[maybe_unused]] uint32_t fixes = 0;  // parity of each stage's fixes
+                uint32_t steps[2] = {0, 0};
+                bool ok = true;
+                for (int k = 0; ok; ++k) {
+                    ok = wait.one(i_full(k), k >> 1 & 1);
+                    if (!ok) break;
+                    const Item &it = item(k);
+                    const int nt = it.nt;
+                    if (nt == 0) break;
+                    const int last = it.toks * p.chunk > kTile ? 1 : 0;
+                    ok = wait.one(q_full, k & 1) && wait.one(full(s), phase);
+                    if (!ok) break;
+                    umma::fence_after();
+                    qk(0, s);
+                    if (last) qk(1, s);
+                    umma::commit(empty(s));
+                    if (nt == 1) umma::commit(q_empty);
+                    advance();
+                    for (int j = 0; j < nt && ok; ++j) {
+                        const int sv = s;
+                        ok = wait.one(full(sv), phase);
+                        if (!kCodes && ok && it.dirty(it.ta + j)) {
+                            ok = wait.one(fixed(sv), fixes >> sv & 1u);
+                            fixes ^= 1u << sv;
                         }
+                        if (!ok) break;
+                        advance();
+                        for (int i = 0; i <= last; ++i) {
+                            ok = wait.one(p_full(i), steps[i] & 1);
+                            if (!ok) break;
+                            ++steps[i];
+                            umma::fence_after();
+                            pv(i, sv, j > 0);
+                            if (i == last) umma::commit(empty(sv));
+                            if (j + 1 < nt) {
+                                if (i == 0) {
+                                    ok = wait.one(full(s), phase);
+                                    if (!ok) break;
+                                    umma::fence_after();
+                                }
+                                qk(i, s);
+                                if (i == last) {
+                                    umma::commit(empty(s));
+                                    if (j + 2 == nt) umma::commit(q_empty);
+                                }
+                            } else {
+                                umma::commit(o_full(i));
+                            }
+                        }
+                        if (j + 1 < nt) advance();
                     }
-                    sv = sk;
-                    phase = kphase;
+                    ptx::mbar_arrive(i_empty(k));
                 }
                 // nothing of this thread's is in flight after this
                 umma::commit(drain);
@@ -695,10 +705,11 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
             }
             __syncwarp();
         } else if (warp == kSoftWarps + 1 || warp == kSoftWarps + 3) {
-            // ------------------------------------------------ loads of the pages
-            // One warp for K, one for V.  A lane per page looks its block up;
-            // one thread issues the copies, 2 KB of a page each (a copy that
-            // every lane issued for itself took 100 cycles of the warp's time).
+            // ------------------------------------------------ loads of Q and the pages
+            // One warp for K and Q, one for V.  A lane per page looks its
+            // block up; one thread issues the copies, 2 KB of a page each (a
+            // copy that every lane issued for itself took 100 cycles of the
+            // warp's time).
             constexpr int R = kCodes ? M::kCodeStages : S;
             constexpr int kBox = kCodes ? kD : 64;                       // values per box
             constexpr int kBoxes = kCodes ? 1 : M::kHalves;
@@ -707,94 +718,176 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
             const uint32_t ring = base + (kCodes ? M::kCodeRing : M::kRing);
             const bool is_v = warp == kSoftWarps + 3;
             const void *tm = is_v ? static_cast<const void *>(&tmv) : &tmk;
-            const int32_t *table =
-                p.block_tables + static_cast<int64_t>(it.seq) * p.max_blocks_per_seq;
-            auto lookup = [&](int j) -> int32_t {  // block of the lane's page, -2: none
-                const int v = (it.ta + j) * kPagesPerTile + lane;
-                return lane < kPagesPerTile && v < it.visited ? __ldg(table + it.real(v)) : -2;
-            };
-            int32_t blk = lookup(0);
-            int j = 0;
-            for (; j < nt; ++j) {
-                const int n = 2 * j + (is_v ? 1 : 0), s = n % R;
-                const bool have = blk >= 0 && blk < p.num_blocks;
-                if (blk != -2 && !have) {
-                    flags[1] = 1;
-                    if (p.dev_status) atomicOr(p.dev_status, PKV_DEV_BAD_BLOCK);
-                }
-                [[maybe_unused]] float scale = 0.f;
-                if constexpr (kCodes)
-                    if (have)
-                        scale = __ldg((is_v ? p.v_scales : p.k_scales) +
-                                      static_cast<int64_t>(blk) * p.num_kv_heads + it.kvh);
-                const int row = (blk * p.num_kv_heads + it.kvh) * kPage;
-                const unsigned pages = __ballot_sync(0xffffffffu, have);
-                const uint32_t fb = kCodes ? cfull(s) : full(s);
-                const uint32_t eb = kCodes ? cempty(s) : empty(s);
-                if (!wait(eb, ((n / R) & 1) ^ 1)) break;
-                if (j + 1 < nt) blk = lookup(j + 1);
-                if constexpr (kCodes) {
-                    if (lane < kPagesPerTile)
-                        (reinterpret_cast<float *>(smem + M::kScales) +
-                         ((it.ta + j) & (M::kScaleTiles - 1)) * 2 * kPagesPerTile +
-                         (is_v ? kPagesPerTile : 0))[lane] = scale;
-                    __syncwarp();
-                }
-                if (umma::elect_one())
-                    ptx::mbar_arrive_expect_tx(fb, __popc(pages) * kBoxes * kBoxBytes);
-                __syncwarp();
-                const uint32_t dst = ring + s * kStageBytes;
-#pragma unroll
-                for (int g = 0; g < kPagesPerTile; ++g) {
-                    const int y = __shfl_sync(0xffffffffu, row, g);
-                    if ((pages >> g & 1u) && umma::elect_one()) {
-#pragma unroll
-                        for (int b = 0; b < kBoxes; ++b)
-                            ptx::tma_load_2d(dst + b * M::kHalfBytes + g * kBoxBytes, tm, b * kBox,
-                                             y, fb);
+            uint32_t tiles = 0;   // tiles of keys so far: ring elements 2 tiles (+ 1)
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                ok = wait(i_full(k), k >> 1 & 1);
+                if (!ok) break;
+                const Item &it = item(k);
+                const int nt = it.nt;
+                if (nt == 0) break;
+                const int32_t *table =
+                    p.block_tables + static_cast<int64_t>(it.seq) * p.max_blocks_per_seq;
+                auto lookup = [&](int j) -> int32_t {  // block of the lane's page, -2: none
+                    const int v = (it.ta + j) * kPagesPerTile + lane;
+                    return lane < kPagesPerTile && v < it.visited ? __ldg(table + it.real(v)) : -2;
+                };
+                int32_t blk = lookup(0);
+                for (int j = 0; j < nt; ++j) {
+                    const uint32_t n = 2 * tiles + (is_v ? 1 : 0);
+                    const int s = n % R;
+                    const bool have = blk >= 0 && blk < p.num_blocks;
+                    if (blk != -2 && !have) {
+                        flags[1 + (k & 1)] = 1;
+                        if (p.dev_status) atomicOr(p.dev_status, PKV_DEV_BAD_BLOCK);
                     }
-                }
-                __syncwarp();
-                if constexpr (!kCodes)
-                    if (is_v && it.dirty(it.ta + j)) {
-                        // rows of V that no row of the item sees may hold
-                        // anything, NaN included (and are not loaded for pages
-                        // past the last): zeros.  The products wait for this,
-                        // so the stage is not filled again meanwhile.
-                        if (!wait(fb, (n / R) & 1)) {
-                            ++j;
-                            break;
-                        }
-                        const int v = (it.ta + j) * kPagesPerTile + lane;
-                        uint32_t lv = 0xffffu;
+                    [[maybe_unused]] float scale = 0.f;
+                    if constexpr (kCodes)
+                        if (have)
+                            scale = __ldg((is_v ? p.v_scales : p.k_scales) +
+                                          static_cast<int64_t>(blk) * p.num_kv_heads + it.kvh);
+                    const int row = (blk * p.num_kv_heads + it.kvh) * kPage;
+                    const unsigned pages = __ballot_sync(0xffffffffu, have);
+                    const uint32_t fb = kCodes ? cfull(s) : full(s);
+                    const uint32_t eb = kCodes ? cempty(s) : empty(s);
+                    ok = wait(eb, ((n / R) & 1) ^ 1);
+                    if (!ok) break;
+                    if (j + 1 < nt) blk = lookup(j + 1);
+                    if constexpr (kCodes) {
                         if (lane < kPagesPerTile)
-                            lv = v < it.visited ? it.live(it.real(v) * kPage) : 0u;
-                        unsigned todo = __ballot_sync(0xffffffffu, lv != 0xffffu);
-                        while (todo) {
-                            const int g = __ffs(todo) - 1;
-                            todo &= todo - 1;
-                            const uint32_t keep = __shfl_sync(0xffffffffu, lv, g);
-                            for (int e = lane; e < kPage * kRowChunks; e += 32) {
-                                const int row = e / kRowChunks, ch = e % kRowChunks;
-                                if (!(keep >> row & 1u))
-                                    st_shared16(dst + (ch >> 3) * M::kHalfBytes +
-                                                    (g * kPage + row) * 128 + ((ch & 7) << 4),
-                                                make_uint4(0, 0, 0, 0));
-                            }
-                        }
-                        ptx::fence_proxy_async_smem();
+                            (reinterpret_cast<float *>(smem + M::kScales) +
+                             (tiles & (M::kScaleTiles - 1)) * 2 * kPagesPerTile +
+                             (is_v ? kPagesPerTile : 0))[lane] = scale;
                         __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(fixed(s));
                     }
+                    if (umma::elect_one())
+                        ptx::mbar_arrive_expect_tx(fb, __popc(pages) * kBoxes * kBoxBytes);
+                    __syncwarp();
+                    const uint32_t dst = ring + s * kStageBytes;
+#pragma unroll
+                    for (int g = 0; g < kPagesPerTile; ++g) {
+                        const int y = __shfl_sync(0xffffffffu, row, g);
+                        if ((pages >> g & 1u) && umma::elect_one()) {
+#pragma unroll
+                            for (int b = 0; b < kBoxes; ++b)
+                                ptx::tma_load_2d(dst + b * M::kHalfBytes + g * kBoxBytes, tm,
+                                                 b * kBox, y, fb);
+                        }
+                    }
+                    __syncwarp();
+                    ++tiles;
+                    if (!is_v && j == 0) {
+                        // the queries: tokens x heads x 64 values, which land as
+                        // the item's rows in their order (rows of heads that
+                        // are not the item's, or behind the batch, do not count)
+                        ok = wait(q_empty, (k & 1) ^ 1);
+                        if (!ok) break;
+                        if (umma::elect_one()) {
+                            ptx::mbar_arrive_expect_tx(q_full,
+                                                       p.tokens * p.chunk * M::kHalves * 128);
+#pragma unroll
+                            for (int b = 0; b < M::kHalves; ++b)
+                                ptx::tma_load_3d(base + b * M::kQHalfBytes, &tmq, b * 64, it.head,
+                                                 it.tok, q_full);
+                        }
+                        __syncwarp();
+                    }
+                    if constexpr (!kCodes)
+                        if (is_v && it.dirty(it.ta + j)) {
+                            // rows of V that no row of the item sees may hold
+                            // anything, NaN included (and are not loaded for
+                            // pages past the last): zeros.  The products wait
+                            // for this, so the stage is not filled meanwhile.
+                            ok = wait(fb, (n / R) & 1);
+                            if (!ok) break;
+                            const int v = (it.ta + j) * kPagesPerTile + lane;
+                            uint32_t lv = 0xffffu;
+                            if (lane < kPagesPerTile)
+                                lv = v < it.visited ? it.live(it.real(v) * kPage) : 0u;
+                            unsigned todo = __ballot_sync(0xffffffffu, lv != 0xffffu);
+                            while (todo) {
+                                const int g = __ffs(todo) - 1;
+                                todo &= todo - 1;
+                                const uint32_t keep = __shfl_sync(0xffffffffu, lv, g);
+                                for (int e = lane; e < kPage * kRowChunks; e += 32) {
+                                    const int row = e / kRowChunks, ch = e % kRowChunks;
+                                    if (!(keep >> row & 1u))
+                                        st_shared16(dst + (ch >> 3) * M::kHalfBytes +
+                                                        (g * kPage + row) * 128 + ((ch & 7) << 4),
+                                                    make_uint4(0, 0, 0, 0));
+                                }
+                            }
+                            ptx::fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(fixed(s));
+                        }
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(i_empty(k));
             }
             // The products have waited for every copy, unless a wait ran out:
             // then leave none of this warp's in flight.
-            if (*wait.abort)
-                for (int e = max(0, j - R); e < j; ++e) {
-                    const int n = 2 * e + (is_v ? 1 : 0);
+            if (!ok) {
+                for (uint32_t e = tiles > R ? tiles - R : 0; e < tiles; ++e) {
+                    const uint32_t n = 2 * e + (is_v ? 1 : 0);
                     ptx::mbar_wait_bounded(kCodes ? cfull(n % R) : full(n % R), (n / R) & 1,
                                            kWaitLimitNs);
                 }
+                if (!is_v) ptx::mbar_wait_bounded(q_full, 0, kWaitLimitNs);
+            }
+        } else {
+            // ------------------------------------------------ the next items
+            int block = blockIdx.x;
+            bool ok = true;
+            int k = 0;
+            for (uint32_t asked = 0; ok; ++asked) {
+                if (umma::elect_one()) {
+                    ptx::mbar_arrive_expect_tx(next_full, 16);
+                    ptx::try_cancel(base + M::kNext, next_full);
+                }
+                __syncwarp();
+                Item it;
+                bool bad = false;
+                const int what = find_item(p, block, it, bad);
+                if (what > 0) {
+                    ok = wait(i_empty(k), (k >> 1 & 1) ^ 1);
+                    if (ok && lane == 0) {
+                        item(k) = it;
+                        flags[1 + (k & 1)] = 0;
+                        ptx::mbar_arrive(i_full(k));
+                    }
+                    __syncwarp();
+                    ++k;
+                } else if (what == 0) {
+                    // a sequence that does not fit (zeros), or a split without keys
+                    if (bad && lane == 0 && p.dev_status) atomicOr(p.dev_status, PKV_DEV_BAD_CTX);
+                    for (int e = lane; e < it.toks * it.heads * kRowChunks; e += 32) {
+                        const int q = e / kRowChunks, t = it.tok + q / it.heads;
+                        const int64_t row =
+                            static_cast<int64_t>(t) * p.num_heads + it.head + q % it.heads;
+                        if (t < 0 || t >= p.num_tokens) continue;
+                        if (p.splits == 1)
+                            reinterpret_cast<uint4 *>(p.out + row * kD)[e % kRowChunks] =
+                                make_uint4(0, 0, 0, 0);
+                        else if (e % kRowChunks == 0)
+                            p.part_ml[static_cast<int64_t>(it.z) * p.num_tokens * p.num_heads +
+                                      row] = make_float2(-INFINITY, 0.f);
+                    }
+                }
+                // (also after a wait that ran out: the answer must have come)
+                if (!wait(next_full, asked & 1)) {
+                    ptx::mbar_wait_bounded(next_full, asked & 1, kWaitLimitNs);
+                    ok = false;
+                }
+                if (!ok || !ptx::cancelled_block(base + M::kNext, block)) break;
+                ptx::fence_proxy_async_smem();  // read before the next answer is written
+            }
+            if (ok) ok = wait(i_empty(k), (k >> 1 & 1) ^ 1);
+            if (ok && lane == 0) {
+                item(k).nt = 0;
+                ptx::mbar_arrive(i_full(k));
+            }
+            __syncwarp();
         }
     } else {
         if constexpr (kCodes) {
@@ -803,47 +896,64 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
             constexpr int R = M::kCodeStages;
             constexpr int kCh = kD / 16;  // 16-byte chunks of codes per row
             const int tid = threadIdx.x - 32 * (kSoftWarps + 4);
-            for (int n = 0; n < 2 * nt; ++n) {
-                if (!wait(cfull(n % R), (n / R) & 1) || !wait(empty(n % S), ((n / S) & 1) ^ 1))
-                    break;
-                const uint32_t src = base + M::kCodeRing + (n % R) * M::kCodeBytes;
-                const uint32_t dst = base + M::kRing + (n % S) * M::kTileBytes;
-                const int v0 = (it.ta + n / 2) * kPagesPerTile;
+            uint32_t n = 0;
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                ok = wait(i_full(k), k >> 1 & 1);
+                if (!ok) break;
+                const Item &it = item(k);
+                const int nt = it.nt;
+                if (nt == 0) break;
+                for (int j = 0; j < 2 * nt; ++j, ++n) {
+                    ok = wait(cfull(n % R), (n / R) & 1) && wait(empty(n % S), ((n / S) & 1) ^ 1);
+                    if (!ok) break;
+                    const uint32_t src = base + M::kCodeRing + (n % R) * M::kCodeBytes;
+                    const uint32_t dst = base + M::kRing + (n % S) * M::kTileBytes;
+                    const int v0 = (it.ta + j / 2) * kPagesPerTile;
+                    const bool dirty = kKv == kKvF8 && (j & 1) && it.dirty(it.ta + j / 2);
 #pragma unroll
-                for (int e = tid; e < kTile * kCh; e += kTile) {
-                    const int row = e / kCh, ch = e % kCh;
-                    const uint32_t sw = kD == 128 ? (ch ^ (row & 7)) : (ch ^ ((row >> 1) & 3));
-                    uint4 w = ptx::lds128(src + row * kD + (sw << 4));
-                    uint4 a, b;
-                    if constexpr (kKv == kKvI8) {
-                        w.x ^= 0x80808080u;
-                        w.y ^= 0x80808080u;
-                        w.z ^= 0x80808080u;
-                        w.w ^= 0x80808080u;
-                        a = make_uint4(ptx::i8pair_exact(w.x, 0x4140u), ptx::i8pair_exact(w.x, 0x4342u),
-                                       ptx::i8pair_exact(w.y, 0x4140u), ptx::i8pair_exact(w.y, 0x4342u));
-                        b = make_uint4(ptx::i8pair_exact(w.z, 0x4140u), ptx::i8pair_exact(w.z, 0x4342u),
-                                       ptx::i8pair_exact(w.w, 0x4140u), ptx::i8pair_exact(w.w, 0x4342u));
-                    } else {
-                        a = make_uint4(ptx::e4m3x2_to_f16x2(w.x), ptx::e4m3x2_to_f16x2(w.x >> 16),
-                                       ptx::e4m3x2_to_f16x2(w.y), ptx::e4m3x2_to_f16x2(w.y >> 16));
-                        b = make_uint4(ptx::e4m3x2_to_f16x2(w.z), ptx::e4m3x2_to_f16x2(w.z >> 16),
-                                       ptx::e4m3x2_to_f16x2(w.w), ptx::e4m3x2_to_f16x2(w.w >> 16));
-                        if (n & 1) {
-                            // rows of V that no row of the item sees
-                            const int v = v0 + (row >> 4);
-                            const uint32_t lv = v < it.visited ? it.live(it.real(v) * kPage) : 0u;
-                            if (!(lv >> (row & 15) & 1u)) a = b = make_uint4(0, 0, 0, 0);
+                    for (int e = tid; e < kTile * kCh; e += kTile) {
+                        const int row = e / kCh, ch = e % kCh;
+                        const uint32_t sx = kD == 128 ? (ch ^ (row & 7)) : (ch ^ ((row >> 1) & 3));
+                        uint4 w = ptx::lds128(src + row * kD + (sx << 4));
+                        uint4 a, b;
+                        if constexpr (kKv == kKvI8) {
+                            w.x ^= 0x80808080u;
+                            w.y ^= 0x80808080u;
+                            w.z ^= 0x80808080u;
+                            w.w ^= 0x80808080u;
+                            a = make_uint4(
+                                ptx::i8pair_exact(w.x, 0x4140u), ptx::i8pair_exact(w.x, 0x4342u),
+                                ptx::i8pair_exact(w.y, 0x4140u), ptx::i8pair_exact(w.y, 0x4342u));
+                            b = make_uint4(
+                                ptx::i8pair_exact(w.z, 0x4140u), ptx::i8pair_exact(w.z, 0x4342u),
+                                ptx::i8pair_exact(w.w, 0x4140u), ptx::i8pair_exact(w.w, 0x4342u));
+                        } else {
+                            a = make_uint4(
+                                ptx::e4m3x2_to_f16x2(w.x), ptx::e4m3x2_to_f16x2(w.x >> 16),
+                                ptx::e4m3x2_to_f16x2(w.y), ptx::e4m3x2_to_f16x2(w.y >> 16));
+                            b = make_uint4(
+                                ptx::e4m3x2_to_f16x2(w.z), ptx::e4m3x2_to_f16x2(w.z >> 16),
+                                ptx::e4m3x2_to_f16x2(w.w), ptx::e4m3x2_to_f16x2(w.w >> 16));
+                            if (dirty) {
+                                // rows of V that no row of the item sees
+                                const int v = v0 + (row >> 4);
+                                const uint32_t lv =
+                                    v < it.visited ? it.live(it.real(v) * kPage) : 0u;
+                                if (!(lv >> (row & 15) & 1u)) a = b = make_uint4(0, 0, 0, 0);
+                            }
                         }
+                        const uint32_t to = dst + (ch >> 2) * M::kHalfBytes + row * 128;
+                        const int c0 = (2 * ch) & 7;
+                        st_shared16(to + ((c0 ^ (row & 7)) << 4), a);
+                        st_shared16(to + (((c0 + 1) ^ (row & 7)) << 4), b);
                     }
-                    const uint32_t to = dst + (ch >> 2) * M::kHalfBytes + row * 128;
-                    const int c0 = (2 * ch) & 7;
-                    st_shared16(to + ((c0 ^ (row & 7)) << 4), a);
-                    st_shared16(to + (((c0 + 1) ^ (row & 7)) << 4), b);
+                    ptx::fence_proxy_async_smem();
+                    ptx::mbar_arrive(full(n % S));
+                    ptx::mbar_arrive(cempty(n % R));
                 }
-                ptx::fence_proxy_async_smem();
-                ptx::mbar_arrive(full(n % S));
-                ptx::mbar_arrive(cempty(n % R));
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(i_empty(k));
             }
         }
     }
@@ -922,6 +1032,7 @@ struct PrefillCall {
 };
 
 struct Plan {
+    int chunk = 0, chunks = 0, tokens = 0;
     int64_t units = 0;
     int splits = 1;
     size_t bytes = 0;
@@ -938,12 +1049,14 @@ pkv_status plan_of(int num_tokens, int num_seqs, int num_heads, int num_kv_heads
         max_context_len < 0 || num_heads % num_kv_heads != 0)
         return PKV_ERR_INVALID_ARG;
     if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
-    const int64_t group = num_heads / num_kv_heads;
-    plan->units = num_tokens * group / kRows + num_seqs;
-    const int64_t items = plan->units * num_kv_heads;
+    const int group = num_heads / num_kv_heads;
+    plan->chunk = group < kRows ? group : kRows;
+    plan->chunks = (group + plan->chunk - 1) / plan->chunk;
+    plan->tokens = kRows / plan->chunk;
+    plan->units = num_tokens / plan->tokens + static_cast<int64_t>(num_seqs);
+    const int64_t items = plan->units * num_kv_heads * plan->chunks;
     const int64_t tiles = (static_cast<int64_t>(max_context_len) + kTile - 1) / kTile + 1;
-    if (plan->units > INT32_MAX || num_tokens * group + kRows > INT32_MAX ||
-        items * kMaxSplits > INT32_MAX)
+    if (plan->units > INT32_MAX || items * kMaxSplits > INT32_MAX)
         return PKV_ERR_UNSUPPORTED;
     int64_t best = 0;
     plan->splits = 1;
@@ -981,10 +1094,12 @@ pkv_status launch_prefill(const PrefillCall &c, const Plan &plan)
             r = true;
         }
     }
-    CUtensorMap tmk, tmv;
+    CUtensorMap tmq, tmk, tmv;
     const uint64_t rows = static_cast<uint64_t>(c.num_blocks) * c.num_kv_heads * kPage;
     const int elem = M::kCodes ? 1 : 2, box = M::kCodes ? kD : 64;
     const int swizzle = box * elem;
+    if (!encode_tmap_3d_f16(&tmq, c.query, kD, c.num_heads, c.num_tokens, 64, plan.chunk, plan.tokens))
+        return PKV_ERR_CUDA;
     if (!encode_tmap_2d(&tmk, c.kpool, elem, kD, rows, box, kPage, swizzle) ||
         !encode_tmap_2d(&tmv, c.vpool, elem, kD, rows, box, kPage, swizzle))
         return PKV_ERR_CUDA;
@@ -1007,6 +1122,9 @@ pkv_status launch_prefill(const PrefillCall &c, const Plan &plan)
     a.num_heads = c.num_heads;
     a.num_kv_heads = c.num_kv_heads;
     a.group = c.num_heads / c.num_kv_heads;
+    a.chunk = plan.chunk;
+    a.chunks = plan.chunks;
+    a.tokens = plan.tokens;
     a.max_blocks_per_seq = c.max_blocks_per_seq;
     a.num_blocks = c.num_blocks;
     const int64_t cap_tab = static_cast<int64_t>(c.max_blocks_per_seq) * kPage;
@@ -1019,7 +1137,8 @@ pkv_status launch_prefill(const PrefillCall &c, const Plan &plan)
     a.cap_inv = c.logit_cap > 0.f ? 1.f / a.cap : 0.f;
 
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(plan.units * c.num_kv_heads * plan.splits));
+    cfg.gridDim =
+        dim3(static_cast<unsigned>(plan.units * c.num_kv_heads * plan.chunks * plan.splits));
     cfg.blockDim = dim3(prefill_threads<kKv>());
     cfg.dynamicSmemBytes = M::kAsk;
     cfg.stream = static_cast<cudaStream_t>(c.stream);
@@ -1028,7 +1147,7 @@ pkv_status launch_prefill(const PrefillCall &c, const Plan &plan)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, tmk, tmv);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, tmq, tmk, tmv);
     if (e == cudaSuccess && plan.splits > 1) {
         const int64_t all = static_cast<int64_t>(c.num_tokens) * c.num_heads;
         cfg.gridDim = dim3(static_cast<unsigned>((all + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));

@@ -98,6 +98,45 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void *tmap, int 
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, int x, int y, int z,
+                                            uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// Cluster launch control: ask for the number of a CTA of this grid that has
+// not started and now never will; the 16-byte answer is written to shared
+// memory (16-byte aligned), completing on an mbarrier.
+__device__ __forceinline__ void try_cancel(uint32_t dst, uint32_t bar)
+{
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+        "[%0], [%1];" ::"r"(dst),
+        "r"(bar)
+        : "memory");
+}
+
+// The answer: whether there was one, and its blockIdx.x.
+__device__ __forceinline__ bool cancelled_block(uint32_t answer, int &block)
+{
+    uint32_t ok, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t"
+        "ld.shared.b128 a, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n\t}"
+        : "=r"(ok), "=r"(x)
+        : "r"(answer)
+        : "memory");
+    if (ok) block = static_cast<int>(x);
+    return ok != 0;
+}
+
 __device__ __forceinline__ uint64_t policy_evict_first()
 {
     uint64_t p;
