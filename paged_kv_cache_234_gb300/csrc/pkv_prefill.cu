@@ -13,8 +13,8 @@
 // shares every key and value that is read -- as two tiles of 128 rows, the M of
 // one tcgen05.mma.  Per 128 keys (eight pages) a tile does
 //   S = Q K^T   (128 x 128 fp32 in TMEM; Q, K in shared memory)
-//   P = 2^(S' - m)  (registers: two threads per row, which exchange their
-//                    maxima through shared memory; back to TMEM as fp16)
+//   P = 2^(S' - m)  (registers: one thread per row, so maxima and sums need no
+//                    exchange between threads; back to TMEM as fp16)
 //   O += P V    (128 x d fp32 in TMEM; P from TMEM, V in shared memory as it
 //                lies in the page, rows of keys)
 // and the two tiles take turns: while one is in its softmax, the tensor core
@@ -25,11 +25,11 @@
 // out over the keys and stays below the rounding of the fp16 output.  Sums,
 // maxima and accumulators are fp32.
 //
-// Roles of the warps: 0-15 the rows of the two tiles (two threads per row, 64
-// columns of S each), 16 issues the products, 17 and 19 the TMA loads of K and
-// V (a ring of tiles of 128 keys, K and V in turn).  INT8 / FP8 pages land in a second ring, and warps 20-23
-// widen them exactly to fp16; the K scales multiply the scores, the V scales enter
-// the probabilities as a ratio to the largest one so far.
+// Roles of the warps: 0-7 the rows of the two tiles, 8 issues the products, 9
+// and 11 the TMA loads of Q, K and V (a ring of tiles of 128 keys, K and V in
+// turn), 10 finds the next item.  INT8 / FP8 pages land in a second ring, and
+// warps 12-15 widen them exactly to fp16; the K scales multiply the scores, the
+// V scales enter the probabilities as a ratio to the largest one so far.
 //
 // Items are numbered by bounds that the host knows (pkv_ragged.cuh), the ones
 // with the most keys first.  When they are fewer than the SMs fill, each is
@@ -39,6 +39,7 @@
 #include <stdint.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "pkv_host.cuh"
 #include "pkv_ptx.cuh"
@@ -53,8 +54,7 @@ constexpr int kRows = 256;      // query rows per item: two tiles
 constexpr int kTile = 128;      // rows per tile, keys per step
 constexpr int kPage = 16;
 constexpr int kPagesPerTile = kTile / kPage;
-constexpr int kCols = kTile / 2;    // columns of S per softmax thread
-constexpr int kSoftWarps = 16;      // two halves of two tiles of four warps
+constexpr int kSoftWarps = 8;   // two tiles of four warps, a thread per row
 constexpr int kSms = 152;       // GB300: what the split over the keys aims to fill
 constexpr int kMaxSplits = 64;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // bounded waits: 1 s
@@ -95,7 +95,7 @@ struct Smem {
     static constexpr int kRing = 2 * kTileBytes;
     static constexpr int kCodeRing = kRing + kStages * kTileBytes;
     static constexpr int kCtl = kCodeRing + kCodeStages * kCodeBytes;
-    static constexpr int kBars = 3 * kStages + 2 * kCodeStages + 16;
+    static constexpr int kBars = 3 * kStages + 2 * kCodeStages + 14;
     // scales [kScaleTiles][K, V][8 pages]: the loads run at most five tiles
     // ahead of the softmax (the code ring, the ring and the tile at work)
     static constexpr int kScaleTiles = 8;
@@ -103,8 +103,7 @@ struct Smem {
     static constexpr int kScales = kNext + 16;
     static constexpr int kItems = kScales + (kCodes ? kScaleTiles * 2 * kPagesPerTile * 4 : 0);
     static constexpr int kFlags = kItems + 2 * 64;
-    static constexpr int kSwap = kFlags + 16;                  // [2 tiles][2 halves][128 rows]
-    static constexpr int kBytes = kSwap + 2 * 2 * kTile * 4;
+    static constexpr int kBytes = kFlags + 16;
     // a second CTA on the SM would wait for TMEM: ask for more than half
     static constexpr int kAsk = kBytes > 120 * 1024 ? kBytes : 120 * 1024;
     static_assert(kAsk <= 227 * 1024, "shared memory of one CTA");
@@ -145,15 +144,20 @@ struct Waiter {
 struct __align__(16) Item {
     int seq, kvh;
     int tok, toks;              // first token (of the batch) and tokens of the item
-    int head, heads;            // first query head and heads
+    int head;                   // first query head
+    int16_t heads, dir;         // heads; order of the tiles (see tile)
     int pos;                    // position of the first token
     int z;                      // split
     int lo, hi, pre;            // keys of the item: lo .. hi and below pre
     int np1, gap, visited;      // pages: np1, a gap, the rest (see the decode)
-    int ta;                     // first tile of keys
+    int ta;                     // tile of keys to begin with
     int nt;                     // tiles of keys; 0: no further item
 
     __device__ __forceinline__ int real(int v) const { return v + (v >= np1 ? gap : 0); }
+
+    // the j-th tile of keys: with a bias by distance (dir -1) from the last one
+    // to the first
+    __device__ __forceinline__ int tile(int j) const { return ta + dir * j; }
 
     // whether a tile of keys holds some that no row sees
     __device__ __forceinline__ bool dirty(int tile) const
@@ -196,7 +200,8 @@ __device__ __forceinline__ int find_item(const PrefillArgs &p, int block, Item &
     it.tok = sr.start + static_cast<int>(t0);
     it.toks = min(p.tokens, sr.len - static_cast<int>(t0));
     it.head = it.kvh * p.group + c * p.chunk;
-    it.heads = min(p.chunk, p.group - c * p.chunk);
+    it.heads = static_cast<int16_t>(min(p.chunk, p.group - c * p.chunk));
+    it.dir = p.slopes ? -1 : 1;
     it.ta = it.nt = 0;
     bad = !sr.ok;
     if (bad) return 0;
@@ -211,6 +216,7 @@ __device__ __forceinline__ int find_item(const PrefillArgs &p, int block, Item &
     const int tiles = (it.visited + kPagesPerTile - 1) / kPagesPerTile;
     it.ta = static_cast<int>(static_cast<int64_t>(tiles) * it.z / p.splits);
     it.nt = static_cast<int>(static_cast<int64_t>(tiles) * (it.z + 1) / p.splits) - it.ta;
+    if (it.dir < 0) it.ta += it.nt - 1;
     return it.nt > 0;
 }
 
@@ -218,27 +224,27 @@ __device__ __forceinline__ int find_item(const PrefillArgs &p, int block, Item &
 template <int kKv>
 __host__ __device__ constexpr int prefill_threads()
 {
-    return kKv == kKvF16 ? 640 : 768;
+    return 32 * kSoftWarps + (kKv == kKvF16 ? 128 : 256);
 }
 
-// Registers: launched with 96 (80 with the widening warps) per thread; the
+// Registers: launched with 168 (128 with the widening warps) per thread; the
 // softmax warps take what the others give back.
 template <int kKv>
 __device__ __forceinline__ void more_registers()
 {
     if constexpr (kKv == kKvF16)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     else
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
 }
 
 template <int kKv>
 __device__ __forceinline__ void fewer_registers()
 {
     if constexpr (kKv == kKvF16)
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     else
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
 }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
@@ -254,57 +260,92 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint4 v)
                  : "memory");
 }
 
-// The largest of a thread's scores.
-__device__ __forceinline__ float row_max(const float (&x)[kCols])
+// Eight codes as fp16 values, exactly.
+template <int kKv>
+__device__ __forceinline__ uint4 widen(uint32_t a, uint32_t b)
 {
-    float m[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-    for (int c = 4; c < kCols; c += 8)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            m[e] = c + 4 + e < kCols ? fmaxf(fmaxf(m[e], x[c + e]), x[c + 4 + e])
-                                     : fmaxf(m[e], x[c + e]);
-    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    if constexpr (kKv == kKvI8) {
+        a ^= 0x80808080u;
+        b ^= 0x80808080u;
+        return make_uint4(ptx::i8pair_exact(a, 0x4140u), ptx::i8pair_exact(a, 0x4342u),
+                          ptx::i8pair_exact(b, 0x4140u), ptx::i8pair_exact(b, 0x4342u));
+    } else {
+        return make_uint4(ptx::e4m3x2_to_f16x2(a), ptx::e4m3x2_to_f16x2(a >> 16),
+                          ptx::e4m3x2_to_f16x2(b), ptx::e4m3x2_to_f16x2(b >> 16));
+    }
 }
 
-// cap_score of a thread's scores, two at a time.  The polynomial alone while no
-// score of the warp's rows passes the cap.
-__device__ __forceinline__ void cap_scores(float (&x)[kCols], float cap, float cap_inv)
+// The largest of 16 values.
+__device__ __forceinline__ float max16(const float *x)
 {
-    float top = 0.f;
+    const float a = fmaxf(fmaxf(x[0], x[1]), x[2]), b = fmaxf(fmaxf(x[3], x[4]), x[5]);
+    const float c = fmaxf(fmaxf(x[6], x[7]), x[8]), d = fmaxf(fmaxf(x[9], x[10]), x[11]);
+    const float e = fmaxf(fmaxf(x[12], x[13]), x[14]);
+    return fmaxf(fmaxf(fmaxf(a, b), fmaxf(c, d)), fmaxf(e, x[15]));
+}
+
+// tanh(u) of two values as u P(u^2): P of degree 6 for |u| <= 1 (tanh_coef),
+// or of degree 3, from the same fit on [0, 0.35], whose relative error there
+// is 4e-8.
+template <int kDegree>
+__device__ __forceinline__ uint64_t tanh2(uint64_t u)
+{
+    constexpr float near[4] = {0.99999994f, -0.333324224f, 0.132957995f, -0.0489582308f};
+    const uint64_t w = ptx::mul2(u, u);
+    const float top = kDegree == 3 ? near[3] : tanh_coef(6);
+    uint64_t q = ptx::f32x2(top, top);
 #pragma unroll
-    for (int c = 0; c < kCols; c += 2) top = fmaxf(fmaxf(top, fabsf(x[c])), fabsf(x[c + 1]));
-    const uint64_t ci = ptx::f32x2(cap_inv, cap_inv);
-    auto poly = [&](int c, uint64_t &u) {
-        const uint64_t x2 = ptx::f32x2(x[c], x[c + 1]);
-        u = ptx::mul2(x2, ci);
-        const uint64_t w = ptx::mul2(u, u);
-        uint64_t q = ptx::f32x2(tanh_coef(6), tanh_coef(6));
+    for (int k = kDegree - 1; k >= 0; --k) {
+        const float c = kDegree == 3 ? near[k] : tanh_coef(k);
+        q = ptx::fma2(q, w, ptx::f32x2(c, c));
+    }
+    return ptx::mul2(u, q);
+}
+
+// x <- tanh(x), by the largest |x| of the warp's rows: a short polynomial
+// (the usual case: scores well inside the cap), a longer one, or the
+// exponential for what lies beyond the cap.
+__device__ __forceinline__ void tanh_row(float (&x)[kTile])
+{
+    float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 5; k >= 0; --k) q = ptx::fma2(q, w, ptx::f32x2(tanh_coef(k), tanh_coef(k)));
-        return ptx::f32x2_parts(ptx::mul2(x2, q));
-    };
-    uint64_t u;
-    if (__all_sync(0xffffffffu, top * cap_inv <= 1.f)) {
+    for (int c = 0; c < kTile; c += 2)
+        top[c / 2 & 3] = fmaxf(fmaxf(top[c / 2 & 3], fabsf(x[c])), fabsf(x[c + 1]));
+    const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    if (__all_sync(0xffffffffu, most <= 0.35f)) {
 #pragma unroll
-        for (int c = 0; c < kCols; c += 2) {
-            const float2 y = poly(c, u);
+        for (int c = 0; c < kTile; c += 2) {
+            const float2 y = ptx::f32x2_parts(tanh2<3>(ptx::f32x2(x[c], x[c + 1])));
+            x[c] = y.x;
+            x[c + 1] = y.y;
+        }
+    } else if (__all_sync(0xffffffffu, most <= 1.f)) {
+#pragma unroll
+        for (int c = 0; c < kTile; c += 2) {
+            const float2 y = ptx::f32x2_parts(tanh2<6>(ptx::f32x2(x[c], x[c + 1])));
             x[c] = y.x;
             x[c + 1] = y.y;
         }
     } else {
 #pragma unroll
-        for (int c = 0; c < kCols; c += 2) {
-            const float2 y = poly(c, u), v = ptx::f32x2_parts(u);
-            x[c] = fabsf(v.x) <= 1.f ? y.x : cap_far(v.x, cap);
-            x[c + 1] = fabsf(v.y) <= 1.f ? y.y : cap_far(v.y, cap);
+        for (int c = 0; c < kTile; c += 2) {
+            const float2 y = ptx::f32x2_parts(tanh2<6>(ptx::f32x2(x[c], x[c + 1])));
+            x[c] = fabsf(x[c]) <= 1.f ? y.x : cap_far(x[c], 1.f);
+            x[c + 1] = fabsf(x[c + 1]) <= 1.f ? y.y : cap_far(x[c + 1], 1.f);
         }
     }
 }
 
-// kMod: any of cap, bias or scales, or a scale that is not positive -- the
-// scores are worked out before their maximum is taken.  Without it the scale
-// is folded into the exponent.
+// kMod: a cap, a bias, or a softmax scale that is not positive -- the scores are
+// worked out before their maximum is taken.  Without it the products stay as
+// they are and their scale (with codes, the page's K scale too) enters with the
+// exponent: 2^(S f - m) is one multiply-add.
+//
+// With a bias by distance, keys are taken from the last tile to the first: the
+// nearest keys have the largest scores, so that the accumulators are hardly
+// ever rescaled.  (Without one the other way is faster, 243 against 251 us for
+// 8 prompts of 2048 tokens: the tile with masks and stale rows, the last one,
+// is then worked on while the pipeline is full.)
 //
 // One CTA per SM, which takes the block numbers of CTAs that have not started
 // (cluster launch control) as long as there are any: a warp asks for the next
@@ -335,11 +376,10 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
     auto s_full = [&](int i) { return one + 32 + 8 * i; };
     auto p_full = [&](int i) { return one + 48 + 8 * i; };
     auto o_full = [&](int i) { return one + 64 + 8 * i; };
-    auto swapped = [&](int i) { return one + 80 + 8 * i; };
-    auto i_full = [&](int k) { return one + 96 + 8 * (k & 1); };
-    auto i_empty = [&](int k) { return one + 112 + 8 * (k & 1); };
+    auto i_full = [&](int k) { return one + 80 + 8 * (k & 1); };
+    auto i_empty = [&](int k) { return one + 96 + 8 * (k & 1); };
     // one per stage: V is fixed tiles ahead of the products
-    [[maybe_unused]] auto fixed = [&](int s) { return one + 128 + 8 * s; };
+    [[maybe_unused]] auto fixed = [&](int s) { return one + 112 + 8 * s; };
     volatile int *flags = reinterpret_cast<volatile int *>(smem + M::kFlags);
     // flags: abort, bad of item slot 0, of slot 1, TMEM address
     const Waiter wait{flags, p.dev_status};
@@ -350,13 +390,13 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            ptx::mbar_init(full(s), kCodes ? 128 : 1);
+            ptx::mbar_init(full(s), kCodes ? 4 : 1);
             ptx::mbar_init(empty(s), 1);
             ptx::mbar_init(fixed(s), 1);
         }
         for (int s = 0; s < M::kCodeStages; ++s) {
             ptx::mbar_init(cfull(s), 1);
-            ptx::mbar_init(cempty(s), 128);
+            ptx::mbar_init(cempty(s), 4);
         }
         ptx::mbar_init(q_full, 1);
         ptx::mbar_init(q_empty, 1);
@@ -366,7 +406,6 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
             ptx::mbar_init(s_full(i), 1);
             ptx::mbar_init(p_full(i), kSoftWarps / 2);
             ptx::mbar_init(o_full(i), 1);
-            ptx::mbar_init(swapped(i), kSoftWarps / 2);
             ptx::mbar_init(i_full(i), 1);
             ptx::mbar_init(i_empty(i), kSoftWarps + 3 + (kCodes ? 4 : 0));
         }
@@ -386,23 +425,18 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
     if (warp < kSoftWarps) {
         // ------------------------------------------------ rows of the tiles
         more_registers<kKv>();
-        const int i = warp >> 3, half = warp >> 2 & 1;  // tile, half of its columns
-        const int rt = threadIdx.x & (kTile - 1);       // row of the tile
-        const int r = kTile * i + rt;                   // row of the item
+        const int i = warp >> 2;                        // tile
+        const int r = threadIdx.x;                      // row of the item
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 (w mod 4)
-        float *sw = reinterpret_cast<float *>(smem + M::kSwap) + i * 2 * kTile;
         const int rj = r / p.chunk, rh = r - rj * p.chunk;  // token and head of the row
-        // log2 units throughout; without kMod x stays as the product left it
-        // and the scale enters with the exponent
-        const float sl = kMod ? 1.f : p.scale_log2;
         uint32_t steps = 0;   // tiles of keys of this tile of rows so far
-        uint32_t swaps = 0, outs = 0;
+        uint32_t outs = 0;
         [[maybe_unused]] uint32_t tiles = 0;  // tiles of keys of the CTA so far
         bool ok = true;
         for (int k = 0; ok; ++k) {
             ok = wait(i_full(k), k >> 1 & 1);
             if (!ok) break;
-            const Item &it = item(k);
+            const Item it = item(k);
             const int nt = it.nt;
             if (nt == 0) break;
             const int rows = it.toks * p.chunk;
@@ -415,31 +449,42 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
             const int pos = it.pos + min(rj, it.toks - 1);
             const int lo = p.window > 0 ? pos - p.window + 1 : 0;
             const int pre = it.pre;
-            // positions of the tile's first and last row: which tiles of keys
-            // all of its rows see
+            // positions of the tile's first and last row; all of its rows see
+            // all keys of the tiles (of 8 pages) clean_a <= t < clean_b, which
+            // lie behind the gap, and t < clean_p, in the prefix
             const int pos_a = it.pos + kTile * i / p.chunk;
             const int pos_b = it.pos + (min(kTile * i + kTile, rows) - 1) / p.chunk;
+            const int first = p.window > 0 ? max(0, pos_b - p.window + kPage) / kPage - it.gap : 0;
+            const int clean_a = (max(first, it.np1) + kPagesPerTile - 1) / kPagesPerTile;
+            const int clean_b = max((pos_a + 1) / kPage - it.gap, 0) / kPagesPerTile;
+            const int clean_p = (it.gap ? min(pre / kPage, it.np1) : pre / kPage) / kPagesPerTile;
             float slope = 0.f;
             if (kMod && p.slopes && rh < it.heads)
                 slope = __ldg(p.slopes + it.head + rh) * 1.4426950408889634f;
             float m = -INFINITY, l = 0.f;
             [[maybe_unused]] float vref = 0.f, vinv = 0.f;
             for (int j = 0; j < nt; ++j) {
+                const int tile = it.tile(j), v0 = tile * kPagesPerTile;
+                // K and V scales of the tile's pages
+                [[maybe_unused]] const float *ks =
+                    reinterpret_cast<const float *>(smem + M::kScales) +
+                    (tiles & (M::kScaleTiles - 1)) * 2 * kPagesPerTile;
+                [[maybe_unused]] const float *vs = ks + kPagesPerTile;
                 ok = wait(s_full(i), steps & 1);
                 if (!ok) break;
                 ++steps;
                 umma::fence_after();
-                // first page of the thread's columns
-                const int v0 = (it.ta + j) * kPagesPerTile + half * (kPagesPerTile / 2);
-                float x[kCols];
+                float x[kTile];
 #pragma unroll
-                for (int c = 0; c < kCols; c += 32)
-                    umma::ld32(t_s(i) + lanes + half * kCols + c, x + c);
-                [[maybe_unused]] const float *vs =
-                    reinterpret_cast<const float *>(smem + M::kScales) +
-                    (tiles & (M::kScaleTiles - 1)) * 2 * kPagesPerTile + kPagesPerTile;
-                [[maybe_unused]] const float *ks = vs - kPagesPerTile + half * (kPagesPerTile / 2);
+                for (int c = 0; c < kTile; c += 32) umma::ld32(t_s(i) + lanes + c, x + c);
                 float ov = 1.f;  // change of the V reference
+                // what a product is multiplied with, in log2 units (a page of
+                // zeros has scale 0: a masked score must stay -inf)
+                auto factor = [&](int g) {
+                    if constexpr (!kCodes) return p.scale_log2;
+                    const float s = ks[g] * p.scale_log2;
+                    return kMod ? s : fmaxf(s, 1e-30f);
+                };
                 if constexpr (kCodes) {
                     ++tiles;
                     float most = 0.f;
@@ -450,36 +495,60 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                         ov = vref * vinv;
                         vref = most;
                     }
-                    vs += half * (kPagesPerTile / 2);
                 }
                 umma::wait_ld();
+                float sl = 1.f;  // kMod: what x is to be multiplied with
                 if constexpr (kMod) {
-                    float f = p.scale_log2;
+                    const float by = p.cap > 0.f ? p.cap_inv : 1.f;
 #pragma unroll
-                    for (int c = 0; c < kCols; c += 2) {
-                        if (kCodes && c % kPage == 0) f = ks[c / kPage] * p.scale_log2;
-                        const float2 y =
-                            ptx::f32x2_parts(ptx::mul2(ptx::f32x2(x[c], x[c + 1]), ptx::f32x2(f, f)));
-                        x[c] = y.x;
-                        x[c + 1] = y.y;
-                    }
-                    if (p.cap > 0.f) cap_scores(x, p.cap, p.cap_inv);
-                    if (p.slopes) {
+                    for (int g = 0; g < kPagesPerTile; ++g) {
+                        const float f = factor(g) * by;
 #pragma unroll
-                        for (int g = 0; g < kPagesPerTile / 2; ++g) {
-                            const float f = static_cast<float>(pos - it.real(v0 + g) * kPage);
-#pragma unroll
-                            for (int c = 0; c < kPage; ++c)
-                                x[kPage * g + c] = fmaf(-slope, fabsf(f - c), x[kPage * g + c]);
+                        for (int c = kPage * g; c < kPage * (g + 1); c += 2) {
+                            const float2 y = ptx::f32x2_parts(
+                                ptx::mul2(ptx::f32x2(x[c], x[c + 1]), ptx::f32x2(f, f)));
+                            x[c] = y.x;
+                            x[c + 1] = y.y;
                         }
                     }
+                    if (p.cap > 0.f) {
+                        tanh_row(x);
+                        sl = p.cap;
+                    }
+                    if (p.slopes) {
+                        // - slope |pos - t|; keys ahead of a row are seen in the
+                        // prefix only
+                        const bool ahead = it.real(v0) * kPage < pre;
+#pragma unroll
+                        for (int g = 0; g < kPagesPerTile; ++g) {
+                            const float f = static_cast<float>(pos - it.real(v0 + g) * kPage);
+                            if (ahead) {
+#pragma unroll
+                                for (int c = 0; c < kPage; ++c)
+                                    x[kPage * g + c] =
+                                        fmaf(x[kPage * g + c], sl, -slope * fabsf(f - c));
+                            } else {
+                                const uint64_t at = ptx::f32x2(-slope * f, -slope * f);
+                                const uint64_t s2 = ptx::f32x2(slope, slope);
+                                const uint64_t by2 = ptx::f32x2(sl, sl);
+#pragma unroll
+                                for (int c = 0; c < kPage; c += 2) {
+                                    const int e = kPage * g + c;
+                                    const float2 y = ptx::f32x2_parts(ptx::fma2(
+                                        ptx::f32x2(x[e], x[e + 1]), by2,
+                                        ptx::fma2(s2, ptx::f32x2(c, c + 1), at)));
+                                    x[e] = y.x;
+                                    x[e + 1] = y.y;
+                                }
+                            }
+                        }
+                        sl = 1.f;
+                    }
                 }
-                const int tmin = it.real(v0) * kPage;
-                const int tmax = it.real(v0 + kPagesPerTile / 2 - 1) * kPage + kPage - 1;
-                if (!((tmax <= pos_a && (p.window <= 0 || tmin > pos_b - p.window)) || tmax < pre)) {
+                if (!((tile >= clean_a && tile < clean_b) || tile < clean_p)) {
                     // some row of the tile does not see some key
 #pragma unroll
-                    for (int g = 0; g < kPagesPerTile / 2; ++g) {
+                    for (int g = 0; g < kPagesPerTile; ++g) {
                         const int t0 = it.real(v0 + g) * kPage;
                         const uint32_t seen =
                             (below(pos + 1 - t0) & ~below(lo - t0)) | below(pre - t0);
@@ -488,17 +557,16 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                             if (!(seen >> c & 1u)) x[kPage * g + c] = -INFINITY;
                     }
                 }
-                // the row's maximum: the other half of its columns has the
-                // other one (the buffer is free again: S of this tile was not
-                // started before both halves of the last one were through)
-                float top = row_max(x) * sl;
-                sw[half * kTile + rt] = top;
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(swapped(i));
-                ok = wait(swapped(i), swaps & 1);
-                if (!ok) break;
-                ++swaps;
-                top = fmaxf(top, sw[(half ^ 1) * kTile + rt]);
+                float top = -INFINITY;
+#pragma unroll
+                for (int g = 0; g < kPagesPerTile; ++g) {
+                    const float t = max16(x + kPage * g);
+                    top = fmaxf(top, kMod || !kCodes ? t : t * factor(g));
+                }
+                if constexpr (kMod)
+                    top *= sl;
+                else if constexpr (!kCodes)
+                    top *= p.scale_log2;
                 if (__any_sync(0xffffffffu, top > m + kLazy || ov != 1.f)) {
                     const float mn = fmaxf(m, top);
                     const float f = m == -INFINITY ? 0.f : ptx::ex2(m - mn);
@@ -507,7 +575,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                     if (j > 0) {
                         const float fo = f * ov;
 #pragma unroll 1
-                        for (int c = half * (kD / 2); c < (half + 1) * (kD / 2); c += 16) {
+                        for (int c = 0; c < kD; c += 16) {
                             float o[16];
                             umma::ld16(t_o(i) + lanes + c, o);
                             umma::wait_ld();
@@ -519,28 +587,29 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                 }
                 // a row that has seen nothing yet: every exponent is -inf
                 const float off = kLift - (m == -INFINITY ? 0.f : m);
-                const uint64_t sl2 = ptx::f32x2(sl, sl), off2 = ptx::f32x2(off, off);
+                const uint64_t off2 = ptx::f32x2(off, off);
                 uint64_t sum[2] = {0, 0};
 #pragma unroll
-                for (int h = 0; h < kCols; h += 32) {
+                for (int h = 0; h < kTile; h += 32) {
                     uint32_t pk[16];
-                    [[maybe_unused]] float vr = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int c = h + 2 * e;
-                        uint64_t y = ptx::f32x2(x[c], x[c + 1]);
-                        y = kMod ? ptx::add2(y, off2) : ptx::fma2(y, sl2, off2);
-                        const float2 z2 = ptx::f32x2_parts(y);
-                        y = ptx::f32x2(ptx::ex2(z2.x), ptx::ex2(z2.y));
-                        sum[e & 1] = ptx::add2(sum[e & 1], y);
-                        if constexpr (kCodes) {
-                            if (c % kPage == 0) vr = vs[c / kPage] * vinv;
-                            y = ptx::mul2(y, ptx::f32x2(vr, vr));
+                    for (int g = h / kPage; g < h / kPage + 2; ++g) {
+                        const float fy = kMod ? sl : factor(g);
+                        const uint64_t f2 = ptx::f32x2(fy, fy);
+                        [[maybe_unused]] float vr = 0.f;
+                        if constexpr (kCodes) vr = vs[g] * vinv;
+#pragma unroll
+                        for (int c = kPage * g; c < kPage * (g + 1); c += 2) {
+                            const float2 z2 = ptx::f32x2_parts(
+                                ptx::fma2(ptx::f32x2(x[c], x[c + 1]), f2, off2));
+                            uint64_t y = ptx::f32x2(ptx::ex2(z2.x), ptx::ex2(z2.y));
+                            sum[c / 2 & 1] = ptx::add2(sum[c / 2 & 1], y);
+                            if constexpr (kCodes) y = ptx::mul2(y, ptx::f32x2(vr, vr));
+                            const float2 pr = ptx::f32x2_parts(y);
+                            pk[(c - h) / 2] = pack2(pr.x, pr.y);
                         }
-                        const float2 pr = ptx::f32x2_parts(y);
-                        pk[e] = pack2(pr.x, pr.y);
                     }
-                    umma::st16(t_s(i) + lanes + half * (kCols / 2) + h / 2, pk);
+                    umma::st16(t_s(i) + lanes + h / 2, pk);
                 }
                 const float2 both = ptx::f32x2_parts(ptx::add2(sum[0], sum[1]));
                 l += both.x + both.y;
@@ -553,14 +622,6 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
             if (!ok) break;
             ++outs;
             umma::fence_after();
-            // the sums of the two halves, in their order
-            sw[half * kTile + rt] = l;
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(swapped(i));
-            ok = wait(swapped(i), swaps & 1);
-            if (!ok) break;
-            ++swaps;
-            l = sw[rt] + sw[kTile + rt];
             const bool bad = flags[1 + (k & 1)] != 0;
             const bool mine = rj < it.toks && rh < it.heads;
             const int64_t row =
@@ -570,7 +631,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                 const float f = l > 0.f ? vs / l : l;  // an empty row: zeros; NaN stays
                 uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * kD);
 #pragma unroll
-                for (int c = half * (kD / 2); c < (half + 1) * (kD / 2); c += 32) {
+                for (int c = 0; c < kD; c += 32) {
                     float o[32];
                     umma::ld32(t_o(i) + lanes + c, o);
                     umma::wait_ld();
@@ -588,9 +649,9 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                 const int64_t at =
                     static_cast<int64_t>(it.z) * p.num_tokens * p.num_heads + row;
                 float4 *dst = reinterpret_cast<float4 *>(p.part_acc + at * kD);
-                if (mine && half == 0) p.part_ml[at] = make_float2(m, bad ? -1.f : l);
+                if (mine) p.part_ml[at] = make_float2(m, bad ? -1.f : l);
 #pragma unroll
-                for (int c = half * (kD / 2); c < (half + 1) * (kD / 2); c += 32) {
+                for (int c = 0; c < kD; c += 32) {
                     float o[32];
                     umma::ld32(t_o(i) + lanes + c, o);
                     umma::wait_ld();
@@ -667,7 +728,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                     for (int j = 0; j < nt && ok; ++j) {
                         const int sv = s;
                         ok = wait.one(full(sv), phase);
-                        if (!kCodes && ok && it.dirty(it.ta + j)) {
+                        if (!kCodes && ok && it.dirty(it.tile(j))) {
                             ok = wait.one(fixed(sv), fixes >> sv & 1u);
                             fixes ^= 1u << sv;
                         }
@@ -729,7 +790,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                 const int32_t *table =
                     p.block_tables + static_cast<int64_t>(it.seq) * p.max_blocks_per_seq;
                 auto lookup = [&](int j) -> int32_t {  // block of the lane's page, -2: none
-                    const int v = (it.ta + j) * kPagesPerTile + lane;
+                    const int v = it.tile(j) * kPagesPerTile + lane;
                     return lane < kPagesPerTile && v < it.visited ? __ldg(table + it.real(v)) : -2;
                 };
                 int32_t blk = lookup(0);
@@ -793,14 +854,14 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                         __syncwarp();
                     }
                     if constexpr (!kCodes)
-                        if (is_v && it.dirty(it.ta + j)) {
+                        if (is_v && it.dirty(it.tile(j))) {
                             // rows of V that no row of the item sees may hold
                             // anything, NaN included (and are not loaded for
                             // pages past the last): zeros.  The products wait
                             // for this, so the stage is not filled meanwhile.
                             ok = wait(fb, (n / R) & 1);
                             if (!ok) break;
-                            const int v = (it.ta + j) * kPagesPerTile + lane;
+                            const int v = it.tile(j) * kPagesPerTile + lane;
                             uint32_t lv = 0xffffu;
                             if (lane < kPagesPerTile)
                                 lv = v < it.visited ? it.live(it.real(v) * kPage) : 0u;
@@ -892,9 +953,10 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
     } else {
         if constexpr (kCodes) {
             // ------------------------------------------------ codes to fp16
-            fewer_registers<kKv>();
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
             constexpr int R = M::kCodeStages;
             constexpr int kCh = kD / 16;  // 16-byte chunks of codes per row
+            constexpr int kStep = 128 / kCh;
             const int tid = threadIdx.x - 32 * (kSoftWarps + 4);
             uint32_t n = 0;
             bool ok = true;
@@ -909,39 +971,26 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                     if (!ok) break;
                     const uint32_t src = base + M::kCodeRing + (n % R) * M::kCodeBytes;
                     const uint32_t dst = base + M::kRing + (n % S) * M::kTileBytes;
-                    const int v0 = (it.ta + j / 2) * kPagesPerTile;
-                    const bool dirty = kKv == kKvF8 && (j & 1) && it.dirty(it.ta + j / 2);
+                    const int v0 = it.tile(j / 2) * kPagesPerTile;
+                    const bool dirty = kKv == kKvF8 && (j & 1) && it.dirty(it.tile(j / 2));
+                    // all loads first: the thread's row advances by kStep
+                    const int ch = tid % kCh, row0 = tid / kCh;
+                    uint4 w[kCh];
 #pragma unroll
-                    for (int e = tid; e < kTile * kCh; e += kTile) {
-                        const int row = e / kCh, ch = e % kCh;
+                    for (int e = 0; e < kCh; ++e) {
+                        const int row = row0 + e * kStep;
                         const uint32_t sx = kD == 128 ? (ch ^ (row & 7)) : (ch ^ ((row >> 1) & 3));
-                        uint4 w = ptx::lds128(src + row * kD + (sx << 4));
-                        uint4 a, b;
-                        if constexpr (kKv == kKvI8) {
-                            w.x ^= 0x80808080u;
-                            w.y ^= 0x80808080u;
-                            w.z ^= 0x80808080u;
-                            w.w ^= 0x80808080u;
-                            a = make_uint4(
-                                ptx::i8pair_exact(w.x, 0x4140u), ptx::i8pair_exact(w.x, 0x4342u),
-                                ptx::i8pair_exact(w.y, 0x4140u), ptx::i8pair_exact(w.y, 0x4342u));
-                            b = make_uint4(
-                                ptx::i8pair_exact(w.z, 0x4140u), ptx::i8pair_exact(w.z, 0x4342u),
-                                ptx::i8pair_exact(w.w, 0x4140u), ptx::i8pair_exact(w.w, 0x4342u));
-                        } else {
-                            a = make_uint4(
-                                ptx::e4m3x2_to_f16x2(w.x), ptx::e4m3x2_to_f16x2(w.x >> 16),
-                                ptx::e4m3x2_to_f16x2(w.y), ptx::e4m3x2_to_f16x2(w.y >> 16));
-                            b = make_uint4(
-                                ptx::e4m3x2_to_f16x2(w.z), ptx::e4m3x2_to_f16x2(w.z >> 16),
-                                ptx::e4m3x2_to_f16x2(w.w), ptx::e4m3x2_to_f16x2(w.w >> 16));
-                            if (dirty) {
-                                // rows of V that no row of the item sees
-                                const int v = v0 + (row >> 4);
-                                const uint32_t lv =
-                                    v < it.visited ? it.live(it.real(v) * kPage) : 0u;
-                                if (!(lv >> (row & 15) & 1u)) a = b = make_uint4(0, 0, 0, 0);
-                            }
+                        w[e] = ptx::lds128(src + row * kD + (sx << 4));
+                    }
+#pragma unroll
+                    for (int e = 0; e < kCh; ++e) {
+                        const int row = row0 + e * kStep;
+                        uint4 a = widen<kKv>(w[e].x, w[e].y), b = widen<kKv>(w[e].z, w[e].w);
+                        if (dirty) {
+                            // rows of V that no row of the item sees
+                            const int v = v0 + (row >> 4);
+                            const uint32_t lv = v < it.visited ? it.live(it.real(v) * kPage) : 0u;
+                            if (!(lv >> (row & 15) & 1u)) a = b = make_uint4(0, 0, 0, 0);
                         }
                         const uint32_t to = dst + (ch >> 2) * M::kHalfBytes + row * 128;
                         const int c0 = (2 * ch) & 7;
@@ -949,8 +998,11 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                         st_shared16(to + (((c0 + 1) ^ (row & 7)) << 4), b);
                     }
                     ptx::fence_proxy_async_smem();
-                    ptx::mbar_arrive(full(n % S));
-                    ptx::mbar_arrive(cempty(n % R));
+                    __syncwarp();
+                    if (lane == 0) {
+                        ptx::mbar_arrive(full(n % S));
+                        ptx::mbar_arrive(cempty(n % R));
+                    }
                 }
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(i_empty(k));
@@ -1189,18 +1241,18 @@ pkv_status prefill_entry(const PrefillCall &c, int kv)
     if (c.num_tokens == 0 || c.num_seqs == 0) return PKV_OK;
     if (plan.bytes > 0 && (!c.workspace || c.workspace_bytes < plan.bytes)) return PKV_ERR_WORKSPACE;
     if (!aligned(c.workspace, 16)) return PKV_ERR_MISALIGNED;
-    const bool mod = codes || c.logit_cap > 0.f || c.slopes || !(c.softmax_scale > 0.f);
-    if (kv == kKvF8)
-        return c.head_dim == 128 ? launch_prefill<kKvF8, 128, true>(c, plan)
-                                 : launch_prefill<kKvF8, 64, true>(c, plan);
-    if (kv == kKvI8)
-        return c.head_dim == 128 ? launch_prefill<kKvI8, 128, true>(c, plan)
-                                 : launch_prefill<kKvI8, 64, true>(c, plan);
-    if (mod)
-        return c.head_dim == 128 ? launch_prefill<kKvF16, 128, true>(c, plan)
-                                 : launch_prefill<kKvF16, 64, true>(c, plan);
-    return c.head_dim == 128 ? launch_prefill<kKvF16, 128, false>(c, plan)
-                             : launch_prefill<kKvF16, 64, false>(c, plan);
+    const bool mod = c.logit_cap > 0.f || c.slopes || !(c.softmax_scale > 0.f);
+    auto pick = [&](auto kind) -> pkv_status {
+        constexpr int kKv = decltype(kind)::value;
+        if (c.head_dim == 128)
+            return mod ? launch_prefill<kKv, 128, true>(c, plan)
+                       : launch_prefill<kKv, 128, false>(c, plan);
+        return mod ? launch_prefill<kKv, 64, true>(c, plan)
+                   : launch_prefill<kKv, 64, false>(c, plan);
+    };
+    if (kv == kKvF8) return pick(std::integral_constant<int, kKvF8>());
+    if (kv == kKvI8) return pick(std::integral_constant<int, kKvI8>());
+    return pick(std::integral_constant<int, kKvF16>());
 }
 
 }  // namespace
