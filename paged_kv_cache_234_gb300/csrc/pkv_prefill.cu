@@ -90,11 +90,12 @@ struct Smem {
     static constexpr int kTileBytes = kHalves * kHalfBytes;    // 128 rows of K or V
     static constexpr int kQHalfBytes = kRows * 128;            // 64 values of the item's rows
     static constexpr int kCodeBytes = kTile * kD;
-    static constexpr int kStages = kCodes ? (kD == 128 ? 3 : 6) : (kD == 128 ? 5 : 10);
-    static constexpr int kCodeStages = kCodes ? 4 : 0;
+    static constexpr int kStages = kCodes ? (kD == 128 ? 3 : 6) : (kD == 128 ? 4 : 8);
+    static constexpr int kCodeStages = kCodes ? 3 : 0;
     static constexpr int kRing = 2 * kTileBytes;
     static constexpr int kCodeRing = kRing + kStages * kTileBytes;
-    static constexpr int kCtl = kCodeRing + kCodeStages * kCodeBytes;
+    static constexpr int kOut = kCodeRing + kCodeStages * kCodeBytes;   // 2 KB per softmax warp
+    static constexpr int kCtl = kOut + kSoftWarps * 2048;
     static constexpr int kBars = 3 * kStages + 2 * kCodeStages + 14;
     // scales [kScaleTiles][K, V][8 pages]: the loads run at most five tiles
     // ahead of the softmax (the code ring, the ring and the tile at work)
@@ -343,7 +344,7 @@ __device__ __forceinline__ void tanh_row(float (&x)[kTile])
 //
 // With a bias by distance, keys are taken from the last tile to the first: the
 // nearest keys have the largest scores, so that the accumulators are hardly
-// ever rescaled.  (Without one the other way is faster, 243 against 251 us for
+// ever rescaled.  (Without one the other way is faster, 254 against 263 us for
 // 8 prompts of 2048 tokens: the tile with masks and stale rows, the last one,
 // is then worked on while the pipeline is full.)
 //
@@ -436,7 +437,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
         for (int k = 0; ok; ++k) {
             ok = wait(i_full(k), k >> 1 & 1);
             if (!ok) break;
-            const Item it = item(k);
+            const Item &it = item(k);
             const int nt = it.nt;
             if (nt == 0) break;
             const int rows = it.toks * p.chunk;
@@ -474,6 +475,36 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                 if (!ok) break;
                 ++steps;
                 umma::fence_after();
+                // Tiles in which some row does not see some key: the rows'
+                // seen keys page by page; true if all rows see the whole page.
+                const bool clean = (tile >= clean_a && tile < clean_b) || tile < clean_p;
+                auto page_seen = [&](int g, uint32_t &seen) {
+                    const int t0 = it.real(v0 + g) * kPage;
+                    seen = (below(pos + 1 - t0) & ~below(lo - t0)) | below(pre - t0);
+                    return (t0 + kPage - 1 <= pos_a && (p.window <= 0 || t0 > pos_b - p.window)) ||
+                           t0 + kPage <= pre;
+                };
+                if constexpr (!kMod) {
+                    // masked where they lie, by a loop of a few instructions:
+                    // unrolled on registers it is 400 that are rarely in the
+                    // instruction cache (2600 cycles a tile)
+                    if (!clean) {
+#pragma unroll 1
+                        for (int g = 0; g < kPagesPerTile; ++g) {
+                            uint32_t seen;
+                            if (page_seen(g, seen)) continue;
+                            float s[kPage];
+                            umma::ld16(t_s(i) + lanes + kPage * g, s);
+                            umma::wait_ld();
+#pragma unroll
+                            for (int c = 0; c < kPage; ++c)
+                                if (!(seen >> c & 1u)) s[c] = -INFINITY;
+                            umma::st16(t_s(i) + lanes + kPage * g,
+                                       reinterpret_cast<const uint32_t *>(s));
+                        }
+                        umma::wait_st();
+                    }
+                }
                 float x[kTile];
 #pragma unroll
                 for (int c = 0; c < kTile; c += 32) umma::ld32(t_s(i) + lanes + c, x + c);
@@ -545,16 +576,16 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                         sl = 1.f;
                     }
                 }
-                if (!((tile >= clean_a && tile < clean_b) || tile < clean_p)) {
-                    // some row of the tile does not see some key
+                if constexpr (kMod) {
+                    if (!clean) {
 #pragma unroll
-                    for (int g = 0; g < kPagesPerTile; ++g) {
-                        const int t0 = it.real(v0 + g) * kPage;
-                        const uint32_t seen =
-                            (below(pos + 1 - t0) & ~below(lo - t0)) | below(pre - t0);
+                        for (int g = 0; g < kPagesPerTile; ++g) {
+                            uint32_t seen;
+                            if (page_seen(g, seen)) continue;
 #pragma unroll
-                        for (int c = 0; c < kPage; ++c)
-                            if (!(seen >> c & 1u)) x[kPage * g + c] = -INFINITY;
+                            for (int c = 0; c < kPage; ++c)
+                                if (!(seen >> c & 1u)) x[kPage * g + c] = -INFINITY;
+                        }
                     }
                 }
                 float top = -INFINITY;
@@ -624,50 +655,73 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
             umma::fence_after();
             const bool bad = flags[1 + (k & 1)] != 0;
             const bool mine = rj < it.toks && rh < it.heads;
-            const int64_t row =
-                static_cast<int64_t>(it.tok + rj) * p.num_heads + it.head + rh;
+            int64_t row = static_cast<int64_t>(it.tok + rj) * p.num_heads + it.head + rh;
+            if (p.splits > 1) row += static_cast<int64_t>(it.z) * p.num_tokens * p.num_heads;
+            // the item is not needed any more (and this release waits for no
+            // store of the rows)
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(i_empty(k));
             const float vs = kCodes ? vref : 1.f;
+            // The warp's rows leave by way of its 2 KB of shared memory, 64
+            // bytes of each at a time, so that a store instruction writes 64
+            // bytes of eight rows and not 16 bytes of 32 (3700 against 1500
+            // cycles).  16-byte chunk c of row r lies at 4 r + (c ^ r / 2 mod 4).
+            const uint32_t out = base + M::kOut + warp * 2048;
+            const uint32_t put = out + lane * 64, get = out + (lane >> 2) * 64;
+            const int px = lane >> 1 & 3, gx = (lane & 3) ^ (lane >> 3 & 3);
+            int64_t rows_of[4];   // the rows that this lane stores to, or -1
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                rows_of[e] = __shfl_sync(0xffffffffu, mine ? row : int64_t(-1), 8 * e + (lane >> 2));
+            auto store = [&](const uint4 (&v)[4], uint8_t *to, int row_bytes) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) st_shared16(put + ((c ^ px) << 4), v[c]);
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint4 w = ptx::lds128(get + e * 512 + (gx << 4));
+                    if (rows_of[e] >= 0)
+                        *reinterpret_cast<uint4 *>(to + rows_of[e] * row_bytes + (lane & 3) * 16) = w;
+                }
+                __syncwarp();
+            };
             if (p.splits == 1) {
                 const float f = l > 0.f ? vs / l : l;  // an empty row: zeros; NaN stays
-                uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * kD);
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < kD; c += 32) {
                     float o[32];
                     umma::ld32(t_o(i) + lanes + c, o);
                     umma::wait_ld();
+                    uint4 v[4];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = bad ? 0.f : o[e] * f;
-                    if (mine) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            dst[(c + e) / 8] = make_uint4(
-                                pack2(o[e], o[e + 1]), pack2(o[e + 2], o[e + 3]),
-                                pack2(o[e + 4], o[e + 5]), pack2(o[e + 6], o[e + 7]));
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        v[e] = make_uint4(
+                            pack2(o[8 * e], o[8 * e + 1]), pack2(o[8 * e + 2], o[8 * e + 3]),
+                            pack2(o[8 * e + 4], o[8 * e + 5]), pack2(o[8 * e + 6], o[8 * e + 7]));
+                    store(v, reinterpret_cast<uint8_t *>(p.out + c), kD * 2);
                 }
             } else {
-                const int64_t at =
-                    static_cast<int64_t>(it.z) * p.num_tokens * p.num_heads + row;
-                float4 *dst = reinterpret_cast<float4 *>(p.part_acc + at * kD);
-                if (mine) p.part_ml[at] = make_float2(m, bad ? -1.f : l);
-#pragma unroll
-                for (int c = 0; c < kD; c += 32) {
-                    float o[32];
-                    umma::ld32(t_o(i) + lanes + c, o);
+                if (mine) p.part_ml[row] = make_float2(m, bad ? -1.f : l);
+#pragma unroll 1
+                for (int c = 0; c < kD; c += 16) {
+                    float o[16];
+                    umma::ld16(t_o(i) + lanes + c, o);
                     umma::wait_ld();
-                    if (mine) {
+                    uint4 v[4];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            dst[(c + e) / 4] = make_float4(o[e] * vs, o[e + 1] * vs,
-                                                           o[e + 2] * vs, o[e + 3] * vs);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        v[e] = make_uint4(__float_as_uint(o[4 * e] * vs),
+                                          __float_as_uint(o[4 * e + 1] * vs),
+                                          __float_as_uint(o[4 * e + 2] * vs),
+                                          __float_as_uint(o[4 * e + 3] * vs));
+                    store(v, reinterpret_cast<uint8_t *>(p.part_acc + c), kD * 4);
                 }
             }
             // (the next item's first product into O waits for this tile's next
             // probabilities, which come after this)
             umma::fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(i_empty(k));
         }
     } else if (warp < kSoftWarps + 4) {
         fewer_registers<kKv>();
