@@ -54,7 +54,21 @@ constexpr int kRows = 256;      // query rows per item: two tiles
 constexpr int kTile = 128;      // rows per tile, keys per step
 constexpr int kPage = 16;
 constexpr int kPagesPerTile = kTile / kPage;
-constexpr int kSoftWarps = 8;   // two tiles of four warps, a thread per row
+
+// Softmax threads per row.  One, with 128 scores each, where a score is one
+// multiply-add and one exponential: nothing is exchanged.  Two, with 64 each,
+// where a score is worked out first (cap, bias): one thread's row would take
+// 2600 cycles, in which the tensor core has done its part of 1024 long since;
+// the two exchange their maxima and sums.
+__host__ __device__ constexpr int row_threads(bool mod)
+{
+    return mod ? 2 : 1;
+}
+
+__host__ __device__ constexpr int soft_warps(bool mod)
+{
+    return 8 * row_threads(mod);
+}
 constexpr int kSms = 152;       // GB300: what the split over the keys aims to fill
 constexpr int kMaxSplits = 64;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // bounded waits: 1 s
@@ -94,9 +108,10 @@ struct Smem {
     static constexpr int kCodeStages = kCodes ? 3 : 0;
     static constexpr int kRing = 2 * kTileBytes;
     static constexpr int kCodeRing = kRing + kStages * kTileBytes;
-    static constexpr int kOut = kCodeRing + kCodeStages * kCodeBytes;   // 2 KB per softmax warp
-    static constexpr int kCtl = kOut + kSoftWarps * 2048;
-    static constexpr int kBars = 3 * kStages + 2 * kCodeStages + 14;
+    static constexpr int kOut = kCodeRing + kCodeStages * kCodeBytes;   // rows on their way out
+    static constexpr int kOutBytes = 16 * 1024;
+    static constexpr int kCtl = kOut + kOutBytes;
+    static constexpr int kBars = 3 * kStages + 2 * kCodeStages + 16;
     // scales [kScaleTiles][K, V][8 pages]: the loads run at most five tiles
     // ahead of the softmax (the code ring, the ring and the tile at work)
     static constexpr int kScaleTiles = 8;
@@ -104,7 +119,8 @@ struct Smem {
     static constexpr int kScales = kNext + 16;
     static constexpr int kItems = kScales + (kCodes ? kScaleTiles * 2 * kPagesPerTile * 4 : 0);
     static constexpr int kFlags = kItems + 2 * 64;
-    static constexpr int kBytes = kFlags + 16;
+    static constexpr int kSwap = kFlags + 16;   // [2 tiles][2 halves of the columns][128 rows]
+    static constexpr int kBytes = kSwap + 2 * 2 * kTile * 4;
     // a second CTA on the SM would wait for TMEM: ask for more than half
     static constexpr int kAsk = kBytes > 120 * 1024 ? kBytes : 120 * 1024;
     static_assert(kAsk <= 227 * 1024, "shared memory of one CTA");
@@ -222,30 +238,39 @@ __device__ __forceinline__ int find_item(const PrefillArgs &p, int block, Item &
 }
 
 // ------------------------------------------------------------------ kernel
-template <int kKv>
+// Softmax warps, four more (products, loads, items), and four that widen codes.
+template <int kKv, bool kMod>
 __host__ __device__ constexpr int prefill_threads()
 {
-    return 32 * kSoftWarps + (kKv == kKvF16 ? 128 : 256);
+    return 32 * (soft_warps(kMod) + (kKv == kKvF16 ? 4 : 8));
 }
 
-// Registers: launched with 168 (128 with the widening warps) per thread; the
-// softmax warps take what the others give back.
-template <int kKv>
-__device__ __forceinline__ void more_registers()
+// Registers: all threads are launched with 65536 / threads, rounded down to a
+// multiple of 8 (fp16: 168 for 384 threads, 96 for 640; codes: 128 for 512, 80
+// for 768).  The softmax warps take what the others give back.
+template <int kKv, bool kMod>
+__device__ __forceinline__ void soft_registers()
 {
-    if constexpr (kKv == kKvF16)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    else
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    if constexpr (kKv == kKvF16 && !kMod) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if constexpr (kKv == kKvF16 && kMod) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    if constexpr (kKv != kKvF16 && !kMod) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    if constexpr (kKv != kKvF16 && kMod) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
 }
 
-template <int kKv>
-__device__ __forceinline__ void fewer_registers()
+template <int kKv, bool kMod>
+__device__ __forceinline__ void issue_registers()
 {
-    if constexpr (kKv == kKvF16)
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    else
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (kKv == kKvF16 && !kMod) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if constexpr (kKv == kKvF16 && kMod) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if constexpr (kKv != kKvF16 && !kMod) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (kKv != kKvF16 && kMod) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+}
+
+template <bool kMod>
+__device__ __forceinline__ void widen_registers()
+{
+    if constexpr (!kMod) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if constexpr (kMod) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
 }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
@@ -306,30 +331,31 @@ __device__ __forceinline__ uint64_t tanh2(uint64_t u)
 // x <- tanh(x), by the largest |x| of the warp's rows: a short polynomial
 // (the usual case: scores well inside the cap), a longer one, or the
 // exponential for what lies beyond the cap.
-__device__ __forceinline__ void tanh_row(float (&x)[kTile])
+template <int kN>
+__device__ __forceinline__ void tanh_row(float (&x)[kN])
 {
     float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int c = 0; c < kTile; c += 2)
+    for (int c = 0; c < kN; c += 2)
         top[c / 2 & 3] = fmaxf(fmaxf(top[c / 2 & 3], fabsf(x[c])), fabsf(x[c + 1]));
     const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
     if (__all_sync(0xffffffffu, most <= 0.35f)) {
 #pragma unroll
-        for (int c = 0; c < kTile; c += 2) {
+        for (int c = 0; c < kN; c += 2) {
             const float2 y = ptx::f32x2_parts(tanh2<3>(ptx::f32x2(x[c], x[c + 1])));
             x[c] = y.x;
             x[c + 1] = y.y;
         }
     } else if (__all_sync(0xffffffffu, most <= 1.f)) {
 #pragma unroll
-        for (int c = 0; c < kTile; c += 2) {
+        for (int c = 0; c < kN; c += 2) {
             const float2 y = ptx::f32x2_parts(tanh2<6>(ptx::f32x2(x[c], x[c + 1])));
             x[c] = y.x;
             x[c + 1] = y.y;
         }
     } else {
 #pragma unroll
-        for (int c = 0; c < kTile; c += 2) {
+        for (int c = 0; c < kN; c += 2) {
             const float2 y = ptx::f32x2_parts(tanh2<6>(ptx::f32x2(x[c], x[c + 1])));
             x[c] = fabsf(x[c]) <= 1.f ? y.x : cap_far(x[c], 1.f);
             x[c + 1] = fabsf(x[c + 1]) <= 1.f ? y.y : cap_far(x[c + 1], 1.f);
@@ -353,7 +379,7 @@ __device__ __forceinline__ void tanh_row(float (&x)[kTile])
 // one, works out its item and hands it to the others, so that loads and
 // products of an item begin while the last one's rows are written.
 template <int kKv, int kD, bool kMod>
-__global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
+__global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
     prefill_kernel(const __grid_constant__ PrefillArgs p, const __grid_constant__ CUtensorMap tmq,
                    const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv)
 {
@@ -361,6 +387,8 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
     constexpr bool kCodes = M::kCodes;
     constexpr int S = M::kStages;
     constexpr int kRowChunks = kD / 8;
+    constexpr int kSoftWarps = soft_warps(kMod), T = row_threads(kMod);
+    constexpr int kCols = kTile / T, kColPages = kCols / kPage;  // of S, per softmax thread
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = ptx::smem_addr(smem);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -379,8 +407,9 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
     auto o_full = [&](int i) { return one + 64 + 8 * i; };
     auto i_full = [&](int k) { return one + 80 + 8 * (k & 1); };
     auto i_empty = [&](int k) { return one + 96 + 8 * (k & 1); };
+    [[maybe_unused]] auto swapped = [&](int i) { return one + 112 + 8 * i; };
     // one per stage: V is fixed tiles ahead of the products
-    [[maybe_unused]] auto fixed = [&](int s) { return one + 112 + 8 * s; };
+    [[maybe_unused]] auto fixed = [&](int s) { return one + 128 + 8 * s; };
     volatile int *flags = reinterpret_cast<volatile int *>(smem + M::kFlags);
     // flags: abort, bad of item slot 0, of slot 1, TMEM address
     const Waiter wait{flags, p.dev_status};
@@ -407,6 +436,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
             ptx::mbar_init(s_full(i), 1);
             ptx::mbar_init(p_full(i), kSoftWarps / 2);
             ptx::mbar_init(o_full(i), 1);
+            ptx::mbar_init(swapped(i), kSoftWarps / 2);
             ptx::mbar_init(i_full(i), 1);
             ptx::mbar_init(i_empty(i), kSoftWarps + 3 + (kCodes ? 4 : 0));
         }
@@ -425,13 +455,27 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
 
     if (warp < kSoftWarps) {
         // ------------------------------------------------ rows of the tiles
-        more_registers<kKv>();
-        const int i = warp >> 2;                        // tile
-        const int r = threadIdx.x;                      // row of the item
+        soft_registers<kKv, kMod>();
+        const int i = warp / (4 * T);                   // tile
+        const int half = T == 2 ? warp >> 2 & 1 : 0;    // which of the row's columns
+        const int rt = threadIdx.x & (kTile - 1);       // row of the tile
+        const int r = kTile * i + rt;                   // row of the item
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 (w mod 4)
         const int rj = r / p.chunk, rh = r - rj * p.chunk;  // token and head of the row
         uint32_t steps = 0;   // tiles of keys of this tile of rows so far
         uint32_t outs = 0;
+        // T == 2: the other thread's value of the row (the buffer is free again
+        // when the next one is due: S is not started before both were through)
+        [[maybe_unused]] uint32_t swaps = 0;
+        [[maybe_unused]] float *sw = reinterpret_cast<float *>(smem + M::kSwap) + i * 2 * kTile;
+        auto swap = [&](float v, float &other) -> bool {
+            sw[half * kTile + rt] = v;
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(swapped(i));
+            if (!wait(swapped(i), swaps++ & 1)) return false;
+            other = sw[(half ^ 1) * kTile + rt];
+            return true;
+        };
         [[maybe_unused]] uint32_t tiles = 0;  // tiles of keys of the CTA so far
         bool ok = true;
         for (int k = 0; ok; ++k) {
@@ -465,11 +509,12 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
             float m = -INFINITY, l = 0.f;
             [[maybe_unused]] float vref = 0.f, vinv = 0.f;
             for (int j = 0; j < nt; ++j) {
-                const int tile = it.tile(j), v0 = tile * kPagesPerTile;
+                const int tile = it.tile(j);
+                const int v0 = tile * kPagesPerTile + half * kColPages;  // the thread's first page
                 // K and V scales of the tile's pages
-                [[maybe_unused]] const float *ks =
-                    reinterpret_cast<const float *>(smem + M::kScales) +
-                    (tiles & (M::kScaleTiles - 1)) * 2 * kPagesPerTile;
+                const float *scales = reinterpret_cast<const float *>(smem + M::kScales) +
+                                      (tiles & (M::kScaleTiles - 1)) * 2 * kPagesPerTile;
+                [[maybe_unused]] const float *ks = scales + half * kColPages;
                 [[maybe_unused]] const float *vs = ks + kPagesPerTile;
                 ok = wait(s_full(i), steps & 1);
                 if (!ok) break;
@@ -505,9 +550,10 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                         umma::wait_st();
                     }
                 }
-                float x[kTile];
+                float x[kCols];
 #pragma unroll
-                for (int c = 0; c < kTile; c += 32) umma::ld32(t_s(i) + lanes + c, x + c);
+                for (int c = 0; c < kCols; c += 32)
+                    umma::ld32(t_s(i) + lanes + half * kCols + c, x + c);
                 float ov = 1.f;  // change of the V reference
                 // what a product is multiplied with, in log2 units (a page of
                 // zeros has scale 0: a masked score must stay -inf)
@@ -520,7 +566,8 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                     ++tiles;
                     float most = 0.f;
 #pragma unroll
-                    for (int g = 0; g < kPagesPerTile; ++g) most = fmaxf(most, vs[g]);
+                    for (int g = 0; g < kPagesPerTile; ++g)
+                        most = fmaxf(most, scales[kPagesPerTile + g]);
                     if (most > kVLazy * vref) {
                         vinv = __frcp_rn(most);
                         ov = vref * vinv;
@@ -532,7 +579,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                 if constexpr (kMod) {
                     const float by = p.cap > 0.f ? p.cap_inv : 1.f;
 #pragma unroll
-                    for (int g = 0; g < kPagesPerTile; ++g) {
+                    for (int g = 0; g < kColPages; ++g) {
                         const float f = factor(g) * by;
 #pragma unroll
                         for (int c = kPage * g; c < kPage * (g + 1); c += 2) {
@@ -551,7 +598,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                         // prefix only
                         const bool ahead = it.real(v0) * kPage < pre;
 #pragma unroll
-                        for (int g = 0; g < kPagesPerTile; ++g) {
+                        for (int g = 0; g < kColPages; ++g) {
                             const float f = static_cast<float>(pos - it.real(v0 + g) * kPage);
                             if (ahead) {
 #pragma unroll
@@ -579,7 +626,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                 if constexpr (kMod) {
                     if (!clean) {
 #pragma unroll
-                        for (int g = 0; g < kPagesPerTile; ++g) {
+                        for (int g = 0; g < kColPages; ++g) {
                             uint32_t seen;
                             if (page_seen(g, seen)) continue;
 #pragma unroll
@@ -590,7 +637,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                 }
                 float top = -INFINITY;
 #pragma unroll
-                for (int g = 0; g < kPagesPerTile; ++g) {
+                for (int g = 0; g < kColPages; ++g) {
                     const float t = max16(x + kPage * g);
                     top = fmaxf(top, kMod || !kCodes ? t : t * factor(g));
                 }
@@ -598,6 +645,12 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                     top *= sl;
                 else if constexpr (!kCodes)
                     top *= p.scale_log2;
+                if constexpr (T == 2) {
+                    float other = 0.f;
+                    ok = swap(top, other);
+                    if (!ok) break;
+                    top = fmaxf(top, other);
+                }
                 if (__any_sync(0xffffffffu, top > m + kLazy || ov != 1.f)) {
                     const float mn = fmaxf(m, top);
                     const float f = m == -INFINITY ? 0.f : ptx::ex2(m - mn);
@@ -606,7 +659,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                     if (j > 0) {
                         const float fo = f * ov;
 #pragma unroll 1
-                        for (int c = 0; c < kD; c += 16) {
+                        for (int c = half * (kD / T); c < (half + 1) * (kD / T); c += 16) {
                             float o[16];
                             umma::ld16(t_o(i) + lanes + c, o);
                             umma::wait_ld();
@@ -621,7 +674,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                 const uint64_t off2 = ptx::f32x2(off, off);
                 uint64_t sum[2] = {0, 0};
 #pragma unroll
-                for (int h = 0; h < kTile; h += 32) {
+                for (int h = 0; h < kCols; h += 32) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int g = h / kPage; g < h / kPage + 2; ++g) {
@@ -640,7 +693,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                             pk[(c - h) / 2] = pack2(pr.x, pr.y);
                         }
                     }
-                    umma::st16(t_s(i) + lanes + h / 2, pk);
+                    umma::st16(t_s(i) + lanes + (half * kCols + h) / 2, pk);
                 }
                 const float2 both = ptx::f32x2_parts(ptx::add2(sum[0], sum[1]));
                 l += both.x + both.y;
@@ -653,6 +706,12 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
             if (!ok) break;
             ++outs;
             umma::fence_after();
+            if constexpr (T == 2) {  // the row's sum, the halves in their order
+                float other = 0.f;
+                ok = swap(l, other);
+                if (!ok) break;
+                l = half == 0 ? l + other : other + l;
+            }
             const bool bad = flags[1 + (k & 1)] != 0;
             const bool mine = rj < it.toks && rh < it.heads;
             int64_t row = static_cast<int64_t>(it.tok + rj) * p.num_heads + it.head + rh;
@@ -662,61 +721,69 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(i_empty(k));
             const float vs = kCodes ? vref : 1.f;
-            // The warp's rows leave by way of its 2 KB of shared memory, 64
-            // bytes of each at a time, so that a store instruction writes 64
-            // bytes of eight rows and not 16 bytes of 32 (3700 against 1500
-            // cycles).  16-byte chunk c of row r lies at 4 r + (c ^ r / 2 mod 4).
-            const uint32_t out = base + M::kOut + warp * 2048;
-            const uint32_t put = out + lane * 64, get = out + (lane >> 2) * 64;
-            const int px = lane >> 1 & 3, gx = (lane & 3) ^ (lane >> 3 & 3);
-            int64_t rows_of[4];   // the rows that this lane stores to, or -1
+            // The warp's rows leave by way of its 2 KB (T == 2: 1 KB) of shared
+            // memory, kPass bytes of each at a time, so that a store instruction
+            // writes whole pieces of a few rows and not 16 bytes of 32.  16-byte
+            // chunk c of row r lies at kCh r + (c ^ r kCh / 8 mod kCh).
+            constexpr int kPass = 64 / T, kCh = kPass / 16;
+            const uint32_t out = base + M::kOut + warp * (32 * kPass);
+            const uint32_t put = out + lane * kPass, get = out + (lane / kCh) * kPass;
+            const int px = lane * kCh / 8 % kCh, gx = (lane % kCh) ^ (lane / kCh * kCh / 8 % kCh);
+            int64_t rows_of[kCh];   // the rows that this lane stores to, or -1
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                rows_of[e] = __shfl_sync(0xffffffffu, mine ? row : int64_t(-1), 8 * e + (lane >> 2));
-            auto store = [&](const uint4 (&v)[4], uint8_t *to, int row_bytes) {
+            for (int e = 0; e < kCh; ++e)
+                rows_of[e] = __shfl_sync(0xffffffffu, mine ? row : int64_t(-1),
+                                         32 / kCh * e + lane / kCh);
+            auto store = [&](const uint4 (&v)[kCh], uint8_t *to, int row_bytes) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) st_shared16(put + ((c ^ px) << 4), v[c]);
+                for (int c = 0; c < kCh; ++c) st_shared16(put + ((c ^ px) << 4), v[c]);
                 __syncwarp();
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint4 w = ptx::lds128(get + e * 512 + (gx << 4));
+                for (int e = 0; e < kCh; ++e) {
+                    const uint4 w = ptx::lds128(get + e * (32 / kCh * kPass) + (gx << 4));
                     if (rows_of[e] >= 0)
-                        *reinterpret_cast<uint4 *>(to + rows_of[e] * row_bytes + (lane & 3) * 16) = w;
+                        *reinterpret_cast<uint4 *>(to + rows_of[e] * row_bytes +
+                                                   (lane % kCh) * 16) = w;
                 }
                 __syncwarp();
             };
+            const int c0 = half * (kD / T), c1 = c0 + kD / T;   // the thread's columns of O
             if (p.splits == 1) {
                 const float f = l > 0.f ? vs / l : l;  // an empty row: zeros; NaN stays
 #pragma unroll 1
-                for (int c = 0; c < kD; c += 32) {
-                    float o[32];
-                    umma::ld32(t_o(i) + lanes + c, o);
+                for (int c = c0; c < c1; c += kPass / 2) {
+                    float o[kPass / 2];
+#pragma unroll
+                    for (int e = 0; e < kPass / 2; e += 16) umma::ld16(t_o(i) + lanes + c + e, o + e);
                     umma::wait_ld();
-                    uint4 v[4];
+                    uint4 v[kCh];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = bad ? 0.f : o[e] * f;
+                    for (int e = 0; e < kPass / 2; ++e) o[e] = bad ? 0.f : o[e] * f;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
+                    for (int e = 0; e < kCh; ++e)
                         v[e] = make_uint4(
                             pack2(o[8 * e], o[8 * e + 1]), pack2(o[8 * e + 2], o[8 * e + 3]),
                             pack2(o[8 * e + 4], o[8 * e + 5]), pack2(o[8 * e + 6], o[8 * e + 7]));
                     store(v, reinterpret_cast<uint8_t *>(p.out + c), kD * 2);
                 }
             } else {
-                if (mine) p.part_ml[row] = make_float2(m, bad ? -1.f : l);
+                if (mine && half == 0) p.part_ml[row] = make_float2(m, bad ? -1.f : l);
 #pragma unroll 1
-                for (int c = 0; c < kD; c += 16) {
+                for (int c = c0; c < c1; c += 16) {
                     float o[16];
                     umma::ld16(t_o(i) + lanes + c, o);
                     umma::wait_ld();
-                    uint4 v[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        v[e] = make_uint4(__float_as_uint(o[4 * e] * vs),
-                                          __float_as_uint(o[4 * e + 1] * vs),
-                                          __float_as_uint(o[4 * e + 2] * vs),
-                                          __float_as_uint(o[4 * e + 3] * vs));
-                    store(v, reinterpret_cast<uint8_t *>(p.part_acc + c), kD * 4);
+                    for (int q = 0; q < 16; q += kPass / 4) {
+                        uint4 v[kCh];
+#pragma unroll
+                        for (int e = 0; e < kCh; ++e)
+                            v[e] = make_uint4(__float_as_uint(o[q + 4 * e] * vs),
+                                              __float_as_uint(o[q + 4 * e + 1] * vs),
+                                              __float_as_uint(o[q + 4 * e + 2] * vs),
+                                              __float_as_uint(o[q + 4 * e + 3] * vs));
+                        store(v, reinterpret_cast<uint8_t *>(p.part_acc + c + q), kD * 4);
+                    }
                 }
             }
             // (the next item's first product into O waits for this tile's next
@@ -724,7 +791,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
             umma::fence_before();
         }
     } else if (warp < kSoftWarps + 4) {
-        fewer_registers<kKv>();
+        issue_registers<kKv, kMod>();
         if (warp == kSoftWarps) {
             // ------------------------------------------------ products
             if (umma::elect_one()) {
@@ -1007,7 +1074,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
     } else {
         if constexpr (kCodes) {
             // ------------------------------------------------ codes to fp16
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+            widen_registers<kMod>();
             constexpr int R = M::kCodeStages;
             constexpr int kCh = kD / 16;  // 16-byte chunks of codes per row
             constexpr int kStep = 128 / kCh;
@@ -1029,27 +1096,33 @@ __global__ void __launch_bounds__(prefill_threads<kKv>(), 1)
                     const bool dirty = kKv == kKvF8 && (j & 1) && it.dirty(it.tile(j / 2));
                     // all loads first: the thread's row advances by kStep
                     const int ch = tid % kCh, row0 = tid / kCh;
-                    uint4 w[kCh];
+                    constexpr int kAt = kMod && kCh > 4 ? 4 : kCh;
 #pragma unroll
-                    for (int e = 0; e < kCh; ++e) {
-                        const int row = row0 + e * kStep;
-                        const uint32_t sx = kD == 128 ? (ch ^ (row & 7)) : (ch ^ ((row >> 1) & 3));
-                        w[e] = ptx::lds128(src + row * kD + (sx << 4));
-                    }
+                    for (int e0 = 0; e0 < kCh; e0 += kAt) {
+                        uint4 w[kAt];
 #pragma unroll
-                    for (int e = 0; e < kCh; ++e) {
-                        const int row = row0 + e * kStep;
-                        uint4 a = widen<kKv>(w[e].x, w[e].y), b = widen<kKv>(w[e].z, w[e].w);
-                        if (dirty) {
-                            // rows of V that no row of the item sees
-                            const int v = v0 + (row >> 4);
-                            const uint32_t lv = v < it.visited ? it.live(it.real(v) * kPage) : 0u;
-                            if (!(lv >> (row & 15) & 1u)) a = b = make_uint4(0, 0, 0, 0);
+                        for (int e = 0; e < kAt; ++e) {
+                            const int row = row0 + (e0 + e) * kStep;
+                            const uint32_t sx =
+                                kD == 128 ? (ch ^ (row & 7)) : (ch ^ ((row >> 1) & 3));
+                            w[e] = ptx::lds128(src + row * kD + (sx << 4));
                         }
-                        const uint32_t to = dst + (ch >> 2) * M::kHalfBytes + row * 128;
-                        const int c0 = (2 * ch) & 7;
-                        st_shared16(to + ((c0 ^ (row & 7)) << 4), a);
-                        st_shared16(to + (((c0 + 1) ^ (row & 7)) << 4), b);
+#pragma unroll
+                        for (int e = 0; e < kAt; ++e) {
+                            const int row = row0 + (e0 + e) * kStep;
+                            uint4 a = widen<kKv>(w[e].x, w[e].y), b = widen<kKv>(w[e].z, w[e].w);
+                            if (dirty) {
+                                // rows of V that no row of the item sees
+                                const int v = v0 + (row >> 4);
+                                const uint32_t lv =
+                                    v < it.visited ? it.live(it.real(v) * kPage) : 0u;
+                                if (!(lv >> (row & 15) & 1u)) a = b = make_uint4(0, 0, 0, 0);
+                            }
+                            const uint32_t to = dst + (ch >> 2) * M::kHalfBytes + row * 128;
+                            const int cc = (2 * ch) & 7;
+                            st_shared16(to + ((cc ^ (row & 7)) << 4), a);
+                            st_shared16(to + (((cc + 1) ^ (row & 7)) << 4), b);
+                        }
                     }
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
@@ -1245,7 +1318,7 @@ pkv_status launch_prefill(const PrefillCall &c, const Plan &plan)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim =
         dim3(static_cast<unsigned>(plan.units * c.num_kv_heads * plan.chunks * plan.splits));
-    cfg.blockDim = dim3(prefill_threads<kKv>());
+    cfg.blockDim = dim3(prefill_threads<kKv, kMod>());
     cfg.dynamicSmemBytes = M::kAsk;
     cfg.stream = static_cast<cudaStream_t>(c.stream);
     cudaLaunchAttribute attr[1];
