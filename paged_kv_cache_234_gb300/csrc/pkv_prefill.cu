@@ -60,14 +60,15 @@ constexpr int kPagesPerTile = kTile / kPage;
 // where a score is worked out first (cap, bias): one thread's row would take
 // 2600 cycles, in which the tensor core has done its part of 1024 long since;
 // the two exchange their maxima and sums.
-__host__ __device__ constexpr int row_threads(bool mod)
+// (Codes keep one: the warps that widen them leave too few registers for two.)
+__host__ __device__ constexpr int row_threads(bool codes, bool mod)
 {
-    return mod ? 2 : 1;
+    return mod && !codes ? 2 : 1;
 }
 
-__host__ __device__ constexpr int soft_warps(bool mod)
+__host__ __device__ constexpr int soft_warps(bool codes, bool mod)
 {
-    return 8 * row_threads(mod);
+    return 8 * row_threads(codes, mod);
 }
 constexpr int kSms = 152;       // GB300: what the split over the keys aims to fill
 constexpr int kMaxSplits = 64;
@@ -242,19 +243,17 @@ __device__ __forceinline__ int find_item(const PrefillArgs &p, int block, Item &
 template <int kKv, bool kMod>
 __host__ __device__ constexpr int prefill_threads()
 {
-    return 32 * (soft_warps(kMod) + (kKv == kKvF16 ? 4 : 8));
+    return 32 * (soft_warps(kKv != kKvF16, kMod) + (kKv == kKvF16 ? 4 : 8));
 }
 
 // Registers: all threads are launched with 65536 / threads, rounded down to a
-// multiple of 8 (fp16: 168 for 384 threads, 96 for 640; codes: 128 for 512, 80
-// for 768).  The softmax warps take what the others give back.
+// multiple of 8 (fp16: 168 for 384 threads, 96 for 640; codes: 128 for 512).  The softmax warps take what the others give back.
 template <int kKv, bool kMod>
 __device__ __forceinline__ void soft_registers()
 {
     if constexpr (kKv == kKvF16 && !kMod) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     if constexpr (kKv == kKvF16 && kMod) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-    if constexpr (kKv != kKvF16 && !kMod) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
-    if constexpr (kKv != kKvF16 && kMod) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+    if constexpr (kKv != kKvF16) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
 }
 
 template <int kKv, bool kMod>
@@ -262,15 +261,12 @@ __device__ __forceinline__ void issue_registers()
 {
     if constexpr (kKv == kKvF16 && !kMod) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if constexpr (kKv == kKvF16 && kMod) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if constexpr (kKv != kKvF16 && !kMod) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if constexpr (kKv != kKvF16 && kMod) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if constexpr (kKv != kKvF16) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
 }
 
-template <bool kMod>
 __device__ __forceinline__ void widen_registers()
 {
-    if constexpr (!kMod) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if constexpr (kMod) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
 }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
@@ -387,7 +383,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
     constexpr bool kCodes = M::kCodes;
     constexpr int S = M::kStages;
     constexpr int kRowChunks = kD / 8;
-    constexpr int kSoftWarps = soft_warps(kMod), T = row_threads(kMod);
+    constexpr int kSoftWarps = soft_warps(kCodes, kMod), T = row_threads(kCodes, kMod);
     constexpr int kCols = kTile / T, kColPages = kCols / kPage;  // of S, per softmax thread
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = ptx::smem_addr(smem);
@@ -1074,7 +1070,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
     } else {
         if constexpr (kCodes) {
             // ------------------------------------------------ codes to fp16
-            widen_registers<kMod>();
+            widen_registers();
             constexpr int R = M::kCodeStages;
             constexpr int kCh = kD / 16;  // 16-byte chunks of codes per row
             constexpr int kStep = 128 / kCh;
@@ -1096,20 +1092,18 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                     const bool dirty = kKv == kKvF8 && (j & 1) && it.dirty(it.tile(j / 2));
                     // all loads first: the thread's row advances by kStep
                     const int ch = tid % kCh, row0 = tid / kCh;
-                    constexpr int kAt = kMod && kCh > 4 ? 4 : kCh;
+                    {
+                        uint4 w[kCh];
 #pragma unroll
-                    for (int e0 = 0; e0 < kCh; e0 += kAt) {
-                        uint4 w[kAt];
-#pragma unroll
-                        for (int e = 0; e < kAt; ++e) {
-                            const int row = row0 + (e0 + e) * kStep;
+                        for (int e = 0; e < kCh; ++e) {
+                            const int row = row0 + e * kStep;
                             const uint32_t sx =
                                 kD == 128 ? (ch ^ (row & 7)) : (ch ^ ((row >> 1) & 3));
                             w[e] = ptx::lds128(src + row * kD + (sx << 4));
                         }
 #pragma unroll
-                        for (int e = 0; e < kAt; ++e) {
-                            const int row = row0 + (e0 + e) * kStep;
+                        for (int e = 0; e < kCh; ++e) {
+                            const int row = row0 + e * kStep;
                             uint4 a = widen<kKv>(w[e].x, w[e].y), b = widen<kKv>(w[e].z, w[e].w);
                             if (dirty) {
                                 // rows of V that no row of the item sees
