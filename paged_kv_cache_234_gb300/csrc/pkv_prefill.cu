@@ -33,7 +33,9 @@
 //
 // Items are numbered by bounds that the host knows (pkv_ragged.cuh), the ones
 // with the most keys first.  When they are fewer than the SMs fill, each is
-// split over its keys and a second kernel joins the parts.
+// split over its keys and a second kernel joins the parts.  An item whose rows
+// fill one tile only (a few drafted tokens) then has the second tile work on
+// the same rows, with every other tile of keys, as a part of its own.
 #include <cuda_fp16.h>
 #include <math.h>
 #include <stdint.h>
@@ -86,8 +88,8 @@ struct PrefillArgs {
     const float *k_scales, *v_scales;
     const float *slopes;
     const int32_t *prefix_lens;
-    float *part_acc;    // [splits][num_tokens * num_heads][head_dim]
-    float2 *part_ml;    // [splits][num_tokens * num_heads]: maximum, sum
+    float *part_acc;    // [2 splits][num_tokens * num_heads][head_dim]
+    float2 *part_ml;    // [2 splits][num_tokens * num_heads]: maximum, sum
     int32_t *dev_status;
     int num_tokens, num_seqs, num_heads, num_kv_heads, group;
     int chunk, chunks;  // heads of a kv head per item (the group, at most 256), chunks of them
@@ -120,8 +122,9 @@ struct Smem {
     static constexpr int kScales = kNext + 16;
     static constexpr int kItems = kScales + (kCodes ? kScaleTiles * 2 * kPagesPerTile * 4 : 0);
     static constexpr int kFlags = kItems + 2 * 64;
-    static constexpr int kSwap = kFlags + 16;   // [2 tiles][2 halves of the columns][128 rows]
-    static constexpr int kBytes = kSwap + 2 * 2 * kTile * 4;
+    // [2 in turn][2 tiles][2 halves of the columns][128 rows]
+    static constexpr int kSwap = kFlags + 16;
+    static constexpr int kBytes = kSwap + (kCodes ? 0 : 2 * 2 * 2 * kTile * 4);
     // a second CTA on the SM would wait for TMEM: ask for more than half
     static constexpr int kAsk = kBytes > 120 * 1024 ? kBytes : 120 * 1024;
     static_assert(kAsk <= 227 * 1024, "shared memory of one CTA");
@@ -194,6 +197,12 @@ struct __align__(16) Item {
 
 static_assert(sizeof(Item) == 64, "an item is 64 bytes of shared memory");
 
+// Whether the two tiles share the rows of the item.
+__device__ __forceinline__ bool paired(const PrefillArgs &p, const Item &it)
+{
+    return p.splits > 1 && it.toks * p.chunk <= kTile;
+}
+
 // The item of a block number: 1 an item with keys, 0 one without (its rows are
 // then zeros), -1 none.  The units with the most keys (the last ones of a
 // sequence) first; kv heads, chunks of heads and key splits side by side.
@@ -206,14 +215,31 @@ __device__ __forceinline__ int find_item(const PrefillArgs &p, int block, Item &
     sub /= p.splits;
     const int c = sub % p.chunks;
     it.kvh = sub / p.chunks;
-    auto base_of = [&](int s) -> int {
-        return __ldg(p.query_starts + s) / p.tokens + s;
-    };
-    it.seq = warp_search(p.num_seqs, u, base_of);
-    if (it.seq < 0) return -1;
     SeqRows sr;
-    sr.load(p.query_starts, p.context_lens, it.seq, p.num_tokens, p.ctx_cap);
-    const int64_t t0 = static_cast<int64_t>(u - base_of(it.seq)) * p.tokens;
+    int pre = 0;   // visible prefix of the sequence
+    if (p.num_seqs <= 32) {
+        // a lane per sequence: all that is asked of the batch in one round trip
+        const int lane = threadIdx.x & 31, s = min(lane, p.num_seqs - 1);
+        const int st = __ldg(p.query_starts + s), en = __ldg(p.query_starts + s + 1);
+        const int ln = __ldg(p.context_lens + s);
+        const int pr = p.prefix_lens ? __ldg(p.prefix_lens + s) : 0;
+        const bool le = lane < p.num_seqs && st / p.tokens + s <= u;
+        const unsigned m = __ballot_sync(0xffffffffu, le);
+        it.seq = (m == 0xffffffffu ? 32 : __ffs(~m) - 1) - 1;
+        if (it.seq < 0) return -1;
+        sr.set(__shfl_sync(0xffffffffu, st, it.seq), __shfl_sync(0xffffffffu, en, it.seq),
+               __shfl_sync(0xffffffffu, ln, it.seq), p.num_tokens, p.ctx_cap);
+        pre = __shfl_sync(0xffffffffu, pr, it.seq);
+    } else {
+        it.seq = warp_search(p.num_seqs, u, [&](int s) -> int64_t {
+            return static_cast<int64_t>(__ldg(p.query_starts + s) / p.tokens) + s;
+        });
+        if (it.seq < 0) return -1;
+        sr.load(p.query_starts, p.context_lens, it.seq, p.num_tokens, p.ctx_cap);
+        if (p.prefix_lens) pre = __ldg(p.prefix_lens + it.seq);
+    }
+    const int base = sr.start / p.tokens + it.seq;
+    const int64_t t0 = static_cast<int64_t>(u - base) * p.tokens;
     if (t0 < 0 || t0 >= sr.len) return -1;
     it.tok = sr.start + static_cast<int>(t0);
     it.toks = min(p.tokens, sr.len - static_cast<int>(t0));
@@ -226,7 +252,7 @@ __device__ __forceinline__ int find_item(const PrefillArgs &p, int block, Item &
     it.pos = sr.ctx - sr.len + static_cast<int>(t0);
     it.hi = it.pos + it.toks - 1;
     it.lo = p.window > 0 && it.pos >= p.window ? it.pos - p.window + 1 : 0;
-    it.pre = p.prefix_lens ? min(max(__ldg(p.prefix_lens + it.seq), 0), sr.ctx) : 0;
+    it.pre = min(max(pre, 0), sr.ctx);
     const int fp = it.lo / kPage;
     it.np1 = min((it.pre + kPage - 1) / kPage, fp);
     it.gap = fp - it.np1;
@@ -253,7 +279,7 @@ __device__ __forceinline__ void soft_registers()
 {
     if constexpr (kKv == kKvF16 && !kMod) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     if constexpr (kKv == kKvF16 && kMod) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-    if constexpr (kKv != kKvF16) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    if constexpr (kKv != kKvF16) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
 }
 
 template <int kKv, bool kMod>
@@ -261,7 +287,7 @@ __device__ __forceinline__ void issue_registers()
 {
     if constexpr (kKv == kKvF16 && !kMod) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if constexpr (kKv == kKvF16 && kMod) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if constexpr (kKv != kKvF16) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (kKv != kKvF16) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
 }
 
 __device__ __forceinline__ void widen_registers()
@@ -455,21 +481,24 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
         const int i = warp / (4 * T);                   // tile
         const int half = T == 2 ? warp >> 2 & 1 : 0;    // which of the row's columns
         const int rt = threadIdx.x & (kTile - 1);       // row of the tile
-        const int r = kTile * i + rt;                   // row of the item
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 (w mod 4)
-        const int rj = r / p.chunk, rh = r - rj * p.chunk;  // token and head of the row
+        // token and head of the thread's row, in its own tile and in the first
+        const int rj_own = (kTile * i + rt) / p.chunk, rj_first = rt / p.chunk;
         uint32_t steps = 0;   // tiles of keys of this tile of rows so far
         uint32_t outs = 0;
-        // T == 2: the other thread's value of the row (the buffer is free again
-        // when the next one is due: S is not started before both were through)
+        // T == 2: the other thread's value of the row.  Two buffers in turn: a
+        // thread that writes one again has passed the other's barrier, where
+        // the other thread arrived after it had read this one.
         [[maybe_unused]] uint32_t swaps = 0;
         [[maybe_unused]] float *sw = reinterpret_cast<float *>(smem + M::kSwap) + i * 2 * kTile;
         auto swap = [&](float v, float &other) -> bool {
-            sw[half * kTile + rt] = v;
+            float *at = sw + (swaps & 1) * 4 * kTile;
+            at[half * kTile + rt] = v;
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(swapped(i));
-            if (!wait(swapped(i), swaps++ & 1)) return false;
-            other = sw[(half ^ 1) * kTile + rt];
+            if (!wait(swapped(i), swaps & 1)) return false;
+            ++swaps;
+            other = at[(half ^ 1) * kTile + rt];
             return true;
         };
         [[maybe_unused]] uint32_t tiles = 0;  // tiles of keys of the CTA so far
@@ -481,20 +510,25 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
             const int nt = it.nt;
             if (nt == 0) break;
             const int rows = it.toks * p.chunk;
-            if (i == 1 && rows <= kTile) {
+            const bool pair = paired(p, it);
+            if (i == 1 && rows <= kTile && !pair) {
                 tiles += nt;
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(i_empty(k));
                 continue;
             }
+            const int row0 = pair ? 0 : kTile * i;          // first row of the tile
+            const int rj = pair ? rj_first : rj_own;        // token of the row
+            const int rh = row0 + rt - rj * p.chunk;        // head of the row
+            const int j0 = pair ? i : 0, step = pair ? 2 : 1;  // its tiles of keys
             const int pos = it.pos + min(rj, it.toks - 1);
             const int lo = p.window > 0 ? pos - p.window + 1 : 0;
             const int pre = it.pre;
             // positions of the tile's first and last row; all of its rows see
             // all keys of the tiles (of 8 pages) clean_a <= t < clean_b, which
             // lie behind the gap, and t < clean_p, in the prefix
-            const int pos_a = it.pos + kTile * i / p.chunk;
-            const int pos_b = it.pos + (min(kTile * i + kTile, rows) - 1) / p.chunk;
+            const int pos_a = it.pos + row0 / p.chunk;
+            const int pos_b = it.pos + (min(row0 + kTile, rows) - 1) / p.chunk;
             const int first = p.window > 0 ? max(0, pos_b - p.window + kPage) / kPage - it.gap : 0;
             const int clean_a = (max(first, it.np1) + kPagesPerTile - 1) / kPagesPerTile;
             const int clean_b = max((pos_a + 1) / kPage - it.gap, 0) / kPagesPerTile;
@@ -504,12 +538,12 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                 slope = __ldg(p.slopes + it.head + rh) * 1.4426950408889634f;
             float m = -INFINITY, l = 0.f;
             [[maybe_unused]] float vref = 0.f, vinv = 0.f;
-            for (int j = 0; j < nt; ++j) {
+            for (int j = j0; j < nt; j += step) {
                 const int tile = it.tile(j);
                 const int v0 = tile * kPagesPerTile + half * kColPages;  // the thread's first page
                 // K and V scales of the tile's pages
                 const float *scales = reinterpret_cast<const float *>(smem + M::kScales) +
-                                      (tiles & (M::kScaleTiles - 1)) * 2 * kPagesPerTile;
+                                      ((tiles + j) & (M::kScaleTiles - 1)) * 2 * kPagesPerTile;
                 [[maybe_unused]] const float *ks = scales + half * kColPages;
                 [[maybe_unused]] const float *vs = ks + kPagesPerTile;
                 ok = wait(s_full(i), steps & 1);
@@ -559,7 +593,6 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                     return kMod ? s : fmaxf(s, 1e-30f);
                 };
                 if constexpr (kCodes) {
-                    ++tiles;
                     float most = 0.f;
 #pragma unroll
                     for (int g = 0; g < kPagesPerTile; ++g)
@@ -652,7 +685,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                     const float f = m == -INFINITY ? 0.f : ptx::ex2(m - mn);
                     l *= f;
                     m = mn;
-                    if (j > 0) {
+                    if (j > j0) {
                         const float fo = f * ov;
 #pragma unroll 1
                         for (int c = half * (kD / T); c < (half + 1) * (kD / T); c += 16) {
@@ -698,10 +731,14 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(p_full(i));
             }
-            ok = ok && wait(o_full(i), outs & 1);
-            if (!ok) break;
-            ++outs;
-            umma::fence_after();
+            tiles += nt;
+            const bool any = j0 < nt;  // the tile had keys to work on
+            if (any) {
+                ok = ok && wait(o_full(i), outs & 1);
+                if (!ok) break;
+                ++outs;
+                umma::fence_after();
+            }
             if constexpr (T == 2) {  // the row's sum, the halves in their order
                 float other = 0.f;
                 ok = swap(l, other);
@@ -711,11 +748,21 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
             const bool bad = flags[1 + (k & 1)] != 0;
             const bool mine = rj < it.toks && rh < it.heads;
             int64_t row = static_cast<int64_t>(it.tok + rj) * p.num_heads + it.head + rh;
-            if (p.splits > 1) row += static_cast<int64_t>(it.z) * p.num_tokens * p.num_heads;
+            if (p.splits > 1) {
+                // part 2 z, or 2 z + 1 for the second tile of a pair; the latter
+                // is empty where the tiles have rows of their own
+                const int64_t all = static_cast<int64_t>(p.num_tokens) * p.num_heads;
+                row += (2 * it.z + (pair ? i : 0)) * all;
+                if (mine && half == 0) {
+                    if (!pair) p.part_ml[row + all] = make_float2(-INFINITY, 0.f);
+                    if (!any) p.part_ml[row] = make_float2(-INFINITY, 0.f);
+                }
+            }
             // the item is not needed any more (and this release waits for no
             // store of the rows)
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(i_empty(k));
+            if (!any) continue;
             const float vs = kCodes ? vref : 1.f;
             // The warp's rows leave by way of its 2 KB (T == 2: 1 KB) of shared
             // memory, kPass bytes of each at a time, so that a store instruction
@@ -797,8 +844,8 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                 const uint32_t q_lo = umma::desc_lo(base, 16);
                 const uint32_t k_lo = umma::desc_lo(base + M::kRing, 16);
                 const uint32_t v_lo = umma::desc_lo(base + M::kRing, M::kHalfBytes);
-                auto qk = [&](int i, int s) {  // S_i = Q_i K^T
-                    const uint32_t a = q_lo + i * (M::kHalfBytes >> 4);
+                auto qk = [&](int i, int rows, int s) {  // S_i = Q_rows K^T
+                    const uint32_t a = q_lo + rows * (M::kHalfBytes >> 4);
                     const uint32_t b = k_lo + s * (M::kTileBytes >> 4);
 #pragma unroll
                     for (int k = 0; k < kD / 16; ++k)
@@ -825,6 +872,15 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                     }
                 };
                 [[maybe_unused]] uint32_t fixes = 0;  // parity of each stage's fixes
+                // V of the j-th tile of keys has landed in stage sv
+                auto v_ready = [&](const Item &it, int j, int sv, uint32_t ph) -> bool {
+                    bool ok = wait.one(full(sv), ph);
+                    if (!kCodes && ok && it.dirty(it.tile(j))) {
+                        ok = wait.one(fixed(sv), fixes >> sv & 1u);
+                        fixes ^= 1u << sv;
+                    }
+                    return ok;
+                };
                 uint32_t steps[2] = {0, 0};
                 bool ok = true;
                 for (int k = 0; ok; ++k) {
@@ -833,47 +889,79 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                     const Item &it = item(k);
                     const int nt = it.nt;
                     if (nt == 0) break;
-                    const int last = it.toks * p.chunk > kTile ? 1 : 0;
                     ok = wait.one(q_full, k & 1) && wait.one(full(s), phase);
                     if (!ok) break;
                     umma::fence_after();
-                    qk(0, s);
-                    if (last) qk(1, s);
-                    umma::commit(empty(s));
-                    if (nt == 1) umma::commit(q_empty);
-                    advance();
-                    for (int j = 0; j < nt && ok; ++j) {
-                        const int sv = s;
-                        ok = wait.one(full(sv), phase);
-                        if (!kCodes && ok && it.dirty(it.tile(j))) {
-                            ok = wait.one(fixed(sv), fixes >> sv & 1u);
-                            fixes ^= 1u << sv;
-                        }
-                        if (!ok) break;
+                    if (!paired(p, it)) {
+                        // every tile of keys for one or two tiles of rows
+                        const int last = it.toks * p.chunk > kTile ? 1 : 0;
+                        qk(0, 0, s);
+                        if (last) qk(1, 1, s);
+                        umma::commit(empty(s));
+                        if (nt == 1) umma::commit(q_empty);
                         advance();
-                        for (int i = 0; i <= last; ++i) {
-                            ok = wait.one(p_full(i), steps[i] & 1);
+                        for (int j = 0; j < nt && ok; ++j) {
+                            const int sv = s;
+                            ok = v_ready(it, j, sv, phase);
                             if (!ok) break;
-                            ++steps[i];
-                            umma::fence_after();
-                            pv(i, sv, j > 0);
-                            if (i == last) umma::commit(empty(sv));
-                            if (j + 1 < nt) {
-                                if (i == 0) {
-                                    ok = wait.one(full(s), phase);
-                                    if (!ok) break;
-                                    umma::fence_after();
+                            advance();
+                            for (int i = 0; i <= last; ++i) {
+                                ok = wait.one(p_full(i), steps[i] & 1);
+                                if (!ok) break;
+                                ++steps[i];
+                                umma::fence_after();
+                                pv(i, sv, j > 0);
+                                if (i == last) umma::commit(empty(sv));
+                                if (j + 1 < nt) {
+                                    if (i == 0) {
+                                        ok = wait.one(full(s), phase);
+                                        if (!ok) break;
+                                        umma::fence_after();
+                                    }
+                                    qk(i, i, s);
+                                    if (i == last) {
+                                        umma::commit(empty(s));
+                                        if (j + 2 == nt) umma::commit(q_empty);
+                                    }
+                                } else {
+                                    umma::commit(o_full(i));
                                 }
-                                qk(i, s);
-                                if (i == last) {
-                                    umma::commit(empty(s));
-                                    if (j + 2 == nt) umma::commit(q_empty);
-                                }
-                            } else {
+                            }
+                            if (j + 1 < nt) advance();
+                        }
+                    } else {
+                        // the tiles of keys in turn for the two tiles, which
+                        // share the rows; K is two elements of the ring ahead
+                        qk(0, 0, s);
+                        umma::commit(empty(s));
+                        if (nt == 1) umma::commit(q_empty);
+                        advance();
+                        for (int j = -1; j < nt && ok; ++j) {
+                            // (j = -1: only the second tile's first product)
+                            const int i = j & 1, sv = s;
+                            const uint32_t ph = phase;
+                            if (j >= 0) {
+                                ok = v_ready(it, j, sv, ph) && wait.one(p_full(i), steps[i] & 1);
+                                if (!ok) break;
+                                ++steps[i];
+                                umma::fence_after();
+                                pv(i, sv, j > 1);
+                                umma::commit(empty(sv));
+                                advance();          // K of j + 1, taken before
+                                if (j + 1 < nt) advance();
+                            }
+                            if (j + 2 < nt) {
+                                const int sk = s + 1 == S ? 0 : s + 1;
+                                ok = wait.one(full(sk), s + 1 == S ? phase ^ 1 : phase);
+                                if (!ok) break;
+                                umma::fence_after();
+                                qk(i, 0, sk);
+                                umma::commit(empty(sk));
+                                if (j + 3 == nt) umma::commit(q_empty);
+                            } else if (j >= 0) {
                                 umma::commit(o_full(i));
                             }
                         }
-                        if (j + 1 < nt) advance();
                     }
                     ptx::mbar_arrive(i_empty(k));
                 }
@@ -1048,8 +1136,9 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                             reinterpret_cast<uint4 *>(p.out + row * kD)[e % kRowChunks] =
                                 make_uint4(0, 0, 0, 0);
                         else if (e % kRowChunks == 0)
-                            p.part_ml[static_cast<int64_t>(it.z) * p.num_tokens * p.num_heads +
-                                      row] = make_float2(-INFINITY, 0.f);
+                            for (int part = 2 * it.z; part < 2 * it.z + 2; ++part)
+                                p.part_ml[static_cast<int64_t>(part) * p.num_tokens * p.num_heads +
+                                          row] = make_float2(-INFINITY, 0.f);
                     }
                 }
                 // (also after a wait that ran out: the answer must have come)
@@ -1134,54 +1223,107 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
     if (warp == kSoftWarps) umma::dealloc(tmem, 512);
 }
 
-// Joins the key splits of every row: a warp per row, lanes along head_dim, the
-// parts in their order.
+// Joins the parts of every row, four warps a row.
 //   out = sum_z 2^(m_z - M) acc_z / sum_z 2^(m_z - M) l_z,  M = max_z m_z
-// A part with l < 0 (a bad block) makes the row zeros.  Rows that no sequence
-// owns have no parts and are left alone.
-constexpr int kJoinThreads = 256;
+// Every lane fetches the maxima and sums of its parts, then the lanes lie along
+// head_dim: warp w adds up parts w, w + 4, .., eight loads in flight, and the
+// warps' sums are added in their order.  A part with l < 0 (a bad block) makes
+// the row zeros.  Rows that no sequence owns have no parts and are left alone.
+constexpr int kJoinWarps = 4;
 
 template <int kD>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ PrefillArgs p)
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ PrefillArgs p)
 {
     constexpr int kC = kD / 32;
-    const int lane = threadIdx.x & 31;
+    __shared__ float sums[kJoinWarps][kD];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t all = static_cast<int64_t>(p.num_tokens) * p.num_heads;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
+    const int64_t row = blockIdx.x;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    if (row >= all) return;
+    // lane z: part z's (and z + 32's ..) maximum and sum
+    constexpr int kPer = 2 * kMaxSplits / 32;
+    const int parts = 2 * p.splits;
+    float pm[kPer], pl[kPer], m = -INFINITY;
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+        const int z = lane + 32 * e;
+        const float2 ml =
+            z < parts ? __ldcg(p.part_ml + z * all + row) : make_float2(-INFINITY, 0.f);
+        pm[e] = ml.x;
+        pl[e] = ml.y;
+        m = fmaxf(m, ml.x);
+        bad |= ml.y < 0.f;
+    }
+    // (whose row it is, while the parts' maxima are on their way)
     const int tok = static_cast<int>(row / p.num_heads);
     const int seq = warp_search(p.num_seqs, tok, [&](int s) { return __ldg(p.query_starts + s); });
     if (seq < 0) return;
     SeqRows sr;
     sr.load(p.query_starts, p.context_lens, seq, p.num_tokens, p.ctx_cap);
     if (tok - sr.start >= sr.len) return;
-    float m = -INFINITY;
-    for (int z = lane; z < p.splits; z += 32) m = fmaxf(m, __ldcg(p.part_ml + z * all + row).x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.f, acc[kC];
-    bool bad = false;
+    bad = __any_sync(0xffffffffu, bad);
+    float l = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+        // the part's factor (0 where no key was seen: it has no accumulators)
+        pm[e] = pl[e] == 0.f ? 0.f : ptx::ex2(pm[e] - m);
+        l += pm[e] * pl[e];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    float acc[kC];
 #pragma unroll
     for (int c = 0; c < kC; ++c) acc[c] = 0.f;
-    for (int z = 0; z < p.splits; ++z) {
-        const float2 ml = __ldcg(p.part_ml + z * all + row);
-        bad |= ml.y < 0.f;
-        if (ml.y == 0.f) continue;  // no key seen (or no part: no accumulators)
-        const float f = ptx::ex2(ml.x - m);
-        l += f * ml.y;
-        const float *a = p.part_acc + (z * all + row) * kD + lane * kC;
+    const float *src = p.part_acc + row * kD + lane * kC;
 #pragma unroll
-        for (int c = 0; c < kC; ++c) acc[c] += f * __ldcg(a + c);
+    for (int e = 0; e < kPer; ++e)
+        if (32 * e < parts) {
+            float v[8][kC], f[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int z = warp + kJoinWarps * u;   // of these 32
+                f[u] = __shfl_sync(0xffffffffu, pm[e], z);
+#pragma unroll
+                for (int c = 0; c < kC; ++c) v[u][c] = 0.f;
+                if (f[u] != 0.f) {
+                    const float *a = src + (32 * e + z) * all * kD;
+                    if constexpr (kC == 4) {
+                        const float4 w = __ldcg(reinterpret_cast<const float4 *>(a));
+                        v[u][0] = w.x;
+                        v[u][1] = w.y;
+                        v[u][2] = w.z;
+                        v[u][3] = w.w;
+                    } else {
+                        const float2 w = __ldcg(reinterpret_cast<const float2 *>(a));
+                        v[u][0] = w.x;
+                        v[u][1] = w.y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+#pragma unroll
+                for (int c = 0; c < kC; ++c) acc[c] += f[u] * v[u][c];
+        }
+#pragma unroll
+    for (int c = 0; c < kC; ++c) sums[warp][lane * kC + c] = acc[c];
+    __syncthreads();
+    const int c = 2 * threadIdx.x;
+    if (c < kD) {
+        float a = 0.f, b = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            a += sums[w][c];
+            b += sums[w][c + 1];
+        }
+        const bool zero = bad || l == 0.f;
+        *reinterpret_cast<__half2 *>(p.out + row * kD + c) =
+            __floats2half2_rn(zero ? 0.f : a / l, zero ? 0.f : b / l);
     }
-    const float f = bad || l == 0.f ? 0.f : 1.f / l;
-    __half *dst = p.out + row * kD + lane * kC;
-#pragma unroll
-    for (int c = 0; c < kC; c += 2)
-        *reinterpret_cast<__half2 *>(dst + c) =
-            __floats2half2_rn(bad || l == 0.f ? 0.f : acc[c] * f,
-                              bad || l == 0.f ? 0.f : acc[c + 1] * f);
 }
 
 // -------------------------------------------------------------------- host
@@ -1241,7 +1383,7 @@ pkv_status plan_of(int num_tokens, int num_seqs, int num_heads, int num_kv_heads
         }
     }
     plan->bytes = plan->splits == 1 ? 0
-                                    : static_cast<size_t>(plan->splits) * num_tokens * num_heads *
+                                    : static_cast<size_t>(2 * plan->splits) * num_tokens * num_heads *
                                           (head_dim + 2) * sizeof(float);
     return PKV_OK;
 }
@@ -1288,7 +1430,7 @@ pkv_status launch_prefill(const PrefillCall &c, const Plan &plan)
     a.prefix_lens = c.prefix_lens;
     a.part_acc = static_cast<float *>(c.workspace);
     a.part_ml = reinterpret_cast<float2 *>(
-        a.part_acc + static_cast<size_t>(plan.splits) * c.num_tokens * c.num_heads * kD);
+        a.part_acc + static_cast<size_t>(2 * plan.splits) * c.num_tokens * c.num_heads * kD);
     a.dev_status = c.dev_status;
     a.num_tokens = c.num_tokens;
     a.num_seqs = c.num_seqs;
@@ -1323,8 +1465,8 @@ pkv_status launch_prefill(const PrefillCall &c, const Plan &plan)
     cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, tmq, tmk, tmv);
     if (e == cudaSuccess && plan.splits > 1) {
         const int64_t all = static_cast<int64_t>(c.num_tokens) * c.num_heads;
-        cfg.gridDim = dim3(static_cast<unsigned>((all + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
-        cfg.blockDim = dim3(kJoinThreads);
+        cfg.gridDim = dim3(static_cast<unsigned>(all));
+        cfg.blockDim = dim3(32 * kJoinWarps);
         cfg.dynamicSmemBytes = 0;
         e = cudaLaunchKernelEx(&cfg, join_kernel<kD>, a);
     }

@@ -49,9 +49,14 @@ struct SeqRows {
                                          const int32_t *__restrict__ lens, int s, int num_tokens,
                                          int ctx_cap)
     {
-        start = __ldg(starts + s);
-        const int64_t l = static_cast<int64_t>(__ldg(starts + s + 1)) - start;
-        ctx = __ldg(lens + s);
+        set(__ldg(starts + s), __ldg(starts + s + 1), __ldg(lens + s), num_tokens, ctx_cap);
+    }
+
+    __device__ __forceinline__ void set(int first, int end, int cached, int num_tokens, int ctx_cap)
+    {
+        start = first;
+        ctx = cached;
+        const int64_t l = static_cast<int64_t>(end) - first;
         ok = start >= 0 && l >= 0 && start + l <= num_tokens && l <= ctx && ctx <= ctx_cap;
         len = l < 0 ? 0 : l > num_tokens ? num_tokens : static_cast<int>(l);
     }

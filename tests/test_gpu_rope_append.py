@@ -142,22 +142,27 @@ def test_against_the_64_bit_rotation(interleaved):
 
 @pytest.mark.parametrize("kind", ["int8", "fp8"])
 def test_codes_next_to_the_plain_quantizers(kind):
-    # the scales differ by 2^-23 at most (a product and its rounded constant
-    # against a quotient, half a step each), so a code differs only where its
-    # quotient lies within 2^-22 of a border, and then by one step
+    # With S = amax / most exactly: the plain quantizers' scale is S within
+    # 2^-24 (one rounding), this one S within 2^-23 (the constant's and the
+    # product's), so they are 1.5 * 2^-23 apart at most (up to 2^-46), and both
+    # fp32 quotients lie within 2^-23 + 2^-24 < 2^-22 of x / S.  Two codes that
+    # differ are therefore neighbours, with their midpoint within 2^-22 of it.
     b = R.make(65, [200], [200], 4, 2, 128, nan_tail=False)
     qkv = qkv_of(b, 65, 200)
     r = Run(b, kind, qkv, table(200, 128))()
     quant = oracle.quantize_fp8 if kind == "fp8" else oracle.quantize
+    value = R.e4m3 if kind == "fp8" else (lambda c: c.astype(np.float64))
+    most = 448.0 if kind == "fp8" else 127.0
     for x, pool in ((0, r.k), (1, r.v)):
-        codes, scales = quant(pool.cpu().numpy())
-        used = b.used
-        got_c, got_s = r.codes[x].cpu().numpy()[used], r.codes[2 + x].cpu().numpy()[used]
-        assert np.all(np.abs(got_s / scales[used].astype(np.float64) - 1) <= 1.01 * 2.0 ** -23)
-        differ = got_c != codes[used]
-        assert np.mean(differ) < 1e-4
-        step = got_c[differ].astype(np.int64) - codes[used][differ].astype(np.int64)
-        assert np.all(np.abs(step) == 1)
+        tiles = pool.cpu().numpy()[b.used].astype(np.float64)
+        codes, scales = (a[b.used] for a in quant(pool.cpu().numpy()))
+        got_c, got_s = r.codes[x].cpu().numpy()[b.used], r.codes[2 + x].cpu().numpy()[b.used]
+        assert np.all(np.abs(got_s / scales.astype(np.float64) - 1) <= 1.51 * 2.0 ** -23)
+        exact = tiles / (np.abs(tiles).max((2, 3), keepdims=True) / most)
+        differ = got_c != codes
+        mid = (value(got_c) + value(codes))[differ] / 2
+        assert np.all(np.abs(got_c[differ].astype(np.int64) - codes[differ].astype(np.int64)) == 1)
+        assert np.all(np.abs(exact[differ] - mid) <= 2.0 ** -22 * np.abs(mid))
 
 
 @pytest.mark.parametrize("kind", ["fp16", "int8"])

@@ -114,8 +114,8 @@ def test_prefill(kind):
 
 
 def test_prefill_workspace_size():
-    # splits * rows * (head_dim + 2) floats; none where the items fill the GPU
-    one = 8 * 4 * (128 + 2) * 4
+    # 2 splits * rows * (head_dim + 2) floats; none where the items fill the GPU
+    one = 2 * 8 * 4 * (128 + 2) * 4
     size = pkv.pkv_prefill_workspace_size(8, 1, 4, 1, 128, 20000)
     assert size % one == 0 and 2 <= size // one <= 64
     assert pkv.pkv_prefill_workspace_size(65536, 16, 32, 8, 128, 4096) == 0
