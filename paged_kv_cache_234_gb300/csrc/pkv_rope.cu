@@ -48,6 +48,7 @@ struct RopeArgs {
     int max_position, rot, interleaved, axes;
     int max_blocks_per_seq, num_tokens, num_seqs, num_heads, num_kv_heads, num_blocks;
     int units;                             // page units of the batch (code caches)
+    int tokens_per_cta;                    // of rope_tokens
     uint8_t axis_of_pair[kMaxPairs];
 };
 
@@ -152,16 +153,17 @@ __device__ __forceinline__ void rotate(const RopeArgs &p, const Pair8 &t, uint4 
     x1 = y1;
 }
 
-// One token's rows by a CTA of kThreads threads: the queries, and with kCache
+// One token's rows by a team of kTeam threads: the queries, and with kCache
 // the keys and values too (into the fp16 pools).  The first rows are on their
 // way while the token's sequence, block and table row are looked up.
-template <int kD, int kThreads, bool kCache>
+template <int kD, int kTeam, bool kCache>
 __device__ __forceinline__ void rope_token(const RopeArgs &p, int tok)
 {
+    const int tid = threadIdx.x % kTeam;
     constexpr int kSlots = kD / 16;              // slots per row
-    constexpr int kRows = kThreads / kSlots;     // rows per pass of the CTA
+    constexpr int kRows = kTeam / kSlots;        // rows per pass of the team
     constexpr int kBatch = 4;                    // rows in flight per thread
-    const int c = threadIdx.x % kSlots, r0 = threadIdx.x / kSlots;
+    const int c = tid % kSlots, r0 = tid / kSlots;
     const int heads = p.num_heads, kv = p.num_kv_heads;
     const int rows = kCache ? heads + 2 * kv : heads;
     int c0, c1;
@@ -197,17 +199,17 @@ __device__ __forceinline__ void rope_token(const RopeArgs &p, int tok)
     if (tok - sr.start >= sr.len) return;  // behind the last sequence: left as it was
     const int pos = sr.ctx - sr.len + (tok - sr.start);
     bool live = sr.ok;
-    report(p, !live && threadIdx.x == 0 && tok == max(sr.start, 0), PKV_DEV_BAD_CTX);
+    report(p, !live && tid == 0 && tok == max(sr.start, 0), PKV_DEV_BAD_CTX);
     if (live && !positions_ok(p, tok, pos)) {
         live = false;
-        report(p, threadIdx.x == 0, PKV_DEV_BAD_POS);
+        report(p, tid == 0, PKV_DEV_BAD_POS);
     }
     int64_t blk = -1;
     if (kCache && live) {
         blk = __ldg(p.block_tables + static_cast<int64_t>(seq) * p.max_blocks_per_seq + (pos >> 4));
         if (blk < 0 || blk >= p.num_blocks) {
             blk = -1;
-            report(p, threadIdx.x == 0, PKV_DEV_BAD_BLOCK);
+            report(p, tid == 0, PKV_DEV_BAD_BLOCK);
         }
     }
     Pair8 t;
@@ -239,44 +241,55 @@ __device__ __forceinline__ void rope_token(const RopeArgs &p, int tok)
     }
 }
 
+// The tokens of a CTA: a warp each where a token has few rows (a CTA to itself
+// would leave most of its threads without any: 64206 tokens of 8 heads of 64
+// took 88 us so, against 52), else one.
+template <int kD, bool kCache>
+__device__ __forceinline__ void rope_tokens(const RopeArgs &p, int group)
+{
+    if (p.tokens_per_cta == 1) {
+        rope_token<kD, kRowThreads, kCache>(p, group);
+    } else {
+        const int tok = group * p.tokens_per_cta + static_cast<int>(threadIdx.x >> 5);
+        if (tok < p.num_tokens) rope_token<kD, 32, kCache>(p, tok);
+    }
+}
+
 template <int kD>
 __global__ void __launch_bounds__(kRowThreads) rope_fp16_kernel(const __grid_constant__ RopeArgs p)
 {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    rope_token<kD, kRowThreads, true>(p, blockIdx.x);
+    rope_tokens<kD, true>(p, blockIdx.x);
 }
 
-// Code caches.  The first CTAs own one (page, kv head, K | V) tile each: a
-// tile's new rows come rotated from the input and go to the fp16 pool, its
-// other rows come from the pool, and all 16 rows are quantized.  The CTAs
-// behind them rotate one token's queries each.
-template <int kD>
-__host__ __device__ constexpr int rope_tile_threads()
-{
-    return kD;  // 16 rows of kD / 16 slots
-}
-
+// Code caches.  The first CTAs own one (page, kv head, K | V) tile each, at
+// head_dim 64 the K and the V tile of a (page, kv head): a tile's new rows come
+// rotated from the input and go to the fp16 pool, its other rows come from the
+// pool, and all 16 rows are quantized.  The CTAs behind them rotate a few
+// tokens' queries each.
 template <int kD, bool kFp8>
-__global__ void __launch_bounds__(rope_tile_threads<kD>())
-    rope_codes_kernel(const __grid_constant__ RopeArgs p)
+__global__ void __launch_bounds__(kRowThreads) rope_codes_kernel(const __grid_constant__ RopeArgs p)
 {
-    constexpr int kThreads = rope_tile_threads<kD>();
+    constexpr int kTileThreads = kD;                     // 16 rows of kD / 16 slots
+    constexpr int kTiles = kRowThreads / kTileThreads;   // per CTA
     constexpr int kSlots = kD / 16, kRowChunks = kD / 8;
-    __shared__ float warp_max[kThreads / 32];
+    __shared__ float warp_max[kRowThreads / 32];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int kv = p.num_kv_heads;
-    const int64_t tiles = static_cast<int64_t>(p.units) * kv * 2;
+    const int per_unit = kv * 2 / kTiles;                // CTAs of a page
+    const int64_t tiles = static_cast<int64_t>(p.units) * per_unit;
     if (blockIdx.x >= tiles) {
-        rope_token<kD, kThreads, false>(p, static_cast<int>(blockIdx.x - tiles));
+        rope_tokens<kD, false>(p, static_cast<int>(blockIdx.x - tiles));
         return;
     }
-    const int unit = static_cast<int>(blockIdx.x / (2 * kv));
-    const int hv = static_cast<int>(blockIdx.x - static_cast<int64_t>(unit) * 2 * kv);
-    const bool is_v = hv >= kv;
-    const int h = is_v ? hv - kv : hv;
-    const bool first = threadIdx.x == 0 && hv == 0;
+    const int unit = static_cast<int>(blockIdx.x / per_unit);
+    const int sub = static_cast<int>(blockIdx.x - static_cast<int64_t>(unit) * per_unit);
+    const int tid = threadIdx.x % kTileThreads;
+    const bool is_v = kTiles == 2 ? threadIdx.x >= kTileThreads : sub >= kv;
+    const int h = kTiles == 2 || sub < kv ? sub : sub - kv;
+    const bool first = threadIdx.x == 0 && sub == 0;
 
     // pages of sequence s: units from floor(starts[s] / 16) + 2 s on (a run
     // of 16 m + r tokens touches at most m + 2 pages)
@@ -296,7 +309,7 @@ __global__ void __launch_bounds__(rope_tile_threads<kD>())
         report(p, first, PKV_DEV_BAD_BLOCK);
         return;
     }
-    const int c = threadIdx.x % kSlots, row = threadIdx.x / kSlots;
+    const int c = tid % kSlots, row = tid / kSlots;
     int c0 = 2 * c, c1 = 2 * c + 1;
     if (!is_v) slot_chunks(p, c, c0, c1);
     const int64_t tile = blk * kv + h;
@@ -323,14 +336,22 @@ __global__ void __launch_bounds__(rope_tile_threads<kD>())
         raw[0] = pool[c0];
         raw[1] = pool[c1];
     }
-    const float amax = cta_absmax<kThreads>(chunks_absmax(raw), warp_max);
+    // the largest magnitude of the tile's threads
+    float amax = chunks_absmax(raw);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kTileThreads / 32; ++w)
+        amax = fmaxf(amax, warp_max[threadIdx.x / kTileThreads * (kTileThreads / 32) + w]);
     const float scale = __fmul_rn(amax, kFp8 ? 1.0f / 448.0f : 1.0f / 127.0f);
     const float rcp = __frcp_rn(scale);
     uint2 *dst = reinterpret_cast<uint2 *>(is_v ? p.v_codes : p.k_codes) +
                  (tile * 16 + row) * kRowChunks;
     dst[c0] = kFp8 ? chunk_codes_fp8(raw[0], scale) : chunk_codes(raw[0], scale, rcp);
     dst[c1] = kFp8 ? chunk_codes_fp8(raw[1], scale) : chunk_codes(raw[1], scale, rcp);
-    if (threadIdx.x == 0) (is_v ? p.v_scales : p.k_scales)[tile] = scale;
+    if (tid == 0) (is_v ? p.v_scales : p.k_scales)[tile] = scale;
 }
 
 struct RopeCall {
@@ -356,13 +377,12 @@ struct RopeCall {
 };
 
 template <typename Kernel>
-pkv_status launch_rope(Kernel kernel, int64_t grid, int threads, const RopeCall &c,
-                       const RopeArgs &a)
+pkv_status launch_rope(Kernel kernel, int64_t grid, const RopeCall &c, const RopeArgs &a)
 {
     if (grid > INT32_MAX) return PKV_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(threads);
+    cfg.blockDim = dim3(kRowThreads);
     cfg.stream = static_cast<cudaStream_t>(c.stream);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -446,21 +466,22 @@ pkv_status rope_entry(const RopeCall &c, int kind)
     a.num_kv_heads = c.num_kv_heads;
     a.num_blocks = c.num_blocks;
     a.units = 0;
+    const int slots = (kind == kRopeF16 ? c.num_heads + 2 * c.num_kv_heads : c.num_heads) *
+                      (c.head_dim / 16);
+    a.tokens_per_cta = slots <= kRowThreads ? kRowThreads / 32 : 1;
+    const int64_t groups = (c.num_tokens + a.tokens_per_cta - 1) / a.tokens_per_cta;
     if (kind == kRopeF16)
-        return c.head_dim == 128
-                   ? launch_rope(rope_fp16_kernel<128>, c.num_tokens, kRowThreads, c, a)
-                   : launch_rope(rope_fp16_kernel<64>, c.num_tokens, kRowThreads, c, a);
+        return c.head_dim == 128 ? launch_rope(rope_fp16_kernel<128>, groups, c, a)
+                                 : launch_rope(rope_fp16_kernel<64>, groups, c, a);
     const int64_t units = static_cast<int64_t>(c.num_tokens) / 16 + 2 * static_cast<int64_t>(c.num_seqs);
     if (units > INT32_MAX) return PKV_ERR_UNSUPPORTED;
     a.units = static_cast<int>(units);
-    const int64_t grid = units * c.num_kv_heads * 2 + c.num_tokens;
+    const int64_t grid = units * c.num_kv_heads * (c.head_dim == 128 ? 2 : 1) + groups;
     if (c.head_dim == 128)
-        return kind == kRopeF8
-                   ? launch_rope(rope_codes_kernel<128, true>, grid, rope_tile_threads<128>(), c, a)
-                   : launch_rope(rope_codes_kernel<128, false>, grid, rope_tile_threads<128>(), c, a);
-    return kind == kRopeF8
-               ? launch_rope(rope_codes_kernel<64, true>, grid, rope_tile_threads<64>(), c, a)
-               : launch_rope(rope_codes_kernel<64, false>, grid, rope_tile_threads<64>(), c, a);
+        return kind == kRopeF8 ? launch_rope(rope_codes_kernel<128, true>, grid, c, a)
+                               : launch_rope(rope_codes_kernel<128, false>, grid, c, a);
+    return kind == kRopeF8 ? launch_rope(rope_codes_kernel<64, true>, grid, c, a)
+                           : launch_rope(rope_codes_kernel<64, false>, grid, c, a);
 }
 
 }  // namespace
