@@ -62,15 +62,14 @@ constexpr int kPagesPerTile = kTile / kPage;
 // where a score is worked out first (cap, bias): one thread's row would take
 // 2600 cycles, in which the tensor core has done its part of 1024 long since;
 // the two exchange their maxima and sums.
-// (Codes keep one: the warps that widen them leave too few registers for two.)
-__host__ __device__ constexpr int row_threads(bool codes, bool mod)
+__host__ __device__ constexpr int row_threads(bool mod)
 {
-    return mod && !codes ? 2 : 1;
+    return mod ? 2 : 1;
 }
 
-__host__ __device__ constexpr int soft_warps(bool codes, bool mod)
+__host__ __device__ constexpr int soft_warps(bool mod)
 {
-    return 8 * row_threads(codes, mod);
+    return 8 * row_threads(mod);
 }
 constexpr int kSms = 152;       // GB300: what the split over the keys aims to fill
 constexpr int kMaxSplits = 64;
@@ -122,9 +121,8 @@ struct Smem {
     static constexpr int kScales = kNext + 16;
     static constexpr int kItems = kScales + (kCodes ? kScaleTiles * 2 * kPagesPerTile * 4 : 0);
     static constexpr int kFlags = kItems + 2 * 64;
-    // [2 in turn][2 tiles][2 halves of the columns][128 rows]
-    static constexpr int kSwap = kFlags + 16;
-    static constexpr int kBytes = kSwap + (kCodes ? 0 : 2 * 2 * 2 * kTile * 4);
+    static constexpr int kSwap = kFlags + 16;   // [2 tiles][2 halves of the columns][128 rows]
+    static constexpr int kBytes = kSwap + 2 * 2 * kTile * 4;
     // a second CTA on the SM would wait for TMEM: ask for more than half
     static constexpr int kAsk = kBytes > 120 * 1024 ? kBytes : 120 * 1024;
     static_assert(kAsk <= 227 * 1024, "shared memory of one CTA");
@@ -269,17 +267,19 @@ __device__ __forceinline__ int find_item(const PrefillArgs &p, int block, Item &
 template <int kKv, bool kMod>
 __host__ __device__ constexpr int prefill_threads()
 {
-    return 32 * (soft_warps(kKv != kKvF16, kMod) + (kKv == kKvF16 ? 4 : 8));
+    return 32 * (soft_warps(kMod) + (kKv == kKvF16 ? 4 : 8));
 }
 
 // Registers: all threads are launched with 65536 / threads, rounded down to a
-// multiple of 8 (fp16: 168 for 384 threads, 96 for 640; codes: 128 for 512).  The softmax warps take what the others give back.
+// multiple of 8 (fp16: 168 for 384 threads, 96 for 640; codes: 128 for 512, 80
+// for 768).  The softmax warps take what the others give back.
 template <int kKv, bool kMod>
 __device__ __forceinline__ void soft_registers()
 {
     if constexpr (kKv == kKvF16 && !kMod) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     if constexpr (kKv == kKvF16 && kMod) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-    if constexpr (kKv != kKvF16) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    if constexpr (kKv != kKvF16 && !kMod) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    if constexpr (kKv != kKvF16 && kMod) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
 }
 
 template <int kKv, bool kMod>
@@ -287,12 +287,15 @@ __device__ __forceinline__ void issue_registers()
 {
     if constexpr (kKv == kKvF16 && !kMod) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if constexpr (kKv == kKvF16 && kMod) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if constexpr (kKv != kKvF16) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if constexpr (kKv != kKvF16 && !kMod) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if constexpr (kKv != kKvF16 && kMod) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
 }
 
+template <bool kMod>
 __device__ __forceinline__ void widen_registers()
 {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if constexpr (!kMod) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if constexpr (kMod) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
 }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
@@ -409,7 +412,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
     constexpr bool kCodes = M::kCodes;
     constexpr int S = M::kStages;
     constexpr int kRowChunks = kD / 8;
-    constexpr int kSoftWarps = soft_warps(kCodes, kMod), T = row_threads(kCodes, kMod);
+    constexpr int kSoftWarps = soft_warps(kMod), T = row_threads(kMod);
     constexpr int kCols = kTile / T, kColPages = kCols / kPage;  // of S, per softmax thread
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = ptx::smem_addr(smem);
@@ -486,19 +489,23 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
         const int rj_own = (kTile * i + rt) / p.chunk, rj_first = rt / p.chunk;
         uint32_t steps = 0;   // tiles of keys of this tile of rows so far
         uint32_t outs = 0;
-        // T == 2: the other thread's value of the row.  Two buffers in turn: a
-        // thread that writes one again has passed the other's barrier, where
-        // the other thread arrived after it had read this one.
+        // T == 2: the other thread's value of the row.  The buffer is free again
+        // when the next one is due: in an item because S is not started before
+        // both threads were through, behind its last one by a barrier that the
+        // next item's first exchange waits for.
         [[maybe_unused]] uint32_t swaps = 0;
+        [[maybe_unused]] bool held = false;
         [[maybe_unused]] float *sw = reinterpret_cast<float *>(smem + M::kSwap) + i * 2 * kTile;
-        auto swap = [&](float v, float &other) -> bool {
-            float *at = sw + (swaps & 1) * 4 * kTile;
-            at[half * kTile + rt] = v;
+        auto swap = [&](float v, float &other, bool last) -> bool {
+            if (held && !wait(swapped(i), swaps++ & 1)) return false;
+            sw[half * kTile + rt] = v;
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(swapped(i));
-            if (!wait(swapped(i), swaps & 1)) return false;
-            ++swaps;
-            other = at[(half ^ 1) * kTile + rt];
+            if (!wait(swapped(i), swaps++ & 1)) return false;
+            other = sw[(half ^ 1) * kTile + rt];
+            held = last;
+            __syncwarp();
+            if (last && lane == 0) ptx::mbar_arrive(swapped(i));
             return true;
         };
         [[maybe_unused]] uint32_t tiles = 0;  // tiles of keys of the CTA so far
@@ -676,7 +683,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                     top *= p.scale_log2;
                 if constexpr (T == 2) {
                     float other = 0.f;
-                    ok = swap(top, other);
+                    ok = swap(top, other, false);
                     if (!ok) break;
                     top = fmaxf(top, other);
                 }
@@ -741,7 +748,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
             }
             if constexpr (T == 2) {  // the row's sum, the halves in their order
                 float other = 0.f;
-                ok = swap(l, other);
+                ok = swap(l, other, true);
                 if (!ok) break;
                 l = half == 0 ? l + other : other + l;
             }
@@ -768,7 +775,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
             // memory, kPass bytes of each at a time, so that a store instruction
             // writes whole pieces of a few rows and not 16 bytes of 32.  16-byte
             // chunk c of row r lies at kCh r + (c ^ r kCh / 8 mod kCh).
-            constexpr int kPass = 64 / T, kCh = kPass / 16;
+            constexpr int kPass = M::kOutBytes / (32 * kSoftWarps), kCh = kPass / 16;
             const uint32_t out = base + M::kOut + warp * (32 * kPass);
             const uint32_t put = out + lane * kPass, get = out + (lane / kCh) * kPass;
             const int px = lane * kCh / 8 % kCh, gx = (lane % kCh) ^ (lane / kCh * kCh / 8 % kCh);
@@ -1159,7 +1166,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
     } else {
         if constexpr (kCodes) {
             // ------------------------------------------------ codes to fp16
-            widen_registers();
+            widen_registers<kMod>();
             constexpr int R = M::kCodeStages;
             constexpr int kCh = kD / 16;  // 16-byte chunks of codes per row
             constexpr int kStep = 128 / kCh;
@@ -1181,18 +1188,20 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                     const bool dirty = kKv == kKvF8 && (j & 1) && it.dirty(it.tile(j / 2));
                     // all loads first: the thread's row advances by kStep
                     const int ch = tid % kCh, row0 = tid / kCh;
-                    {
-                        uint4 w[kCh];
+                    constexpr int kAt = kMod && kCh > 4 ? 4 : kCh;   // registers
 #pragma unroll
-                        for (int e = 0; e < kCh; ++e) {
-                            const int row = row0 + e * kStep;
+                    for (int e0 = 0; e0 < kCh; e0 += kAt) {
+                        uint4 w[kAt];
+#pragma unroll
+                        for (int e = 0; e < kAt; ++e) {
+                            const int row = row0 + (e0 + e) * kStep;
                             const uint32_t sx =
                                 kD == 128 ? (ch ^ (row & 7)) : (ch ^ ((row >> 1) & 3));
                             w[e] = ptx::lds128(src + row * kD + (sx << 4));
                         }
 #pragma unroll
-                        for (int e = 0; e < kCh; ++e) {
-                            const int row = row0 + e * kStep;
+                        for (int e = 0; e < kAt; ++e) {
+                            const int row = row0 + (e0 + e) * kStep;
                             uint4 a = widen<kKv>(w[e].x, w[e].y), b = widen<kKv>(w[e].z, w[e].w);
                             if (dirty) {
                                 // rows of V that no row of the item sees
