@@ -330,7 +330,7 @@ PKV_API pkv_status pkv_append_fp8(void *k_cache, void *v_cache, uint8_t *k_codes
  *   out         fp16 [num_seqs][num_heads][head_dim], 16-byte aligned (the
  *               type of the query and of the projection that follows; the
  *               fp32 result is rounded once)
- *   logit_cap   0: no cap; finite, >= 0
+ *   logit_cap   0: no cap; else 1e-30 .. 1e30
  *   window      0: no window (every t <= i is seen); else tokens at a
  *               distance below it are seen
  *   slopes      fp32 [num_heads] in device memory, or NULL: no bias

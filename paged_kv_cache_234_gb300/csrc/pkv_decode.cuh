@@ -2129,7 +2129,8 @@ pkv_status decode_entry(const DecodeCall &call, int kv)
     if (!(call.softmax_scale == call.softmax_scale) || call.softmax_scale > 3.0e38f ||
         call.softmax_scale < -3.0e38f)
         return PKV_ERR_INVALID_ARG;
-    if (kScored && (!(call.logit_cap >= 0.f) || call.logit_cap > 3.0e38f || call.window < 0))
+    if (kScored && (!(fabsf(call.softmax_scale) <= 2.0e38f) || !valid_cap(call.logit_cap) ||
+                    call.window < 0))
         return PKV_ERR_INVALID_ARG;
     Shape sh;
     const pkv_status st = check_shape(call.num_seqs, call.num_heads, call.num_kv_heads,

@@ -31,6 +31,10 @@
 // warps 12-15 widen them exactly to fp16; the K scales multiply the scores, the
 // V scales enter the probabilities as a ratio to the largest one so far.
 //
+// Measured on GB300, 32 / 8 heads, head_dim 128: 2048 tokens over 8192 in 170 us
+// (1410 TFLOP/s, 0.75 of the measured bf16 rate), capped 269, INT8 205; 8
+// prompts of 2048 in 231 us (0.63; 245 among other inputs in turn).
+//
 // Items are numbered by bounds that the host knows (pkv_ragged.cuh), the ones
 // with the most keys first.  When they are fewer than the SMs fill, each is
 // split over its keys and a second kernel joins the parts.  An item whose rows
@@ -529,7 +533,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
             const int rh = row0 + rt - rj * p.chunk;        // head of the row
             const int j0 = pair ? i : 0, step = pair ? 2 : 1;  // its tiles of keys
             const int pos = it.pos + min(rj, it.toks - 1);
-            const int lo = p.window > 0 ? pos - p.window + 1 : 0;
+            const int lo = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
             const int pre = it.pre;
             // positions of the tile's first and last row; all of its rows see
             // all keys of the tiles (of 8 pages) clean_a <= t < clean_b, which
@@ -567,9 +571,11 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                            t0 + kPage <= pre;
                 };
                 if constexpr (!kMod) {
-                    // masked where they lie, by a loop of a few instructions:
-                    // unrolled on registers it is 400 that are rarely in the
-                    // instruction cache (2600 cycles a tile)
+                    // masked where they lie, by a loop of a few instructions.  Its
+                    // own gain was not measured: the first masked tile took 2600
+                    // cycles more than a clean one unrolled on registers and so
+                    // alike.  Rolled together with the rows' way out: 8 prompts of
+                    // 2048 in 239 against 243 us, 32 of 512 in 114 against 133.
                     if (!clean) {
 #pragma unroll 1
                         for (int g = 0; g < kPagesPerTile; ++g) {
@@ -773,8 +779,11 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
             const float vs = kCodes ? vref : 1.f;
             // The warp's rows leave by way of its 2 KB (T == 2: 1 KB) of shared
             // memory, kPass bytes of each at a time, so that a store instruction
-            // writes whole pieces of a few rows and not 16 bytes of 32.  16-byte
-            // chunk c of row r lies at kCh r + (c ^ r kCh / 8 mod kCh).
+            // writes whole pieces of a few rows and not 16 bytes of 32.  By itself
+            // that gained nothing (an item's end took 3700 cycles with direct
+            // stores, 4000 staged, both unrolled); staged by a rolled loop it
+            // takes 2700.  Direct stores by a rolled loop were not measured.
+            // 16-byte chunk c of row r lies at kCh r + (c ^ r kCh / 8 mod kCh).
             constexpr int kPass = M::kOutBytes / (32 * kSoftWarps), kCh = kPass / 16;
             const uint32_t out = base + M::kOut + warp * (32 * kPass);
             const uint32_t put = out + lane * kPass, get = out + (lane / kCh) * kPass;
@@ -980,9 +989,9 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
         } else if (warp == kSoftWarps + 1 || warp == kSoftWarps + 3) {
             // ------------------------------------------------ loads of Q and the pages
             // One warp for K and Q, one for V.  A lane per page looks its
-            // block up; one thread issues the copies, 2 KB of a page each (a
-            // copy that every lane issued for itself took 100 cycles of the
-            // warp's time).
+            // block up; one thread issues the copies, 2 KB of a page each (16
+            // copies and the loop around them: 1000 to 1100 cycles, and 1600 to
+            // 2000 when every lane issued its own).
             constexpr int R = kCodes ? M::kCodeStages : S;
             constexpr int kBox = kCodes ? kD : 64;                       // values per box
             constexpr int kBoxes = kCodes ? 1 : M::kHalves;
@@ -1026,13 +1035,12 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                     ok = wait(eb, ((n / R) & 1) ^ 1);
                     if (!ok) break;
                     if (j + 1 < nt) blk = lookup(j + 1);
-                    if constexpr (kCodes) {
+                    if constexpr (kCodes)
                         if (lane < kPagesPerTile)
                             (reinterpret_cast<float *>(smem + M::kScales) +
                              (tiles & (M::kScaleTiles - 1)) * 2 * kPagesPerTile +
                              (is_v ? kPagesPerTile : 0))[lane] = scale;
-                        __syncwarp();
-                    }
+                    __syncwarp();  // (the flag and the scales are behind the arrival)
                     if (umma::elect_one())
                         ptx::mbar_arrive_expect_tx(fb, __popc(pages) * kBoxes * kBoxBytes);
                     __syncwarp();
@@ -1495,8 +1503,7 @@ pkv_status prefill_entry(const PrefillCall &c, int kv)
     if (codes && (!c.k_scales || !c.v_scales)) return PKV_ERR_INVALID_ARG;
     if (c.num_blocks <= 0 || c.block_size <= 0 || c.max_blocks_per_seq < 0 || c.window < 0)
         return PKV_ERR_INVALID_ARG;
-    if (!(fabsf(c.softmax_scale) <= 3.0e38f) || !(c.logit_cap >= 0.f) || c.logit_cap > 3.0e38f)
-        return PKV_ERR_INVALID_ARG;
+    if (!(fabsf(c.softmax_scale) <= 2.0e38f) || !valid_cap(c.logit_cap)) return PKV_ERR_INVALID_ARG;
     Plan plan;
     const pkv_status st = plan_of(c.num_tokens, c.num_seqs, c.num_heads, c.num_kv_heads, c.head_dim,
                                   c.max_context_len, &plan);

@@ -8,6 +8,13 @@
 
 namespace pkv {
 
+// A cap that the host lets through: none, or one whose value and reciprocal in
+// log2 units are normal fp32 numbers.
+inline bool valid_cap(float cap)
+{
+    return cap == 0.f || (cap >= 1e-30f && cap <= 1e30f);
+}
+
 // The 16-bit mask of a page's tokens (its first is t0) below ctx that lie
 // in the window (from lo on) or in the prefix (below pre).
 __device__ __forceinline__ uint32_t below(int n)

@@ -21,6 +21,7 @@ OPTIONS = {
     "bias": dict(bias=True),
     "window": dict(window=40),
     "window1": dict(window=1),
+    "window_all": dict(window=2 ** 31 - 1, prefix=3),
     "prefix": dict(prefix=50),
     "window_prefix": dict(window=40, prefix=21),
     "all": dict(cap=20.0, bias=True, window=100, prefix=5),

@@ -41,6 +41,7 @@ def test_scored_decode(kind):
     for name in ("out", "query", "k", "v", "tables", "lens"):
         assert c(**{name: None}) == INVALID
     assert c(cap=-1.0) == c(cap=float("nan")) == c(cap=float("inf")) == INVALID
+    assert c(cap=1e-31) == c(cap=1e31) == c(scale=2.5e38) == INVALID
     assert c(window=-1) == c(n=-1) == c(hq=7) == c(num_blocks=0) == INVALID
     assert c(scale=float("nan")) == c(scale=float("inf")) == INVALID
     assert c(d=96) == c(bs=32) == c(n=9000) == UNSUPPORTED
@@ -97,6 +98,7 @@ def test_prefill(kind):
     for name in ("out", "query", "k", "v", "tables", "starts", "lens"):
         assert c(**{name: None}) == INVALID
     assert c(cap=-1.0) == c(cap=float("nan")) == c(cap=float("inf")) == INVALID
+    assert c(cap=1e-31) == c(cap=1e31) == c(scale=2.5e38) == INVALID
     assert c(window=-1) == c(t=-1) == c(n=-1) == c(hq=7) == c(mb=-1) == c(max_ctx=-1) == INVALID
     assert c(scale=float("nan")) == c(scale=float("-inf")) == INVALID
     assert c(d=96) == c(bs=32) == c(num_blocks=1 << 27) == c(t=1 << 30) == UNSUPPORTED
