@@ -533,20 +533,22 @@ def _scored(fn_name, out, query, kp, vp, ks, vs, block_tables, context_lens, max
     n, hq, d = query.shape
     nb, hkv, bs, _ = kp.shape
     _shape("out", out, n, hq, d)
+    _shape("pool", kp, nb, hkv, bs, d)
     _shape("context_lens", context_lens, n)
     _shape("slopes", slopes, hq)
     _shape("prefix_lens", prefix_lens, n)
+    if block_tables.dim() != 2 or block_tables.shape[0] != n:
+        raise ValueError("block_tables must be [num_seqs][max_blocks_per_seq]")
     _same_device(("out", out), ("query", query), ("k", kp), ("v", vp), ("k_scales", ks),
                  ("v_scales", vs), ("block_tables", block_tables), ("context_lens", context_lens),
                  ("workspace", workspace), ("slopes", slopes), ("prefix_lens", prefix_lens),
                  ("dev_status", dev_status))
-    mb = block_tables.shape[1] if block_tables.dim() == 2 else 0
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     args = [_ptr(out), _ptr(query), _ptr(kp), _ptr(vp)]
     if ks is not None:
         args += [_ptr(ks), _ptr(vs)]
-    args += [nb, _ptr(block_tables), mb, _ptr(context_lens), int(max_context_len), n, hq, hkv,
-             d, bs, float(softmax_scale), float(logit_cap), int(window), _ptr(slopes),
+    args += [nb, _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
+             int(max_context_len), n, hq, hkv, d, bs, float(softmax_scale), float(logit_cap), int(window), _ptr(slopes),
              _ptr(prefix_lens), _ptr(workspace), ws_bytes, _ptr(dev_status), _stream(stream)]
     return fn_name, args
 

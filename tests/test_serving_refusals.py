@@ -169,3 +169,28 @@ def test_rope_table_is_rounded_once():
     assert np.max(np.abs(own - tab)) <= 2.0 ** -23
     with pytest.raises(ValueError):
         pkv.rope_table(70, 32, inv_freq=f[:3], device="cpu")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_scored_decode_shapes_are_checked(kind, monkeypatch):
+    # the device checks aside, so that CPU tensors do; nothing is launched
+    monkeypatch.setattr(pkv, "_check", lambda *a, **k: None)
+    monkeypatch.setattr(pkv, "_same_device", lambda *a: None)
+    monkeypatch.setattr(pkv, "_stream", lambda s: None)
+    codes = {"fp16": torch.float16, "int8": torch.int8, "fp8": torch.uint8}[kind]
+
+    def prepare(dim=64, rows=2, table_dims=2):
+        a = tensors()
+        pool = torch.zeros(4, 2, 16, dim, dtype=codes)
+        scales = () if kind == "fp16" else (torch.ones(4, 2), torch.ones(4, 2))
+        bt = torch.zeros(rows, 2, dtype=torch.int32)
+        return getattr(pkv, "prepare_paged_decode_scored_" + kind)(
+            a["out"], a["q"], pool, pool, *scales, bt if table_dims == 2 else bt[0], a["cl"], 32,
+            0.125, a["ws"])
+    prepare()
+    for dim in (32, 128):
+        with pytest.raises(ValueError, match="pool"):
+            prepare(dim=dim)
+    for kw in (dict(rows=1), dict(rows=3), dict(table_dims=1)):
+        with pytest.raises(ValueError, match="block_tables"):
+            prepare(**kw)
