@@ -13,8 +13,8 @@
 // shares every key and value that is read -- as two tiles of 128 rows, the M of
 // one tcgen05.mma.  Per 128 keys (eight pages) a tile does
 //   S = Q K^T   (128 x 128 fp32 in TMEM; Q, K in shared memory)
-//   P = 2^(S' - m)  (registers: one thread per row, so maxima and sums need no
-//                    exchange between threads; back to TMEM as fp16)
+//   P = 2^(S' - m)  (registers: one thread per row, two where scores are worked
+//                    out first; back to TMEM as fp16)
 //   O += P V    (128 x d fp32 in TMEM; P from TMEM, V in shared memory as it
 //                lies in the page, rows of keys)
 // and the two tiles take turns: while one is in its softmax, the tensor core
@@ -25,11 +25,12 @@
 // out over the keys and stays below the rounding of the fp16 output.  Sums,
 // maxima and accumulators are fp32.
 //
-// Roles of the warps: 0-7 the rows of the two tiles, 8 issues the products, 9
-// and 11 the TMA loads of Q, K and V (a ring of tiles of 128 keys, K and V in
-// turn), 10 finds the next item.  INT8 / FP8 pages land in a second ring, and
-// warps 12-15 widen them exactly to fp16; the K scales multiply the scores, the
-// V scales enter the probabilities as a ratio to the largest one so far.
+// Roles of the warps: 0-7 the rows of the two tiles (0-15 with two threads per
+// row, and the others 8 further on), 8 issues the products, 9 and 11 the TMA
+// loads of Q, K and V (a ring of tiles of 128 keys, K and V in turn), 10 finds
+// the next item.  INT8 / FP8 pages land in a second ring, and warps 12-15 widen
+// them exactly to fp16; the K scales multiply the scores, the V scales enter
+// the probabilities as a ratio to the largest one so far.
 //
 // Measured on GB300, 32 / 8 heads, head_dim 128: 2048 tokens over 8192 in 170 us
 // (1410 TFLOP/s, 0.75 of the measured bf16 rate), capped 269, INT8 205; 8
