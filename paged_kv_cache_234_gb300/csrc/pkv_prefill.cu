@@ -119,8 +119,15 @@ struct Smem {
     static constexpr int kOutBytes = 16 * 1024;
     static constexpr int kCtl = kOut + kOutBytes;
     static constexpr int kBars = 3 * kStages + 2 * kCodeStages + 16;
-    // scales [kScaleTiles][K, V][8 pages]: the loads run at most five tiles
-    // ahead of the softmax (the code ring, the ring and the tile at work)
+    // scales [kScaleTiles][K, V][8 pages].  The K warp writes both of a tile
+    // before it arrives for the tile's K codes; their widening waits for that,
+    // the product Q K^T for the widening and the softmax for the product, so
+    // every read of a tile's scales is behind their writes.  (V's own barriers
+    // are not on that way: the products wait for V only after the softmax.)
+    // A slot is written again eight tiles later, when the K codes of three
+    // elements before (V of tile n - 2) are widened: they went to a stage that
+    // the products have given back, so the softmax is through with tile n - 5
+    // at least (head_dim 128: n - 4; two tiles on the same rows: n - 5).
     static constexpr int kScaleTiles = 8;
     static constexpr int kNext = (kCtl + 8 * kBars + 15) & ~15;   // answer of the launch queue
     static constexpr int kScales = kNext + 16;
@@ -1024,11 +1031,14 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                         flags[1 + (k & 1)] = 1;
                         if (p.dev_status) atomicOr(p.dev_status, PKV_DEV_BAD_BLOCK);
                     }
-                    [[maybe_unused]] float scale = 0.f;
+                    // both scales by the K warp: see Smem::kScales
+                    [[maybe_unused]] float k_scale = 0.f, v_scale = 0.f;
                     if constexpr (kCodes)
-                        if (have)
-                            scale = __ldg((is_v ? p.v_scales : p.k_scales) +
-                                          static_cast<int64_t>(blk) * p.num_kv_heads + it.kvh);
+                        if (have && !is_v) {
+                            const int64_t at = static_cast<int64_t>(blk) * p.num_kv_heads + it.kvh;
+                            k_scale = __ldg(p.k_scales + at);
+                            v_scale = __ldg(p.v_scales + at);
+                        }
                     const int row = (blk * p.num_kv_heads + it.kvh) * kPage;
                     const unsigned pages = __ballot_sync(0xffffffffu, have);
                     const uint32_t fb = kCodes ? cfull(s) : full(s);
@@ -1037,11 +1047,13 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                     if (!ok) break;
                     if (j + 1 < nt) blk = lookup(j + 1);
                     if constexpr (kCodes)
-                        if (lane < kPagesPerTile)
-                            (reinterpret_cast<float *>(smem + M::kScales) +
-                             (tiles & (M::kScaleTiles - 1)) * 2 * kPagesPerTile +
-                             (is_v ? kPagesPerTile : 0))[lane] = scale;
-                    __syncwarp();  // (the flag and the scales are behind the arrival)
+                        if (!is_v && lane < kPagesPerTile) {
+                            float *to = reinterpret_cast<float *>(smem + M::kScales) +
+                                        (tiles & (M::kScaleTiles - 1)) * 2 * kPagesPerTile + lane;
+                            to[0] = k_scale;
+                            to[kPagesPerTile] = v_scale;
+                        }
+                    __syncwarp();  // (the arrival is behind the flag and the scales)
                     if (umma::elect_one())
                         ptx::mbar_arrive_expect_tx(fb, __popc(pages) * kBoxes * kBoxBytes);
                     __syncwarp();
