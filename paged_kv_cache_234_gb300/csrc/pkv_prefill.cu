@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
     auto i_full = [&](int k) { return one + 80 + 8 * (k & 1); };
     auto i_empty = [&](int k) { return one + 96 + 8 * (k & 1); };
     [[maybe_unused]] auto swapped = [&](int i) { return one + 112 + 8 * i; };
-    // one per stage: V is fixed tiles ahead of the products
+    // one per stage: rows are zeroed tiles ahead of the products
     [[maybe_unused]] auto fixed = [&](int s) { return one + 128 + 8 * s; };
     volatile int *flags = reinterpret_cast<volatile int *>(smem + M::kFlags);
     // flags: abort, bad of item slot 0, of slot 1, TMEM address
@@ -540,6 +540,13 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
             const int rj = pair ? rj_first : rj_own;        // token of the row
             const int rh = row0 + rt - rj * p.chunk;        // head of the row
             const int j0 = pair ? i : 0, step = pair ? 2 : 1;  // its tiles of keys
+            // Whether the row is one of the item's.  The others hold queries of
+            // other tokens or heads, or what was in shared memory before.  So that
+            // the item's results depend on its own rows alone, they have no say
+            // where a warp decides something for its rows together: their maximum
+            // begins at +inf, which nothing exceeds, and their capped scores are
+            // 0 (or NaN, which a maximum leaves out).
+            const bool mine = rj < it.toks && rh < it.heads;
             const int pos = it.pos + min(rj, it.toks - 1);
             const int lo = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
             const int pre = it.pre;
@@ -555,7 +562,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
             float slope = 0.f;
             if (kMod && p.slopes && rh < it.heads)
                 slope = __ldg(p.slopes + it.head + rh) * 1.4426950408889634f;
-            float m = -INFINITY, l = 0.f;
+            float m = mine ? -INFINITY : INFINITY, l = 0.f;
             [[maybe_unused]] float vref = 0.f, vinv = 0.f;
             for (int j = j0; j < nt; j += step) {
                 const int tile = it.tile(j);
@@ -627,7 +634,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                 umma::wait_ld();
                 float sl = 1.f;  // kMod: what x is to be multiplied with
                 if constexpr (kMod) {
-                    const float by = p.cap > 0.f ? p.cap_inv : 1.f;
+                    const float by = p.cap > 0.f ? (m < INFINITY ? p.cap_inv : 0.f) : 1.f;
 #pragma unroll
                     for (int g = 0; g < kColPages; ++g) {
                         const float f = factor(g) * by;
@@ -767,7 +774,6 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                 l = half == 0 ? l + other : other + l;
             }
             const bool bad = flags[1 + (k & 1)] != 0;
-            const bool mine = rj < it.toks && rh < it.heads;
             int64_t row = static_cast<int64_t>(it.tok + rj) * p.num_heads + it.head + rh;
             if (p.splits > 1) {
                 // part 2 z, or 2 z + 1 for the second tile of a pair; the latter
@@ -896,14 +902,20 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                     }
                 };
                 [[maybe_unused]] uint32_t fixes = 0;  // parity of each stage's fixes
-                // V of the j-th tile of keys has landed in stage sv
-                auto v_ready = [&](const Item &it, int j, int sv, uint32_t ph) -> bool {
+                // K or V of the j-th tile of keys has landed in stage sv
+                auto ready = [&](bool fix, const Item &it, int j, int sv, uint32_t ph) -> bool {
                     bool ok = wait.one(full(sv), ph);
-                    if (!kCodes && ok && it.dirty(it.tile(j))) {
+                    if (!kCodes && fix && ok && it.dirty(it.tile(j))) {
                         ok = wait.one(fixed(sv), fixes >> sv & 1u);
                         fixes ^= 1u << sv;
                     }
                     return ok;
+                };
+                auto v_ready = [&](const Item &it, int j, int sv, uint32_t ph) -> bool {
+                    return ready(true, it, j, sv, ph);
+                };
+                auto k_ready = [&](const Item &it, int j, int sv, uint32_t ph) -> bool {
+                    return ready(kMod && p.cap > 0.f, it, j, sv, ph);
                 };
                 uint32_t steps[2] = {0, 0};
                 bool ok = true;
@@ -913,7 +925,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                     const Item &it = item(k);
                     const int nt = it.nt;
                     if (nt == 0) break;
-                    ok = wait.one(q_full, k & 1) && wait.one(full(s), phase);
+                    ok = wait.one(q_full, k & 1) && k_ready(it, 0, s, phase);
                     if (!ok) break;
                     umma::fence_after();
                     if (!paired(p, it)) {
@@ -938,7 +950,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                                 if (i == last) umma::commit(empty(sv));
                                 if (j + 1 < nt) {
                                     if (i == 0) {
-                                        ok = wait.one(full(s), phase);
+                                        ok = k_ready(it, j + 1, s, phase);
                                         if (!ok) break;
                                         umma::fence_after();
                                     }
@@ -976,7 +988,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                             }
                             if (j + 2 < nt) {
                                 const int sk = s + 1 == S ? 0 : s + 1;
-                                ok = wait.one(full(sk), s + 1 == S ? phase ^ 1 : phase);
+                                ok = k_ready(it, j + 2, sk, s + 1 == S ? phase ^ 1 : phase);
                                 if (!ok) break;
                                 umma::fence_after();
                                 qk(i, 0, sk);
@@ -1087,11 +1099,15 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                         __syncwarp();
                     }
                     if constexpr (!kCodes)
-                        if (is_v && it.dirty(it.tile(j))) {
+                        if ((is_v || (kMod && p.cap > 0.f)) && it.dirty(it.tile(j))) {
                             // rows of V that no row of the item sees may hold
                             // anything, NaN included (and are not loaded for
-                            // pages past the last): zeros.  The products wait
-                            // for this, so the stage is not filled meanwhile.
+                            // pages past the last): zeros.  So are K's ahead of a
+                            // cap, whose polynomial the largest score chooses (2048
+                            // over 8192, capped: 271 us; with the scores of unseen
+                            // keys set to 0 in TMEM 275, in registers 281).  The
+                            // products wait for this, so the stage is not filled
+                            // meanwhile.
                             ok = wait(fb, (n / R) & 1);
                             if (!ok) break;
                             const int v = it.tile(j) * kPagesPerTile + lane;
@@ -1206,7 +1222,9 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                     const uint32_t src = base + M::kCodeRing + (n % R) * M::kCodeBytes;
                     const uint32_t dst = base + M::kRing + (n % S) * M::kTileBytes;
                     const int v0 = it.tile(j / 2) * kPagesPerTile;
-                    const bool dirty = kKv == kKvF8 && (j & 1) && it.dirty(it.tile(j / 2));
+                    // (INT8 codes are finite; for K see the load warps)
+                    const bool dirty = (j & 1 ? kKv == kKvF8 : kMod && p.cap > 0.f) &&
+                                       it.dirty(it.tile(j / 2));
                     // all loads first: the thread's row advances by kStep
                     const int ch = tid % kCh, row0 = tid / kCh;
                     constexpr int kAt = kMod && kCh > 4 ? 4 : kCh;   // registers
@@ -1223,20 +1241,28 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
 #pragma unroll
                         for (int e = 0; e < kAt; ++e) {
                             const int row = row0 + (e0 + e) * kStep;
-                            uint4 a = widen<kKv>(w[e].x, w[e].y), b = widen<kKv>(w[e].z, w[e].w);
-                            if (dirty) {
-                                // rows of V that no row of the item sees
-                                const int v = v0 + (row >> 4);
-                                const uint32_t lv =
-                                    v < it.visited ? it.live(it.real(v) * kPage) : 0u;
-                                if (!(lv >> (row & 15) & 1u)) a = b = make_uint4(0, 0, 0, 0);
-                            }
+                            const uint4 a = widen<kKv>(w[e].x, w[e].y);
+                            const uint4 b = widen<kKv>(w[e].z, w[e].w);
                             const uint32_t to = dst + (ch >> 2) * M::kHalfBytes + row * 128;
                             const int cc = (2 * ch) & 7;
                             st_shared16(to + ((cc ^ (row & 7)) << 4), a);
                             st_shared16(to + (((cc + 1) ^ (row & 7)) << 4), b);
                         }
                     }
+                    // the thread's rows that no row of the item sees (in a loop of
+                    // their own: next to the widening FP8 took 227 against 207 us)
+                    if (dirty)
+#pragma unroll 1
+                        for (int row = row0; row < kTile; row += kStep) {
+                            const int v = v0 + (row >> 4);
+                            const uint32_t lv = v < it.visited ? it.live(it.real(v) * kPage) : 0u;
+                            if (lv >> (row & 15) & 1u) continue;
+                            const uint32_t to = dst + (ch >> 2) * M::kHalfBytes + row * 128;
+                            const int cc = (2 * ch) & 7;
+                            const uint4 zero = make_uint4(0, 0, 0, 0);
+                            st_shared16(to + ((cc ^ (row & 7)) << 4), zero);
+                            st_shared16(to + (((cc + 1) ^ (row & 7)) << 4), zero);
+                        }
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
