@@ -124,6 +124,8 @@ def debug_lib() -> ctypes.CDLL:
                 getattr(L, name).argtypes = [ctypes.c_int]
             L.pkv_debug_set_stage_wait_ns.restype = ctypes.c_int
             L.pkv_debug_set_stage_wait_ns.argtypes = [ctypes.c_longlong]
+            L.pkv_debug_set_prefill.restype = ctypes.c_int
+            L.pkv_debug_set_prefill.argtypes = [ctypes.c_int] * 4
             _debug_lib = L
         return _debug_lib
 

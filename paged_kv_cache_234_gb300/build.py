@@ -75,14 +75,16 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     return LIB_PATH
 
 
-DEBUG_SOURCES = ("pkv_decode.cu", "pkv_decode_scored.cu", "pkv_evict.cu")  # the kernels with PKV_DEBUG checks
+# the kernels with PKV_DEBUG checks and settings
+DEBUG_SOURCES = ("pkv_decode.cu", "pkv_decode_scored.cu", "pkv_prefill.cu", "pkv_evict.cu")
 
 
 def build_debug() -> str:
     """libpkv_debug.so: the library with the decode and eviction kernels built
     with PKV_DEBUG (shared-memory address and index checks, read back by
-    pkv_debug_flags / pkv_debug_evict_flags).  For tests; the release library
-    is untouched."""
+    pkv_debug_flags / pkv_debug_evict_flags) and the prefill's with settings of
+    its waits (pkv_debug_set_prefill).  For tests; the release library is
+    untouched."""
     build()
     if os.path.exists(DEBUG_LIB_PATH) and all(
             os.path.getmtime(f) <= os.path.getmtime(DEBUG_LIB_PATH) for f in _inputs()):

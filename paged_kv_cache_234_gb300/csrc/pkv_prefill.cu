@@ -134,23 +134,51 @@ struct Smem {
     static constexpr int kItems = kScales + (kCodes ? kScaleTiles * 2 * kPagesPerTile * 4 : 0);
     static constexpr int kFlags = kItems + 2 * 64;
     static constexpr int kSwap = kFlags + 16;   // [2 tiles][2 halves of the columns][128 rows]
-    static constexpr int kBytes = kSwap + 2 * 2 * kTile * 4;
+    static constexpr int kIssued = kSwap + 2 * 2 * kTile * 4;   // see drain_copies
+    static constexpr int kBytes = kIssued + 16;
     // a second CTA on the SM would wait for TMEM: ask for more than half
     static constexpr int kAsk = kBytes > 120 * 1024 ? kBytes : 120 * 1024;
     static_assert(kAsk <= 227 * 1024, "shared memory of one CTA");
 };
 
+// What a warp does; its waits are counted by role in the debug build.
+enum Role { kRoleRows, kRoleProducts, kRoleLoadK, kRoleLoadV, kRoleItems, kRoleWiden, kRoles };
+
+#ifdef PKV_DEBUG
+// Settable through pkv_debug_set_prefill: wait number give_at of every warp of
+// give_role gives up, as if its limit had run out, and every wait of slow_role
+// begins slow_ns later (role -2: none; warps without a role have -1).
+struct PrefillDebug {
+    int give_role, give_at, slow_role, slow_ns;
+};
+__device__ PrefillDebug g_prefill_debug = {-2, 0, -2, 0};
+#endif
+
 struct Waiter {
     volatile int *abort;
     int32_t *dev_status;
+#ifdef PKV_DEBUG
+    int role = -1;
+    mutable int waits = 0;
+#endif
+    __device__ __forceinline__ Waiter as([[maybe_unused]] Role r) const
+    {
+        Waiter w = *this;
+#ifdef PKV_DEBUG
+        w.role = r;
+#endif
+        return w;
+    }
     // Bounded waits; false once any wait of the CTA ran out.  By one thread:
     __device__ __forceinline__ bool one(uint32_t bar, uint32_t parity) const
     {
+        if (gives_up()) return false;
         return ptx::mbar_try_wait(bar, parity) || slow(bar, parity);
     }
     // by a whole warp, all lanes with the same outcome:
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const
     {
+        if (gives_up()) return false;
         if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
         return __all_sync(0xffffffffu, slow(bar, parity));
     }
@@ -163,11 +191,25 @@ struct Waiter {
             if (*abort) return false;
             const uint64_t now = ptx::globaltimer_ns();
             if (t0 == 0) t0 = now;
-            if (now - t0 > kWaitLimitNs) {
-                *abort = 1;
-                if (dev_status) atomicOr(dev_status, PKV_DEV_TIMEOUT);
-            }
+            if (now - t0 > kWaitLimitNs) give_up();
         }
+    }
+    __device__ __forceinline__ void give_up() const
+    {
+        *abort = 1;
+        if (dev_status) atomicOr(dev_status, PKV_DEV_TIMEOUT);
+    }
+    __device__ __forceinline__ bool gives_up() const
+    {
+#ifdef PKV_DEBUG
+        const PrefillDebug d = g_prefill_debug;
+        if (role == d.slow_role) __nanosleep(d.slow_ns);
+        if (role == d.give_role && waits++ == d.give_at) {
+            give_up();
+            return true;
+        }
+#endif
+        return false;
     }
 };
 
@@ -272,6 +314,23 @@ __device__ __forceinline__ int find_item(const PrefillArgs &p, int block, Item &
     it.nt = static_cast<int>(static_cast<int64_t>(tiles) * (it.z + 1) / p.splits) - it.ta;
     if (it.dir < 0) it.ta += it.nt - 1;
     return it.nt > 0;
+}
+
+// After a wait that ran out, with every warp behind a barrier of the CTA: waits
+// (bounded) for the copies that may still write into its shared memory.  K and
+// V tile t are elements 2 t and 2 t + 1 of a ring of R stages, and a stage is
+// filled again only after its element was used up, so only the last element of
+// each stage can be in flight; of the queries only the last item's.
+template <int R>
+__device__ void drain_copies(uint32_t full0, uint32_t q_full, int k_tiles, int v_tiles, int items)
+{
+    for (int s = 0; s < R; ++s)
+        for (int n = 2 * max(k_tiles, v_tiles) - 1; n >= 0; --n)
+            if (n % R == s && n / 2 < (n & 1 ? v_tiles : k_tiles)) {
+                ptx::mbar_wait_bounded(full0 + 8 * s, n / R & 1, kWaitLimitNs);
+                break;
+            }
+    if (items > 0) ptx::mbar_wait_bounded(q_full, (items - 1) & 1, kWaitLimitNs);
 }
 
 // ------------------------------------------------------------------ kernel
@@ -449,7 +508,9 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
     [[maybe_unused]] auto fixed = [&](int s) { return one + 128 + 8 * s; };
     volatile int *flags = reinterpret_cast<volatile int *>(smem + M::kFlags);
     // flags: abort, bad of item slot 0, of slot 1, TMEM address
-    const Waiter wait{flags, p.dev_status};
+    const Waiter waiter{flags, p.dev_status};
+    // what was issued: K tiles, V tiles, items' queries
+    volatile int *issued = reinterpret_cast<volatile int *>(smem + M::kIssued);
     // the k-th item of this CTA
     auto item = [&](int k) -> Item & {
         return *reinterpret_cast<Item *>(smem + M::kItems + 64 * (k & 1));
@@ -479,6 +540,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
         }
         ptx::fence_mbar_init();
         flags[0] = flags[1] = flags[2] = 0;
+        issued[0] = issued[1] = issued[2] = 0;
     }
     if (warp == kSoftWarps) umma::alloc(base + M::kFlags + 12, 512);
     umma::fence_before();
@@ -493,6 +555,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
     if (warp < kSoftWarps) {
         // ------------------------------------------------ rows of the tiles
         soft_registers<kKv, kMod>();
+        const Waiter wait = waiter.as(kRoleRows);
         const int i = warp / (4 * T);                   // tile
         const int half = T == 2 ? warp >> 2 & 1 : 0;    // which of the row's columns
         const int rt = threadIdx.x & (kTile - 1);       // row of the tile
@@ -867,6 +930,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
         issue_registers<kKv, kMod>();
         if (warp == kSoftWarps) {
             // ------------------------------------------------ products
+            const Waiter wait = waiter.as(kRoleProducts);
             if (umma::elect_one()) {
                 constexpr uint32_t kQk = umma::f16_idesc(kTile, kTile, false);
                 constexpr uint32_t kPv = umma::f16_idesc(kTile, kD, true);
@@ -1019,8 +1083,10 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
             constexpr int kStageBytes = kCodes ? M::kCodeBytes : M::kTileBytes;
             const uint32_t ring = base + (kCodes ? M::kCodeRing : M::kRing);
             const bool is_v = warp == kSoftWarps + 3;
+            const Waiter wait = waiter.as(is_v ? kRoleLoadV : kRoleLoadK);
             const void *tm = is_v ? static_cast<const void *>(&tmv) : &tmk;
             uint32_t tiles = 0;   // tiles of keys so far: ring elements 2 tiles (+ 1)
+            int queries = 0;      // items whose queries were asked for
             bool ok = true;
             for (int k = 0; ok; ++k) {
                 ok = wait(i_full(k), k >> 1 & 1);
@@ -1097,6 +1163,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                                                  it.tok, q_full);
                         }
                         __syncwarp();
+                        ++queries;
                     }
                     if constexpr (!kCodes)
                         if ((is_v || (kMod && p.cap > 0.f)) && it.dirty(it.tile(j))) {
@@ -1136,17 +1203,14 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                 if (lane == 0) ptx::mbar_arrive(i_empty(k));
             }
             // The products have waited for every copy, unless a wait ran out:
-            // then leave none of this warp's in flight.
-            if (!ok) {
-                for (uint32_t e = tiles > R ? tiles - R : 0; e < tiles; ++e) {
-                    const uint32_t n = 2 * e + (is_v ? 1 : 0);
-                    ptx::mbar_wait_bounded(kCodes ? cfull(n % R) : full(n % R), (n / R) & 1,
-                                           kWaitLimitNs);
-                }
-                if (!is_v) ptx::mbar_wait_bounded(q_full, 0, kWaitLimitNs);
+            // what was issued, for the drain behind it.
+            if (lane == 0) {
+                issued[is_v] = static_cast<int>(tiles);
+                if (!is_v) issued[2] = queries;
             }
         } else {
             // ------------------------------------------------ the next items
+            const Waiter wait = waiter.as(kRoleItems);
             int block = blockIdx.x;
             bool ok = true;
             int k = 0;
@@ -1204,6 +1268,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
         if constexpr (kCodes) {
             // ------------------------------------------------ codes to fp16
             widen_registers<kMod>();
+            const Waiter wait = waiter.as(kRoleWiden);
             constexpr int R = M::kCodeStages;
             constexpr int kCh = kD / 16;  // 16-byte chunks of codes per row
             constexpr int kStep = 128 / kCh;
@@ -1276,6 +1341,12 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
         }
     }
     __syncthreads();
+    if (flags[0]) {  // a wait ran out (the same for all: nobody waits any more)
+        if (warp == kSoftWarps + 1)
+            drain_copies<kCodes ? M::kCodeStages : S>(kCodes ? cfull(0) : full(0), q_full,
+                                                      issued[0], issued[1], issued[2]);
+        __syncthreads();
+    }
     if (warp == kSoftWarps) umma::dealloc(tmem, 512);
 }
 
@@ -1635,3 +1706,24 @@ extern "C" size_t pkv_prefill_workspace_size(int num_tokens, int num_seqs, int n
         return 0;
     return plan.bytes;
 }
+
+#ifdef PKV_DEBUG
+// Debug builds only: see PrefillDebug (roles 0 rows, 1 products, 2 K and query
+// loads, 3 V loads, 4 items, 5 widening of codes).  A negative role resets its
+// setting.  Synchronises with the device; returns 0, or -1 if the CUDA runtime
+// fails or an argument is out of range.
+extern "C" __attribute__((visibility("default"))) int pkv_debug_set_prefill(int give_role,
+                                                                            int give_at,
+                                                                            int slow_role,
+                                                                            int slow_ns)
+{
+    if (give_role >= pkv::kRoles || slow_role >= pkv::kRoles || slow_ns < 0 || slow_ns > 1000000)
+        return -1;
+    const pkv::PrefillDebug d = {give_role < 0 ? -2 : give_role, give_at,
+                                 slow_role < 0 ? -2 : slow_role, slow_ns};
+    if (cudaDeviceSynchronize() != cudaSuccess ||
+        cudaMemcpyToSymbol(pkv::g_prefill_debug, &d, sizeof(d)) != cudaSuccess)
+        return -1;
+    return 0;
+}
+#endif
