@@ -458,11 +458,13 @@ PKV_API pkv_status pkv_rope_append_fp8(
  *   z'' = z' - slopes[h] * |i - t|          if slopes is given, else z'
  *   t is seen if  (t <= i and i - t < window)  or  t < prefix_lens[s]
  *   out[row][h] = sum over seen t of softmax(z'')_t * V_t
- * with FP32 sums, maxima and accumulators; the probabilities enter the second
- * product rounded to fp16.  A key that no query row of the same work item (256
- * rows: tokens times heads of a kv head) sees has no effect, whatever its slot
- * holds, and the blocks that only hold such keys are not read.  Keys and
- * values that a query of the call sees must be finite.
+ * with FP32 sums, maxima and accumulators; the probabilities (for code caches,
+ * their products with the V scales) enter the second product rounded to fp16:
+ * 11 bits, fewer below 2^-17 of the row's largest probability times the largest
+ * V scale that it sees, off by 2^-28 of that at most.  A key that no query row
+ * of the same work item (256 rows: tokens times heads of a kv head) sees has no
+ * effect, whatever its slot holds, and the blocks that only hold such keys are
+ * not read.  Keys and values that a query of the call sees must be finite.
  *
  *   out, query  fp16 [num_tokens][num_heads][head_dim], 16-byte aligned
  *   query_starts, context_lens, num_tokens  the ragged batch (above);

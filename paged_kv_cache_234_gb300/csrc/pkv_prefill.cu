@@ -30,7 +30,7 @@
 // loads of Q, K and V (a ring of tiles of 128 keys, K and V in turn), 10 finds
 // the next item.  INT8 / FP8 pages land in a second ring, and warps 12-15 widen
 // them exactly to fp16; the K scales multiply the scores, the V scales enter
-// the probabilities as a ratio to the largest one so far.
+// the probabilities as a ratio to a reference per row (kVLazy).
 //
 // Measured on GB300, 32 / 8 heads, head_dim 128: 2048 tokens over 8192 in 170 us
 // (1410 TFLOP/s, 0.75 of the measured bf16 rate), capped 269, INT8 205; 8
@@ -82,6 +82,16 @@ constexpr uint64_t kWaitLimitNs = 1000000000ull;  // bounded waits: 1 s
 constexpr float kLazy = 6.f;    // log2 growth of a maximum that is left in the sums
 constexpr float kLift = 6.f;    // log2 factor of the probabilities
 constexpr float kVLazy = 8.f;   // growth of a V scale that is left in the ratio
+
+// V scales of code caches: the accumulators of a row are in units of a reference
+// scale, and a page's scale over the reference multiplies its probabilities on
+// their way to fp16.  The reference is at most kVLazy times the largest scale of
+// the pages that the row sees, whose scales of earlier tiles count with the
+// factor by which the maximum has grown since, and at least that over kVLazy.
+// Products below 2^-14 (lifted by 2^6; the row's largest probability is 2^6 at
+// least) are subnormal, and rounded by up to 2^-25: with P the row's largest
+// probability and V that largest scale, a key's probability times its page's
+// scale is off by up to 2^-28 P V and keeps fewer than 11 bits below 2^-17 P V.
 
 constexpr int kKvF16 = 0, kKvI8 = 1, kKvF8 = 2;
 
@@ -675,7 +685,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
 #pragma unroll
                 for (int c = 0; c < kCols; c += 32)
                     umma::ld32(t_s(i) + lanes + half * kCols + c, x + c);
-                float ov = 1.f;  // change of the V reference
+                [[maybe_unused]] float most = 0.f;  // largest V scale of the tile's pages
                 // what a product is multiplied with, in log2 units (a page of
                 // zeros has scale 0: a masked score must stay -inf)
                 auto factor = [&](int g) {
@@ -684,15 +694,9 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                     return kMod ? s : fmaxf(s, 1e-30f);
                 };
                 if constexpr (kCodes) {
-                    float most = 0.f;
 #pragma unroll
                     for (int g = 0; g < kPagesPerTile; ++g)
                         most = fmaxf(most, scales[kPagesPerTile + g]);
-                    if (most > kVLazy * vref) {
-                        vinv = __frcp_rn(most);
-                        ov = vref * vinv;
-                        vref = most;
-                    }
                 }
                 umma::wait_ld();
                 float sl = 1.f;  // kMod: what x is to be multiplied with
@@ -771,13 +775,40 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                     if (!ok) break;
                     top = fmaxf(top, other);
                 }
-                if (__any_sync(0xffffffffu, top > m + kLazy || ov != 1.f)) {
+                if (__any_sync(0xffffffffu, top > m + kLazy || (kCodes && most > kVLazy * vref))) {
                     const float mn = fmaxf(m, top);
                     const float f = m == -INFINITY ? 0.f : ptx::ex2(m - mn);
                     l *= f;
                     m = mn;
+                    float fo = f;
+                    if constexpr (kCodes) {
+                        // the V reference: the largest of the tile's pages that the
+                        // row sees, or what that of earlier pages weighs now
+                        if (!clean && most > kVLazy * vref) {
+                            float least = most;
+#pragma unroll
+                            for (int g = 0; g < kPagesPerTile; ++g) {
+                                const float y = scales[kPagesPerTile + g];
+                                least = y > 0.f ? fminf(least, y) : least;
+                            }
+                            // (scales that are nearly alike: no need to ask which)
+                            if (most > kVLazy * least) {
+                                most = 0.f;
+#pragma unroll 1
+                                for (int g = 0; g < kPagesPerTile; ++g) {
+                                    const int t0 = it.real(tile * kPagesPerTile + g) * kPage;
+                                    if ((t0 <= pos && t0 + kPage > lo) || t0 < pre)
+                                        most = fmaxf(most, scales[kPagesPerTile + g]);
+                                }
+                            }
+                        }
+                        if (most <= kVLazy * vref) most = fminf(most, vref);
+                        const float vn = fmaxf(fmaxf(most, vref * f), 1e-30f);
+                        vinv = __frcp_rn(vn);
+                        fo *= vref * vinv;
+                        vref = vn;
+                    }
                     if (j > j0) {
-                        const float fo = f * ov;
 #pragma unroll 1
                         for (int c = half * (kD / T); c < (half + 1) * (kD / T); c += 16) {
                             float o[16];
@@ -801,7 +832,8 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                         const float fy = kMod ? sl : factor(g);
                         const uint64_t f2 = ptx::f32x2(fy, fy);
                         [[maybe_unused]] float vr = 0.f;
-                        if constexpr (kCodes) vr = vs[g] * vinv;
+                        // (pages that the row does not see have probabilities of 0)
+                        if constexpr (kCodes) vr = fminf(vs[g] * vinv, 2.f * kVLazy);
 #pragma unroll
                         for (int c = kPage * g; c < kPage * (g + 1); c += 2) {
                             const float2 z2 = ptx::f32x2_parts(

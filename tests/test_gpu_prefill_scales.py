@@ -9,8 +9,10 @@ from test_gpu_prefill import Run, bound, expand
 pytestmark = pytest.mark.gpu
 
 
-def attend(b, kv64, scale, **o):
-    """R.attend with the rows of a (sequence, head) at once."""
+def attend(b, kv64, scale, top=None, **o):
+    """R.attend with the rows of a (sequence, head) at once.  top [T][Hq] gets the
+    largest |V| of the keys whose probability is above 2^-40 of the row's
+    largest, and of the pages these are in as far as the row sees them."""
     k64, v64 = kv64
     out, mass = np.zeros(b.q.shape), np.zeros(b.q.shape)
     for s in range(b.ctx.size):
@@ -29,6 +31,12 @@ def attend(b, kv64, scale, **o):
                 z = z - float(o["slopes"][h]) * np.abs(i - t)
             z = np.where(seen, z, -np.inf)
             p = np.exp(z - z.max(1, keepdims=True))
+            if top is not None:
+                big = np.where(seen, np.abs(vv).max(1)[None], 0.0)
+                for page in range(-(-c // R.BS)):
+                    x = big[:, page * R.BS:(page + 1) * R.BS]
+                    x[:] = x.max(1, keepdims=True)
+                top[r:r + n, h] = np.where(p > 2.0 ** -40, big, 0.0).max(1)
             p /= p.sum(1, keepdims=True)
             out[r:r + n, h], mass[r:r + n, h] = p @ vv, p @ np.abs(vv)
     return out, mass
@@ -58,5 +66,39 @@ def test_value_scales_by_powers_of_two_over_thousands_of_items(kind, dim, option
     # are rounded by up to 2^-25: 2^-31 of the largest value for each key.
     small = int(b.ctx.max()) * 2.0 ** -31 * np.abs(kv64[1][b.used]).max()
     assert status == 0
+    worst = np.max(np.abs(got - ref) / (bound(b, kind, o, ref, mass) + small))
+    assert worst <= 1.0, worst
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+@pytest.mark.parametrize("option", ["plain", "cap"])
+@pytest.mark.parametrize("why", ["ahead", "left", "outweighed"])
+def test_pages_that_do_not_count_for_a_row_cost_it_no_bits(kind, option, why):
+    # One page's values are 2^25 times the others'.  Rows that do not see it (it
+    # lies ahead, or their window has left it), and rows whose later scores
+    # outweigh it, are as exact as if it were not there.
+    o = dict(cap=200.0) if option == "cap" else {}
+    if why == "ahead":
+        b, page = R.make(31, [40], [120], 4, 1, 64, q_std=0.05, nan_tail=False), 7
+    elif why == "left":
+        b, page = R.make(32, [100], [120], 4, 1, 64, q_std=0.05, nan_tail=False), 0
+        o["window"] = 40
+    else:
+        b, page = R.make(33, [30], [160], 4, 1, 64, q_std=0.05, nan_tail=False), 0
+        b.q[:, :, 0] = 8.0                                    # 40 for the keys from 128 on
+        for g in range(10):
+            b.k[b.tables[0, g], :, :, 0] = 0.0 if g < 8 else 40.0
+    for g in range(-(-int(b.ctx[0]) // 16)):
+        b.v[b.tables[0, g]] *= np.float16(2.0 ** (13 if g == page else -12))
+    o = expand(b, o)
+    pools, kv64 = R.cache(b, kind)
+    got, status = Run(b, kind, pools, **o)()
+    top = np.zeros(b.q.shape[:2])
+    ref, mass = attend(b, kv64, 0.125, top, **o)
+    # (small products, as above; the reference may be 8 times the largest scale
+    # that counts for the row: 2^-28 of its largest value for each key)
+    small = int(b.ctx[0]) * 2.0 ** -28 * top[:, :, None]
+    assert status == 0
+    assert (top < 1.0).sum() >= 100  # rows that the page does not count for
     worst = np.max(np.abs(got - ref) / (bound(b, kind, o, ref, mass) + small))
     assert worst <= 1.0, worst
