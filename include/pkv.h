@@ -373,9 +373,9 @@ PKV_API pkv_status pkv_paged_decode_scored_fp8(
  * tokens, positions ctx - n .. ctx - 1.  n == 0 means no token.  Rows from
  * query_starts[num_seqs] on belong to nobody: nothing is done for them, and
  * their outputs are left as they were.  A sequence whose rows do not lie in
- * [0, num_tokens], or with n > ctx or ctx beyond the block table (for the
- * prefill: beyond max_context_len), sets PKV_DEV_BAD_CTX; its outputs become
- * zeros and nothing is written for it.
+ * [0, num_tokens] or run backwards, or with n > ctx or ctx beyond the block
+ * table (for the prefill: beyond max_context_len), sets PKV_DEV_BAD_CTX; its
+ * outputs become zeros and nothing is written for it.
  */
 
 /*

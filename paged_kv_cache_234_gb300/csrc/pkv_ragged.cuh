@@ -12,6 +12,8 @@
 
 #include <stdint.h>
 
+#include "../../include/pkv.h"
+
 namespace pkv {
 
 // Largest s in [0, n) with key(s) <= x for a nondecreasing key; -1 if there
@@ -61,5 +63,22 @@ struct SeqRows {
         len = l < 0 ? 0 : l > num_tokens ? num_tokens : static_cast<int>(l);
     }
 };
+
+// Sets PKV_DEV_BAD_CTX if a sequence with rows does not fit, wherever its rows
+// would begin.  By `threads` threads, of which this is number t.
+__device__ __forceinline__ void report_bad_sequences(const int32_t *__restrict__ starts,
+                                                     const int32_t *__restrict__ lens, int num_seqs,
+                                                     int num_tokens, int ctx_cap,
+                                                     int32_t *dev_status, int t, int threads)
+{
+    bool bad = false;
+    for (int s = t; s < num_seqs; s += threads) {
+        SeqRows sr;
+        const int first = __ldg(starts + s), end = __ldg(starts + s + 1);
+        sr.set(first, end, __ldg(lens + s), num_tokens, ctx_cap);
+        bad |= first != end && !sr.ok;
+    }
+    if (bad) atomicOr(dev_status, static_cast<int32_t>(PKV_DEV_BAD_CTX));
+}
 
 }  // namespace pkv

@@ -200,8 +200,7 @@ __device__ __forceinline__ void rope_token(const RopeArgs &p, int tok)
     sr.load(p.query_starts, p.context_lens, seq, p.num_tokens, p.max_blocks_per_seq * 16);
     if (tok - sr.start >= sr.len) return;  // behind the last sequence: left as it was
     const int pos = sr.ctx - sr.len + (tok - sr.start);
-    bool live = sr.ok;
-    report(p, !live && tid == 0 && tok == max(sr.start, 0), PKV_DEV_BAD_CTX);
+    bool live = sr.ok;  // (see check_sequences)
     if (live && !positions_ok(p, tok, pos)) {
         live = false;
         report(p, tid == 0, PKV_DEV_BAD_POS);
@@ -257,11 +256,22 @@ __device__ __forceinline__ void rope_tokens(const RopeArgs &p, int group)
     }
 }
 
+// The last CTA of a call with a status word looks at every sequence: one that
+// does not fit need not have a token that a CTA works on.
+__device__ __forceinline__ bool check_sequences(const RopeArgs &p)
+{
+    if (!p.dev_status || blockIdx.x != gridDim.x - 1) return false;
+    report_bad_sequences(p.query_starts, p.context_lens, p.num_seqs, p.num_tokens,
+                         p.max_blocks_per_seq * 16, p.dev_status, threadIdx.x, kRowThreads);
+    return true;
+}
+
 template <int kD>
 __global__ void __launch_bounds__(kRowThreads) rope_fp16_kernel(const __grid_constant__ RopeArgs p)
 {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
+    if (check_sequences(p)) return;
     rope_tokens<kD, true>(p, blockIdx.x);
 }
 
@@ -279,6 +289,7 @@ __global__ void __launch_bounds__(kRowThreads) rope_codes_kernel(const __grid_co
     __shared__ float warp_max[kRowThreads / 32];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
+    if (check_sequences(p)) return;
     const int kv = p.num_kv_heads;
     const int per_unit = kv * 2 / kTiles;                // CTAs of a page
     const int64_t tiles = static_cast<int64_t>(p.units) * per_unit;
@@ -302,7 +313,7 @@ __global__ void __launch_bounds__(kRowThreads) rope_codes_kernel(const __grid_co
     if (seq < 0) return;
     SeqRows sr;
     sr.load(p.query_starts, p.context_lens, seq, p.num_tokens, p.max_blocks_per_seq * 16);
-    if (sr.len == 0 || !sr.ok) return;  // reported by the query CTAs
+    if (sr.len == 0 || !sr.ok) return;
     const int old = sr.ctx - sr.len;
     const int64_t page = (old >> 4) + (unit - base_of(seq));
     if (page > (sr.ctx - 1) >> 4) return;
@@ -381,6 +392,7 @@ struct RopeCall {
 template <typename Kernel>
 pkv_status launch_rope(Kernel kernel, int64_t grid, const RopeCall &c, const RopeArgs &a)
 {
+    if (c.dev_status) ++grid;  // check_sequences
     if (grid > INT32_MAX) return PKV_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
