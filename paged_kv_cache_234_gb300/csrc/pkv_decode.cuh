@@ -973,7 +973,7 @@ __global__ void __launch_bounds__(kThreads, kG == 1 ? Cfg<kKv, kD>::kMinCtas : (
             if constexpr (kScored) {
                 const int ctx = kClust ? cctx : ctxs[PKV_IDX(cc.seq, p.num_seqs)];
                 lo_tok = p.window > 0 ? max(0, ctx - p.window) : 0;
-                pre_tok = p.prefix_lens ? __ldg(p.prefix_lens + cc.seq) : 0;
+                pre_tok = p.prefix_lens ? max(__ldg(p.prefix_lens + cc.seq), 0) : 0;
 #pragma unroll
                 for (int gi = 0; gi < kG; ++gi) {
                     const int hA = kLoCols ? (2 * c) & 3 : kItemHeads * gi + 2 * c;

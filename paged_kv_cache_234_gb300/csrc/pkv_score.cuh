@@ -16,7 +16,8 @@ inline bool valid_cap(float cap)
 }
 
 // The 16-bit mask of a page's tokens (its first is t0) below ctx that lie
-// in the window (from lo on) or in the prefix (below pre).
+// in the window (from lo on) or in the prefix (below pre).  None of the bounds
+// is negative.
 __device__ __forceinline__ uint32_t below(int n)
 {
     return n >= 16 ? 0xffffu : n <= 0 ? 0u : (1u << n) - 1u;
