@@ -336,7 +336,8 @@ PKV_API pkv_status pkv_append_fp8(void *k_cache, void *v_cache, uint8_t *k_codes
  *   slopes      fp32 [num_heads] in device memory, or NULL: no bias
  *   prefix_lens int32 [num_seqs] in device memory, or NULL: no prefix (a
  *               negative length counts as 0, one beyond ctx as ctx)
- * Everything else, the workspace and its size included, is as for
+ * With num_seqs == 0 nothing is launched, and arrays without elements may be
+ * NULL.  Everything else, the workspace and its size included, is as for
  * pkv_paged_decode_fp16 / _int8 / _fp8.
  */
 PKV_API pkv_status pkv_paged_decode_scored_fp16(
@@ -375,7 +376,9 @@ PKV_API pkv_status pkv_paged_decode_scored_fp8(
  * their outputs are left as they were.  A sequence whose rows do not lie in
  * [0, num_tokens] or run backwards, or with n > ctx or ctx beyond the block
  * table (for the prefill: beyond max_context_len), sets PKV_DEV_BAD_CTX; its
- * outputs become zeros and nothing is written for it.
+ * outputs become zeros and nothing is written for it.  Without tokens or
+ * without sequences nothing is launched; arrays that have no elements then may
+ * be NULL.
  */
 
 /*

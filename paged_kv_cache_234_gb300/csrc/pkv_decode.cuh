@@ -2121,8 +2121,10 @@ template <bool kScored>
 pkv_status decode_entry(const DecodeCall &call, int kv)
 {
     const bool int8 = kv != kKvF16;
-    if (!call.out || !call.query || !call.kpool || !call.vpool || !call.block_tables ||
-        !call.context_lens)
+    if (!call.kpool || !call.vpool) return PKV_ERR_INVALID_ARG;
+    // (scored: arrays without elements may be null)
+    if (!(kScored && call.num_seqs == 0) &&
+        (!call.out || !call.query || !call.block_tables || !call.context_lens))
         return PKV_ERR_INVALID_ARG;
     if (int8 && (!call.k_scales || !call.v_scales)) return PKV_ERR_INVALID_ARG;
     if (call.num_blocks <= 0 || call.block_size <= 0) return PKV_ERR_INVALID_ARG;

@@ -1645,8 +1645,10 @@ pkv_status launch_prefill(const PrefillCall &c, const Plan &plan)
 pkv_status prefill_entry(const PrefillCall &c, int kv)
 {
     const bool codes = kv != kKvF16;
-    if (!c.out || !c.query || !c.kpool || !c.vpool || !c.block_tables || !c.query_starts ||
-        !c.context_lens)
+    if (!c.kpool || !c.vpool || !c.query_starts) return PKV_ERR_INVALID_ARG;
+    // (arrays without elements may be null)
+    if (c.num_tokens != 0 && (!c.out || !c.query)) return PKV_ERR_INVALID_ARG;
+    if (c.num_seqs != 0 && (!c.context_lens || (!c.block_tables && c.max_blocks_per_seq != 0)))
         return PKV_ERR_INVALID_ARG;
     if (codes && (!c.k_scales || !c.v_scales)) return PKV_ERR_INVALID_ARG;
     if (c.num_blocks <= 0 || c.block_size <= 0 || c.max_blocks_per_seq < 0 || c.window < 0)

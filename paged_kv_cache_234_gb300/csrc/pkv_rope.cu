@@ -414,9 +414,10 @@ enum { kRopeF16 = 0, kRopeI8 = 1, kRopeF8 = 2 };
 
 pkv_status rope_entry(const RopeCall &c, int kind)
 {
-    if (!c.q_out || !c.k_cache || !c.v_cache || !c.q || !c.k || !c.v || !c.cos_sin ||
-        !c.query_starts || !c.context_lens)
-        return PKV_ERR_INVALID_ARG;
+    if (!c.k_cache || !c.v_cache || !c.cos_sin || !c.query_starts) return PKV_ERR_INVALID_ARG;
+    // (arrays without elements may be null)
+    if (c.num_tokens != 0 && (!c.q_out || !c.q || !c.k || !c.v)) return PKV_ERR_INVALID_ARG;
+    if (c.num_seqs != 0 && !c.context_lens) return PKV_ERR_INVALID_ARG;
     if (kind != kRopeF16 && (!c.k_codes || !c.v_codes || !c.k_scales || !c.v_scales))
         return PKV_ERR_INVALID_ARG;
     if (c.num_blocks <= 0 || c.max_position <= 0 || c.rot_dim <= 0 || c.num_axes <= 0 ||
@@ -425,7 +426,8 @@ pkv_status rope_entry(const RopeCall &c, int kind)
         return PKV_ERR_INVALID_ARG;
     if (!c.block_tables && c.max_blocks_per_seq > 0 && c.num_seqs > 0) return PKV_ERR_INVALID_ARG;
     // several axes: a position for each, and an axis for each pair
-    if (c.num_axes > 1 && (!c.rope_positions || !c.axis_of_pair)) return PKV_ERR_INVALID_ARG;
+    if (c.num_axes > 1 && ((c.num_tokens != 0 && !c.rope_positions) || !c.axis_of_pair))
+        return PKV_ERR_INVALID_ARG;
     if (c.block_size != 16 || (c.head_dim != 64 && c.head_dim != 128) || c.rot_dim % 16 != 0 ||
         c.num_axes > 255)
         return PKV_ERR_UNSUPPORTED;
