@@ -425,7 +425,7 @@ __device__ __forceinline__ float max16(const float *x)
 
 // tanh(u) of two values as u P(u^2): P of degree 6 for |u| <= 1 (tanh_coef),
 // or of degree 3, from the same fit on [0, 0.35], whose relative error there
-// is 4e-8.
+// is 6.1e-8 (2^-23.9) with its coefficients in fp32, 2^-22.6 as evaluated.
 template <int kDegree>
 __device__ __forceinline__ uint64_t tanh2(uint64_t u)
 {
