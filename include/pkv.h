@@ -512,7 +512,11 @@ PKV_API pkv_status pkv_paged_prefill_fp8(
 
 /*
  * Bytes of workspace a prefill call with these sizes needs (any KV variant);
- * 0 for most large batches, and for invalid sizes.  Pure host arithmetic.
+ * 0 for most prompts by themselves, for large batches (where tokens / (256 /
+ * group) + sequences, times num_kv_heads, are 608 or more), and for invalid
+ * sizes.  Few rows over long contexts are split over their keys, which takes
+ * memory, so the size is not monotone: a smaller batch can need more.  One workspace for
+ * several batches takes the largest of their sizes.  Pure host arithmetic.
  */
 PKV_API size_t pkv_prefill_workspace_size(int num_tokens, int num_seqs, int num_heads,
                                           int num_kv_heads, int head_dim, int max_context_len);

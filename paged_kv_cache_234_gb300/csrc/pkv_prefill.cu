@@ -37,8 +37,8 @@
 // prompts of 2048 in 231 us (0.63; 245 among other inputs in turn).
 //
 // Items are numbered by bounds that the host knows (pkv_ragged.cuh), the ones
-// with the most keys first.  When they are fewer than the SMs fill, each is
-// split over its keys and a second kernel joins the parts.  An item whose rows
+// with the most keys first.  Few items over long contexts are split over their
+// keys, and a second kernel joins the parts (plan_of).  An item whose rows
 // fill one tile only (a few drafted tokens) then has the second tile work on
 // the same rows, with every other tile of keys, as a part of its own.
 #include <cuda_fp16.h>
@@ -1518,10 +1518,23 @@ struct Plan {
     size_t bytes = 0;
 };
 
-// Units of the batch and the number of key splits, from the sizes alone.  An
-// SM works on one item at a time; a split costs it about three tiles' time
-// (start, queries, epilogue) and the join about two.  The number of splits is
-// the one with the smallest sum of waves * (tiles of a split + 3).
+// Units of the batch and the number of key splits, from the sizes alone: the one
+// with the least time by this model, fitted to fp16 calls of 8 to 464 items with
+// 1 to 19 splits (times in us).
+//   A tile (128 keys for 256 rows) takes 1.45 at head_dim 128, half of that at
+//   64, and an item 2 more (queries, epilogue).  Where items hold one tile of
+//   rows on average and do not fill the SMs, split ones share theirs: 0.63 of it.
+//   With contexts of max_context_len, whose last tokens the rows are, items have
+//   from `least` to `most` tiles.  w = items / SMs of them come one after the
+//   other on an SM, the longest first: the SMs are through after w mean items,
+//   and where w is not whole some of them a short item later, but no earlier
+//   than the longest item.
+//   Splits write their accumulators in fp32 and a launch joins them: 1.5, and
+//   1.05 + 0.125 splits for every 1000 rows (tokens times heads).
+// Unsplit against two splits: one prompt of 4096 (32 / 8 heads, head_dim 128) 113
+// and 277 us, of 2048 (28 / 4) 40 and 115, 4096 tokens over 16384 650 and 756
+// (capped 1021 and 1089); the other way around, 256 over 4096: 51 and 44 (37 with
+// three), 128 over 8192: 95 and 60 (33 with six).
 pkv_status plan_of(int num_tokens, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
                    int max_context_len, Plan *plan)
 {
@@ -1538,13 +1551,25 @@ pkv_status plan_of(int num_tokens, int num_seqs, int num_heads, int num_kv_heads
     const int64_t tiles = (static_cast<int64_t>(max_context_len) + kTile - 1) / kTile + 1;
     if (plan->units > INT32_MAX || items * kMaxSplits > INT32_MAX)
         return PKV_ERR_UNSUPPORTED;
-    int64_t best = 0;
     plan->splits = 1;
-    for (int z = 1; z <= kMaxSplits && z <= tiles; ++z) {
-        const int64_t cost = (items * z + kSms - 1) / kSms * ((tiles + z - 1) / z + 3) + (z > 1 ? 2 : 0);
-        if (z == 1 || cost < best) {
-            best = cost;
-            plan->splits = z;
+    if (num_seqs > 0 && items < 4 * kSms) {  // (beyond, at most a fourth of the time is idle)
+        const double krows = static_cast<double>(num_tokens) * num_heads / 1000;
+        const double own = static_cast<double>(num_tokens) / num_seqs;
+        const double most = static_cast<double>(max_context_len) / kTile;
+        const double least = most > own / kTile ? most - own / kTile : 0.0;
+        const double tile = 1.45 * head_dim / 128, item = 2.0;
+        double best = 0.0;
+        for (int z = 1; z <= kMaxSplits && z <= tiles; ++z) {
+            const double w = static_cast<double>(items) * z / kSms;
+            const bool shared = z > 1 && w <= 1.0 && own * plan->chunk <= kTile;
+            const double t = (shared ? 0.63 * tile : tile) / z;
+            double us = w * ((most + least) / 2 * t + item) + (ceil(w) - w) * (least * t + item);
+            if (us < most * t + item) us = most * t + item;
+            if (z > 1) us += 1.5 + (1.05 + 0.125 * z) * krows;
+            if (z == 1 || us < best) {
+                best = us;
+                plan->splits = z;
+            }
         }
     }
     plan->bytes = plan->splits == 1 ? 0
