@@ -119,11 +119,12 @@ def debug_lib() -> ctypes.CDLL:
         if _debug_lib is None:
             from . import build as _build
             L = _declare(ctypes.CDLL(_build.build_debug()))
-            for name in ("pkv_debug_flags", "pkv_debug_evict_flags"):
+            for name in ("pkv_debug_flags", "pkv_debug_scored_flags", "pkv_debug_evict_flags"):
                 getattr(L, name).restype = ctypes.c_uint
                 getattr(L, name).argtypes = [ctypes.c_int]
-            L.pkv_debug_set_stage_wait_ns.restype = ctypes.c_int
-            L.pkv_debug_set_stage_wait_ns.argtypes = [ctypes.c_longlong]
+            for name in ("pkv_debug_set_stage_wait_ns", "pkv_debug_set_scored_stage_wait_ns"):
+                getattr(L, name).restype = ctypes.c_int
+                getattr(L, name).argtypes = [ctypes.c_longlong]
             L.pkv_debug_set_prefill.restype = ctypes.c_int
             L.pkv_debug_set_prefill.argtypes = [ctypes.c_int] * 4
             _debug_lib = L

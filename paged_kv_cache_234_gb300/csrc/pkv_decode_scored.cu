@@ -81,4 +81,16 @@ extern "C" __attribute__((visibility("default"))) unsigned int pkv_debug_scored_
     }
     return v;
 }
+
+// pkv_debug_set_stage_wait_ns for the kernels of this file.
+extern "C" __attribute__((visibility("default"))) int pkv_debug_set_scored_stage_wait_ns(
+    long long ns)
+{
+    const unsigned long long v =
+        ns < 0 ? pkv::kWaitLimitNs : static_cast<unsigned long long>(ns);
+    if (cudaDeviceSynchronize() != cudaSuccess ||
+        cudaMemcpyToSymbol(pkv::g_debug_stage_wait_ns, &v, sizeof(v)) != cudaSuccess)
+        return -1;
+    return 0;
+}
 #endif
