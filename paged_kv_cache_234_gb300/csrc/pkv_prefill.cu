@@ -325,8 +325,7 @@ __device__ __forceinline__ int find_item(const PrefillArgs &p, int block, Item &
     return it.nt > 0;
 }
 
-// Sequences that do not fit need not have an item.  (Out of line: inlined into
-// the items' warp it moved the others' code, 8 prompts INT8 326 against 300 us.)
+// Sequences that do not fit need not have an item.
 __device__ __noinline__ void check_sequences(const PrefillArgs &p, int lane)
 {
     report_bad_sequences(p.query_starts, p.context_lens, p.num_seqs, p.num_tokens, p.ctx_cap,
@@ -1253,6 +1252,14 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
             int block = blockIdx.x;
             bool ok = true;
             int k = 0;
+            // Where the sequences are looked at changes nothing but where the other
+            // roles' code lies, and with it the time.  Out of line next to the item /
+            // inlined behind the loop: INT8 with bias and window (12 chunks) 294 /
+            // 283 us, 4 prompts capped at head_dim 64 116 / 108, 8 prompts capped
+            // INT8 476 / 464; the other way around 8 prompts capped fp16 369 / 393,
+            // INT8 299 / 307.
+            constexpr bool kLate = kMod && (kCodes || kD == 64);
+            [[maybe_unused]] bool first = false;
             for (uint32_t asked = 0; ok; ++asked) {
                 if (umma::elect_one()) {
                     ptx::mbar_arrive_expect_tx(next_full, 16);
@@ -1286,7 +1293,10 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                                           row] = make_float2(-INFINITY, 0.f);
                     }
                 }
-                if (block == 0 && p.dev_status) check_sequences(p, lane);
+                if constexpr (kLate)
+                    first |= block == 0;
+                else if (block == 0 && p.dev_status)
+                    check_sequences(p, lane);
                 // (also after a wait that ran out: the answer must have come)
                 if (!wait(next_full, asked & 1)) {
                     ptx::mbar_wait_bounded(next_full, asked & 1, kWaitLimitNs);
@@ -1295,6 +1305,9 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                 if (!ok || !ptx::cancelled_block(base + M::kNext, block)) break;
                 ptx::fence_proxy_async_smem();  // read before the next answer is written
             }
+            if (kLate && first && p.dev_status)
+                report_bad_sequences(p.query_starts, p.context_lens, p.num_seqs, p.num_tokens,
+                                     p.ctx_cap, p.dev_status, lane, 32);
             if (ok) ok = wait(i_empty(k), (k >> 1 & 1) ^ 1);
             if (ok && lane == 0) {
                 item(k).nt = 0;

@@ -28,15 +28,16 @@ def test_append(kind, starts):
     r.check(*R.rope_append(b, qkv, tab, None, None, False, (b.k, b.v)))
 
 
-@pytest.mark.parametrize("kind", ["fp16", "int8"])
+@pytest.mark.parametrize("kind,dim", [("fp16", 64), ("fp16", 128), ("int8", 64)])
+@pytest.mark.parametrize("cap", [0.0, 9.0])
 @pytest.mark.parametrize("starts", STARTS)
-def test_prefill(kind, starts):
-    b = R.make(101, [8, 0, 0], [20, 30, 40], 8, 2, 64)
+def test_prefill(kind, dim, cap, starts):
+    b = R.make(101, [8, 0, 0], [20, 30, 40], 8, 2, dim)
     pools, kv64 = R.cache(b, kind)
-    got, status = P.Run(b, kind, pools, starts=np.asarray(STARTS[starts], np.int32))()
+    got, status = P.Run(b, kind, pools, starts=np.asarray(STARTS[starts], np.int32), cap=cap)()
     assert status == pkv.PKV_DEV_BAD_CTX
-    ref, mass = R.attend(b, kv64, 0.125)
-    o = dict(slopes=None, prefix=None)
+    ref, mass = R.attend(b, kv64, dim ** -0.5, cap=cap)
+    o = dict(slopes=None, prefix=None, cap=cap)
     assert np.all(np.abs(got - ref) <= P.bound(b, kind, o, ref, mass))
 
 
