@@ -32,9 +32,10 @@
 // them exactly to fp16; the K scales multiply the scores, the V scales enter
 // the probabilities as a ratio to a reference per row (kVLazy).
 //
-// Measured on GB300, 32 / 8 heads, head_dim 128: 2048 tokens over 8192 in 170 us
-// (1410 TFLOP/s, 0.75 of the measured bf16 rate), capped 269, INT8 205; 8
-// prompts of 2048 in 231 us (0.63; 245 among other inputs in turn).
+// Measured on GB300, 32 / 8 heads, head_dim 128: 2048 tokens over 8192 in 171 us
+// (1408 TFLOP/s, 0.75 of the measured bf16 rate), capped 274 (scores up to the
+// cap 315, beyond it 452), INT8 203, FP8 204; 8 prompts of 2048 in 234 us (0.62;
+// 245 among other inputs in turn), one of 4096 in 112 (0.65).
 //
 // Items are numbered by bounds that the host knows (pkv_ragged.cuh), the ones
 // with the most keys first.  Few items over long contexts are split over their
