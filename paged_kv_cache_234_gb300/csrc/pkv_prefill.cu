@@ -34,7 +34,7 @@
 //
 // Measured on GB300, 32 / 8 heads, head_dim 128: 2048 tokens over 8192 in 171 us
 // (1408 TFLOP/s, 0.75 of the measured bf16 rate), capped 274 (scores up to the
-// cap 315, beyond it 452), INT8 203, FP8 204; 8 prompts of 2048 in 234 us (0.62;
+// cap 312, beyond it 452), INT8 203, FP8 204; 8 prompts of 2048 in 234 us (0.62;
 // 245 among other inputs in turn), one of 4096 in 112 (0.65).
 //
 // Items are numbered by bounds that the host knows (pkv_ragged.cuh), the ones
