@@ -840,7 +840,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                         const uint64_t f2 = ptx::f32x2(fy, fy);
                         [[maybe_unused]] float vr = 0.f;
                         // (pages that the row does not see have probabilities of 0)
-                        if constexpr (kCodes) vr = fminf(vs[g] * vinv, 2.f * kVLazy);
+                        if constexpr (kCodes) vr = ptx::min_nan(vs[g] * vinv, 2.f * kVLazy);
 #pragma unroll
                         for (int c = kPage * g; c < kPage * (g + 1); c += 2) {
                             const float2 z2 = ptx::f32x2_parts(

@@ -102,3 +102,18 @@ def test_pages_that_do_not_count_for_a_row_cost_it_no_bits(kind, option, why):
     assert (top < 1.0).sum() >= 100  # rows that the page does not count for
     worst = np.max(np.abs(got - ref) / (bound(b, kind, o, ref, mass) + small))
     assert worst <= 1.0, worst
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+@pytest.mark.parametrize("option", ["plain", "all"])
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+def test_scales_that_are_not_finite_show(kind, option, value):
+    # in every row that sees the page, and not in other sequences
+    b = R.make(34, [40, 9], [120, 90], 4, 1, 64, nan_tail=False)
+    o = expand(b, dict(cap=20.0, bias=True) if option == "all" else option)
+    pools, _ = R.cache(b, kind)
+    pools[3][b.tables[0, 3]] = value                       # tokens 48 .. 63
+    got, status = Run(b, kind, pools, **o)()
+    assert status == 0
+    assert not np.any(np.isfinite(got[:40]).all(axis=2))   # rows 80 .. 119
+    assert np.all(np.isfinite(got[40:]))
