@@ -82,6 +82,8 @@ typedef enum pkv_status {
                                 beyond max_blocks_per_seq * block_size */
 #define PKV_DEV_TIMEOUT 4u   /* a bounded wait for an asynchronous copy ran out */
 #define PKV_DEV_BAD_POS 8u   /* a rotary position outside [0, max_position) */
+#define PKV_DEV_BAD_TREE 16u /* a parent that is neither -1 nor an earlier row */
+#define PKV_DEV_BAD_KEEP 32u /* kept rows that are not the sequence's, or do not rise */
 
 /*
  * pkv_quantize_blocks -- symmetric per-(block, kv head) INT8 quantization
@@ -520,6 +522,163 @@ PKV_API pkv_status pkv_paged_prefill_fp8(
  */
 PKV_API size_t pkv_prefill_workspace_size(int num_tokens, int num_seqs, int num_heads,
                                           int num_kv_heads, int head_dim, int max_context_len);
+
+/*
+ * A tree of drafted tokens, as pkv_paged_tree_* and pkv_tree_accept take it: a
+ * ragged batch (above), with parents[row] the row of a token's parent within
+ * its sequence (0 for the sequence's first row), always an earlier one, or -1:
+ * the token follows the cached context itself.  A token's depth is the number
+ * of its ancestors in the tree, its position ctx - n + depth, although its keys
+ * and values lie in slot ctx - n + row of the cache: with rope_positions of
+ * pkv_rope_append_* set to the positions, an accepted path needs no rotation
+ * when its rows are moved together.  A parent that is neither -1 nor an earlier
+ * row sets PKV_DEV_BAD_TREE for its whole sequence.
+ */
+
+/*
+ * pkv_paged_tree_fp16 / _int8 / _fp8 -- attention of trees of drafted tokens
+ * over the paged cache, which already holds them ([GLO] section 2.1, Kernel
+ * Mechanics).  For the token in row r of sequence s, at position i, and a cached
+ * token t at position p(t) -- t itself in the context, t < ctx - n, and ctx - n
+ * + depth for a token of the tree:
+ *   z   = softmax_scale * <query[row][h], K_t>
+ *   z'  = logit_cap * tanh(z / logit_cap)   if logit_cap > 0, else z
+ *   z'' = z' - slopes[h] * (i - p(t))       if slopes is given, else z'
+ *   a token of the context is seen if  i - t < window  or  t < prefix_lens[s];
+ *   of the tree's, the token itself and its ancestors with  i - p(t) < window
+ *   out[row][h] = sum over seen t of softmax(z'')_t * V_t
+ * with FP32 sums, maxima and accumulators; the probabilities (for code caches,
+ * times the V scales) enter the second product rounded to fp16, as in
+ * pkv_paged_prefill_*, relative to the largest such product of the row.  V
+ * scales must not be negative; one that is, or is not finite, makes the rows
+ * NaN that see its page.  Keys that no row of the same work item (up to 128 rows:
+ * tokens times heads of a kv head) sees have no effect, whatever their slots
+ * hold.  Keys and values that a row of the call sees must be finite.
+ *
+ *   out, query  fp16 [num_tokens][num_heads][head_dim], 16-byte aligned
+ *   query_starts, context_lens, num_tokens  the ragged batch;
+ *               max_context_len bounds context_lens and sizes the launch
+ *   parents     int32 [num_tokens] in device memory
+ *   max_tree_len  host bound on the rows of every sequence (sizes the launch;
+ *               a sequence with more sets PKV_DEV_BAD_CTX)
+ *   logit_cap, window, slopes, prefix_lens  as for the scored decode (the
+ *               prefix covers the context at most)
+ *   workspace   device scratch of at least pkv_tree_workspace_size() bytes,
+ *               16-byte aligned; needs no initialisation
+ * A sequence with a bad parent gets zeros.  A block id outside [0, num_blocks)
+ * sets PKV_DEV_BAD_BLOCK; the outputs of every work item that needs the block
+ * become zeros.  Two calls sharing a workspace must not overlap on the GPU.
+ */
+PKV_API pkv_status pkv_paged_tree_fp16(
+    void *out, const void *query, const void *k_cache, const void *v_cache,
+    int num_blocks, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *query_starts, const int32_t *context_lens, const int32_t *parents,
+    int max_context_len, int max_tree_len, int num_tokens, int num_seqs, int num_heads,
+    int num_kv_heads, int head_dim, int block_size, float softmax_scale, float logit_cap,
+    int window, const float *slopes, const int32_t *prefix_lens, void *workspace,
+    size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+PKV_API pkv_status pkv_paged_tree_int8(
+    void *out, const void *query, const int8_t *k_codes, const int8_t *v_codes,
+    const float *k_scales, const float *v_scales,
+    int num_blocks, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *query_starts, const int32_t *context_lens, const int32_t *parents,
+    int max_context_len, int max_tree_len, int num_tokens, int num_seqs, int num_heads,
+    int num_kv_heads, int head_dim, int block_size, float softmax_scale, float logit_cap,
+    int window, const float *slopes, const int32_t *prefix_lens, void *workspace,
+    size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+PKV_API pkv_status pkv_paged_tree_fp8(
+    void *out, const void *query, const uint8_t *k_codes, const uint8_t *v_codes,
+    const float *k_scales, const float *v_scales,
+    int num_blocks, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *query_starts, const int32_t *context_lens, const int32_t *parents,
+    int max_context_len, int max_tree_len, int num_tokens, int num_seqs, int num_heads,
+    int num_kv_heads, int head_dim, int block_size, float softmax_scale, float logit_cap,
+    int window, const float *slopes, const int32_t *prefix_lens, void *workspace,
+    size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
+ * Bytes of workspace a tree call with these sizes needs (any KV variant); 0 for
+ * invalid sizes.  Not monotone: one workspace for several batches takes the
+ * largest of their sizes.  Pure host arithmetic.
+ */
+PKV_API size_t pkv_tree_workspace_size(int num_tokens, int num_seqs, int num_heads,
+                                       int num_kv_heads, int head_dim, int max_context_len,
+                                       int max_tree_len);
+
+/*
+ * pkv_tree_accept -- the path of every tree that the model confirms.  With
+ * targets[row] the token that the model answered with after row (its largest
+ * logit, or a sample): from the sequence's row 0, which is always accepted, the
+ * walk goes on to the first row whose parent is the present one and whose
+ * token is the present one's target, as long as there is such a row.  Rows
+ * with parent -1 other than row 0 are never reached.  Following the tokens
+ * that the model drew leaves their distribution as it is.
+ *
+ *   kept        int32 [num_tokens]: in the sequence's rows, the rows of the
+ *               path (numbers within the sequence, rising), then -1
+ *   kept_lens   int32 [num_seqs]: rows of the path; 0 without rows
+ *   next_tokens int32 [num_seqs]: the last row's target, which the path is
+ *               followed by; -1 without rows
+ *   tokens, targets, parents  int32 [num_tokens] in device memory
+ *   query_starts  int32 [num_seqs + 1] (the ragged batch)
+ * kept and kept_lens are what pkv_compact_* takes.  A sequence whose rows do
+ * not lie in [0, num_tokens] sets PKV_DEV_BAD_CTX, one with a bad parent
+ * PKV_DEV_BAD_TREE; its path is empty (and next_tokens -1).
+ */
+PKV_API pkv_status pkv_tree_accept(int32_t *kept, int32_t *kept_lens, int32_t *next_tokens,
+                                   const int32_t *tokens, const int32_t *targets,
+                                   const int32_t *parents, const int32_t *query_starts,
+                                   int num_tokens, int num_seqs, int32_t *dev_status,
+                                   void *stream);
+
+/*
+ * pkv_compact_fp16 / _int8 / _fp8 -- the rows that stay, moved together in
+ * place: of the last n = query_starts[s + 1] - query_starts[s] tokens of
+ * sequence s (the ragged batch; all of them where n = ctx), the m =
+ * kept_lens[s] listed ones, in kept[query_starts[s] ..], strictly rising numbers
+ * in [0, n).  Position ctx - n + j gets the keys and values of position
+ * ctx - n + kept[j], for every j < m and kv head, and
+ *   new_context_lens[s] = ctx - n + m.
+ * Rows that stay where they are (kept[j] == j) are not written, and slots behind
+ * the new end keep what they held.  _int8 / _fp8 move the rows of the fp16
+ * pools and then quantize every (block, kv head) tile that got a row, all 16
+ * slots, bit for bit as pkv_quantize_blocks[_fp8] does.  The blocks behind the
+ * new end are the caller's to free (pkv_bm_free).
+ *
+ *   k_cache ..  pools as for pkv_append_fp16 / _int8 / _fp8
+ *   kept        int32 [num_tokens] in device memory; entries behind a
+ *               sequence's m are not read
+ *   kept_lens   int32 [num_seqs] in device memory
+ *   new_context_lens  int32 [num_seqs], device, or NULL; not context_lens itself
+ * A sequence that does not fit (the ragged batch; n > ctx, ctx beyond the block
+ * table) sets PKV_DEV_BAD_CTX, one with m outside [0, n] PKV_DEV_BAD_KEEP:
+ * nothing of it is moved and its length stays.  An entry outside [0, n) or not
+ * above the one before sets PKV_DEV_BAD_KEEP and its row is not moved; what
+ * rows the others get is then not specified.  A block id outside
+ * [0, num_blocks) sets PKV_DEV_BAD_BLOCK, and the row is not moved.  No written
+ * block may belong to two sequences (copy it first: pkv_bm_cow).
+ */
+PKV_API pkv_status pkv_compact_fp16(
+    void *k_cache, void *v_cache, int num_blocks, const int32_t *kept, const int32_t *kept_lens,
+    int32_t *new_context_lens, const int32_t *query_starts, const int32_t *context_lens,
+    const int32_t *block_tables, int max_blocks_per_seq, int num_tokens, int num_seqs,
+    int num_kv_heads, int head_dim, int block_size, int32_t *dev_status, void *stream);
+
+PKV_API pkv_status pkv_compact_int8(
+    void *k_cache, void *v_cache, int8_t *k_codes, int8_t *v_codes, float *k_scales,
+    float *v_scales, int num_blocks, const int32_t *kept, const int32_t *kept_lens,
+    int32_t *new_context_lens, const int32_t *query_starts, const int32_t *context_lens,
+    const int32_t *block_tables, int max_blocks_per_seq, int num_tokens, int num_seqs,
+    int num_kv_heads, int head_dim, int block_size, int32_t *dev_status, void *stream);
+
+PKV_API pkv_status pkv_compact_fp8(
+    void *k_cache, void *v_cache, uint8_t *k_codes, uint8_t *v_codes, float *k_scales,
+    float *v_scales, int num_blocks, const int32_t *kept, const int32_t *kept_lens,
+    int32_t *new_context_lens, const int32_t *query_starts, const int32_t *context_lens,
+    const int32_t *block_tables, int max_blocks_per_seq, int num_tokens, int num_seqs,
+    int num_kv_heads, int head_dim, int block_size, int32_t *dev_status, void *stream);
 
 /*
  * pkv_evict_select -- score every physical block for eviction and choose

@@ -19,6 +19,11 @@ The functions carry the C names and take torch tensors:
                               batch of new tokens (``pkv_prefill_workspace_size``)
 * ``pkv_rope_append_fp16`` / ``_int8`` / ``_fp8``  rotate the queries and keys of
                               a ragged batch of new tokens, append keys and values
+* ``pkv_paged_tree_fp16`` / ``_int8`` / ``_fp8``  attention of trees of drafted
+                              tokens (``pkv_tree_workspace_size``)
+* ``pkv_tree_accept``         the path of every tree that the model confirms
+* ``pkv_compact_fp16`` / ``_int8`` / ``_fp8``  move the cached rows that stay
+                              together (an accepted path, a thinned context)
 * ``pkv_append_fp16``         write one new token per sequence into fp16 pools
 * ``pkv_append_int8``         the same, re-quantizing every tile it writes
 * ``pkv_evict_select``        eviction scores of every block + the k to evict
@@ -30,6 +35,7 @@ The functions carry the C names and take torch tensors:
 
 ``prepare_paged_decode_fp16`` / ``_int8`` / ``_fp8``,
 ``prepare_paged_decode_scored_*``, ``prepare_paged_prefill_*``,
+``prepare_paged_tree_*``, ``prepare_tree_accept``, ``prepare_compact_*``,
 ``prepare_rope_append_*`` and
 ``prepare_quantize_blocks`` / ``_fp8`` take the same arguments as the calls
 above and return a ``PreparedCall``: the arguments checked and marshalled
@@ -58,6 +64,8 @@ PKV_DEV_BAD_BLOCK = 1
 PKV_DEV_BAD_CTX = 2
 PKV_DEV_TIMEOUT = 4
 PKV_DEV_BAD_POS = 8
+PKV_DEV_BAD_TREE = 16
+PKV_DEV_BAD_KEEP = 32
 
 EXPORTED = ("pkv_quantize_blocks", "pkv_paged_decode_fp16", "pkv_paged_decode_int8",
             "pkv_quantize_blocks_fp8", "pkv_paged_decode_fp8",
@@ -66,6 +74,9 @@ EXPORTED = ("pkv_quantize_blocks", "pkv_paged_decode_fp16", "pkv_paged_decode_in
             "pkv_paged_decode_scored_fp8", "pkv_rope_append_fp16", "pkv_rope_append_int8",
             "pkv_rope_append_fp8", "pkv_paged_prefill_fp16", "pkv_paged_prefill_int8",
             "pkv_paged_prefill_fp8", "pkv_prefill_workspace_size",
+            "pkv_paged_tree_fp16", "pkv_paged_tree_int8", "pkv_paged_tree_fp8",
+            "pkv_tree_workspace_size", "pkv_tree_accept", "pkv_compact_fp16",
+            "pkv_compact_int8", "pkv_compact_fp8",
             "pkv_evict_select", "pkv_bm_create", "pkv_bm_destroy", "pkv_bm_allocate",
             "pkv_bm_free", "pkv_bm_fork", "pkv_bm_cow", "pkv_bm_set_fill", "pkv_bm_stats",
             "pkv_bm_refcounts", "pkv_copy_blocks", "pkv_decode_workspace_size",
@@ -160,8 +171,18 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     prefill = [P, P, P, P, I, P, I, P, P, I, I, I, I, I, I, I, F, F, I, P, P, P, Z, P, P]
     L.pkv_prefill_workspace_size.restype = Z
     L.pkv_prefill_workspace_size.argtypes = [I] * 6
+    tree = prefill[:9] + [P, I] + prefill[9:]
+    compact = [P, P, I, P, P, P, P, P, P, I, I, I, I, I, I, P, P]
+    L.pkv_tree_workspace_size.restype = Z
+    L.pkv_tree_workspace_size.argtypes = [I] * 7
+    L.pkv_tree_accept.restype = I
+    L.pkv_tree_accept.argtypes = [P] * 7 + [I, I, P, P]
     for kind in ("fp16", "int8", "fp8"):
         codes = [] if kind == "fp16" else [P, P]
+        fn = getattr(L, "pkv_paged_tree_" + kind)
+        fn.restype, fn.argtypes = I, tree[:4] + codes + tree[4:]
+        fn = getattr(L, "pkv_compact_" + kind)
+        fn.restype, fn.argtypes = I, compact[:2] + 2 * codes + compact[2:]
         fn = getattr(L, "pkv_paged_decode_scored_" + kind)
         fn.restype, fn.argtypes = I, scored[:4] + codes + scored[4:]
         fn = getattr(L, "pkv_paged_prefill_" + kind)
@@ -941,6 +962,262 @@ def prepare_rope_append_fp8(q_out, k_cache, v_cache, k_codes, v_codes, k_scales,
     return PreparedCall(fn, args, keep=(q_out, k_cache, v_cache, k_codes, v_codes, k_scales, v_scales, q, k, v,
                                         cos_sin, query_starts, context_lens, block_tables,
                                         rope_positions, axis, dev_status))
+
+
+# -------------------------------- trees of drafted tokens, and rows that stay
+def _tree(fn_name, out, query, kp, vp, ks, vs, block_tables, query_starts, context_lens, parents,
+          max_context_len, max_tree_len, softmax_scale, workspace, logit_cap, window, slopes,
+          prefix_lens, dev_status, stream):
+    """Checks and marshals a tree attention call: (C function name, arguments)."""
+    import torch
+    _check(parents, "parents", torch.int32)
+    _, args = _prefill(fn_name, out, query, kp, vp, ks, vs, block_tables, query_starts,
+                       context_lens, max_context_len, softmax_scale, workspace, logit_cap, window,
+                       slopes, prefix_lens, dev_status, stream)
+    _shape("parents", parents, query.shape[0])
+    _same_device(("parents", parents))
+    at = 9 if ks is None else 11   # max_context_len
+    return fn_name, args[:at] + [_ptr(parents), args[at], int(max_tree_len)] + args[at + 1:]
+
+
+def pkv_tree_workspace_size(num_tokens, num_seqs, num_heads, num_kv_heads, head_dim,
+                            max_context_len, max_tree_len) -> int:
+    return int(lib().pkv_tree_workspace_size(num_tokens, num_seqs, num_heads, num_kv_heads,
+                                             head_dim, max_context_len, max_tree_len))
+
+
+def tree_workspace(num_tokens, num_seqs, num_heads, num_kv_heads, head_dim, max_context_len,
+                   max_tree_len, device=None):
+    """A uint8 CUDA tensor big enough to serve as a workspace of tree attention."""
+    import torch
+    nbytes = pkv_tree_workspace_size(num_tokens, num_seqs, num_heads, num_kv_heads, head_dim,
+                                     max_context_len, max_tree_len)
+    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def pkv_paged_tree_fp16(out, query, k_cache, v_cache, block_tables, query_starts,
+                        context_lens, parents, max_context_len, max_tree_len, softmax_scale,
+                        workspace, logit_cap=0.0, window=0, slopes=None, prefix_lens=None,
+                        dev_status=None, stream=None) -> None:
+    """out[T][Hq][d] fp16 = attention of trees of drafted tokens over fp16 pools: a
+    token sees its sequence's context, its ancestors (parents[T]: rows within
+    the sequence, -1 for none) and itself."""
+    _invoke(*_tree("pkv_paged_tree_fp16", out, query, k_cache, v_cache, None, None,
+                   block_tables, query_starts, context_lens, parents, max_context_len,
+                   max_tree_len, softmax_scale, workspace, logit_cap, window, slopes, prefix_lens,
+                   dev_status, stream))
+
+
+def prepare_paged_tree_fp16(out, query, k_cache, v_cache, block_tables, query_starts,
+                            context_lens, parents, max_context_len, max_tree_len, softmax_scale,
+                            workspace, logit_cap=0.0, window=0, slopes=None, prefix_lens=None,
+                            dev_status=None, stream=None) -> PreparedCall:
+    """``pkv_paged_tree_fp16`` with its arguments marshalled once."""
+    return PreparedCall(*_tree("pkv_paged_tree_fp16", out, query, k_cache, v_cache, None, None,
+                               block_tables, query_starts, context_lens, parents,
+                               max_context_len, max_tree_len, softmax_scale, workspace,
+                               logit_cap, window, slopes, prefix_lens, dev_status, stream),
+                        keep=(out, query, k_cache, v_cache, block_tables,
+                              query_starts, context_lens, parents, workspace, slopes,
+                              prefix_lens, dev_status))
+
+
+def pkv_paged_tree_int8(out, query, k_codes, v_codes, k_scales, v_scales, block_tables, query_starts,
+                        context_lens, parents, max_context_len, max_tree_len, softmax_scale,
+                        workspace, logit_cap=0.0, window=0, slopes=None, prefix_lens=None,
+                        dev_status=None, stream=None) -> None:
+    """out[T][Hq][d] fp16 = attention of trees of drafted tokens over INT8 pools: a
+    token sees its sequence's context, its ancestors (parents[T]: rows within
+    the sequence, -1 for none) and itself."""
+    _invoke(*_tree("pkv_paged_tree_int8", out, query, k_codes, v_codes, k_scales, v_scales,
+                   block_tables, query_starts, context_lens, parents, max_context_len,
+                   max_tree_len, softmax_scale, workspace, logit_cap, window, slopes, prefix_lens,
+                   dev_status, stream))
+
+
+def prepare_paged_tree_int8(out, query, k_codes, v_codes, k_scales, v_scales, block_tables, query_starts,
+                            context_lens, parents, max_context_len, max_tree_len, softmax_scale,
+                            workspace, logit_cap=0.0, window=0, slopes=None, prefix_lens=None,
+                            dev_status=None, stream=None) -> PreparedCall:
+    """``pkv_paged_tree_int8`` with its arguments marshalled once."""
+    return PreparedCall(*_tree("pkv_paged_tree_int8", out, query, k_codes, v_codes, k_scales, v_scales,
+                               block_tables, query_starts, context_lens, parents,
+                               max_context_len, max_tree_len, softmax_scale, workspace,
+                               logit_cap, window, slopes, prefix_lens, dev_status, stream),
+                        keep=(out, query, k_codes, v_codes, k_scales, v_scales, block_tables,
+                              query_starts, context_lens, parents, workspace, slopes,
+                              prefix_lens, dev_status))
+
+
+def pkv_paged_tree_fp8(out, query, k_codes, v_codes, k_scales, v_scales, block_tables, query_starts,
+                        context_lens, parents, max_context_len, max_tree_len, softmax_scale,
+                        workspace, logit_cap=0.0, window=0, slopes=None, prefix_lens=None,
+                        dev_status=None, stream=None) -> None:
+    """out[T][Hq][d] fp16 = attention of trees of drafted tokens over FP8 pools: a
+    token sees its sequence's context, its ancestors (parents[T]: rows within
+    the sequence, -1 for none) and itself."""
+    _invoke(*_tree("pkv_paged_tree_fp8", out, query, k_codes, v_codes, k_scales, v_scales,
+                   block_tables, query_starts, context_lens, parents, max_context_len,
+                   max_tree_len, softmax_scale, workspace, logit_cap, window, slopes, prefix_lens,
+                   dev_status, stream))
+
+
+def prepare_paged_tree_fp8(out, query, k_codes, v_codes, k_scales, v_scales, block_tables, query_starts,
+                            context_lens, parents, max_context_len, max_tree_len, softmax_scale,
+                            workspace, logit_cap=0.0, window=0, slopes=None, prefix_lens=None,
+                            dev_status=None, stream=None) -> PreparedCall:
+    """``pkv_paged_tree_fp8`` with its arguments marshalled once."""
+    return PreparedCall(*_tree("pkv_paged_tree_fp8", out, query, k_codes, v_codes, k_scales, v_scales,
+                               block_tables, query_starts, context_lens, parents,
+                               max_context_len, max_tree_len, softmax_scale, workspace,
+                               logit_cap, window, slopes, prefix_lens, dev_status, stream),
+                        keep=(out, query, k_codes, v_codes, k_scales, v_scales, block_tables,
+                              query_starts, context_lens, parents, workspace, slopes,
+                              prefix_lens, dev_status))
+
+
+def _accept(kept, kept_lens, next_tokens, tokens, targets, parents, query_starts, dev_status,
+            stream):
+    """Checks and marshals an acceptance call: (C function name, arguments)."""
+    import torch
+    named = (("kept", kept), ("kept_lens", kept_lens), ("next_tokens", next_tokens),
+             ("tokens", tokens), ("targets", targets), ("parents", parents),
+             ("query_starts", query_starts), ("dev_status", dev_status))
+    for name, x in named:
+        _check(x, name, torch.int32)
+    t, n = tokens.numel(), kept_lens.numel()
+    for name, x in (("kept", kept), ("tokens", tokens), ("targets", targets), ("parents", parents)):
+        _shape(name, x, t)
+    _shape("kept_lens", kept_lens, n)
+    _shape("next_tokens", next_tokens, n)
+    _shape("query_starts", query_starts, n + 1)
+    _same_device(*named)
+    return "pkv_tree_accept", [_ptr(kept), _ptr(kept_lens), _ptr(next_tokens), _ptr(tokens),
+                               _ptr(targets), _ptr(parents), _ptr(query_starts), t, n,
+                               _ptr(dev_status), _stream(stream)]
+
+
+def pkv_tree_accept(kept, kept_lens, next_tokens, tokens, targets, parents, query_starts,
+                    dev_status=None, stream=None) -> None:
+    """Walk every tree from its row 0 along the model's answers (targets[T], the
+    token after each row): kept[T] gets the rows of the path and -1 behind them,
+    kept_lens[N] their number, next_tokens[N] the answer after the last one."""
+    _invoke(*_accept(kept, kept_lens, next_tokens, tokens, targets, parents, query_starts,
+                     dev_status, stream))
+
+
+def prepare_tree_accept(kept, kept_lens, next_tokens, tokens, targets, parents, query_starts,
+                        dev_status=None, stream=None) -> PreparedCall:
+    """``pkv_tree_accept`` with its arguments marshalled once."""
+    return PreparedCall(*_accept(kept, kept_lens, next_tokens, tokens, targets, parents,
+                                 query_starts, dev_status, stream),
+                        keep=(kept, kept_lens, next_tokens, tokens, targets, parents,
+                              query_starts, dev_status))
+
+
+def _compact(fn_name, k_cache, v_cache, codes, kept, kept_lens, new_context_lens, query_starts,
+             context_lens, block_tables, dev_status, stream):
+    """Checks and marshals a compaction call: (C function name, arguments)."""
+    import torch
+    _check(k_cache, "k_cache", torch.float16)
+    _check(v_cache, "v_cache", torch.float16)
+    ints = (("kept", kept), ("kept_lens", kept_lens), ("new_context_lens", new_context_lens),
+            ("query_starts", query_starts), ("context_lens", context_lens),
+            ("block_tables", block_tables), ("dev_status", dev_status))
+    for name, x in ints:
+        _check(x, name, torch.int32)
+    nb, hkv, bs, d = k_cache.shape
+    n = context_lens.numel()
+    _shape("v_cache", v_cache, *k_cache.shape)
+    _shape("kept", kept, kept.numel())
+    _shape("kept_lens", kept_lens, n)
+    _shape("new_context_lens", new_context_lens, n)
+    _shape("query_starts", query_starts, n + 1)
+    if block_tables.dim() != 2 or block_tables.shape[0] != n:
+        raise ValueError("block_tables must be [num_seqs][max_blocks_per_seq]")
+    args = [_ptr(k_cache), _ptr(v_cache)]
+    if codes is not None:
+        kc, vc, ks, vs = codes
+        _check_pools(fn_name, kc, vc, ks, vs)
+        _shape("k_codes", kc, *k_cache.shape)
+        args += [_ptr(kc), _ptr(vc), _ptr(ks), _ptr(vs)]
+    _same_device(("k_cache", k_cache), ("v_cache", v_cache), *ints,
+                 *(("codes", x) for x in codes or ()))
+    args += [nb, _ptr(kept), _ptr(kept_lens), _ptr(new_context_lens), _ptr(query_starts),
+             _ptr(context_lens), _ptr(block_tables), block_tables.shape[1], kept.numel(), n, hkv,
+             d, bs, _ptr(dev_status), _stream(stream)]
+    return fn_name, args
+
+
+def pkv_compact_fp16(k_cache, v_cache, kept, kept_lens,
+                     new_context_lens, query_starts, context_lens, block_tables, dev_status=None,
+                     stream=None) -> None:
+    """Of the last query_starts[s + 1] - query_starts[s] cached tokens of every
+    sequence, move the rows of the kept_lens[s] ones listed in kept (rising) to
+    the front of them; new_context_lens gets the lengths."""
+    _invoke(*_compact("pkv_compact_fp16", k_cache, v_cache, None,
+                      kept, kept_lens, new_context_lens, query_starts, context_lens,
+                      block_tables, dev_status, stream))
+
+
+def prepare_compact_fp16(k_cache, v_cache, kept, kept_lens,
+                         new_context_lens, query_starts, context_lens, block_tables,
+                         dev_status=None, stream=None) -> PreparedCall:
+    """``pkv_compact_fp16`` with its arguments marshalled once."""
+    return PreparedCall(*_compact("pkv_compact_fp16", k_cache, v_cache, None,
+                                  kept, kept_lens, new_context_lens, query_starts, context_lens,
+                                  block_tables, dev_status, stream),
+                        keep=(k_cache, v_cache, kept, kept_lens,
+                              new_context_lens, query_starts, context_lens, block_tables,
+                              dev_status))
+
+
+def pkv_compact_int8(k_cache, v_cache, k_codes, v_codes, k_scales, v_scales, kept, kept_lens,
+                     new_context_lens, query_starts, context_lens, block_tables, dev_status=None,
+                     stream=None) -> None:
+    """Of the last query_starts[s + 1] - query_starts[s] cached tokens of every
+    sequence, move the rows of the kept_lens[s] ones listed in kept (rising) to
+    the front of them; new_context_lens gets the lengths.
+    Every tile that got a row is quantized again."""
+    _invoke(*_compact("pkv_compact_int8", k_cache, v_cache, (k_codes, v_codes, k_scales, v_scales),
+                      kept, kept_lens, new_context_lens, query_starts, context_lens,
+                      block_tables, dev_status, stream))
+
+
+def prepare_compact_int8(k_cache, v_cache, k_codes, v_codes, k_scales, v_scales, kept, kept_lens,
+                         new_context_lens, query_starts, context_lens, block_tables,
+                         dev_status=None, stream=None) -> PreparedCall:
+    """``pkv_compact_int8`` with its arguments marshalled once."""
+    return PreparedCall(*_compact("pkv_compact_int8", k_cache, v_cache, (k_codes, v_codes, k_scales, v_scales),
+                                  kept, kept_lens, new_context_lens, query_starts, context_lens,
+                                  block_tables, dev_status, stream),
+                        keep=(k_cache, v_cache, k_codes, v_codes, k_scales, v_scales, kept, kept_lens,
+                              new_context_lens, query_starts, context_lens, block_tables,
+                              dev_status))
+
+
+def pkv_compact_fp8(k_cache, v_cache, k_codes, v_codes, k_scales, v_scales, kept, kept_lens,
+                     new_context_lens, query_starts, context_lens, block_tables, dev_status=None,
+                     stream=None) -> None:
+    """Of the last query_starts[s + 1] - query_starts[s] cached tokens of every
+    sequence, move the rows of the kept_lens[s] ones listed in kept (rising) to
+    the front of them; new_context_lens gets the lengths.
+    Every tile that got a row is quantized again."""
+    _invoke(*_compact("pkv_compact_fp8", k_cache, v_cache, (k_codes, v_codes, k_scales, v_scales),
+                      kept, kept_lens, new_context_lens, query_starts, context_lens,
+                      block_tables, dev_status, stream))
+
+
+def prepare_compact_fp8(k_cache, v_cache, k_codes, v_codes, k_scales, v_scales, kept, kept_lens,
+                         new_context_lens, query_starts, context_lens, block_tables,
+                         dev_status=None, stream=None) -> PreparedCall:
+    """``pkv_compact_fp8`` with its arguments marshalled once."""
+    return PreparedCall(*_compact("pkv_compact_fp8", k_cache, v_cache, (k_codes, v_codes, k_scales, v_scales),
+                                  kept, kept_lens, new_context_lens, query_starts, context_lens,
+                                  block_tables, dev_status, stream),
+                        keep=(k_cache, v_cache, k_codes, v_codes, k_scales, v_scales, kept, kept_lens,
+                              new_context_lens, query_starts, context_lens, block_tables,
+                              dev_status))
 
 
 def pkv_evict_select(refcnt, last_used, current_tick, k, evict_ids, num_evicted, scores=None,
