@@ -136,8 +136,9 @@ def debug_lib() -> ctypes.CDLL:
             for name in ("pkv_debug_set_stage_wait_ns", "pkv_debug_set_scored_stage_wait_ns"):
                 getattr(L, name).restype = ctypes.c_int
                 getattr(L, name).argtypes = [ctypes.c_longlong]
-            L.pkv_debug_set_prefill.restype = ctypes.c_int
-            L.pkv_debug_set_prefill.argtypes = [ctypes.c_int] * 4
+            for name in ("pkv_debug_set_prefill", "pkv_debug_set_tree"):
+                getattr(L, name).restype = ctypes.c_int
+                getattr(L, name).argtypes = [ctypes.c_int] * 4
             _debug_lib = L
         return _debug_lib
 

@@ -76,14 +76,16 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
 
 
 # the kernels with PKV_DEBUG checks and settings
-DEBUG_SOURCES = ("pkv_decode.cu", "pkv_decode_scored.cu", "pkv_prefill.cu", "pkv_evict.cu")
+DEBUG_SOURCES = ("pkv_decode.cu", "pkv_decode_scored.cu", "pkv_prefill.cu", "pkv_tree.cu",
+                 "pkv_evict.cu")
 
 
 def build_debug() -> str:
     """libpkv_debug.so: the library with the decode and eviction kernels built
     with PKV_DEBUG (shared-memory address and index checks, read back by
-    pkv_debug_flags / pkv_debug_evict_flags) and the prefill's with settings of
-    its waits (pkv_debug_set_prefill).  For tests; the release library is
+    pkv_debug_flags / pkv_debug_evict_flags) and the prefill's and the tree
+    attention's with settings of their waits (pkv_debug_set_prefill,
+    pkv_debug_set_tree).  For tests; the release library is
     untouched."""
     build()
     if os.path.exists(DEBUG_LIB_PATH) and all(

@@ -54,6 +54,7 @@
 #include "pkv_ragged.cuh"
 #include "pkv_score.cuh"
 #include "pkv_umma.cuh"
+#include "pkv_wait.cuh"
 
 namespace pkv {
 namespace {
@@ -79,7 +80,6 @@ __host__ __device__ constexpr int soft_warps(bool mod)
 }
 constexpr int kSms = 152;       // GB300: what the split over the keys aims to fill
 constexpr int kMaxSplits = 64;
-constexpr uint64_t kWaitLimitNs = 1000000000ull;  // bounded waits: 1 s
 constexpr float kLazy = 6.f;    // log2 growth of a maximum that is left in the sums
 constexpr float kLift = 6.f;    // log2 factor of the probabilities
 constexpr float kVLazy = 8.f;   // growth of a V scale that is left in the ratio
@@ -154,75 +154,6 @@ struct Smem {
 
 // What a warp does; its waits are counted by role in the debug build.
 enum Role { kRoleRows, kRoleProducts, kRoleLoadK, kRoleLoadV, kRoleItems, kRoleWiden, kRoles };
-
-#ifdef PKV_DEBUG
-// Settable through pkv_debug_set_prefill: wait number give_at of every warp of
-// give_role gives up, as if its limit had run out, and every wait of slow_role
-// begins slow_ns later (role -2: none; warps without a role have -1).
-struct PrefillDebug {
-    int give_role, give_at, slow_role, slow_ns;
-};
-__device__ PrefillDebug g_prefill_debug = {-2, 0, -2, 0};
-#endif
-
-struct Waiter {
-    volatile int *abort;
-    int32_t *dev_status;
-#ifdef PKV_DEBUG
-    int role = -1;
-    mutable int waits = 0;
-#endif
-    __device__ __forceinline__ Waiter as([[maybe_unused]] Role r) const
-    {
-        Waiter w = *this;
-#ifdef PKV_DEBUG
-        w.role = r;
-#endif
-        return w;
-    }
-    // Bounded waits; false once any wait of the CTA ran out.  By one thread:
-    __device__ __forceinline__ bool one(uint32_t bar, uint32_t parity) const
-    {
-        if (gives_up()) return false;
-        return ptx::mbar_try_wait(bar, parity) || slow(bar, parity);
-    }
-    // by a whole warp, all lanes with the same outcome:
-    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const
-    {
-        if (gives_up()) return false;
-        if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
-        return __all_sync(0xffffffffu, slow(bar, parity));
-    }
-    __device__ __forceinline__ bool slow(uint32_t bar, uint32_t parity) const
-    {
-        uint64_t t0 = 0;  // the timer is slow to read: only after many tries
-        for (;;) {
-            for (int i = 0; i < 4096; ++i)
-                if (ptx::mbar_try_wait(bar, parity)) return true;
-            if (*abort) return false;
-            const uint64_t now = ptx::globaltimer_ns();
-            if (t0 == 0) t0 = now;
-            if (now - t0 > kWaitLimitNs) give_up();
-        }
-    }
-    __device__ __forceinline__ void give_up() const
-    {
-        *abort = 1;
-        if (dev_status) atomicOr(dev_status, PKV_DEV_TIMEOUT);
-    }
-    __device__ __forceinline__ bool gives_up() const
-    {
-#ifdef PKV_DEBUG
-        const PrefillDebug d = g_prefill_debug;
-        if (role == d.slow_role) __nanosleep(d.slow_ns);
-        if (role == d.give_role && waits++ == d.give_at) {
-            give_up();
-            return true;
-        }
-#endif
-        return false;
-    }
-};
 
 // ------------------------------------------------------------------- items
 struct __align__(16) Item {
@@ -331,23 +262,6 @@ __device__ __noinline__ void check_sequences(const PrefillArgs &p, int lane)
 {
     report_bad_sequences(p.query_starts, p.context_lens, p.num_seqs, p.num_tokens, p.ctx_cap,
                          p.dev_status, lane, 32);
-}
-
-// After a wait that ran out, with every warp behind a barrier of the CTA: waits
-// (bounded) for the copies that may still write into its shared memory.  K and
-// V tile t are elements 2 t and 2 t + 1 of a ring of R stages, and a stage is
-// filled again only after its element was used up, so only the last element of
-// each stage can be in flight; of the queries only the last item's.
-template <int R>
-__device__ void drain_copies(uint32_t full0, uint32_t q_full, int k_tiles, int v_tiles, int items)
-{
-    for (int s = 0; s < R; ++s)
-        for (int n = 2 * max(k_tiles, v_tiles) - 1; n >= 0; --n)
-            if (n % R == s && n / 2 < (n & 1 ? v_tiles : k_tiles)) {
-                ptx::mbar_wait_bounded(full0 + 8 * s, n / R & 1, kWaitLimitNs);
-                break;
-            }
-    if (items > 0) ptx::mbar_wait_bounded(q_full, (items - 1) & 1, kWaitLimitNs);
 }
 
 // ------------------------------------------------------------------ kernel
@@ -1787,7 +1701,7 @@ extern "C" size_t pkv_prefill_workspace_size(int num_tokens, int num_seqs, int n
 }
 
 #ifdef PKV_DEBUG
-// Debug builds only: see PrefillDebug (roles 0 rows, 1 products, 2 K and query
+// Debug builds only: see WaitDebug (roles 0 rows, 1 products, 2 K and query
 // loads, 3 V loads, 4 items, 5 widening of codes).  A negative role resets its
 // setting.  Synchronises with the device; returns 0, or -1 if the CUDA runtime
 // fails or an argument is out of range.
@@ -1798,10 +1712,10 @@ extern "C" __attribute__((visibility("default"))) int pkv_debug_set_prefill(int 
 {
     if (give_role >= pkv::kRoles || slow_role >= pkv::kRoles || slow_ns < 0 || slow_ns > 1000000)
         return -1;
-    const pkv::PrefillDebug d = {give_role < 0 ? -2 : give_role, give_at,
+    const pkv::WaitDebug d = {give_role < 0 ? -2 : give_role, give_at,
                                  slow_role < 0 ? -2 : slow_role, slow_ns};
     if (cudaDeviceSynchronize() != cudaSuccess ||
-        cudaMemcpyToSymbol(pkv::g_prefill_debug, &d, sizeof(d)) != cudaSuccess)
+        cudaMemcpyToSymbol(pkv::g_wait_debug, &d, sizeof(d)) != cudaSuccess)
         return -1;
     return 0;
 }

@@ -43,12 +43,25 @@ __device__ __forceinline__ uint64_t desc(uint32_t lo)
     return static_cast<uint64_t>(hi) << 32 | lo;
 }
 
+// Shared-memory operand without a swizzle, MN-major: 8 values of M or N by 8 of K
+// are 128 contiguous bytes, 8 rows (K) of 16.  The next 8 of K follow at once, the
+// next 8 of M or N `block` bytes further on.
+__device__ __forceinline__ uint64_t desc_plain(uint32_t addr, uint32_t block)
+{
+    const uint32_t lo = ((addr & 0x3ffffu) >> 4) | ((128u >> 4) << 16);
+    const uint32_t hi = (block >> 4) | (1u << 14);
+    return static_cast<uint64_t>(hi) << 32 | lo;
+}
+
 // fp16 x fp16 -> fp32, M x N per instruction (K = 16); b_mn: B is MN-major.
 __host__ __device__ constexpr uint32_t f16_idesc(int m, int n, bool b_mn)
 {
     return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
            (static_cast<uint32_t>(m >> 4) << 24);
 }
+
+// The bit of an instruction descriptor that says that A is MN-major.
+constexpr uint32_t kAMn = 1u << 15;
 
 // True in one lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one()

@@ -51,6 +51,9 @@ def test_tree(kind):
     for name in ("slopes", "prefix", "lens", "starts", "tables", "parents", "status"):
         assert c(**{name: FAKE + 2}) == MISALIGNED
     assert c(out=FAKE + 8) == c(k=FAKE + 4) == c(query=FAKE + 2) == MISALIGNED
+    need = pkv.pkv_tree_workspace_size(10, 2, 8, 2, 64, 64, 8)
+    assert need > 0 and c(ws=None) == c(ws_bytes=need - 1) == WORKSPACE
+    assert c(ws=FAKE + 4) == MISALIGNED
     assert c(t=0) == c(n=0) == pkv.PKV_OK
     assert c(t=0, out=None, query=None, parents=None) == pkv.PKV_OK
     if kind != "fp16":
@@ -98,6 +101,16 @@ def test_compact(kind):
 
 
 def test_workspace_size():
+    # for each of the pieces' CTAs two parts of 32 or 128 rows, d values and two
+    # numbers each, and 32 bytes that say whose they are
+    def expect(ctas, rows, d):
+        return ctas * (2 * rows * (d + 2) * 4 + 32)
+    assert pkv.pkv_tree_workspace_size(64, 8, 8, 8, 128, 512, 8) == expect(152, 32, 128)
+    assert pkv.pkv_tree_workspace_size(64, 8, 32, 8, 128, 512, 8) == expect(152, 32, 128)
+    assert pkv.pkv_tree_workspace_size(64, 8, 32, 8, 128, 512, 9) == expect(152, 128, 128)
+    assert pkv.pkv_tree_workspace_size(64, 1, 32, 8, 64, 512, 64) == expect(2 * 76, 128, 64)
+    # a bound above the batch's tokens does not count
+    assert pkv.pkv_tree_workspace_size(4, 1, 8, 1, 64, 512, 4096) == expect(152, 32, 64)
     assert pkv.pkv_tree_workspace_size(8, 1, 4, 3, 128, 20000, 8) == 0
     assert pkv.pkv_tree_workspace_size(8, 1, 4, 1, 96, 20000, 8) == 0
     assert pkv.pkv_tree_workspace_size(-1, 1, 4, 1, 64, 20000, 8) == 0
