@@ -40,6 +40,14 @@ __device__ __forceinline__ constexpr float tanh_coef(int k)
     return c[k];
 }
 
+// The same for |u| <= 0.5, of degree 4: 2^-25 with its coefficients in fp32, 2^-23
+// as evaluated.
+__device__ __forceinline__ constexpr float tanh_close(int k)
+{
+    constexpr float close[5] = {1.f, -0.333330691f, 0.133247808f, -0.0529861338f, 0.0171351079f};
+    return close[k];
+}
+
 __device__ __forceinline__ float cap_poly(float x, float u)
 {
     const float w = u * u;

@@ -1,0 +1,1407 @@
+// pkv_tree.cuh -- attention of trees of drafted tokens over the paged cache: a
+// token sees its sequence's context (window, visible prefix), its ancestors in
+// the tree and itself, with the scores of the scored decode (tanh cap, bias by
+// distance).
+//
+// For the token at position i (the context's length plus its depth), a key t at
+// position p(t) and z = softmax_scale <q, K_t>:
+//   z' = cap tanh(z / cap)  (cap > 0),   z'' = z' - slope[h] (i - p(t)),
+//   out = sum over seen t of softmax(z'')_t V_t.
+//
+// Bound by memory: a tree has few rows (tokens times the heads of a kv head), and
+// every cached key and value is read once for all of them.  So the keys are the
+// long side of both products: per tile of 128 keys (eight pages)
+//   S^T = K Q^T     (128 keys x N rows, fp32 in TMEM; K as it lies in the page)
+//   P^T = 2^(S' - m)  (a thread per key, half of the rows each; fp16, to shared
+//                    memory in the layout of a product's operand)
+//   O^T += V^T P^T  (head_dim x N, fp32 in TMEM; V as it lies in the page)
+// With rows as the N of the products, 32 rows take a quarter of the time of 128,
+// and the exponentials of all rows are spread over all threads.  Since a row's
+// scores lie across threads, its maximum is not taken for every tile: the
+// exponentials are relative to a reference per row, and a tile whose scores
+// exceed it by more than 2^6 (every row's first, hardly any other) makes all
+// threads take the maxima and rescale sums and accumulators.  The probabilities
+// enter the product with a factor 2^6, so up to that much smaller ones are normal
+// fp16 numbers.  Sums, maxima and accumulators are fp32.
+//
+// The tiles of all (sequence, kv head) pairs form one line, which is cut into as
+// many equal pieces as there are SMs: a CTA walks its piece, whatever the lengths
+// of the sequences.  Where a cut lies inside a pair, the parts are joined by a
+// second kernel.  Trees with more than N rows take a CTA for every N of them, side
+// by side on the same piece, so that they read the same pages at the same time.
+//
+// Roles of the warps: 0-7 scores and rows, 8 issues the products, 9 and 11 the TMA
+// loads of K and Q, and of V (a ring of tiles, K and V in turn), 10 the items.
+// INT8 / FP8 pages land in a second ring, and further warps widen them exactly to
+// fp16.  The K scale of a page multiplies its keys' scores.  Its V scale enters
+// the exponent, 2^(S' + log2 v - m), so that the reference is that of the largest
+// contribution p V, and the sums take the probability times 1 / v.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <mutex>
+
+#include "pkv_host.cuh"
+#include "pkv_ptx.cuh"
+#include "pkv_ragged.cuh"
+#include "pkv_score.cuh"
+#include "pkv_tree_call.h"
+#include "pkv_umma.cuh"
+#include "pkv_wait.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kPage = 16;
+constexpr int kTile = 128;      // keys per step
+constexpr int kPagesPerTile = kTile / kPage;
+constexpr int kKvF16 = 0, kKvI8 = 1, kKvF8 = 2;
+constexpr int kGroup = 128;     // threads that share rows: one per key of a tile
+constexpr int kSms = 152;       // GB300: pieces of the line of tiles
+constexpr int kPieceTiles = 2;  // tiles of a piece at least
+constexpr float kLift = 6.f;    // log2 factor of the probabilities
+constexpr float kLazy = 9.f;    // log2 excess over the reference that is let be
+constexpr float kNone = -3.0e38f;        // reference of a row that has seen nothing
+constexpr float kLeastV = 0x1p-60f;      // V scales below (zero) count as this
+constexpr int kParents = 512;   // parents of a sequence kept in shared memory
+
+// Score warps: a group of four, a thread per key, for up to 64 rows each.  A tile's
+// chain (scores, reference, exponentials, product) has more waits than work; two
+// groups with rows of their own and nothing to tell each other fill these.
+__host__ __device__ constexpr int tree_groups(int rows)
+{
+    return rows > 32 ? 2 : 1;
+}
+
+__host__ __device__ constexpr int soft_warps(int rows)
+{
+    return 4 * tree_groups(rows);
+}
+
+// Warps that widen codes: 128 rows leave registers for four.
+__host__ __device__ constexpr int widen_warps(int kv, int rows)
+{
+    return kv == kKvF16 ? 0 : rows > 64 ? 4 : 8;
+}
+
+__host__ __device__ constexpr int tree_threads(int kv, int rows)
+{
+    return 32 * (soft_warps(rows) + 4 + widen_warps(kv, rows));
+}
+
+struct TreeMeta {               // the part of an item that a piece ends in
+    int tok, toks, head, heads, parts;
+    int unused[3];
+};
+static_assert(sizeof(TreeMeta) == kTreeMetaBytes, "what the plan counts");
+
+struct TreeArgs {
+    __half *out;
+    const int32_t *block_tables, *query_starts, *context_lens, *parents;
+    const float *k_scales, *v_scales;
+    const float *slopes;
+    const int32_t *prefix_lens;
+    float *part_acc;    // [2 CTAs][kN][head_dim]: the part a piece begins with, ends in
+    float2 *part_ml;    // [2 CTAs][kN]: reference, sum
+    TreeMeta *meta;     // [CTAs]
+    int32_t *dev_status;
+    int num_tokens, num_seqs, num_heads, num_kv_heads, group;
+    int chunk, chunks;  // heads of a kv head per item (the group, at most 128), chunks of them
+    int tokens;         // tokens per item
+    int sides;          // CTAs side by side on a piece, for every sides-th item of a tree
+    int pieces;
+    int max_blocks_per_seq, num_blocks, ctx_cap, max_tree_len, window;
+    float scale_log2, cap, cap_inv;
+};
+
+// ------------------------------------------------------------ shared memory
+template <int kKv, int kD, int kN>
+struct TreeSmem {
+    static constexpr bool kCodes = kKv != kKvF16;
+    static constexpr int kHalves = kD / 64;
+    static constexpr int kHalfBytes = kTile * 128;             // 64 values of 128 keys
+    static constexpr int kTileBytes = kHalves * kHalfBytes;
+    static constexpr int kQHalfBytes = kN * 128;               // 64 values of the rows
+    static constexpr int kPBytes = kN * kTile * 2;
+    static constexpr int kPBufs = !kCodes && kN == 128 ? 1 : 2;
+    static constexpr int kCodeBytes = kTile * kD;
+    static constexpr int kMore = 128 / kD;
+    static constexpr int kStages =
+        kMore * (kCodes ? (kN <= 64 ? 3 : 2) : kN <= 32 ? 6 : kN <= 64 ? 5 : 4);
+    static constexpr int kCodeStages = kCodes ? kMore * (kN <= 32 ? 6 : kN <= 64 ? 4 : 3) : 0;
+    // A waiting warp must not be two phases of a barrier off.  K and V have a producer
+    // each, which has seen the element S + 2 before its next one given back and takes
+    // for granted that the one 2 S before it was.  With an even number of stages these
+    // are both K or both V.  With an odd one, V's producer has seen a K, whose product
+    // follows the one with V of two tiles before: 5 stages will do, 3 will not.  (Codes
+    // are widened in their order, by the same warps.)
+    static_assert(kCodes || kStages % 2 == 0 || kStages >= 5, "phases of the ring");
+    static constexpr int kP = kHalves * kQHalfBytes;
+    static constexpr int kRing = kP + kPBufs * kPBytes;
+    static constexpr int kCodeRing = kRing + kStages * kTileBytes;
+    static constexpr int kCtl = kCodeRing + kCodeStages * kCodeBytes;
+    static constexpr int kBars = 2 * kStages + 2 * kCodeStages + 19;
+    static constexpr int kItems = (kCtl + 8 * kBars + 15) & ~15;
+    static constexpr int kFlags = kItems + 2 * 80;
+    static constexpr int kIssued = kFlags + 32;   // see drain_copies
+    // scales [kScaleTiles][K, V][8 pages], written by the K warp ahead of its
+    // arrival for the tile's K codes; the scores of the tile are behind that.  The
+    // warp runs ahead by the elements of both rings and one that it holds, and the
+    // scores lag behind the products by two tiles.
+    static constexpr int kScaleTiles = 16;
+    static_assert((kStages + kCodeStages + 1) / 2 + 3 <= kScaleTiles, "scales overwritten");
+    static constexpr int kScales = kIssued + 16;
+    static constexpr int kOff = kScales + (kCodes ? kScaleTiles * 2 * kPagesPerTile * 4 : 0);
+    static constexpr int kMax = kOff + 4 * kN;      // a row's reference
+    static constexpr int kFac = kMax + 4 * kN;      // factor of its sums; 1 / sum at the end
+    static constexpr int kSlope = kFac + 4 * kN;
+    static constexpr int kAt = kSlope + 4 * kN;     // the row's place in the output, or -1
+    static constexpr int kSums = kAt + 8 * kN;      // [4 quarters of the keys][kN]
+    static constexpr int kMask = kSums + 16 * kN;   // [4 quarters of the keys][kN]: bits
+    static constexpr int kScan = kMask + 16 * kN;   // sums of the warps, where the piece begins
+    static constexpr int kUp = kScan + 8 * 32;      // parents
+    static constexpr int kBytes = kUp + 2 * 4 * kParents;   // of both item slots
+    // a second CTA on the SM would wait for TMEM: ask for more than half
+    static constexpr int kAsk = kBytes > 120 * 1024 ? kBytes : 120 * 1024;
+    static_assert(kAsk <= 227 * 1024, "shared memory of one CTA");
+    static_assert(kRing % 1024 == 0 && kCodeRing % 1024 == 0, "swizzled tiles");
+};
+
+enum Role { kRoleRows, kRoleProducts, kRoleLoadK, kRoleLoadV, kRoleItems, kRoleWiden, kRoles };
+
+// ------------------------------------------------------------------- items
+// Keys of a sequence that some row sees: lo .. and below pre, as pages np1, a gap,
+// the rest; `tiles` of 8 pages.
+struct SeqKeys {
+    int base, lo, pre, np1, gap, tiles;
+
+    __device__ __forceinline__ void set(const TreeArgs &p, int ctx, int n, int prefix)
+    {
+        base = ctx - n;
+        lo = p.window > 0 && base >= p.window ? base - p.window + 1 : 0;
+        pre = min(max(prefix, 0), base);
+        const int fp = lo / kPage;
+        np1 = min((pre + kPage - 1) / kPage, fp);
+        gap = fp - np1;
+        tiles = ((ctx + kPage - 1) / kPage - gap + kPagesPerTile - 1) / kPagesPerTile;
+    }
+};
+
+struct __align__(16) TreeItem {
+    int seq, kvh;
+    int tok, toks;              // first token (of the batch) and tokens of the item
+    int head, heads;            // first query head, heads
+    int row;                    // row of the first token in its sequence
+    int start, n;               // first token of the sequence, its tokens
+    int base, lo, pre;          // see SeqKeys
+    int np1, gap, visited;      // visited: pages up to the item's last token
+    int ta, nt;                 // tiles of keys: the first, how many; 0: no further item
+    int part;                   // -1: the whole item; else part 0 or 1 of the CTA
+    int unused[2];
+
+    __device__ __forceinline__ int real(int v) const { return v + (v >= np1 ? gap : 0); }
+};
+static_assert(sizeof(TreeItem) == 80, "an item is 80 bytes of shared memory");
+
+// ------------------------------------------------------------------ kernel
+// Registers: all threads are launched with 65536 / threads, rounded down to a
+// multiple of 8 (fp16: 168 for 384 threads; codes: 128 for 512, 96 for 640).  With
+// two groups their threads take what the others give back.
+template <int kKv, int kN>
+__device__ __forceinline__ void soft_registers()
+{
+    if constexpr (kKv == kKvF16 && kN == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if constexpr (kKv != kKvF16 && kN == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    if constexpr (kKv != kKvF16 && kN == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+}
+
+template <int kKv, int kN>
+__device__ __forceinline__ void issue_registers()
+{
+    if constexpr (kN == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if constexpr (kKv != kKvF16 && kN == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+}
+
+template <int kKv, int kN>
+__device__ __forceinline__ void widen_registers()
+{
+    if constexpr (kKv != kKvF16 && kN == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if constexpr (kKv != kKvF16 && kN == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+}
+
+// Barriers of a group of score warps alone.
+__device__ __forceinline__ void group_sync(int i)
+{
+    asm volatile("bar.sync %0, 128;" ::"r"(i + 1) : "memory");
+}
+
+__device__ __forceinline__ bool group_any(int i, bool x)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(x ? 1u : 0u), "r"(i + 1)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+                 "r"(v.w)
+                 : "memory");
+}
+
+__device__ __forceinline__ float log2_of(float x)
+{
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The largest of the warp's values (NaN aside).
+__device__ __forceinline__ float warp_max(float x)
+{
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Eight codes as fp16 values, exactly.
+template <int kKv>
+__device__ __forceinline__ uint4 widen(uint32_t a, uint32_t b)
+{
+    if constexpr (kKv == kKvI8) {
+        a ^= 0x80808080u;
+        b ^= 0x80808080u;
+        return make_uint4(ptx::i8pair_exact(a, 0x4140u), ptx::i8pair_exact(a, 0x4342u),
+                          ptx::i8pair_exact(b, 0x4140u), ptx::i8pair_exact(b, 0x4342u));
+    } else {
+        return make_uint4(ptx::e4m3x2_to_f16x2(a), ptx::e4m3x2_to_f16x2(a >> 16),
+                          ptx::e4m3x2_to_f16x2(b), ptx::e4m3x2_to_f16x2(b >> 16));
+    }
+}
+
+// tanh(u) of two values as u P(u^2), P of degree 4 for |u| <= 0.5 or of degree 6 for
+// |u| <= 1 (tanh_close, tanh_coef).
+template <int kDegree>
+__device__ __forceinline__ uint64_t tanh2(uint64_t u)
+{
+    auto coef = [](int k) { return kDegree == 4 ? tanh_close(k) : tanh_coef(k); };
+    const uint64_t w = ptx::mul2(u, u);
+    uint64_t q = ptx::f32x2(coef(kDegree), coef(kDegree));
+#pragma unroll
+    for (int k = kDegree - 1; k >= 0; --k) q = ptx::fma2(q, w, ptx::f32x2(coef(k), coef(k)));
+    return ptx::mul2(u, q);
+}
+
+// x <- tanh(x), by the largest |x| of the warp: the short polynomial (the usual case:
+// scores inside half the cap), the longer one, or the exponential for what lies
+// beyond the cap.
+template <int kC>
+__device__ __forceinline__ void tanh_all(float (&x)[kC])
+{
+    float top[2] = {0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < kC; c += 2)
+        top[c / 2 & 1] = fmaxf(fmaxf(top[c / 2 & 1], fabsf(x[c])), fabsf(x[c + 1]));
+    const float most = fmaxf(top[0], top[1]);
+    if (__all_sync(0xffffffffu, most <= 0.5f)) {
+#pragma unroll
+        for (int c = 0; c < kC; c += 2) {
+            const float2 y = ptx::f32x2_parts(tanh2<4>(ptx::f32x2(x[c], x[c + 1])));
+            x[c] = y.x;
+            x[c + 1] = y.y;
+        }
+    } else if (__all_sync(0xffffffffu, most <= 1.f)) {
+#pragma unroll
+        for (int c = 0; c < kC; c += 2) {
+            const float2 y = ptx::f32x2_parts(tanh2<6>(ptx::f32x2(x[c], x[c + 1])));
+            x[c] = y.x;
+            x[c + 1] = y.y;
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < kC; ++c) x[c] = cap_score(x[c], 1.f, 1.f);
+    }
+}
+
+// Sums of 32 columns over the lanes of the warp: afterwards v[0] of a lane is the
+// column of its number.
+__device__ __forceinline__ void lane_sums(float *v, int lane)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+    }
+}
+
+template <int kKv, int kD, int kN>
+__global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
+    tree_kernel(const __grid_constant__ TreeArgs p, const __grid_constant__ CUtensorMap tmq,
+                const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv)
+{
+    using M = TreeSmem<kKv, kD, kN>;
+    constexpr bool kCodes = M::kCodes;
+    constexpr int S = M::kStages;
+    constexpr int kGroups = tree_groups(kN), kSoftWarps = soft_warps(kN);
+    constexpr int kWidenWarps = widen_warps(kKv, kN);
+    constexpr int kC = kN / kGroups;    // rows of a group
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = ptx::smem_addr(smem);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+
+    auto full = [&](int s) { return base + M::kCtl + 8 * s; };
+    auto empty = [&](int s) { return base + M::kCtl + 8 * (S + s); };
+    [[maybe_unused]] auto cfull = [&](int s) { return base + M::kCtl + 8 * (2 * S + s); };
+    [[maybe_unused]] auto cempty = [&](int s) {
+        return base + M::kCtl + 8 * (2 * S + M::kCodeStages + s);
+    };
+    const uint32_t one = base + M::kCtl + 8 * (2 * S + 2 * M::kCodeStages);
+    const uint32_t q_full = one, q_empty = one + 8, drain = one + 16;
+    // of tile number g of the CTA and group i: scores there, probabilities there,
+    // product done
+    auto s_full = [&](uint32_t g) { return one + 24 + 8 * (g & 1); };
+    auto p_full = [&](int i, uint32_t g) { return one + 40 + 8 * (2 * i + (g & 1)); };
+    auto pv_done = [&](int i, uint32_t g) { return one + 72 + 8 * (2 * i + (g & 1)); };
+    auto i_full = [&](int k) { return one + 104 + 8 * (k & 1); };
+    auto i_empty = [&](int k) { return one + 120 + 8 * (k & 1); };
+    auto t_full = [&](int k) { return one + 136 + 8 * (k & 1); };   // the item's tree is there
+    volatile int *flags = reinterpret_cast<volatile int *>(smem + M::kFlags);
+    // flags: abort, bad block in item slot 0, in slot 1, TMEM address, bad tree in slots
+    const Waiter waiter{flags, p.dev_status};
+    // what was issued: K tiles, V tiles, items' queries
+    volatile int *issued = reinterpret_cast<volatile int *>(smem + M::kIssued);
+    auto item = [&](int k) -> TreeItem & {
+        return *reinterpret_cast<TreeItem *>(smem + M::kItems + sizeof(TreeItem) * (k & 1));
+    };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            ptx::mbar_init(full(s), kCodes ? kWidenWarps : 1);
+            ptx::mbar_init(empty(s), 1);
+        }
+        for (int s = 0; s < M::kCodeStages; ++s) {
+            ptx::mbar_init(cfull(s), 1);
+            ptx::mbar_init(cempty(s), kWidenWarps);
+        }
+        ptx::mbar_init(q_full, 1);
+        ptx::mbar_init(q_empty, 1);
+        ptx::mbar_init(drain, 1);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(s_full(i), 1);
+            for (int h = 0; h < 2; ++h) {
+                ptx::mbar_init(p_full(h, i), 4);
+                ptx::mbar_init(pv_done(h, i), 1);
+            }
+            ptx::mbar_init(i_full(i), 1);
+            ptx::mbar_init(t_full(i), 1);
+            ptx::mbar_init(i_empty(i), kSoftWarps + 3 + (kCodes ? kWidenWarps : 0));
+        }
+        ptx::fence_mbar_init();
+        flags[0] = flags[1] = flags[2] = 0;
+        issued[0] = issued[1] = issued[2] = 0;
+        ptx::prefetch_tmap(&tmq);
+        ptx::prefetch_tmap(&tmk);
+        ptx::prefetch_tmap(&tmv);
+    }
+    if (warp == kSoftWarps) umma::alloc(base + M::kFlags + 12, 512);
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+
+    // ------------------------------------------------ this CTA's piece of the line
+    const int side = blockIdx.x % p.sides, piece = blockIdx.x / p.sides;
+    int64_t *scan = reinterpret_cast<int64_t *>(smem + M::kScan);
+    // A sequence: its keys, and this side's items of it for a kv head's chunk of heads
+    // (tiles 1 where they only get zeros).
+    struct Seq {
+        SeqRows rows;
+        SeqKeys keys;
+        int items;
+        bool zeros;
+    };
+    auto sequence = [&](int s) -> Seq {
+        Seq q;
+        const int first = __ldg(p.query_starts + s), last = __ldg(p.query_starts + s + 1);
+        q.rows.set(first, last, __ldg(p.context_lens + s), p.num_tokens, p.ctx_cap);
+        q.zeros = first != last && (!q.rows.ok || q.rows.len > p.max_tree_len);
+        q.items = 0;
+        q.keys = SeqKeys{};
+        if (q.rows.len == 0) return q;
+        if (q.zeros) {
+            q.items = side == 0;
+            q.keys.tiles = 1;
+        } else {
+            const int all = (q.rows.len - 1) / p.tokens + 1;
+            q.items = all > side ? (all - 1 - side) / p.sides + 1 : 0;
+            q.keys.set(p, q.rows.ctx, q.rows.len, p.prefix_lens ? __ldg(p.prefix_lens + s) : 0);
+        }
+        return q;
+    };
+    auto tiles_of = [&](const Seq &q) -> int64_t {   // on the line
+        return static_cast<int64_t>(q.keys.tiles) * q.items * (p.num_kv_heads * p.chunks);
+    };
+    constexpr int kWarps = tree_threads(kKv, kN) / 32;
+    const int seg = (p.num_seqs + 32 * kWarps - 1) / (32 * kWarps);
+    int64_t own = 0, before = 0, begin = 0, end = 0, quo = 0, rem = 0;
+    // the whole line, and the i-th cut
+    auto cut = [&](int64_t i) { return quo * i + min(i, rem); };
+    // twice over the thread's sequences: their tiles, then who holds the piece's first
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        int64_t at = before;
+        if (pass == 0 || (begin < end && before <= begin && begin < before + own)) {
+            bool any = false;
+            const int s1 = min((static_cast<int>(threadIdx.x) + 1) * seg, p.num_seqs);
+#pragma unroll 1
+            for (int s = threadIdx.x * seg; s < s1; ++s) {
+                const Seq q = sequence(s);
+                const int64_t here = tiles_of(q);
+                any |= q.zeros;
+                if (pass == 0) {
+                    own += here;
+                } else if (begin < at + here) {
+                    scan[kWarps] = s;
+                    scan[kWarps + 1] = begin - at;
+                    break;
+                }
+                at += here;
+            }
+            if (pass == 0 && any && blockIdx.x == 0 && p.dev_status)
+                atomicOr(p.dev_status, static_cast<int32_t>(PKV_DEV_BAD_CTX));
+        }
+        if (pass == 0) {
+            int64_t sum = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            if (lane == 31) scan[warp] = sum;
+            __syncthreads();
+            int64_t total = 0;
+            before = sum - own;
+#pragma unroll 1
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) before += scan[w];
+                total += scan[w];
+            }
+            const int64_t most = total / kPieceTiles;
+            const int pieces = most < p.pieces ? max(static_cast<int>(most), 1) : p.pieces;
+            quo = total <= INT32_MAX ? static_cast<int>(total) / pieces : total / pieces;
+            rem = total - quo * pieces;
+            begin = piece < pieces ? cut(piece) : total;
+            end = piece < pieces ? cut(piece + 1) : total;
+        }
+    }
+    umma::fence_before();
+    __syncthreads();
+    umma::fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, static_cast<uint32_t>(flags[3]), 0);
+
+    auto t_s = [&](uint32_t g) { return tmem + kN * (g & 1); };   // S^T of tile g
+    const uint32_t t_o = tmem + 2 * kN;                           // O^T
+
+    if (warp < kSoftWarps) {
+        // ------------------------------------------------ scores and rows
+        soft_registers<kKv, kN>();
+        const Waiter wait = waiter.as(kRoleRows);
+        const int i = warp >> 2, quad = warp & 3;       // the group; its quarter of the keys
+        const int key = threadIdx.x & (kGroup - 1);     // the thread's key of a tile
+        const int c0 = i * kC;                          // the group's rows
+        const uint32_t lanes = static_cast<uint32_t>(quad) << 21;   // TMEM lane 32 quad
+        // the row that a thread looks after, if key < kC
+        const int t = c0 + key;
+        float *off = reinterpret_cast<float *>(smem + M::kOff);   // kLift - reference
+        float *ref = reinterpret_cast<float *>(smem + M::kMax);
+        float *fac = reinterpret_cast<float *>(smem + M::kFac);
+        float *slp = reinterpret_cast<float *>(smem + M::kSlope);
+        int64_t *place = reinterpret_cast<int64_t *>(smem + M::kAt);
+        float *sums = reinterpret_cast<float *>(smem + M::kSums);
+        uint32_t *mask = reinterpret_cast<uint32_t *>(smem + M::kMask);
+        auto four = [](const float *v, int c) { return *reinterpret_cast<const float4 *>(v + c); };
+        uint32_t g = 0;        // tiles of keys of the CTA so far
+        bool fail = false;     // of this warp's waits; a group leaves together, at a barrier
+        for (int k = 0;; ++k) {
+            fail |= !wait(i_full(k), k >> 1 & 1);
+            const TreeItem &it = item(k);
+            const int nt = it.nt, n = it.n, ctx = it.base, pre = it.pre, np1 = it.np1, gap = it.gap;
+            auto real = [&](int v) { return v + (v >= np1 ? gap : 0); };
+            const int rj = t / p.chunk, rh = t - rj * p.chunk;   // token and head of row t
+            const bool mine = key < kC && rj < it.toks && rh < it.heads;
+            if (key < kC && nt > 0) {
+                // rows that are not the item's: a reference that nothing exceeds
+                off[t] = mine ? kLift - kNone : -INFINITY;
+                ref[t] = kNone;
+                place[t] = mine ? static_cast<int64_t>(it.tok + rj) * p.num_heads + it.head + rh
+                                : int64_t(-1);
+                if (p.slopes)
+                    slp[t] = mine && !fail ? __ldg(p.slopes + it.head + rh) * 1.4426950408889634f
+                                           : 0.f;
+            }
+            fail |= !wait(t_full(k), k >> 1 & 1);
+            if (group_any(i, fail)) break;
+            if (nt == 0) break;
+            const bool bad_tree = flags[4 + (k & 1)] != 0;
+            const int *up = reinterpret_cast<const int *>(smem + M::kUp) + kParents * (k & 1);
+            const int32_t *par = p.parents + it.start;
+            auto parent = [&](int j) { return j < kParents ? up[j] : __ldg(par + j); };
+            const int node = mine && !bad_tree ? it.row + rj : -1;
+            int lo = 0;
+            if (p.window > 0) {
+                int pos = ctx;
+                if (node >= 0)
+                    for (int j = parent(node); j >= 0; j = parent(j)) ++pos;
+                lo = max(pos - p.window + 1, 0);
+            }
+            uint64_t l[kC / 2];   // the thread's share of the rows' sums
+#pragma unroll
+            for (int c = 0; c < kC / 2; ++c) l[c] = 0;
+            bool left = false;
+            for (int j = 0; j < nt; ++j, ++g) {
+                const int v0 = (it.ta + j) * kPagesPerTile;
+                const int t0 = real(v0) * kPage;
+                const int t1 = real(v0 + kPagesPerTile - 1) * kPage + kPage - 1;
+                // whether all rows see all keys
+                const bool clean =
+                    (t1 < ctx && (p.window <= 0 || ctx + n - 1 - t0 < p.window)) || t1 < pre;
+                const int at = real(v0 + (key >> 4)) * kPage + (key & 15);   // the key's slot
+                if (!clean) {
+                    // bits of the keys that row t sees
+                    if (key < kC) {
+                        uint32_t w[4] = {0, 0, 0, 0};
+                        if (mine) {
+#pragma unroll
+                            for (int q = 0; q < kPagesPerTile; ++q) {
+                                const int k0 = real(v0 + q) * kPage;
+                                const uint32_t seen =
+                                    (below(ctx - k0) & ~below(lo - k0)) | below(pre - k0);
+                                w[q >> 1] |= seen << (q & 1) * 16;
+                            }
+                            if (t1 >= ctx)
+                                for (int a = node, far = 0;
+                                     a >= 0 && (p.window <= 0 || far < p.window);
+                                     a = parent(a), ++far) {
+                                    const int e = ((ctx + a) >> 4 << 4) - (gap + v0) * kPage +
+                                                  ((ctx + a) & 15);   // (behind the gap)
+                                    if (e < 0) break;
+                                    const uint32_t bit = 1u << (e & 31);
+                                    if (e < 32) w[0] |= bit;
+                                    else if (e < 64) w[1] |= bit;
+                                    else if (e < 96) w[2] |= bit;
+                                    else if (e < kTile) w[3] |= bit;
+                                }
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) mask[q * kN + t] = w[q];
+                    }
+                    group_sync(i);
+                }
+                fail |= !wait(s_full(g), g >> 1 & 1);
+                umma::fence_after();
+                float x[kC];
+#pragma unroll
+                for (int c = 0; c < kC; c += 32) umma::ld32(t_s(g) + lanes + c0 + c, x + c);
+                // (meanwhile: the probabilities' buffer was read by the product before)
+                const uint32_t was = g - M::kPBufs;
+                if (g >= M::kPBufs) fail |= !wait(pv_done(i, was), was >> 1 & 1);
+                // what a product is multiplied with, log2 of the page's V scale, and
+                // the scale's reciprocal
+                float f = p.scale_log2;
+                [[maybe_unused]] float lv = 0.f, rv = 1.f;
+                if constexpr (kCodes) {
+                    const float *sc = reinterpret_cast<const float *>(smem + M::kScales) +
+                                      (g & (M::kScaleTiles - 1)) * 2 * kPagesPerTile + (key >> 4);
+                    const float vs = sc[kPagesPerTile], vc = fmaxf(vs, kLeastV);
+                    f *= sc[0];
+                    lv = vs >= 0.f && vs < INFINITY ? log2_of(vc) : NAN;
+                    rv = __frcp_rn(vc);
+                }
+                umma::wait_ld();
+                const uint32_t *words = mask + quad * kN + c0;
+                auto scale_all = [&](float by, float add) {
+                    const uint64_t b2 = ptx::f32x2(by, by), a2 = ptx::f32x2(add, add);
+#pragma unroll
+                    for (int c = 0; c < kC; c += 2) {
+                        const float2 y =
+                            ptx::f32x2_parts(ptx::fma2(ptx::f32x2(x[c], x[c + 1]), b2, a2));
+                        x[c] = y.x;
+                        x[c + 1] = y.y;
+                    }
+                };
+                // x of the keys that a row does not see
+                auto hide = [&](float value) {
+#pragma unroll
+                    for (int c = 0; c < kC; c += 4) {
+                        const uint4 w = *reinterpret_cast<const uint4 *>(words + c);
+                        if (!(w.x >> lane & 1u)) x[c] = value;
+                        if (!(w.y >> lane & 1u)) x[c + 1] = value;
+                        if (!(w.z >> lane & 1u)) x[c + 2] = value;
+                        if (!(w.w >> lane & 1u)) x[c + 3] = value;
+                    }
+                };
+                if (p.cap > 0.f) {
+                    scale_all(f * p.cap_inv, 0.f);
+                    f = p.cap;
+                    // (unseen keys and other rows have no say in how it is evaluated)
+                    if (!clean) hide(0.f);
+#pragma unroll
+                    for (int c = 0; c < kC; c += 4) {
+                        const float4 o = four(off, c0 + c);
+                        if (o.x == -INFINITY) x[c] = 0.f;
+                        if (o.y == -INFINITY) x[c + 1] = 0.f;
+                        if (o.z == -INFINITY) x[c + 2] = 0.f;
+                        if (o.w == -INFINITY) x[c + 3] = 0.f;
+                    }
+                    tanh_all(x);
+                }
+                if (kCodes || p.slopes || !clean) {
+                    scale_all(f, lv);
+                    f = 1.f;
+                }
+                if (p.slopes) {
+                    // slope (p(t) - ctx): what a row's own position adds is the same for
+                    // all of its keys, and the softmax does not see it
+                    int far = at - ctx;
+                    if (far >= 0 && !bad_tree) {
+                        int b = far < n ? parent(far) : -1;
+                        for (far = 0; b >= 0; b = parent(b)) ++far;
+                    }
+                    const float d = static_cast<float>(far);
+#pragma unroll
+                    for (int c = 0; c < kC; c += 4) {
+                        const float4 s = four(slp, c0 + c);
+                        x[c] = fmaf(s.x, d, x[c]);
+                        x[c + 1] = fmaf(s.y, d, x[c + 1]);
+                        x[c + 2] = fmaf(s.z, d, x[c + 2]);
+                        x[c + 3] = fmaf(s.w, d, x[c + 3]);
+                    }
+                }
+                if (!clean) hide(-INFINITY);
+                const uint64_t f2 = ptx::f32x2(f, f);
+                // x f - reference + kLift of rows c and c + 1
+                auto exponents = [&](int c, float a, float b) {
+                    return ptx::f32x2_parts(
+                        ptx::fma2(ptx::f32x2(x[c], x[c + 1]), f2, ptx::f32x2(a, b)));
+                };
+                if (!clean) {
+                    // V rows of keys that no row of the tree sees may hold anything, NaN
+                    // included (and are not loaded for pages past the item's last):
+                    // zeros.  The product waits for this; the other group writes the same.
+                    const bool dead = v0 + (key >> 4) >= it.visited || at >= ctx + n ||
+                                      (at < it.lo && at >= pre);
+                    if (__any_sync(0xffffffffu, dead)) {
+                        // (the stage's element before this one must have landed: it is K
+                        // of a tile before, or V of one whose product is done)
+                        if (S == 2 && g > 0) fail |= !wait(pv_done(i, g - 1), (g - 1) >> 1 & 1);
+                        static_assert(S % 2 ? S >= 3 : S == 2 || S / 2 >= M::kPBufs,
+                                      "phase of the stage");
+                        const uint32_t e = 2 * g + 1;
+                        fail |= !wait(full(e % S), (e / S) & 1);
+                        const uint32_t row =
+                            base + M::kRing + (e % S) * M::kTileBytes + key * 128;
+                        if (dead)
+#pragma unroll
+                            for (int b = 0; b < kD / 8; ++b)
+                                st_shared16(row + (b >> 3) * M::kHalfBytes + (b & 7) * 16,
+                                            make_uint4(0, 0, 0, 0));
+                    }
+                }
+                const uint32_t to = base + M::kP + (g % M::kPBufs) * M::kPBytes +
+                                    c0 / 8 * (16 * kTile) + key * 16;
+                [[maybe_unused]] const uint64_t rv2 = ptx::f32x2(rv, rv);
+                // The probabilities, by the references as they are.  Should one exceed its
+                // reference by too much, what they added to the sums is taken off again,
+                // the references follow, and they are worked out once more.
+#pragma unroll 1
+                for (int pass = 0;; ++pass) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < kC; c += 8) {
+                        uint32_t pk[4];
+#pragma unroll
+                        for (int e = 0; e < 8; e += 4) {
+                            const float4 o = four(off, c0 + c + e);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int r = c + e + 2 * h;
+                                const float2 z =
+                                    h == 0 ? exponents(r, o.x, o.y) : exponents(r, o.z, o.w);
+                                top = fmaxf(fmaxf(top, z.x), z.y);
+                                const float2 y = make_float2(ptx::ex2(z.x), ptx::ex2(z.y));
+                                const uint64_t y2 = ptx::f32x2(y.x, y.y);
+                                l[r / 2] = kCodes ? ptx::fma2(y2, rv2, l[r / 2])
+                                                  : ptx::add2(l[r / 2], y2);
+                                pk[e / 2 + h] = pack2(y.x, y.y);
+                            }
+                        }
+                        st_shared16(to + c / 8 * (16 * kTile),
+                                    make_uint4(pk[0], pk[1], pk[2], pk[3]));
+                    }
+                    if (!group_any(i, fail || (pass == 0 && top > kLift + kLazy))) break;
+                    if (group_any(i, fail)) {
+                        left = true;
+                        break;
+                    }
+                    if (j == 0) {
+#pragma unroll
+                        for (int c = 0; c < kC / 2; ++c) l[c] = 0;
+                    } else {
+                        // (beyond 2^100 the sums so far will be nothing; else the reference
+                        // grows by 2^kLazy at least, and with it the rounding of a sum that
+                        // held too much goes below the sum's own)
+#pragma unroll
+                        for (int c = 0; c < kC; c += 2) {
+                            const float2 z = exponents(c, off[c0 + c], off[c0 + c + 1]);
+                            float2 y = ptx::f32x2_parts(l[c / 2]);
+                            y.x = z.x > 100.f ? 0.f : fmaf(-ptx::ex2(z.x), rv, y.x);
+                            y.y = z.y > 100.f ? 0.f : fmaf(-ptx::ex2(z.y), rv, y.y);
+                            l[c / 2] = ptx::f32x2(y.x, y.y);
+                        }
+                    }
+                    // the rows' maxima over the tile
+                    float fm = f;
+                    asm volatile("" : "+f"(fm));   // (products not kept from pass to pass)
+#pragma unroll
+                    for (int c = 0; c < kC; c += 4) {
+                        const float4 m =
+                            make_float4(warp_max(x[c] * fm), warp_max(x[c + 1] * fm),
+                                        warp_max(x[c + 2] * fm), warp_max(x[c + 3] * fm));
+                        if (lane == 0) *reinterpret_cast<float4 *>(sums + quad * kN + c0 + c) = m;
+                    }
+                    group_sync(i);
+                    if (key < kC) {
+                        float m = ref[t];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) m = fmaxf(m, sums[q * kN + t]);
+                        fac[t] = ptx::ex2(ref[t] - m);
+                        ref[t] = m;
+                        if (mine) off[t] = kLift - m;
+                    }
+                    group_sync(i);
+                    if (j > 0) {
+#pragma unroll
+                        for (int c = 0; c < kC; c += 4) {
+                            const float4 y = four(fac, c0 + c);
+                            l[c / 2] = ptx::mul2(l[c / 2], ptx::f32x2(y.x, y.y));
+                            l[c / 2 + 1] = ptx::mul2(l[c / 2 + 1], ptx::f32x2(y.z, y.w));
+                        }
+                        fail |= !wait(pv_done(i, g - 1), (g - 1) >> 1 & 1);
+                        umma::fence_after();
+#pragma unroll 1
+                        for (int c = c0; c < c0 + kC; c += 16) {
+                            float o[16];
+                            umma::ld16(t_o + lanes + c, o);
+                            umma::wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= fac[c + e];
+                            umma::st16(t_o + lanes + c, reinterpret_cast<const uint32_t *>(o));
+                        }
+                        umma::wait_st();
+                    }
+                }
+                if (left) break;
+                ptx::fence_proxy_async_smem();
+                umma::fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(p_full(i, g));
+            }
+            if (left) break;
+            // the rows' sums, the quarters of the keys in their order
+            fail |= !wait(pv_done(i, g - 1), (g - 1) >> 1 & 1);
+            umma::fence_after();
+#pragma unroll
+            for (int c = 0; c < kC; c += 32) {
+                float v[32];
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const float2 y = ptx::f32x2_parts(l[(c + e) / 2]);
+                    v[e] = y.x;
+                    v[e + 1] = y.y;
+                }
+                lane_sums(v, lane);
+                sums[quad * kN + c0 + c + lane] = v[0];
+            }
+            if (group_any(i, fail)) break;
+            const bool bad = bad_tree || flags[1 + (k & 1)] != 0;
+            const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + max(it.part, 0);
+            if (key < kC) {
+                const float a = sums[t] + sums[kN + t] + sums[2 * kN + t] + sums[3 * kN + t];
+                fac[t] = a > 0.f ? 1.f / a : a;   // a row that saw nothing: zeros; NaN stays
+                if (it.part >= 0) p.part_ml[slot * kN + t] = make_float2(ref[t], bad ? -1.f : a);
+            }
+            group_sync(i);
+            const int dim = kD == 128 ? key : 16 * quad + lane;   // M = 64 has 16 of 32 lanes
+            const bool has = kD == 128 || lane < 16, odd = lane & 1;
+#pragma unroll 1
+            for (int c = c0; c < c0 + kC; c += 16) {
+                float o[16];
+                umma::ld16(t_o + lanes + c, o);
+                umma::wait_ld();
+                if (it.part < 0) {
+                    // two neighbouring values of a row to a lane: even lanes store row e,
+                    // odd ones row e + 1
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        const float a = bad ? 0.f : o[e] * fac[c + e];
+                        const float b = bad ? 0.f : o[e + 1] * fac[c + e + 1];
+                        const float y = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+                        const int64_t row = place[c + e + odd];
+                        if (row >= 0 && has)
+                            *reinterpret_cast<uint32_t *>(p.out + row * kD + (dim & ~1)) =
+                                odd ? pack2(y, b) : pack2(a, y);
+                    }
+                } else if (has) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (place[c + e] >= 0) p.part_acc[(slot * kN + c + e) * kD + dim] = o[e];
+                }
+            }
+            // (the next item's first product into O waits for its probabilities,
+            // which come after this)
+            umma::fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(i_empty(k));
+        }
+    } else if (warp < kSoftWarps + 4) {
+        issue_registers<kKv, kN>();
+        if (warp == kSoftWarps) {
+            // ------------------------------------------------ products
+            const Waiter wait = waiter.as(kRoleProducts);
+            if (umma::elect_one()) {
+                constexpr uint32_t kQk = umma::f16_idesc(kTile, kN, false);
+                constexpr uint32_t kPv = umma::f16_idesc(kD, kC, true) | umma::kAMn;
+                const uint32_t q_lo = umma::desc_lo(base, 16);
+                const uint32_t k_lo = umma::desc_lo(base + M::kRing, 16);
+                const uint32_t v_lo = umma::desc_lo(base + M::kRing, M::kHalfBytes);
+                const uint64_t p_at = umma::desc_plain(base + M::kP, 16 * kTile);
+                auto qk = [&](uint32_t g) -> bool {   // S^T = K Q^T
+                    const uint32_t n = 2 * g, s = n % S;
+                    if (!wait.one(full(s), (n / S) & 1)) return false;
+                    umma::fence_after();
+                    const uint32_t a = k_lo + s * (M::kTileBytes >> 4);
+#pragma unroll
+                    for (int k = 0; k < kD / 16; ++k)
+                        umma::mma_ss(
+                            t_s(g),
+                            umma::desc(a + (((k >> 2) * M::kHalfBytes + (k & 3) * 32) >> 4)),
+                            umma::desc(q_lo + (((k >> 2) * M::kQHalfBytes + (k & 3) * 32) >> 4)),
+                            kQk, k > 0);
+                    umma::commit(s_full(g));
+                    umma::commit(empty(s));
+                    return true;
+                };
+                uint32_t g = 0;
+                bool ok = true;
+                for (int k = 0; ok; ++k) {
+                    ok = wait.one(i_full(k), k >> 1 & 1);
+                    if (!ok) break;
+                    const int nt = item(k).nt;
+                    if (nt == 0) break;
+                    ok = wait.one(q_full, k & 1) && qk(g);
+                    if (!ok) break;
+                    if (nt == 1) umma::commit(q_empty);
+                    for (int j = 0; j < nt; ++j, ++g) {
+                        if (j + 1 < nt) {
+                            ok = qk(g + 1);
+                            if (!ok) break;
+                            if (j + 2 == nt) umma::commit(q_empty);
+                        }
+                        const uint32_t n = 2 * g + 1, s = n % S;
+                        ok = wait.one(full(s), (n / S) & 1);
+                        const uint32_t a = v_lo + s * (M::kTileBytes >> 4);
+                        for (int i = 0; i < kGroups && ok; ++i) {
+                            ok = wait.one(p_full(i, g), g >> 1 & 1);
+                            if (!ok) break;
+                            umma::fence_after();
+                            const uint64_t b =
+                                p_at + ((g % M::kPBufs * M::kPBytes + i * (kC * 2 * kTile)) >> 4);
+#pragma unroll
+                            for (int k2 = 0; k2 < kTile / 16; ++k2)   // O^T += V^T P^T
+                                umma::mma_ss(t_o + i * kC, umma::desc(a + k2 * (2048 >> 4)),
+                                             b + k2 * (256 >> 4), kPv, j > 0 || k2 > 0);
+                            umma::commit(pv_done(i, g));
+                        }
+                        if (!ok) break;
+                        umma::commit(empty(s));
+                    }
+                    if (ok) ptx::mbar_arrive(i_empty(k));
+                }
+                // nothing of this thread's is in flight after this
+                umma::commit(drain);
+                ptx::mbar_wait_bounded(drain, 0, kWaitLimitNs);
+            }
+            __syncwarp();
+        } else if (warp == kSoftWarps + 1 || warp == kSoftWarps + 3) {
+            // ------------------------------------------------ loads of Q and the pages
+            // A lane per page looks its block up; one thread issues the copies, 2 KB
+            // of a page each.
+            constexpr int R = kCodes ? M::kCodeStages : S;
+            constexpr int kBox = kCodes ? kD : 64;                       // values per box
+            constexpr int kBoxes = kCodes ? 1 : M::kHalves;
+            constexpr int kBoxBytes = kPage * kBox * (kCodes ? 1 : 2);
+            constexpr int kStageBytes = kCodes ? M::kCodeBytes : M::kTileBytes;
+            const uint32_t ring = base + (kCodes ? M::kCodeRing : M::kRing);
+            const bool is_v = warp == kSoftWarps + 3;
+            const Waiter wait = waiter.as(is_v ? kRoleLoadV : kRoleLoadK);
+            const void *tm = is_v ? static_cast<const void *>(&tmv) : &tmk;
+            uint32_t tiles = 0;   // tiles of keys so far: ring elements 2 tiles (+ 1)
+            int queries = 0;      // items whose queries were asked for
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                ok = wait(i_full(k), k >> 1 & 1);
+                if (!ok) break;
+                const TreeItem &it = item(k);
+                const int nt = it.nt;
+                if (nt == 0) break;
+                const int32_t *table =
+                    p.block_tables + static_cast<int64_t>(it.seq) * p.max_blocks_per_seq;
+                auto lookup = [&](int j) -> int32_t {  // block of the lane's page, -2: none
+                    const int v = (it.ta + j) * kPagesPerTile + lane;
+                    if (lane >= kPagesPerTile || v >= it.visited) return -2;
+                    const int32_t b = __ldg(table + it.real(v));
+                    return b >= 0 && b < p.num_blocks ? b : -1;
+                };
+                int32_t blk = lookup(0);
+                for (int j = 0; j < nt; ++j) {
+                    const uint32_t n = 2 * tiles + (is_v ? 1 : 0);
+                    const int s = n % R;
+                    const bool have = blk >= 0;
+                    if (blk == -1) {
+                        flags[1 + (k & 1)] = 1;
+                        if (p.dev_status)
+                            atomicOr(p.dev_status, static_cast<int32_t>(PKV_DEV_BAD_BLOCK));
+                    }
+                    [[maybe_unused]] float k_scale = 0.f, v_scale = 0.f;
+                    if constexpr (kCodes)
+                        if (have && !is_v) {
+                            const int64_t at = static_cast<int64_t>(blk) * p.num_kv_heads + it.kvh;
+                            k_scale = __ldg(p.k_scales + at);
+                            v_scale = __ldg(p.v_scales + at);
+                        }
+                    const int row = (blk * p.num_kv_heads + it.kvh) * kPage;
+                    const unsigned pages = __ballot_sync(0xffffffffu, have);
+                    const uint32_t fb = kCodes ? cfull(s) : full(s);
+                    const uint32_t eb = kCodes ? cempty(s) : empty(s);
+                    if (j + 1 < nt) blk = lookup(j + 1);
+                    ok = wait(eb, ((n / R) & 1) ^ 1);
+                    if (!ok) break;
+                    if constexpr (kCodes)
+                        if (!is_v && lane < kPagesPerTile) {
+                            float *to = reinterpret_cast<float *>(smem + M::kScales) +
+                                        (tiles & (M::kScaleTiles - 1)) * 2 * kPagesPerTile + lane;
+                            to[0] = k_scale;
+                            to[kPagesPerTile] = v_scale;
+                        }
+                    __syncwarp();  // (the arrival is behind the flag and the scales)
+                    if (umma::elect_one())
+                        ptx::mbar_arrive_expect_tx(fb, __popc(pages) * kBoxes * kBoxBytes);
+                    __syncwarp();
+                    const uint32_t dst = ring + s * kStageBytes;
+#pragma unroll
+                    for (int q = 0; q < kPagesPerTile; ++q) {
+                        const int y = __shfl_sync(0xffffffffu, row, q);
+                        if ((pages >> q & 1u) && umma::elect_one()) {
+#pragma unroll
+                            for (int b = 0; b < kBoxes; ++b)
+                                ptx::tma_load_2d(dst + b * M::kHalfBytes + q * kBoxBytes, tm,
+                                                 b * kBox, y, fb);
+                        }
+                    }
+                    __syncwarp();
+                    ++tiles;
+                    if (!is_v && j == 0) {
+                        // the queries: tokens x heads x 64 values, which land as the item's
+                        // rows in their order (rows of heads that are not the item's, or
+                        // behind the batch, do not count)
+                        ok = wait(q_empty, (k & 1) ^ 1);
+                        if (!ok) break;
+                        if (umma::elect_one()) {
+                            ptx::mbar_arrive_expect_tx(q_full, p.tokens * p.chunk * M::kHalves * 128);
+    #pragma unroll
+                            for (int b = 0; b < M::kHalves; ++b)
+                                ptx::tma_load_3d(base + b * M::kQHalfBytes, &tmq, b * 64, it.head,
+                                                 it.tok, q_full);
+                        }
+                        __syncwarp();
+                        ++queries;
+                    }
+                }
+                __syncwarp();
+                if (ok && lane == 0) ptx::mbar_arrive(i_empty(k));
+            }
+            // what was issued, for the drain behind a wait that ran out
+            if (lane == 0) {
+                issued[is_v] = static_cast<int>(tiles);
+                if (!is_v) issued[2] = queries;
+            }
+        } else {
+            // ------------------------------------------------ the items of the piece
+            const Waiter wait = waiter.as(kRoleItems);
+            TreeMeta tail = {};
+            bool ok = true;
+            int k = 0;
+            int64_t at = begin;
+            int seq = 0;
+            int64_t rest = 0;   // tiles of the sequence before `at`
+            if (begin < end) {
+                seq = static_cast<int>(scan[kWarps]);
+                rest = scan[kWarps + 1];
+            }
+            for (; at < end && ok; ++seq, rest = 0) {
+                const Seq q = sequence(seq);
+                const int tiles = q.keys.tiles;
+                const int items = q.items * p.num_kv_heads * p.chunks;
+                TreeItem it;
+                it.seq = seq;
+                it.start = q.rows.start;
+                it.n = q.rows.len;
+                it.base = q.keys.base;
+                it.lo = q.keys.lo;
+                it.pre = q.keys.pre;
+                it.np1 = q.keys.np1;
+                it.gap = q.keys.gap;
+                // kv heads, chunks of heads, the side's rows of the tree
+                for (int i = rest > 0 ? static_cast<int>(rest / tiles) : 0; i < items && at < end && ok;
+                     ++i) {
+                    it.ta = static_cast<int>(rest - static_cast<int64_t>(i) * tiles);
+                    it.nt = static_cast<int>(min(static_cast<int64_t>(tiles - it.ta), end - at));
+                    const int64_t stop = at + (tiles - it.ta);   // the item's end on the line
+                    it.part = it.ta > 0 ? 0 : it.nt < tiles ? 1 : -1;
+                    const int hc = i / q.items;
+                    it.kvh = hc / p.chunks;
+                    const int c = hc - it.kvh * p.chunks;
+                    it.head = it.kvh * p.group + c * p.chunk;
+                    it.heads = min(p.chunk, p.group - c * p.chunk);
+                    it.row = ((i - hc * q.items) * p.sides + side) * p.tokens;
+                    it.tok = it.start + it.row;
+                    it.toks = min(p.tokens, it.n - it.row);
+                    it.visited = (it.base + it.row + it.toks - 1) / kPage + 1 - it.gap;
+                    at += it.nt;
+                    rest += it.nt;
+                    if (q.zeros) {
+                        // (all of the sequence's rows)
+                        for (int64_t e = lane;
+                             e < static_cast<int64_t>(it.n) * it.heads * (kD / 8); e += 32) {
+                            const int64_t r = e / (kD / 8);
+                            const int64_t tk = it.start + r / it.heads;
+                            if (tk < 0 || tk >= p.num_tokens) continue;
+                            const int64_t row = tk * p.num_heads + it.head + r % it.heads;
+                            reinterpret_cast<uint4 *>(p.out + row * kD)[e % (kD / 8)] =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        continue;
+                    }
+                    if (it.part == 1) {
+                        // pieces that the rest of the item lies in
+                        int last = piece + 1;
+                        while (cut(last + 1) < stop) ++last;
+                        tail.tok = it.tok;
+                        tail.toks = it.toks;
+                        tail.head = it.head;
+                        tail.heads = it.heads;
+                        tail.parts = last - piece + 1;
+                    }
+                    ok = wait(i_empty(k), (k >> 1 & 1) ^ 1);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        item(k) = it;
+                        flags[1 + (k & 1)] = 0;
+                        ptx::mbar_arrive(i_full(k));
+                    }
+                    // its tree: every parent an earlier row
+                    int *up = reinterpret_cast<int *>(smem + M::kUp) + kParents * (k & 1);
+                    bool wrong = false;
+                    for (int j = lane; j < it.n; j += 32) {
+                        const int a = __ldg(p.parents + it.start + j);
+                        wrong |= a < -1 || a >= j;
+                        if (j < kParents) up[j] = a;
+                    }
+                    wrong = __any_sync(0xffffffffu, wrong);
+                    if (lane == 0) {
+                        flags[4 + (k & 1)] = wrong;
+                        if (wrong && p.dev_status)
+                            atomicOr(p.dev_status, static_cast<int32_t>(PKV_DEV_BAD_TREE));
+                    }
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(t_full(k));
+                    ++k;
+                }
+            }
+            if (lane == 0) p.meta[blockIdx.x] = tail;
+            if (ok) ok = wait(i_empty(k), (k >> 1 & 1) ^ 1);
+            if (ok && lane == 0) {
+                item(k).nt = 0;
+                ptx::mbar_arrive(i_full(k));
+                ptx::mbar_arrive(t_full(k));
+            }
+            __syncwarp();
+        }
+    } else {
+        if constexpr (kCodes) {
+            // ------------------------------------------------ codes to fp16
+            widen_registers<kKv, kN>();
+            const Waiter wait = waiter.as(kRoleWiden);
+            constexpr int R = M::kCodeStages;
+            constexpr int kCh = kD / 16;  // 16-byte chunks of codes per key
+            constexpr int kStep = 32 * kWidenWarps / kCh;
+            constexpr int kLoads = kTile / kStep;
+            const int tid = threadIdx.x - 32 * (kSoftWarps + 4);
+            // Eight lanes take four chunks of two rows: r and r ^ 5 of eight at head_dim
+            // 128, r and r + 1 at 64, whose swizzles put the loads and both stores on
+            // different banks.
+            static_assert(kTile % kStep == 0 && kStep % 8 == 0, "whole groups of eight rows");
+            int ch = tid % kCh, row0 = tid / kCh;
+            if constexpr (kD == 128) {
+                // bits of tid: chunk 0-1, row of the pair 2, half 3, pair 4-5, rows by eight
+                ch = (tid & 3) | (tid >> 1 & 4);
+                row0 = ((tid >> 4 & 3) ^ (tid & 4 ? 5 : 0)) | (tid >> 6) << 3;
+            }
+            uint32_t n = 0;
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                ok = wait(i_full(k), k >> 1 & 1);
+                if (!ok) break;
+                const int nt = item(k).nt;
+                if (nt == 0) break;
+                for (int j = 0; j < 2 * nt; ++j, ++n) {
+                    ok = wait(cfull(n % R), (n / R) & 1) && wait(empty(n % S), ((n / S) & 1) ^ 1);
+                    if (!ok) break;
+                    const uint32_t src = base + M::kCodeRing + (n % R) * M::kCodeBytes;
+                    const uint32_t dst = base + M::kRing + (n % S) * M::kTileBytes;
+                    // all loads first; rows advance by whole groups of eight, so the
+                    // swizzles stay
+                    const uint32_t sx = kD == 128 ? (ch ^ (row0 & 7)) : (ch ^ ((row0 >> 1) & 3));
+                    const uint32_t from = src + row0 * kD + (sx << 4);
+                    const uint32_t to = dst + (ch >> 2) * M::kHalfBytes + row0 * 128;
+                    const int c_a = ((2 * ch) & 7) ^ (row0 & 7);
+                    uint4 w[kLoads];
+#pragma unroll
+                    for (int e = 0; e < kLoads; ++e) w[e] = ptx::lds128(from + e * kStep * kD);
+#pragma unroll
+                    for (int e = 0; e < kLoads; ++e) {
+                        st_shared16(to + e * kStep * 128 + (c_a << 4), widen<kKv>(w[e].x, w[e].y));
+                        st_shared16(to + e * kStep * 128 + ((c_a ^ 1) << 4),
+                                    widen<kKv>(w[e].z, w[e].w));
+                    }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        ptx::mbar_arrive(full(n % S));
+                        ptx::mbar_arrive(cempty(n % R));
+                    }
+                }
+                __syncwarp();
+                if (ok && lane == 0) ptx::mbar_arrive(i_empty(k));
+            }
+        }
+    }
+    __syncthreads();
+    if (flags[0]) {  // a wait ran out (the same for all: nobody waits any more)
+        if (warp == kSoftWarps + 1)
+            drain_copies<kCodes ? M::kCodeStages : S>(kCodes ? cfull(0) : full(0), q_full,
+                                                      issued[0], issued[1], issued[2]);
+        __syncthreads();
+    }
+    if (warp == kSoftWarps) umma::dealloc(tmem, 512);
+}
+
+// Joins the parts of the items that the cuts went through, a warp a row.
+//   out = sum_z 2^(m_z - M) acc_z / sum_z 2^(m_z - M) l_z,  M = max_z m_z
+// A part with l < 0 (a bad block or tree) makes the row zeros.
+constexpr int kJoinWarps = 8;
+
+template <int kD, int kN>
+__global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid_constant__ TreeArgs p)
+{
+    constexpr int kC = kD / 32, kPer = (kSms + 31) / 32;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int owner = blockIdx.x / (kN / kJoinWarps);
+    const int r = blockIdx.x % (kN / kJoinWarps) * kJoinWarps + warp;
+    const TreeMeta meta = p.meta[owner];
+    const int rj = r / p.chunk, rh = r - rj * p.chunk;
+    if (meta.parts <= 0 || rj >= meta.toks || rh >= meta.heads) return;
+    // part 0 is the owner's last one, the others are the first of the pieces behind
+    auto at = [&](int z) -> int64_t {
+        return (2 * (static_cast<int64_t>(owner) + static_cast<int64_t>(z) * p.sides) + (z == 0)) *
+                   kN + r;
+    };
+    float pm[kPer], pl[kPer], m = kNone;
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+        const int z = lane + 32 * e;
+        const float2 ml = z < meta.parts ? __ldcg(p.part_ml + at(z)) : make_float2(kNone, 0.f);
+        pm[e] = ml.x;
+        pl[e] = ml.y;
+        m = fmaxf(m, ml.x);
+        bad |= ml.y < 0.f;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    bad = __any_sync(0xffffffffu, bad);
+    float l = 0.f, acc[kC];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+        pm[e] = ptx::ex2(pm[e] - m);
+        l += pm[e] * pl[e];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll
+    for (int c = 0; c < kC; ++c) acc[c] = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e)
+#pragma unroll 1
+        for (int z0 = 32 * e; z0 < meta.parts && z0 < 32 * e + 32; z0 += 8) {
+            float v[8][kC];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+#pragma unroll
+                for (int c = 0; c < kC; ++c) {
+                    const int z = z0 + u;
+                    v[u][c] = z < meta.parts ? __ldcg(p.part_acc + at(z) * kD + 32 * c + lane) : 0.f;
+                }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float f = __shfl_sync(0xffffffffu, pm[e], (z0 + u) & 31);
+#pragma unroll
+                for (int c = 0; c < kC; ++c) acc[c] += f * v[u][c];
+            }
+        }
+    const bool zero = bad || l == 0.f;
+    const int64_t row = static_cast<int64_t>(meta.tok + rj) * p.num_heads + meta.head + rh;
+#pragma unroll
+    for (int c = 0; c < kC; ++c)
+        p.out[row * kD + 32 * c + lane] = __float2half_rn(zero ? 0.f : acc[c] / l);
+}
+
+// -------------------------------------------------------------------- host
+template <int kKv, int kD, int kN>
+pkv_status launch_tree(const TreeCall &c, const TreePlan &plan)
+{
+    using M = TreeSmem<kKv, kD, kN>;
+    DeviceInfo di;
+    if (!current_device_info(&di)) return PKV_ERR_CUDA;
+    if (M::kAsk > static_cast<int>(di.max_smem_optin)) return PKV_ERR_UNSUPPORTED;
+    auto kern = tree_kernel<kKv, kD, kN>;
+    {
+        static bool ready[64] = {};
+        std::lock_guard<std::mutex> lock(g_cfg_mu);
+        bool &r = ready[di.device & 63];
+        if (!r) {
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, M::kAsk) !=
+                cudaSuccess) {
+                cudaGetLastError();
+                return PKV_ERR_CUDA;
+            }
+            r = true;
+        }
+    }
+    CUtensorMap tmq, tmk, tmv;
+    const uint64_t rows = static_cast<uint64_t>(c.num_blocks) * c.num_kv_heads * kPage;
+    const int elem = M::kCodes ? 1 : 2, box = M::kCodes ? kD : 64;
+    if (!encode_tmap_3d_f16(&tmq, c.query, kD, c.num_heads, c.num_tokens, 64, plan.chunk,
+                            plan.tokens) ||
+        !encode_tmap_2d(&tmk, c.kpool, elem, kD, rows, box, kPage, box * elem) ||
+        !encode_tmap_2d(&tmv, c.vpool, elem, kD, rows, box, kPage, box * elem))
+        return PKV_ERR_CUDA;
+    const int64_t ctas = static_cast<int64_t>(plan.sides) * plan.pieces;
+    TreeArgs a;
+    a.out = static_cast<__half *>(c.out);
+    a.block_tables = c.block_tables;
+    a.query_starts = c.query_starts;
+    a.context_lens = c.context_lens;
+    a.parents = c.parents;
+    a.k_scales = c.k_scales;
+    a.v_scales = c.v_scales;
+    a.slopes = c.slopes;
+    a.prefix_lens = c.prefix_lens;
+    a.part_acc = static_cast<float *>(c.workspace);
+    a.part_ml = reinterpret_cast<float2 *>(a.part_acc + 2 * ctas * kN * kD);
+    a.meta = reinterpret_cast<TreeMeta *>(a.part_ml + 2 * ctas * kN);
+    a.dev_status = c.dev_status;
+    a.num_tokens = c.num_tokens;
+    a.num_seqs = c.num_seqs;
+    a.num_heads = c.num_heads;
+    a.num_kv_heads = c.num_kv_heads;
+    a.group = c.num_heads / c.num_kv_heads;
+    a.chunk = plan.chunk;
+    a.chunks = plan.chunks;
+    a.tokens = plan.tokens;
+    a.sides = plan.sides;
+    a.pieces = plan.pieces;
+    a.max_blocks_per_seq = c.max_blocks_per_seq;
+    a.num_blocks = c.num_blocks;
+    const int64_t cap_tab = static_cast<int64_t>(c.max_blocks_per_seq) * kPage;
+    a.ctx_cap = static_cast<int>(c.max_context_len < cap_tab ? c.max_context_len : cap_tab);
+    a.max_tree_len = c.max_tree_len;
+    a.window = c.window;
+    a.scale_log2 = c.softmax_scale * 1.4426950408889634f;
+    a.cap = c.logit_cap * 1.4426950408889634f;
+    a.cap_inv = c.logit_cap > 0.f ? 1.f / a.cap : 0.f;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(tree_threads(kKv, kN));
+    cfg.dynamicSmemBytes = M::kAsk;
+    cfg.stream = static_cast<cudaStream_t>(c.stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, tmq, tmk, tmv);
+    if (e == cudaSuccess) {
+        cfg.gridDim = dim3(static_cast<unsigned>(ctas * (kN / kJoinWarps)));
+        cfg.blockDim = dim3(32 * kJoinWarps);
+        cfg.dynamicSmemBytes = 0;
+        e = cudaLaunchKernelEx(&cfg, tree_join_kernel<kD, kN>, a);
+    }
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return PKV_ERR_CUDA;
+    }
+    return PKV_OK;
+}
+
+template <int kKv>
+pkv_status launch_tree(const TreeCall &c, const TreePlan &plan)
+{
+    if (c.head_dim == 128)
+        return plan.rows == 32   ? launch_tree<kKv, 128, 32>(c, plan)
+               : plan.rows == 64 ? launch_tree<kKv, 128, 64>(c, plan)
+                                 : launch_tree<kKv, 128, 128>(c, plan);
+    return plan.rows == 32   ? launch_tree<kKv, 64, 32>(c, plan)
+           : plan.rows == 64 ? launch_tree<kKv, 64, 64>(c, plan)
+                             : launch_tree<kKv, 64, 128>(c, plan);
+}
+
+#ifdef PKV_DEBUG
+inline int set_waits(int give_role, int give_at, int slow_role, int slow_ns)
+{
+    const WaitDebug d = {give_role < 0 ? -2 : give_role, give_at, slow_role < 0 ? -2 : slow_role,
+                         slow_ns};
+    return cudaMemcpyToSymbol(g_wait_debug, &d, sizeof(d)) == cudaSuccess ? 0 : -1;
+}
+#endif
+
+}  // namespace
+}  // namespace pkv

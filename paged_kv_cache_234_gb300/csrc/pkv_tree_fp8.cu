@@ -1,0 +1,18 @@
+// pkv_tree_fp8.cu -- tree attention over FP8 caches (pkv_tree.cuh).
+#include "pkv_tree.cuh"
+
+namespace pkv {
+
+pkv_status launch_tree_fp8(const TreeCall &c, const TreePlan &plan)
+{
+    return launch_tree<kKvF8>(c, plan);
+}
+
+#ifdef PKV_DEBUG
+int set_tree_waits_fp8(int give_role, int give_at, int slow_role, int slow_ns)
+{
+    return set_waits(give_role, give_at, slow_role, slow_ns);
+}
+#endif
+
+}  // namespace pkv

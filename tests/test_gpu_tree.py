@@ -136,6 +136,15 @@ def test_long_contexts(kind, dim, option):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dim,heads", [(64, 8), (128, 8), (128, 2)])
+@pytest.mark.parametrize("option", ["plain", "all"])
+def test_large_trees_over_long_contexts(kind, dim, heads, option):
+    # several work items of a tree side by side, many times around the rings
+    o = dict(OPTIONS[option], window=8000) if option == "all" else option
+    check(R.make(22, [70, 33], [9000, 6000], heads, 1, dim), kind, o)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_every_page_boundary(kind):
     # contexts whose trees begin and end anywhere in a page and in a tile of keys
     q = [n for n in (1, 2, 15, 16, 17) for _ in range(9)]
