@@ -70,6 +70,12 @@ pkv_status tree_entry(const TreeCall &c, bool codes, Launch launch)
         !aligned(c.prefix_lens, 4))
         return PKV_ERR_MISALIGNED;
     if (c.num_tokens == 0 || c.num_seqs == 0) return PKV_OK;
+    // the line of tiles is counted in 32 bits
+    const int64_t cap = static_cast<int64_t>(c.max_blocks_per_seq) * kPage;
+    const int64_t most = (c.max_context_len < cap ? c.max_context_len : cap) / kTile + 2;
+    const int64_t line = static_cast<int64_t>(plan.chunks) * c.num_kv_heads *
+                         (c.num_tokens / plan.tokens + static_cast<int64_t>(c.num_seqs));
+    if (line > INT32_MAX || line * most > INT32_MAX) return PKV_ERR_UNSUPPORTED;
     // Where the keys that all CTAs read for an item are likely to be in L2 still when
     // they come to the next item of the tree, items follow one another: that fits
     // trees of any lengths.

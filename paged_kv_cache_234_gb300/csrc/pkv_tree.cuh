@@ -161,8 +161,7 @@ struct TreeSmem {
     static constexpr int kAt = kSlope + 4 * kN;     // the row's place in the output, or -1
     static constexpr int kSums = kAt + 8 * kN;      // [4 quarters of the keys][kN]
     static constexpr int kMask = kSums + 16 * kN;   // [4 quarters of the keys][kN]: bits
-    static constexpr int kScan = kMask + 16 * kN;   // sums of the warps, where the piece begins
-    static constexpr int kUp = kScan + 8 * 32;      // parents
+    static constexpr int kUp = kMask + 16 * kN;     // parents
     static constexpr int kBytes = kUp + 2 * 4 * kParents;   // of both item slots
     // a second CTA on the SM would wait for TMEM: ask for more than half
     static constexpr int kAsk = kBytes > 120 * 1024 ? kBytes : 120 * 1024;
@@ -261,6 +260,13 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint4 v)
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
                  "r"(v.w)
                  : "memory");
+}
+
+// The same for bytes that this thread does not read, so that loads may pass it.
+__device__ __forceinline__ void put_shared16(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+                 "r"(v.w));
 }
 
 __device__ __forceinline__ float log2_of(float x)
@@ -422,99 +428,12 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
         ptx::prefetch_tmap(&tmv);
     }
     if (warp == kSoftWarps) umma::alloc(base + M::kFlags + 12, 512);
-    ptx::griddep_wait();
-    ptx::griddep_launch_dependents();
-
-    // ------------------------------------------------ this CTA's piece of the line
-    const int side = blockIdx.x % p.sides, piece = blockIdx.x / p.sides;
-    int64_t *scan = reinterpret_cast<int64_t *>(smem + M::kScan);
-    // A sequence: its keys, and this side's items of it for a kv head's chunk of heads
-    // (tiles 1 where they only get zeros).
-    struct Seq {
-        SeqRows rows;
-        SeqKeys keys;
-        int items;
-        bool zeros;
-    };
-    auto sequence = [&](int s) -> Seq {
-        Seq q;
-        const int first = __ldg(p.query_starts + s), last = __ldg(p.query_starts + s + 1);
-        q.rows.set(first, last, __ldg(p.context_lens + s), p.num_tokens, p.ctx_cap);
-        q.zeros = first != last && (!q.rows.ok || q.rows.len > p.max_tree_len);
-        q.items = 0;
-        q.keys = SeqKeys{};
-        if (q.rows.len == 0) return q;
-        if (q.zeros) {
-            q.items = side == 0;
-            q.keys.tiles = 1;
-        } else {
-            const int all = (q.rows.len - 1) / p.tokens + 1;
-            q.items = all > side ? (all - 1 - side) / p.sides + 1 : 0;
-            q.keys.set(p, q.rows.ctx, q.rows.len, p.prefix_lens ? __ldg(p.prefix_lens + s) : 0);
-        }
-        return q;
-    };
-    auto tiles_of = [&](const Seq &q) -> int64_t {   // on the line
-        return static_cast<int64_t>(q.keys.tiles) * q.items * (p.num_kv_heads * p.chunks);
-    };
-    constexpr int kWarps = tree_threads(kKv, kN) / 32;
-    const int seg = (p.num_seqs + 32 * kWarps - 1) / (32 * kWarps);
-    int64_t own = 0, before = 0, begin = 0, end = 0, quo = 0, rem = 0;
-    // the whole line, and the i-th cut
-    auto cut = [&](int64_t i) { return quo * i + min(i, rem); };
-    // twice over the thread's sequences: their tiles, then who holds the piece's first
-#pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-        int64_t at = before;
-        if (pass == 0 || (begin < end && before <= begin && begin < before + own)) {
-            bool any = false;
-            const int s1 = min((static_cast<int>(threadIdx.x) + 1) * seg, p.num_seqs);
-#pragma unroll 1
-            for (int s = threadIdx.x * seg; s < s1; ++s) {
-                const Seq q = sequence(s);
-                const int64_t here = tiles_of(q);
-                any |= q.zeros;
-                if (pass == 0) {
-                    own += here;
-                } else if (begin < at + here) {
-                    scan[kWarps] = s;
-                    scan[kWarps + 1] = begin - at;
-                    break;
-                }
-                at += here;
-            }
-            if (pass == 0 && any && blockIdx.x == 0 && p.dev_status)
-                atomicOr(p.dev_status, static_cast<int32_t>(PKV_DEV_BAD_CTX));
-        }
-        if (pass == 0) {
-            int64_t sum = own;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += v;
-            }
-            if (lane == 31) scan[warp] = sum;
-            __syncthreads();
-            int64_t total = 0;
-            before = sum - own;
-#pragma unroll 1
-            for (int w = 0; w < kWarps; ++w) {
-                if (w < warp) before += scan[w];
-                total += scan[w];
-            }
-            const int64_t most = total / kPieceTiles;
-            const int pieces = most < p.pieces ? max(static_cast<int>(most), 1) : p.pieces;
-            quo = total <= INT32_MAX ? static_cast<int>(total) / pieces : total / pieces;
-            rem = total - quo * pieces;
-            begin = piece < pieces ? cut(piece) : total;
-            end = piece < pieces ? cut(piece + 1) : total;
-        }
-    }
     umma::fence_before();
     __syncthreads();
     umma::fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, static_cast<uint32_t>(flags[3]), 0);
-
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     auto t_s = [&](uint32_t g) { return tmem + kN * (g & 1); };   // S^T of tile g
     const uint32_t t_o = tmem + 2 * kN;                           // O^T
 
@@ -728,41 +647,43 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 [[maybe_unused]] const uint64_t rv2 = ptx::f32x2(rv, rv);
                 // The probabilities, by the references as they are.  Should one exceed its
                 // reference by too much, what they added to the sums is taken off again,
-                // the references follow, and they are worked out once more.
+                // the references follow, and they are worked out once more.  In the first
+                // tile the references come first.
 #pragma unroll 1
-                for (int pass = 0;; ++pass) {
-                    float top = -INFINITY;
+                for (int pass = j > 0 ? 0 : -1;; ++pass) {
+                    bool again = pass < 0;
+                    if (pass >= 0) {
+                        float top = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < kC; c += 8) {
-                        uint32_t pk[4];
+                        for (int c = 0; c < kC; c += 8) {
+                            uint32_t pk[4];
 #pragma unroll
-                        for (int e = 0; e < 8; e += 4) {
-                            const float4 o = four(off, c0 + c + e);
+                            for (int e = 0; e < 8; e += 4) {
+                                const float4 o = four(off, c0 + c + e);
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const int r = c + e + 2 * h;
-                                const float2 z =
-                                    h == 0 ? exponents(r, o.x, o.y) : exponents(r, o.z, o.w);
-                                top = fmaxf(fmaxf(top, z.x), z.y);
-                                const float2 y = make_float2(ptx::ex2(z.x), ptx::ex2(z.y));
-                                const uint64_t y2 = ptx::f32x2(y.x, y.y);
-                                l[r / 2] = kCodes ? ptx::fma2(y2, rv2, l[r / 2])
-                                                  : ptx::add2(l[r / 2], y2);
-                                pk[e / 2 + h] = pack2(y.x, y.y);
+                                for (int h = 0; h < 2; ++h) {
+                                    const int r = c + e + 2 * h;
+                                    const float2 z =
+                                        h == 0 ? exponents(r, o.x, o.y) : exponents(r, o.z, o.w);
+                                    top = fmaxf(fmaxf(top, z.x), z.y);
+                                    const float2 y = make_float2(ptx::ex2(z.x), ptx::ex2(z.y));
+                                    const uint64_t y2 = ptx::f32x2(y.x, y.y);
+                                    l[r / 2] = kCodes ? ptx::fma2(y2, rv2, l[r / 2])
+                                                      : ptx::add2(l[r / 2], y2);
+                                    pk[e / 2 + h] = pack2(y.x, y.y);
+                                }
                             }
+                            put_shared16(to + c / 8 * (16 * kTile),
+                                         make_uint4(pk[0], pk[1], pk[2], pk[3]));
                         }
-                        st_shared16(to + c / 8 * (16 * kTile),
-                                    make_uint4(pk[0], pk[1], pk[2], pk[3]));
+                        again = pass == 0 && top > kLift + kLazy;
+                        if (!group_any(i, fail || again)) break;
                     }
-                    if (!group_any(i, fail || (pass == 0 && top > kLift + kLazy))) break;
                     if (group_any(i, fail)) {
                         left = true;
                         break;
                     }
-                    if (j == 0) {
-#pragma unroll
-                        for (int c = 0; c < kC / 2; ++c) l[c] = 0;
-                    } else {
+                    if (pass >= 0) {
                         // (beyond 2^100 the sums so far will be nothing; else the reference
                         // grows by 2^kLazy at least, and with it the rounding of a sum that
                         // held too much goes below the sum's own)
@@ -978,7 +899,19 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                     const int32_t b = __ldg(table + it.real(v));
                     return b >= 0 && b < p.num_blocks ? b : -1;
                 };
-                int32_t blk = lookup(0);
+                // scales of the lane's page, both by the K warp: see TreeSmem::kScales
+                auto scales_of = [&](int32_t b, float &ks, float &vs) {
+                    ks = vs = 0.f;
+                    if constexpr (kCodes)
+                        if (b >= 0 && !is_v) {
+                            const int64_t at = static_cast<int64_t>(b) * p.num_kv_heads + it.kvh;
+                            ks = __ldg(p.k_scales + at);
+                            vs = __ldg(p.v_scales + at);
+                        }
+                };
+                int32_t blk = lookup(0), next = nt > 1 ? lookup(1) : -2;
+                float k_scale, v_scale;
+                scales_of(blk, k_scale, v_scale);
                 for (int j = 0; j < nt; ++j) {
                     const uint32_t n = 2 * tiles + (is_v ? 1 : 0);
                     const int s = n % R;
@@ -988,18 +921,14 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                         if (p.dev_status)
                             atomicOr(p.dev_status, static_cast<int32_t>(PKV_DEV_BAD_BLOCK));
                     }
-                    [[maybe_unused]] float k_scale = 0.f, v_scale = 0.f;
-                    if constexpr (kCodes)
-                        if (have && !is_v) {
-                            const int64_t at = static_cast<int64_t>(blk) * p.num_kv_heads + it.kvh;
-                            k_scale = __ldg(p.k_scales + at);
-                            v_scale = __ldg(p.v_scales + at);
-                        }
                     const int row = (blk * p.num_kv_heads + it.kvh) * kPage;
                     const unsigned pages = __ballot_sync(0xffffffffu, have);
                     const uint32_t fb = kCodes ? cfull(s) : full(s);
                     const uint32_t eb = kCodes ? cempty(s) : empty(s);
-                    if (j + 1 < nt) blk = lookup(j + 1);
+                    // (ahead: the blocks of the tile after the next, the next one's scales)
+                    const int32_t after = j + 2 < nt ? lookup(j + 2) : -2;
+                    float k_next, v_next;
+                    scales_of(next, k_next, v_next);
                     ok = wait(eb, ((n / R) & 1) ^ 1);
                     if (!ok) break;
                     if constexpr (kCodes)
@@ -1026,6 +955,10 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                     }
                     __syncwarp();
                     ++tiles;
+                    blk = next;
+                    next = after;
+                    k_scale = k_next;
+                    v_scale = v_next;
                     if (!is_v && j == 0) {
                         // the queries: tokens x heads x 64 values, which land as the item's
                         // rows in their order (rows of heads that are not the item's, or
@@ -1054,20 +987,91 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
         } else {
             // ------------------------------------------------ the items of the piece
             const Waiter wait = waiter.as(kRoleItems);
+            const int side = blockIdx.x % p.sides, piece = blockIdx.x / p.sides;
+            // A sequence: its keys, and this side's items of it for a kv head's chunk of
+            // heads (one tile where they only get zeros).
+            struct Seq {
+                SeqRows rows;
+                SeqKeys keys;
+                int items;
+                bool zeros;
+            };
+            auto sequence = [&](int s) -> Seq {
+                Seq q;
+                const int first = __ldg(p.query_starts + s), last = __ldg(p.query_starts + s + 1);
+                const int len = __ldg(p.context_lens + s);
+                const int pre = p.prefix_lens ? __ldg(p.prefix_lens + s) : 0;
+                q.rows.set(first, last, len, p.num_tokens, p.ctx_cap);
+                q.zeros = first != last && (!q.rows.ok || q.rows.len > p.max_tree_len);
+                q.items = 0;
+                q.keys = SeqKeys{};
+                if (q.rows.len == 0) return q;
+                if (q.zeros) {
+                    q.items = side == 0;
+                    q.keys.tiles = 1;
+                } else {
+                    const int all = (q.rows.len - 1) / p.tokens + 1;
+                    q.items = all > side ? (all - 1 - side) / p.sides + 1 : 0;
+                    q.keys.set(p, q.rows.ctx, q.rows.len, pre);
+                }
+                return q;
+            };
+            const int heads = p.num_kv_heads * p.chunks;   // items of a sequence's row chunk
+            // The whole line, then where the piece begins: twice over the sequences, 32
+            // at a time.
+            int total = 0, begin = 0, end = 0, quo = 0, rem = 0;
+            auto cut = [&](int i) { return quo * i + min(i, rem); };
+            int seq = 0, rest = 0;   // the present sequence, its tiles before `at`
+            int before = 0;
+            bool any = false;
+#pragma unroll 1
+            for (int s0 = 0, pass = 0;; s0 += 32) {
+                if (s0 >= p.num_seqs) {
+                    if (pass == 1 || total == 0) break;
+                    // (cuts are whole tiles, pieces not below kPieceTiles where they can)
+                    const int pieces = max(min(total / kPieceTiles, p.pieces), 1);
+                    quo = total / pieces;
+                    rem = total - quo * pieces;
+                    begin = piece < pieces ? cut(piece) : total;
+                    end = piece < pieces ? cut(piece + 1) : total;
+                    if (begin >= end) break;
+                    pass = 1;
+                    s0 = 0;
+                }
+                int t = 0;
+                if (s0 + lane < p.num_seqs) {
+                    const Seq q = sequence(s0 + lane);
+                    t = q.keys.tiles * q.items * heads;
+                    any |= q.zeros;
+                }
+                int sum = t;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, sum, o);
+                    if (lane >= o) sum += v;
+                }
+                const int all = __shfl_sync(0xffffffffu, sum, 31);
+                if (pass == 0) {
+                    total += all;
+                } else if (begin < before + all) {
+                    const unsigned m = __ballot_sync(0xffffffffu, begin < before + sum);
+                    const int l0 = __ffs(m) - 1;
+                    seq = s0 + l0;
+                    rest = begin - before - __shfl_sync(0xffffffffu, sum - t, l0);
+                    break;
+                } else {
+                    before += all;
+                }
+            }
+            if (any && blockIdx.x == 0 && p.dev_status)
+                atomicOr(p.dev_status, static_cast<int32_t>(PKV_DEV_BAD_CTX));
             TreeMeta tail = {};
             bool ok = true;
-            int k = 0;
-            int64_t at = begin;
-            int seq = 0;
-            int64_t rest = 0;   // tiles of the sequence before `at`
-            if (begin < end) {
-                seq = static_cast<int>(scan[kWarps]);
-                rest = scan[kWarps + 1];
-            }
+            int k = 0, at = begin;
             for (; at < end && ok; ++seq, rest = 0) {
                 const Seq q = sequence(seq);
                 const int tiles = q.keys.tiles;
-                const int items = q.items * p.num_kv_heads * p.chunks;
+                const int items = q.items * heads;
                 TreeItem it;
                 it.seq = seq;
                 it.start = q.rows.start;
@@ -1078,11 +1082,10 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 it.np1 = q.keys.np1;
                 it.gap = q.keys.gap;
                 // kv heads, chunks of heads, the side's rows of the tree
-                for (int i = rest > 0 ? static_cast<int>(rest / tiles) : 0; i < items && at < end && ok;
-                     ++i) {
-                    it.ta = static_cast<int>(rest - static_cast<int64_t>(i) * tiles);
-                    it.nt = static_cast<int>(min(static_cast<int64_t>(tiles - it.ta), end - at));
-                    const int64_t stop = at + (tiles - it.ta);   // the item's end on the line
+                for (int i = rest > 0 ? rest / tiles : 0; i < items && at < end && ok; ++i) {
+                    it.ta = rest - i * tiles;
+                    it.nt = min(tiles - it.ta, end - at);
+                    const int stop = at + (tiles - it.ta);   // the item's end on the line
                     it.part = it.ta > 0 ? 0 : it.nt < tiles ? 1 : -1;
                     const int hc = i / q.items;
                     it.kvh = hc / p.chunks;
