@@ -43,6 +43,7 @@
 #include <stdint.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "pkv_host.cuh"
 #include "pkv_ptx.cuh"
@@ -81,15 +82,15 @@ __host__ __device__ constexpr int soft_warps(int rows)
     return 4 * tree_groups(rows);
 }
 
-// Warps that widen codes: 128 rows leave registers for four.
-__host__ __device__ constexpr int widen_warps(int kv, int rows)
+// Warps that widen codes.
+__host__ __device__ constexpr int widen_warps(int kv)
 {
-    return kv == kKvF16 ? 0 : rows > 64 ? 4 : 8;
+    return kv == kKvF16 ? 0 : 8;
 }
 
 __host__ __device__ constexpr int tree_threads(int kv, int rows)
 {
-    return 32 * (soft_warps(rows) + 4 + widen_warps(kv, rows));
+    return 32 * (soft_warps(rows) + 4 + widen_warps(kv));
 }
 
 struct TreeMeta {               // the part of an item that a piece ends in
@@ -157,7 +158,8 @@ struct TreeSmem {
     static constexpr int kOff = kScales + (kCodes ? kScaleTiles * 2 * kPagesPerTile * 4 : 0);
     static constexpr int kMax = kOff + 4 * kN;      // a row's reference
     static constexpr int kFac = kMax + 4 * kN;      // factor of its sums; 1 / sum at the end
-    static constexpr int kSlope = kFac + 4 * kN;
+    static constexpr int kOld = kFac + 4 * kN;      // kOff before the last change
+    static constexpr int kSlope = kOld + 4 * kN;
     static constexpr int kAt = kSlope + 4 * kN;     // the row's place in the output, or -1
     static constexpr int kSums = kAt + 8 * kN;      // [4 quarters of the keys][kN]
     static constexpr int kMask = kSums + 16 * kN;   // [4 quarters of the keys][kN]: bits
@@ -207,28 +209,18 @@ static_assert(sizeof(TreeItem) == 80, "an item is 80 bytes of shared memory");
 
 // ------------------------------------------------------------------ kernel
 // Registers: all threads are launched with 65536 / threads, rounded down to a
-// multiple of 8 (fp16: 168 for 384 threads; codes: 128 for 512, 96 for 640).  With
-// two groups their threads take what the others give back.
+// multiple of 8 (168 for 384 threads, 128 for 512, 96 for 640).  The score threads,
+// which hold 32 scores and 32 sums, take what the others give back.
 template <int kKv, int kN>
 __device__ __forceinline__ void soft_registers()
 {
-    if constexpr (kKv == kKvF16 && kN == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    if constexpr (kKv != kKvF16 && kN == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-    if constexpr (kKv != kKvF16 && kN == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    if constexpr (kKv != kKvF16 && kN > 32) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
 }
 
 template <int kKv, int kN>
-__device__ __forceinline__ void issue_registers()
+__device__ __forceinline__ void other_registers()
 {
-    if constexpr (kN == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if constexpr (kKv != kKvF16 && kN == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-}
-
-template <int kKv, int kN>
-__device__ __forceinline__ void widen_registers()
-{
-    if constexpr (kKv != kKvF16 && kN == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if constexpr (kKv != kKvF16 && kN == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if constexpr (kKv != kKvF16 && kN > 32) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
 }
 
 // Barriers of a group of score warps alone.
@@ -367,7 +359,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
     constexpr bool kCodes = M::kCodes;
     constexpr int S = M::kStages;
     constexpr int kGroups = tree_groups(kN), kSoftWarps = soft_warps(kN);
-    constexpr int kWidenWarps = widen_warps(kKv, kN);
+    constexpr int kWidenWarps = widen_warps(kKv);
     constexpr int kC = kN / kGroups;    // rows of a group
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = ptx::smem_addr(smem);
@@ -428,6 +420,22 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
         ptx::prefetch_tmap(&tmv);
     }
     if (warp == kSoftWarps) umma::alloc(base + M::kFlags + 12, 512);
+    {
+        // what the CTAs look up one after the other, on its way to L2
+        const int64_t at = 128 * (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x);
+        auto fetch = [&](const void *from, int64_t bytes) {
+            if (at < bytes) ptx::prefetch_l2(static_cast<const char *>(from) + at);
+        };
+        fetch(p.query_starts, 4 * static_cast<int64_t>(p.num_seqs));
+        fetch(p.context_lens, 4 * static_cast<int64_t>(p.num_seqs));
+        fetch(p.parents, 4 * static_cast<int64_t>(p.num_tokens));
+        fetch(p.block_tables, 4 * static_cast<int64_t>(p.num_seqs) * p.max_blocks_per_seq);
+        const int64_t scales = 4 * static_cast<int64_t>(p.num_blocks) * p.num_kv_heads;
+        if (kCodes && scales <= (1 << 20)) {
+            fetch(p.k_scales, scales);
+            fetch(p.v_scales, scales);
+        }
+    }
     umma::fence_before();
     __syncthreads();
     umma::fence_after();
@@ -436,6 +444,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
     ptx::griddep_launch_dependents();
     auto t_s = [&](uint32_t g) { return tmem + kN * (g & 1); };   // S^T of tile g
     const uint32_t t_o = tmem + 2 * kN;                           // O^T
+    const uint32_t t_l = tmem + 3 * kN;   // the threads' shares of the rows' sums
 
     if (warp < kSoftWarps) {
         // ------------------------------------------------ scores and rows
@@ -450,6 +459,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
         float *off = reinterpret_cast<float *>(smem + M::kOff);   // kLift - reference
         float *ref = reinterpret_cast<float *>(smem + M::kMax);
         float *fac = reinterpret_cast<float *>(smem + M::kFac);
+        float *old = reinterpret_cast<float *>(smem + M::kOld);
         float *slp = reinterpret_cast<float *>(smem + M::kSlope);
         int64_t *place = reinterpret_cast<int64_t *>(smem + M::kAt);
         float *sums = reinterpret_cast<float *>(smem + M::kSums);
@@ -457,13 +467,19 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
         auto four = [](const float *v, int c) { return *reinterpret_cast<const float4 *>(v + c); };
         uint32_t g = 0;        // tiles of keys of the CTA so far
         bool fail = false;     // of this warp's waits; a group leaves together, at a barrier
-        for (int k = 0;; ++k) {
-            fail |= !wait(i_full(k), k >> 1 & 1);
-            const TreeItem &it = item(k);
-            const int nt = it.nt, n = it.n, ctx = it.base, pre = it.pre, np1 = it.np1, gap = it.gap;
+        // While the first loads are on their way the warps walk through an item of one
+        // tile and no rows (k = -1), without its waits and arrivals: so the instructions
+        // are there when the first tile is, some 8 KB that otherwise arrive line by line.
+        for (int k = -1;; ++k) {
+            const bool trial = k < 0;
+            if (!trial) fail |= !wait(i_full(k), k >> 1 & 1);
+            const TreeItem &it = item(max(k, 0));
+            const int nt = trial ? 1 : it.nt, n = trial ? 0 : it.n, ctx = trial ? 0 : it.base;
+            const int pre = trial ? INT32_MAX : it.pre, np1 = trial ? 0 : it.np1;
+            const int gap = trial ? 0 : it.gap, ta = trial ? 0 : it.ta, part = trial ? -1 : it.part;
             auto real = [&](int v) { return v + (v >= np1 ? gap : 0); };
             const int rj = t / p.chunk, rh = t - rj * p.chunk;   // token and head of row t
-            const bool mine = key < kC && rj < it.toks && rh < it.heads;
+            const bool mine = !trial && key < kC && rj < it.toks && rh < it.heads;
             if (key < kC && nt > 0) {
                 // rows that are not the item's: a reference that nothing exceeds
                 off[t] = mine ? kLift - kNone : -INFINITY;
@@ -474,12 +490,12 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                     slp[t] = mine && !fail ? __ldg(p.slopes + it.head + rh) * 1.4426950408889634f
                                            : 0.f;
             }
-            fail |= !wait(t_full(k), k >> 1 & 1);
+            if (!trial) fail |= !wait(t_full(k), k >> 1 & 1);
             if (group_any(i, fail)) break;
             if (nt == 0) break;
-            const bool bad_tree = flags[4 + (k & 1)] != 0;
+            const bool bad_tree = !trial && flags[4 + (k & 1)] != 0;
             const int *up = reinterpret_cast<const int *>(smem + M::kUp) + kParents * (k & 1);
-            const int32_t *par = p.parents + it.start;
+            const int32_t *par = p.parents + (trial ? 0 : it.start);
             auto parent = [&](int j) { return j < kParents ? up[j] : __ldg(par + j); };
             const int node = mine && !bad_tree ? it.row + rj : -1;
             int lo = 0;
@@ -489,12 +505,12 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                     for (int j = parent(node); j >= 0; j = parent(j)) ++pos;
                 lo = max(pos - p.window + 1, 0);
             }
-            uint64_t l[kC / 2];   // the thread's share of the rows' sums
-#pragma unroll
-            for (int c = 0; c < kC / 2; ++c) l[c] = 0;
             bool left = false;
-            for (int j = 0; j < nt; ++j, ++g) {
-                const int v0 = (it.ta + j) * kPagesPerTile;
+            float l[32];   // the thread's shares of the sums (two walks of 32 rows: in TMEM)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) l[e] = 0.f;
+            for (int j = 0; j < nt; ++j) {
+                const int v0 = (ta + j) * kPagesPerTile;
                 const int t0 = real(v0) * kPage;
                 const int t1 = real(v0 + kPagesPerTile - 1) * kPage + kPage - 1;
                 // whether all rows see all keys
@@ -532,93 +548,22 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                     }
                     group_sync(i);
                 }
-                fail |= !wait(s_full(g), g >> 1 & 1);
-                umma::fence_after();
-                float x[kC];
-#pragma unroll
-                for (int c = 0; c < kC; c += 32) umma::ld32(t_s(g) + lanes + c0 + c, x + c);
-                // (meanwhile: the probabilities' buffer was read by the product before)
-                const uint32_t was = g - M::kPBufs;
-                if (g >= M::kPBufs) fail |= !wait(pv_done(i, was), was >> 1 & 1);
-                // what a product is multiplied with, log2 of the page's V scale, and
-                // the scale's reciprocal
-                float f = p.scale_log2;
-                [[maybe_unused]] float lv = 0.f, rv = 1.f;
-                if constexpr (kCodes) {
-                    const float *sc = reinterpret_cast<const float *>(smem + M::kScales) +
-                                      (g & (M::kScaleTiles - 1)) * 2 * kPagesPerTile + (key >> 4);
-                    const float vs = sc[kPagesPerTile], vc = fmaxf(vs, kLeastV);
-                    f *= sc[0];
-                    lv = vs >= 0.f && vs < INFINITY ? log2_of(vc) : NAN;
-                    rv = __frcp_rn(vc);
-                }
-                umma::wait_ld();
-                const uint32_t *words = mask + quad * kN + c0;
-                auto scale_all = [&](float by, float add) {
-                    const uint64_t b2 = ptx::f32x2(by, by), a2 = ptx::f32x2(add, add);
-#pragma unroll
-                    for (int c = 0; c < kC; c += 2) {
-                        const float2 y =
-                            ptx::f32x2_parts(ptx::fma2(ptx::f32x2(x[c], x[c + 1]), b2, a2));
-                        x[c] = y.x;
-                        x[c + 1] = y.y;
-                    }
-                };
-                // x of the keys that a row does not see
-                auto hide = [&](float value) {
-#pragma unroll
-                    for (int c = 0; c < kC; c += 4) {
-                        const uint4 w = *reinterpret_cast<const uint4 *>(words + c);
-                        if (!(w.x >> lane & 1u)) x[c] = value;
-                        if (!(w.y >> lane & 1u)) x[c + 1] = value;
-                        if (!(w.z >> lane & 1u)) x[c + 2] = value;
-                        if (!(w.w >> lane & 1u)) x[c + 3] = value;
-                    }
-                };
-                if (p.cap > 0.f) {
-                    scale_all(f * p.cap_inv, 0.f);
-                    f = p.cap;
-                    // (unseen keys and other rows have no say in how it is evaluated)
-                    if (!clean) hide(0.f);
-#pragma unroll
-                    for (int c = 0; c < kC; c += 4) {
-                        const float4 o = four(off, c0 + c);
-                        if (o.x == -INFINITY) x[c] = 0.f;
-                        if (o.y == -INFINITY) x[c + 1] = 0.f;
-                        if (o.z == -INFINITY) x[c + 2] = 0.f;
-                        if (o.w == -INFINITY) x[c + 3] = 0.f;
-                    }
-                    tanh_all(x);
-                }
-                if (kCodes || p.slopes || !clean) {
-                    scale_all(f, lv);
-                    f = 1.f;
-                }
+                float far = 0.f;   // p(t) - ctx
                 if (p.slopes) {
-                    // slope (p(t) - ctx): what a row's own position adds is the same for
-                    // all of its keys, and the softmax does not see it
-                    int far = at - ctx;
-                    if (far >= 0 && !bad_tree) {
-                        int b = far < n ? parent(far) : -1;
-                        for (far = 0; b >= 0; b = parent(b)) ++far;
+                    int d = at - ctx;
+                    if (d >= 0 && !bad_tree) {
+                        int b = d < n ? parent(d) : -1;
+                        for (d = 0; b >= 0; b = parent(b)) ++d;
                     }
-                    const float d = static_cast<float>(far);
-#pragma unroll
-                    for (int c = 0; c < kC; c += 4) {
-                        const float4 s = four(slp, c0 + c);
-                        x[c] = fmaf(s.x, d, x[c]);
-                        x[c + 1] = fmaf(s.y, d, x[c + 1]);
-                        x[c + 2] = fmaf(s.z, d, x[c + 2]);
-                        x[c + 3] = fmaf(s.w, d, x[c + 3]);
-                    }
+                    far = static_cast<float>(d);
                 }
-                if (!clean) hide(-INFINITY);
-                const uint64_t f2 = ptx::f32x2(f, f);
-                // x f - reference + kLift of rows c and c + 1
-                auto exponents = [&](int c, float a, float b) {
-                    return ptx::f32x2_parts(
-                        ptx::fma2(ptx::f32x2(x[c], x[c + 1]), f2, ptx::f32x2(a, b)));
-                };
+                // the probabilities' buffer was read by the product before
+                const uint32_t was = g - M::kPBufs;
+                if (!trial) {
+                    fail |= !wait(s_full(g), g >> 1 & 1);
+                    if (g >= M::kPBufs) fail |= !wait(pv_done(i, was), was >> 1 & 1);
+                }
+                umma::fence_after();
                 if (!clean) {
                     // V rows of keys that no row of the tree sees may hold anything, NaN
                     // included (and are not loaded for pages past the item's last):
@@ -636,75 +581,154 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                         const uint32_t row =
                             base + M::kRing + (e % S) * M::kTileBytes + key * 128;
                         if (dead)
-#pragma unroll
+#pragma unroll 1
                             for (int b = 0; b < kD / 8; ++b)
                                 st_shared16(row + (b >> 3) * M::kHalfBytes + (b & 7) * 16,
                                             make_uint4(0, 0, 0, 0));
                     }
                 }
-                const uint32_t to = base + M::kP + (g % M::kPBufs) * M::kPBytes +
-                                    c0 / 8 * (16 * kTile) + key * 16;
-                [[maybe_unused]] const uint64_t rv2 = ptx::f32x2(rv, rv);
-                // The probabilities, by the references as they are.  Should one exceed its
-                // reference by too much, what they added to the sums is taken off again,
-                // the references follow, and they are worked out once more.  In the first
-                // tile the references come first.
-#pragma unroll 1
-                for (int pass = j > 0 ? 0 : -1;; ++pass) {
-                    bool again = pass < 0;
-                    if (pass >= 0) {
-                        float top = -INFINITY;
+                // what a product is multiplied with, log2 of the page's V scale, and
+                // the scale's reciprocal
+                float f0 = p.scale_log2;
+                [[maybe_unused]] float lv = 0.f, rv = 1.f;
+                if constexpr (kCodes) {
+                    const float *sc = reinterpret_cast<const float *>(smem + M::kScales) +
+                                      (g & (M::kScaleTiles - 1)) * 2 * kPagesPerTile + (key >> 4);
+                    const float vs = sc[kPagesPerTile], vc = fmaxf(vs, kLeastV);
+                    f0 *= sc[0];
+                    lv = vs >= 0.f && vs < INFINITY ? log2_of(vc) : NAN;
+                    rv = __frcp_rn(vc);
+                }
+                const uint64_t rv2 = ptx::f32x2(rv, rv);
+                const uint32_t *words = mask + quad * kN;
+                const uint32_t to = base + M::kP + (g % M::kPBufs) * M::kPBytes + key * 16;
+                // The walks over the tile's scores, 32 rows at a time.  Each begins with the
+                // scores x, which times f are in log2 units.
+                auto scores = [&](int c, float (&x)[32], float &f, auto simple) {
+                    constexpr bool kSimple = decltype(simple)::value;
+                    umma::wait_ld();
+                    f = f0;
+                    auto scale_all = [&](float by, float add) {
+                        const uint64_t b2 = ptx::f32x2(by, by), a2 = ptx::f32x2(add, add);
 #pragma unroll
-                        for (int c = 0; c < kC; c += 8) {
+                        for (int e = 0; e < 32; e += 2) {
+                            const float2 y =
+                                ptx::f32x2_parts(ptx::fma2(ptx::f32x2(x[e], x[e + 1]), b2, a2));
+                            x[e] = y.x;
+                            x[e + 1] = y.y;
+                        }
+                    };
+                    // x of the keys that a row does not see
+                    auto hide = [&](float value) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const uint4 w = *reinterpret_cast<const uint4 *>(words + c + e);
+                            if (!(w.x >> lane & 1u)) x[e] = value;
+                            if (!(w.y >> lane & 1u)) x[e + 1] = value;
+                            if (!(w.z >> lane & 1u)) x[e + 2] = value;
+                            if (!(w.w >> lane & 1u)) x[e + 3] = value;
+                        }
+                    };
+                    if constexpr (!kSimple) {
+                        if (p.cap > 0.f) {
+                            scale_all(f * p.cap_inv, 0.f);
+                            f = p.cap;
+                            // (unseen keys and other rows have no say in how it is
+                            // evaluated)
+                            if (!clean) hide(0.f);
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 o = four(off, c + e);
+                                if (o.x == -INFINITY) x[e] = 0.f;
+                                if (o.y == -INFINITY) x[e + 1] = 0.f;
+                                if (o.z == -INFINITY) x[e + 2] = 0.f;
+                                if (o.w == -INFINITY) x[e + 3] = 0.f;
+                            }
+                            tanh_all(x);
+                        }
+                    }
+                    if (kCodes || !kSimple) {
+                        scale_all(f, lv);
+                        f = 1.f;
+                    }
+                    if constexpr (!kSimple) {
+                        if (p.slopes) {
+                            // slope (p(t) - ctx): what a row's own position adds is the same
+                            // for all of its keys, and the softmax does not see it
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 s = four(slp, c + e);
+                                x[e] = fmaf(s.x, far, x[e]);
+                                x[e + 1] = fmaf(s.y, far, x[e + 1]);
+                                x[e + 2] = fmaf(s.z, far, x[e + 2]);
+                                x[e + 3] = fmaf(s.w, far, x[e + 3]);
+                            }
+                        }
+                        if (!clean) hide(-INFINITY);
+                    }
+                };
+                // x f - reference + kLift of two rows
+                auto exponents = [](const float (&x)[32], float f, int e, float a, float b) {
+                    return ptx::f32x2_parts(ptx::fma2(ptx::f32x2(x[e], x[e + 1]), ptx::f32x2(f, f),
+                                                      ptx::f32x2(a, b)));
+                };
+                // The probabilities, by the references as they are: into shared memory, and
+                // into the sums.  Returns the largest exponent.
+                auto probabilities = [&](auto simple) -> float {
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int c = c0; c < c0 + kC; c += 32) {
+                        float x[32], f;
+                        umma::ld32(t_s(g) + lanes + c, x);
+                        if constexpr (kC > 32) {
+                            if (j > 0) {
+                                umma::ld32(t_l + lanes + c, l);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) l[e] = 0.f;
+                            }
+                        }
+                        scores(c, x, f, simple);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
                             uint32_t pk[4];
 #pragma unroll
-                            for (int e = 0; e < 8; e += 4) {
-                                const float4 o = four(off, c0 + c + e);
-#pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    const int r = c + e + 2 * h;
-                                    const float2 z =
-                                        h == 0 ? exponents(r, o.x, o.y) : exponents(r, o.z, o.w);
-                                    top = fmaxf(fmaxf(top, z.x), z.y);
-                                    const float2 y = make_float2(ptx::ex2(z.x), ptx::ex2(z.y));
-                                    const uint64_t y2 = ptx::f32x2(y.x, y.y);
-                                    l[r / 2] = kCodes ? ptx::fma2(y2, rv2, l[r / 2])
-                                                      : ptx::add2(l[r / 2], y2);
-                                    pk[e / 2 + h] = pack2(y.x, y.y);
-                                }
+                            for (int q = 0; q < 8; q += 2) {
+                                const float2 o =
+                                    *reinterpret_cast<const float2 *>(off + c + e + q);
+                                const float2 z = exponents(x, f, e + q, o.x, o.y);
+                                top = fmaxf(fmaxf(top, z.x), z.y);
+                                const float2 y = make_float2(ptx::ex2(z.x), ptx::ex2(z.y));
+                                const uint64_t y2 = ptx::f32x2(y.x, y.y);
+                                const uint64_t l2 = ptx::f32x2(l[e + q], l[e + q + 1]);
+                                const float2 s = ptx::f32x2_parts(kCodes ? ptx::fma2(y2, rv2, l2)
+                                                                         : ptx::add2(l2, y2));
+                                l[e + q] = s.x;
+                                l[e + q + 1] = s.y;
+                                pk[q / 2] = pack2(y.x, y.y);
                             }
-                            put_shared16(to + c / 8 * (16 * kTile),
+                            put_shared16(to + (c + e) / 8 * (16 * kTile),
                                          make_uint4(pk[0], pk[1], pk[2], pk[3]));
                         }
-                        again = pass == 0 && top > kLift + kLazy;
-                        if (!group_any(i, fail || again)) break;
+                        if constexpr (kC > 32) umma::st32(t_l + lanes + c, l);
                     }
-                    if (group_any(i, fail)) {
-                        left = true;
-                        break;
-                    }
-                    if (pass >= 0) {
-                        // (beyond 2^100 the sums so far will be nothing; else the reference
-                        // grows by 2^kLazy at least, and with it the rounding of a sum that
-                        // held too much goes below the sum's own)
+                    if constexpr (kC > 32) umma::wait_st();
+                    return top;
+                };
+                // New references: the rows' maxima over the tile, where these are above.
+                auto references = [&]() {
+#pragma unroll 1
+                    for (int c = c0; c < c0 + kC; c += 32) {
+                        float x[32], f;
+                        umma::ld32(t_s(g) + lanes + c, x);
+                        scores(c, x, f, std::false_type());
 #pragma unroll
-                        for (int c = 0; c < kC; c += 2) {
-                            const float2 z = exponents(c, off[c0 + c], off[c0 + c + 1]);
-                            float2 y = ptx::f32x2_parts(l[c / 2]);
-                            y.x = z.x > 100.f ? 0.f : fmaf(-ptx::ex2(z.x), rv, y.x);
-                            y.y = z.y > 100.f ? 0.f : fmaf(-ptx::ex2(z.y), rv, y.y);
-                            l[c / 2] = ptx::f32x2(y.x, y.y);
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 m =
+                                make_float4(warp_max(x[e] * f), warp_max(x[e + 1] * f),
+                                            warp_max(x[e + 2] * f), warp_max(x[e + 3] * f));
+                            if (lane == 0) *reinterpret_cast<float4 *>(sums + quad * kN + c + e) = m;
                         }
-                    }
-                    // the rows' maxima over the tile
-                    float fm = f;
-                    asm volatile("" : "+f"(fm));   // (products not kept from pass to pass)
-#pragma unroll
-                    for (int c = 0; c < kC; c += 4) {
-                        const float4 m =
-                            make_float4(warp_max(x[c] * fm), warp_max(x[c + 1] * fm),
-                                        warp_max(x[c + 2] * fm), warp_max(x[c + 3] * fm));
-                        if (lane == 0) *reinterpret_cast<float4 *>(sums + quad * kN + c0 + c) = m;
                     }
                     group_sync(i);
                     if (key < kC) {
@@ -713,59 +737,86 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                         for (int q = 0; q < 4; ++q) m = fmaxf(m, sums[q * kN + t]);
                         fac[t] = ptx::ex2(ref[t] - m);
                         ref[t] = m;
+                        old[t] = off[t];
                         if (mine) off[t] = kLift - m;
                     }
                     group_sync(i);
-                    if (j > 0) {
-#pragma unroll
-                        for (int c = 0; c < kC; c += 4) {
-                            const float4 y = four(fac, c0 + c);
-                            l[c / 2] = ptx::mul2(l[c / 2], ptx::f32x2(y.x, y.y));
-                            l[c / 2 + 1] = ptx::mul2(l[c / 2 + 1], ptx::f32x2(y.z, y.w));
-                        }
-                        fail |= !wait(pv_done(i, g - 1), (g - 1) >> 1 & 1);
-                        umma::fence_after();
+                };
+                // What the probabilities added to the sums is taken off again, and sums and
+                // accumulators follow the new references.  (Beyond 2^100 the sums so far will
+                // be nothing; else the reference grows by 2^kLazy at least, and with it the
+                // rounding of a sum that held too much goes below the sum's own.)
+                auto follow = [&]() {
 #pragma unroll 1
-                        for (int c = c0; c < c0 + kC; c += 16) {
-                            float o[16];
-                            umma::ld16(t_o + lanes + c, o);
-                            umma::wait_ld();
+                    for (int c = c0; c < c0 + kC; c += 32) {
+                        float x[32], f;
+                        umma::ld32(t_s(g) + lanes + c, x);
+                        if constexpr (kC > 32) umma::ld32(t_l + lanes + c, l);
+                        scores(c, x, f, std::false_type());
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] *= fac[c + e];
-                            umma::st16(t_o + lanes + c, reinterpret_cast<const uint32_t *>(o));
+                        for (int e = 0; e < 32; e += 2) {
+                            const float2 z = exponents(x, f, e, old[c + e], old[c + e + 1]);
+                            const float a = fmaf(-ptx::ex2(z.x), rv, l[e]);
+                            const float b = fmaf(-ptx::ex2(z.y), rv, l[e + 1]);
+                            l[e] = z.x > 100.f ? 0.f : a * fac[c + e];
+                            l[e + 1] = z.y > 100.f ? 0.f : b * fac[c + e + 1];
                         }
-                        umma::wait_st();
+                        if constexpr (kC > 32) umma::st32(t_l + lanes + c, l);
                     }
+                    fail |= !wait(pv_done(i, g - 1), (g - 1) >> 1 & 1);
+                    umma::fence_after();
+#pragma unroll 1
+                    for (int c = c0; c < c0 + kC; c += 16) {
+                        float o[16];
+                        umma::ld16(t_o + lanes + c, o);
+                        umma::wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] *= fac[c + e];
+                        umma::st16(t_o + lanes + c, reinterpret_cast<const uint32_t *>(o));
+                    }
+                    umma::wait_st();
+                };
+                // In an item's first tile the references come first, so that its
+                // probabilities hold; later an exponent too far above its reference makes
+                // the tile's be worked out once more.
+                if (j == 0) references();
+                const bool simple = clean && !(p.cap > 0.f) && !p.slopes;
+                const float top = simple ? probabilities(std::true_type())
+                                         : probabilities(std::false_type());
+                if (group_any(i, fail || (j > 0 && top > kLift + kLazy))) {
+                    left = group_any(i, fail);
+                    if (left) break;
+                    references();
+                    follow();
+                    probabilities(std::false_type());
                 }
-                if (left) break;
                 ptx::fence_proxy_async_smem();
                 umma::fence_before();
                 __syncwarp();
+                if (trial) break;
                 if (lane == 0) ptx::mbar_arrive(p_full(i, g));
+                ++g;
             }
             if (left) break;
             // the rows' sums, the quarters of the keys in their order
-            fail |= !wait(pv_done(i, g - 1), (g - 1) >> 1 & 1);
+            if (!trial) fail |= !wait(pv_done(i, g - 1), (g - 1) >> 1 & 1);
             umma::fence_after();
-#pragma unroll
-            for (int c = 0; c < kC; c += 32) {
-                float v[32];
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float2 y = ptx::f32x2_parts(l[(c + e) / 2]);
-                    v[e] = y.x;
-                    v[e + 1] = y.y;
+#pragma unroll 1
+            for (int c = c0; c < c0 + kC; c += 32) {
+                if constexpr (kC > 32) {
+                    umma::ld32(t_l + lanes + c, l);
+                    umma::wait_ld();
                 }
-                lane_sums(v, lane);
-                sums[quad * kN + c0 + c + lane] = v[0];
+                lane_sums(l, lane);
+                sums[quad * kN + c + lane] = l[0];
             }
             if (group_any(i, fail)) break;
             const bool bad = bad_tree || flags[1 + (k & 1)] != 0;
-            const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + max(it.part, 0);
+            const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + max(part, 0);
             if (key < kC) {
                 const float a = sums[t] + sums[kN + t] + sums[2 * kN + t] + sums[3 * kN + t];
                 fac[t] = a > 0.f ? 1.f / a : a;   // a row that saw nothing: zeros; NaN stays
-                if (it.part >= 0) p.part_ml[slot * kN + t] = make_float2(ref[t], bad ? -1.f : a);
+                if (part >= 0) p.part_ml[slot * kN + t] = make_float2(ref[t], bad ? -1.f : a);
             }
             group_sync(i);
             const int dim = kD == 128 ? key : 16 * quad + lane;   // M = 64 has 16 of 32 lanes
@@ -775,7 +826,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 float o[16];
                 umma::ld16(t_o + lanes + c, o);
                 umma::wait_ld();
-                if (it.part < 0) {
+                if (part < 0) {
                     // two neighbouring values of a row to a lane: even lanes store row e,
                     // odd ones row e + 1
 #pragma unroll
@@ -795,13 +846,13 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 }
             }
             // (the next item's first product into O waits for its probabilities,
-            // which come after this)
+            // which come after this; its rows' places are written behind a barrier)
             umma::fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(i_empty(k));
+            group_sync(i);
+            if (!trial && lane == 0) ptx::mbar_arrive(i_empty(k));
         }
     } else if (warp < kSoftWarps + 4) {
-        issue_registers<kKv, kN>();
+        other_registers<kKv, kN>();
         if (warp == kSoftWarps) {
             // ------------------------------------------------ products
             const Waiter wait = waiter.as(kRoleProducts);
@@ -1159,7 +1210,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
     } else {
         if constexpr (kCodes) {
             // ------------------------------------------------ codes to fp16
-            widen_registers<kKv, kN>();
+            other_registers<kKv, kN>();
             const Waiter wait = waiter.as(kRoleWiden);
             constexpr int R = M::kCodeStages;
             constexpr int kCh = kD / 16;  // 16-byte chunks of codes per key
