@@ -69,28 +69,32 @@ constexpr float kNone = -3.0e38f;        // reference of a row that has seen not
 constexpr float kLeastV = 0x1p-60f;      // V scales below (zero) count as this
 constexpr int kParents = 512;   // parents of a sequence kept in shared memory
 
-// Score warps: a group of four, a thread per key, for up to 64 rows each.  A tile's
-// chain (scores, reference, exponentials, product) has more waits than work; two
-// groups with rows of their own and nothing to tell each other fill these.
-__host__ __device__ constexpr int tree_groups(int rows)
-{
-    return rows > 32 ? 2 : 1;
-}
+// Score warps: a group of four, a thread per key, for every 32 rows.  A tile's chain
+// (scores, exponentials, reference, product) has more waits than work, which groups
+// with rows of their own and nothing to tell each other fill.
+constexpr int kRows = 32;       // of a group
 
 __host__ __device__ constexpr int soft_warps(int rows)
 {
-    return 4 * tree_groups(rows);
+    return 4 * (rows / kRows);
 }
 
-// Warps that widen codes.
-__host__ __device__ constexpr int widen_warps(int kv)
+// Rows of one product V^T P^T, whose groups are waited for together: with fewer than 64
+// it would read V from shared memory more often than it computes.
+__host__ __device__ constexpr int product_rows(int rows)
 {
-    return kv == kKvF16 ? 0 : 8;
+    return rows < 64 ? rows : 64;
+}
+
+// Warps that widen codes: 128 rows leave registers for four.
+__host__ __device__ constexpr int widen_warps(int kv, int rows)
+{
+    return kv == kKvF16 ? 0 : rows > 64 ? 4 : 8;
 }
 
 __host__ __device__ constexpr int tree_threads(int kv, int rows)
 {
-    return 32 * (soft_warps(rows) + 4 + widen_warps(kv));
+    return 32 * (soft_warps(rows) + 4 + widen_warps(kv, rows));
 }
 
 struct TreeMeta {               // the part of an item that a piece ends in
@@ -209,18 +213,23 @@ static_assert(sizeof(TreeItem) == 80, "an item is 80 bytes of shared memory");
 
 // ------------------------------------------------------------------ kernel
 // Registers: all threads are launched with 65536 / threads, rounded down to a
-// multiple of 8 (168 for 384 threads, 128 for 512, 96 for 640).  The score threads,
-// which hold 32 scores and 32 sums, take what the others give back.
+// multiple of 8 (fp16: 96 for the 640 threads of 128 rows; codes: 96 for the 640 of 64
+// rows, 80 for the 768 of 128).  The score threads, which hold 32 scores and 32 sums,
+// take what the others give back.
 template <int kKv, int kN>
 __device__ __forceinline__ void soft_registers()
 {
-    if constexpr (kKv != kKvF16 && kN > 32) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    if constexpr (kKv == kKvF16 && kN == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    if constexpr (kKv != kKvF16 && kN == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    if constexpr (kKv != kKvF16 && kN == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
 }
 
 template <int kKv, int kN>
 __device__ __forceinline__ void other_registers()
 {
-    if constexpr (kKv != kKvF16 && kN > 32) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (kKv == kKvF16 && kN == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if constexpr (kKv != kKvF16 && kN == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (kKv != kKvF16 && kN == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
 }
 
 // Barriers of a group of score warps alone.
@@ -358,9 +367,9 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
     using M = TreeSmem<kKv, kD, kN>;
     constexpr bool kCodes = M::kCodes;
     constexpr int S = M::kStages;
-    constexpr int kGroups = tree_groups(kN), kSoftWarps = soft_warps(kN);
-    constexpr int kWidenWarps = widen_warps(kKv);
-    constexpr int kC = kN / kGroups;    // rows of a group
+    constexpr int kSoftWarps = soft_warps(kN);
+    constexpr int kP = product_rows(kN), kProducts = kN / kP;
+    constexpr int kWidenWarps = widen_warps(kKv, kN);
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = ptx::smem_addr(smem);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -373,11 +382,11 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
     };
     const uint32_t one = base + M::kCtl + 8 * (2 * S + 2 * M::kCodeStages);
     const uint32_t q_full = one, q_empty = one + 8, drain = one + 16;
-    // of tile number g of the CTA and group i: scores there, probabilities there,
+    // of tile number g of the CTA and product q: scores there, probabilities there,
     // product done
     auto s_full = [&](uint32_t g) { return one + 24 + 8 * (g & 1); };
-    auto p_full = [&](int i, uint32_t g) { return one + 40 + 8 * (2 * i + (g & 1)); };
-    auto pv_done = [&](int i, uint32_t g) { return one + 72 + 8 * (2 * i + (g & 1)); };
+    auto p_full = [&](int q, uint32_t g) { return one + 40 + 8 * (2 * q + (g & 1)); };
+    auto pv_done = [&](int q, uint32_t g) { return one + 72 + 8 * (2 * q + (g & 1)); };
     auto i_full = [&](int k) { return one + 104 + 8 * (k & 1); };
     auto i_empty = [&](int k) { return one + 120 + 8 * (k & 1); };
     auto t_full = [&](int k) { return one + 136 + 8 * (k & 1); };   // the item's tree is there
@@ -405,7 +414,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(s_full(i), 1);
             for (int h = 0; h < 2; ++h) {
-                ptx::mbar_init(p_full(h, i), 4);
+                ptx::mbar_init(p_full(h, i), 4 * (kP / kRows));
                 ptx::mbar_init(pv_done(h, i), 1);
             }
             ptx::mbar_init(i_full(i), 1);
@@ -444,7 +453,6 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
     ptx::griddep_launch_dependents();
     auto t_s = [&](uint32_t g) { return tmem + kN * (g & 1); };   // S^T of tile g
     const uint32_t t_o = tmem + 2 * kN;                           // O^T
-    const uint32_t t_l = tmem + 3 * kN;   // the threads' shares of the rows' sums
 
     if (warp < kSoftWarps) {
         // ------------------------------------------------ scores and rows
@@ -452,9 +460,9 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
         const Waiter wait = waiter.as(kRoleRows);
         const int i = warp >> 2, quad = warp & 3;       // the group; its quarter of the keys
         const int key = threadIdx.x & (kGroup - 1);     // the thread's key of a tile
-        const int c0 = i * kC;                          // the group's rows
+        const int c0 = i * kRows, pr = c0 / kP;         // the group's rows, their product
         const uint32_t lanes = static_cast<uint32_t>(quad) << 21;   // TMEM lane 32 quad
-        // the row that a thread looks after, if key < kC
+        // the row that a thread looks after, if key < kRows
         const int t = c0 + key;
         float *off = reinterpret_cast<float *>(smem + M::kOff);   // kLift - reference
         float *ref = reinterpret_cast<float *>(smem + M::kMax);
@@ -479,8 +487,8 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
             const int gap = trial ? 0 : it.gap, ta = trial ? 0 : it.ta, part = trial ? -1 : it.part;
             auto real = [&](int v) { return v + (v >= np1 ? gap : 0); };
             const int rj = t / p.chunk, rh = t - rj * p.chunk;   // token and head of row t
-            const bool mine = !trial && key < kC && rj < it.toks && rh < it.heads;
-            if (key < kC && nt > 0) {
+            const bool mine = !trial && key < kRows && rj < it.toks && rh < it.heads;
+            if (key < kRows && nt > 0) {
                 // rows that are not the item's: a reference that nothing exceeds
                 off[t] = mine ? kLift - kNone : -INFINITY;
                 ref[t] = kNone;
@@ -506,9 +514,9 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 lo = max(pos - p.window + 1, 0);
             }
             bool left = false;
-            float l[32];   // the thread's shares of the sums (two walks of 32 rows: in TMEM)
+            float l[kRows];   // the thread's shares of the rows' sums
 #pragma unroll
-            for (int e = 0; e < 32; ++e) l[e] = 0.f;
+            for (int e = 0; e < kRows; ++e) l[e] = 0.f;
             for (int j = 0; j < nt; ++j) {
                 const int v0 = (ta + j) * kPagesPerTile;
                 const int t0 = real(v0) * kPage;
@@ -519,7 +527,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 const int at = real(v0 + (key >> 4)) * kPage + (key & 15);   // the key's slot
                 if (!clean) {
                     // bits of the keys that row t sees
-                    if (key < kC) {
+                    if (key < kRows) {
                         uint32_t w[4] = {0, 0, 0, 0};
                         if (mine) {
 #pragma unroll
@@ -561,7 +569,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 const uint32_t was = g - M::kPBufs;
                 if (!trial) {
                     fail |= !wait(s_full(g), g >> 1 & 1);
-                    if (g >= M::kPBufs) fail |= !wait(pv_done(i, was), was >> 1 & 1);
+                    if (g >= M::kPBufs) fail |= !wait(pv_done(pr, was), was >> 1 & 1);
                 }
                 umma::fence_after();
                 if (!clean) {
@@ -573,7 +581,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                     if (__any_sync(0xffffffffu, dead)) {
                         // (the stage's element before this one must have landed: it is K
                         // of a tile before, or V of one whose product is done)
-                        if (S == 2 && g > 0) fail |= !wait(pv_done(i, g - 1), (g - 1) >> 1 & 1);
+                        if (S == 2 && g > 0) fail |= !wait(pv_done(pr, g - 1), (g - 1) >> 1 & 1);
                         static_assert(S % 2 ? S >= 3 : S == 2 || S / 2 >= M::kPBufs,
                                       "phase of the stage");
                         const uint32_t e = 2 * g + 1;
@@ -602,10 +610,10 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 const uint64_t rv2 = ptx::f32x2(rv, rv);
                 const uint32_t *words = mask + quad * kN;
                 const uint32_t to = base + M::kP + (g % M::kPBufs) * M::kPBytes + key * 16;
-                // The walks over the tile's scores, 32 rows at a time.  Each begins with the
-                // scores x, which times f are in log2 units.
-                auto scores = [&](int c, float (&x)[32], float &f, auto simple) {
+                // The scores x of the tile, which times f are in log2 units.
+                auto scores = [&](float (&x)[kRows], float &f, auto simple) {
                     constexpr bool kSimple = decltype(simple)::value;
+                    umma::ld32(t_s(g) + lanes + c0, x);
                     umma::wait_ld();
                     f = f0;
                     auto scale_all = [&](float by, float add) {
@@ -622,7 +630,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                     auto hide = [&](float value) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
-                            const uint4 w = *reinterpret_cast<const uint4 *>(words + c + e);
+                            const uint4 w = *reinterpret_cast<const uint4 *>(words + c0 + e);
                             if (!(w.x >> lane & 1u)) x[e] = value;
                             if (!(w.y >> lane & 1u)) x[e + 1] = value;
                             if (!(w.z >> lane & 1u)) x[e + 2] = value;
@@ -638,7 +646,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                             if (!clean) hide(0.f);
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
-                                const float4 o = four(off, c + e);
+                                const float4 o = four(off, c0 + e);
                                 if (o.x == -INFINITY) x[e] = 0.f;
                                 if (o.y == -INFINITY) x[e + 1] = 0.f;
                                 if (o.z == -INFINITY) x[e + 2] = 0.f;
@@ -657,7 +665,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                             // for all of its keys, and the softmax does not see it
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
-                                const float4 s = four(slp, c + e);
+                                const float4 s = four(slp, c0 + e);
                                 x[e] = fmaf(s.x, far, x[e]);
                                 x[e + 1] = fmaf(s.y, far, x[e + 1]);
                                 x[e + 2] = fmaf(s.z, far, x[e + 2]);
@@ -668,70 +676,49 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                     }
                 };
                 // x f - reference + kLift of two rows
-                auto exponents = [](const float (&x)[32], float f, int e, float a, float b) {
+                auto exponents = [](const float (&x)[kRows], float f, int e, float a, float b) {
                     return ptx::f32x2_parts(ptx::fma2(ptx::f32x2(x[e], x[e + 1]), ptx::f32x2(f, f),
                                                       ptx::f32x2(a, b)));
                 };
                 // The probabilities, by the references as they are: into shared memory, and
                 // into the sums.  Returns the largest exponent.
                 auto probabilities = [&](auto simple) -> float {
-                    float top = -INFINITY;
-#pragma unroll 1
-                    for (int c = c0; c < c0 + kC; c += 32) {
-                        float x[32], f;
-                        umma::ld32(t_s(g) + lanes + c, x);
-                        if constexpr (kC > 32) {
-                            if (j > 0) {
-                                umma::ld32(t_l + lanes + c, l);
-                            } else {
+                    float top = -INFINITY, x[kRows], f;
+                    scores(x, f, simple);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) l[e] = 0.f;
-                            }
+                    for (int e = 0; e < kRows; e += 8) {
+                        uint32_t pk[4];
+#pragma unroll
+                        for (int q = 0; q < 8; q += 2) {
+                            const float2 o = *reinterpret_cast<const float2 *>(off + c0 + e + q);
+                            const float2 z = exponents(x, f, e + q, o.x, o.y);
+                            top = fmaxf(fmaxf(top, z.x), z.y);
+                            const float2 y = make_float2(ptx::ex2(z.x), ptx::ex2(z.y));
+                            const uint64_t y2 = ptx::f32x2(y.x, y.y);
+                            const uint64_t l2 = ptx::f32x2(l[e + q], l[e + q + 1]);
+                            const float2 s = ptx::f32x2_parts(kCodes ? ptx::fma2(y2, rv2, l2)
+                                                                     : ptx::add2(l2, y2));
+                            l[e + q] = s.x;
+                            l[e + q + 1] = s.y;
+                            pk[q / 2] = pack2(y.x, y.y);
                         }
-                        scores(c, x, f, simple);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint32_t pk[4];
-#pragma unroll
-                            for (int q = 0; q < 8; q += 2) {
-                                const float2 o =
-                                    *reinterpret_cast<const float2 *>(off + c + e + q);
-                                const float2 z = exponents(x, f, e + q, o.x, o.y);
-                                top = fmaxf(fmaxf(top, z.x), z.y);
-                                const float2 y = make_float2(ptx::ex2(z.x), ptx::ex2(z.y));
-                                const uint64_t y2 = ptx::f32x2(y.x, y.y);
-                                const uint64_t l2 = ptx::f32x2(l[e + q], l[e + q + 1]);
-                                const float2 s = ptx::f32x2_parts(kCodes ? ptx::fma2(y2, rv2, l2)
-                                                                         : ptx::add2(l2, y2));
-                                l[e + q] = s.x;
-                                l[e + q + 1] = s.y;
-                                pk[q / 2] = pack2(y.x, y.y);
-                            }
-                            put_shared16(to + (c + e) / 8 * (16 * kTile),
-                                         make_uint4(pk[0], pk[1], pk[2], pk[3]));
-                        }
-                        if constexpr (kC > 32) umma::st32(t_l + lanes + c, l);
+                        put_shared16(to + (c0 + e) / 8 * (16 * kTile),
+                                     make_uint4(pk[0], pk[1], pk[2], pk[3]));
                     }
-                    if constexpr (kC > 32) umma::wait_st();
                     return top;
                 };
                 // New references: the rows' maxima over the tile, where these are above.
                 auto references = [&]() {
-#pragma unroll 1
-                    for (int c = c0; c < c0 + kC; c += 32) {
-                        float x[32], f;
-                        umma::ld32(t_s(g) + lanes + c, x);
-                        scores(c, x, f, std::false_type());
+                    float x[kRows], f;
+                    scores(x, f, std::false_type());
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 m =
-                                make_float4(warp_max(x[e] * f), warp_max(x[e + 1] * f),
-                                            warp_max(x[e + 2] * f), warp_max(x[e + 3] * f));
-                            if (lane == 0) *reinterpret_cast<float4 *>(sums + quad * kN + c + e) = m;
-                        }
+                    for (int e = 0; e < kRows; e += 4) {
+                        const float4 m = make_float4(warp_max(x[e] * f), warp_max(x[e + 1] * f),
+                                                     warp_max(x[e + 2] * f), warp_max(x[e + 3] * f));
+                        if (lane == 0) *reinterpret_cast<float4 *>(sums + quad * kN + c0 + e) = m;
                     }
                     group_sync(i);
-                    if (key < kC) {
+                    if (key < kRows) {
                         float m = ref[t];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) m = fmaxf(m, sums[q * kN + t]);
@@ -747,26 +734,20 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 // be nothing; else the reference grows by 2^kLazy at least, and with it the
                 // rounding of a sum that held too much goes below the sum's own.)
                 auto follow = [&]() {
-#pragma unroll 1
-                    for (int c = c0; c < c0 + kC; c += 32) {
-                        float x[32], f;
-                        umma::ld32(t_s(g) + lanes + c, x);
-                        if constexpr (kC > 32) umma::ld32(t_l + lanes + c, l);
-                        scores(c, x, f, std::false_type());
+                    float x[kRows], f;
+                    scores(x, f, std::false_type());
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const float2 z = exponents(x, f, e, old[c + e], old[c + e + 1]);
-                            const float a = fmaf(-ptx::ex2(z.x), rv, l[e]);
-                            const float b = fmaf(-ptx::ex2(z.y), rv, l[e + 1]);
-                            l[e] = z.x > 100.f ? 0.f : a * fac[c + e];
-                            l[e + 1] = z.y > 100.f ? 0.f : b * fac[c + e + 1];
-                        }
-                        if constexpr (kC > 32) umma::st32(t_l + lanes + c, l);
+                    for (int e = 0; e < kRows; e += 2) {
+                        const float2 z = exponents(x, f, e, old[c0 + e], old[c0 + e + 1]);
+                        const float a = fmaf(-ptx::ex2(z.x), rv, l[e]);
+                        const float b = fmaf(-ptx::ex2(z.y), rv, l[e + 1]);
+                        l[e] = z.x > 100.f ? 0.f : a * fac[c0 + e];
+                        l[e + 1] = z.y > 100.f ? 0.f : b * fac[c0 + e + 1];
                     }
-                    fail |= !wait(pv_done(i, g - 1), (g - 1) >> 1 & 1);
+                    fail |= !wait(pv_done(pr, g - 1), (g - 1) >> 1 & 1);
                     umma::fence_after();
 #pragma unroll 1
-                    for (int c = c0; c < c0 + kC; c += 16) {
+                    for (int c = c0; c < c0 + kRows; c += 16) {
                         float o[16];
                         umma::ld16(t_o + lanes + c, o);
                         umma::wait_ld();
@@ -794,26 +775,19 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 umma::fence_before();
                 __syncwarp();
                 if (trial) break;
-                if (lane == 0) ptx::mbar_arrive(p_full(i, g));
+                if (lane == 0) ptx::mbar_arrive(p_full(pr, g));
                 ++g;
             }
             if (left) break;
             // the rows' sums, the quarters of the keys in their order
-            if (!trial) fail |= !wait(pv_done(i, g - 1), (g - 1) >> 1 & 1);
+            if (!trial) fail |= !wait(pv_done(pr, g - 1), (g - 1) >> 1 & 1);
             umma::fence_after();
-#pragma unroll 1
-            for (int c = c0; c < c0 + kC; c += 32) {
-                if constexpr (kC > 32) {
-                    umma::ld32(t_l + lanes + c, l);
-                    umma::wait_ld();
-                }
-                lane_sums(l, lane);
-                sums[quad * kN + c + lane] = l[0];
-            }
+            lane_sums(l, lane);
+            sums[quad * kN + c0 + lane] = l[0];
             if (group_any(i, fail)) break;
             const bool bad = bad_tree || flags[1 + (k & 1)] != 0;
             const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + max(part, 0);
-            if (key < kC) {
+            if (key < kRows) {
                 const float a = sums[t] + sums[kN + t] + sums[2 * kN + t] + sums[3 * kN + t];
                 fac[t] = a > 0.f ? 1.f / a : a;   // a row that saw nothing: zeros; NaN stays
                 if (part >= 0) p.part_ml[slot * kN + t] = make_float2(ref[t], bad ? -1.f : a);
@@ -822,7 +796,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
             const int dim = kD == 128 ? key : 16 * quad + lane;   // M = 64 has 16 of 32 lanes
             const bool has = kD == 128 || lane < 16, odd = lane & 1;
 #pragma unroll 1
-            for (int c = c0; c < c0 + kC; c += 16) {
+            for (int c = c0; c < c0 + kRows; c += 16) {
                 float o[16];
                 umma::ld16(t_o + lanes + c, o);
                 umma::wait_ld();
@@ -858,7 +832,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
             const Waiter wait = waiter.as(kRoleProducts);
             if (umma::elect_one()) {
                 constexpr uint32_t kQk = umma::f16_idesc(kTile, kN, false);
-                constexpr uint32_t kPv = umma::f16_idesc(kD, kC, true) | umma::kAMn;
+                constexpr uint32_t kPv = umma::f16_idesc(kD, kP, true) | umma::kAMn;
                 const uint32_t q_lo = umma::desc_lo(base, 16);
                 const uint32_t k_lo = umma::desc_lo(base + M::kRing, 16);
                 const uint32_t v_lo = umma::desc_lo(base + M::kRing, M::kHalfBytes);
@@ -898,17 +872,17 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                         const uint32_t n = 2 * g + 1, s = n % S;
                         ok = wait.one(full(s), (n / S) & 1);
                         const uint32_t a = v_lo + s * (M::kTileBytes >> 4);
-                        for (int i = 0; i < kGroups && ok; ++i) {
-                            ok = wait.one(p_full(i, g), g >> 1 & 1);
+                        for (int q = 0; q < kProducts && ok; ++q) {
+                            ok = wait.one(p_full(q, g), g >> 1 & 1);
                             if (!ok) break;
                             umma::fence_after();
                             const uint64_t b =
-                                p_at + ((g % M::kPBufs * M::kPBytes + i * (kC * 2 * kTile)) >> 4);
+                                p_at + ((g % M::kPBufs * M::kPBytes + q * (kP * 2 * kTile)) >> 4);
 #pragma unroll
                             for (int k2 = 0; k2 < kTile / 16; ++k2)   // O^T += V^T P^T
-                                umma::mma_ss(t_o + i * kC, umma::desc(a + k2 * (2048 >> 4)),
+                                umma::mma_ss(t_o + q * kP, umma::desc(a + k2 * (2048 >> 4)),
                                              b + k2 * (256 >> 4), kPv, j > 0 || k2 > 0);
-                            umma::commit(pv_done(i, g));
+                            umma::commit(pv_done(q, g));
                         }
                         if (!ok) break;
                         umma::commit(empty(s));
@@ -1239,20 +1213,25 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                     if (!ok) break;
                     const uint32_t src = base + M::kCodeRing + (n % R) * M::kCodeBytes;
                     const uint32_t dst = base + M::kRing + (n % S) * M::kTileBytes;
-                    // all loads first; rows advance by whole groups of eight, so the
-                    // swizzles stay
+                    // loads first; rows advance by whole groups of eight, so the swizzles
+                    // stay
                     const uint32_t sx = kD == 128 ? (ch ^ (row0 & 7)) : (ch ^ ((row0 >> 1) & 3));
                     const uint32_t from = src + row0 * kD + (sx << 4);
                     const uint32_t to = dst + (ch >> 2) * M::kHalfBytes + row0 * 128;
                     const int c_a = ((2 * ch) & 7) ^ (row0 & 7);
-                    uint4 w[kLoads];
+                    constexpr int kAt = kLoads < 4 ? kLoads : 4;   // registers
 #pragma unroll
-                    for (int e = 0; e < kLoads; ++e) w[e] = ptx::lds128(from + e * kStep * kD);
+                    for (int e0 = 0; e0 < kLoads; e0 += kAt) {
+                        uint4 w[kAt];
 #pragma unroll
-                    for (int e = 0; e < kLoads; ++e) {
-                        st_shared16(to + e * kStep * 128 + (c_a << 4), widen<kKv>(w[e].x, w[e].y));
-                        st_shared16(to + e * kStep * 128 + ((c_a ^ 1) << 4),
-                                    widen<kKv>(w[e].z, w[e].w));
+                        for (int e = 0; e < kAt; ++e)
+                            w[e] = ptx::lds128(from + (e0 + e) * kStep * kD);
+#pragma unroll
+                        for (int e = 0; e < kAt; ++e) {
+                            const uint32_t at = to + (e0 + e) * kStep * 128;
+                            st_shared16(at + (c_a << 4), widen<kKv>(w[e].x, w[e].y));
+                            st_shared16(at + ((c_a ^ 1) << 4), widen<kKv>(w[e].z, w[e].w));
+                        }
                     }
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
