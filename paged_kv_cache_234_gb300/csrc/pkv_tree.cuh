@@ -285,6 +285,13 @@ __device__ __forceinline__ float warp_max(float x)
     return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // Eight codes as fp16 values, exactly.
 template <int kKv>
 __device__ __forceinline__ uint4 widen(uint32_t a, uint32_t b)
@@ -429,28 +436,13 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
         ptx::prefetch_tmap(&tmv);
     }
     if (warp == kSoftWarps) umma::alloc(base + M::kFlags + 12, 512);
-    {
-        // what the CTAs look up one after the other, on its way to L2
-        const int64_t at = 128 * (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x);
-        auto fetch = [&](const void *from, int64_t bytes) {
-            if (at < bytes) ptx::prefetch_l2(static_cast<const char *>(from) + at);
-        };
-        fetch(p.query_starts, 4 * static_cast<int64_t>(p.num_seqs));
-        fetch(p.context_lens, 4 * static_cast<int64_t>(p.num_seqs));
-        fetch(p.parents, 4 * static_cast<int64_t>(p.num_tokens));
-        fetch(p.block_tables, 4 * static_cast<int64_t>(p.num_seqs) * p.max_blocks_per_seq);
-        const int64_t scales = 4 * static_cast<int64_t>(p.num_blocks) * p.num_kv_heads;
-        if (kCodes && scales <= (1 << 20)) {
-            fetch(p.k_scales, scales);
-            fetch(p.v_scales, scales);
-        }
-    }
     umma::fence_before();
     __syncthreads();
     umma::fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, static_cast<uint32_t>(flags[3]), 0);
-    ptx::griddep_wait();
+    // (each role waits for the work before this launch where it touches its data)
     ptx::griddep_launch_dependents();
+
     auto t_s = [&](uint32_t g) { return tmem + kN * (g & 1); };   // S^T of tile g
     const uint32_t t_o = tmem + 2 * kN;                           // O^T
 
@@ -475,19 +467,15 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
         auto four = [](const float *v, int c) { return *reinterpret_cast<const float4 *>(v + c); };
         uint32_t g = 0;        // tiles of keys of the CTA so far
         bool fail = false;     // of this warp's waits; a group leaves together, at a barrier
-        // While the first loads are on their way the warps walk through an item of one
-        // tile and no rows (k = -1), without its waits and arrivals: so the instructions
-        // are there when the first tile is, some 8 KB that otherwise arrive line by line.
-        for (int k = -1;; ++k) {
-            const bool trial = k < 0;
-            if (!trial) fail |= !wait(i_full(k), k >> 1 & 1);
-            const TreeItem &it = item(max(k, 0));
-            const int nt = trial ? 1 : it.nt, n = trial ? 0 : it.n, ctx = trial ? 0 : it.base;
-            const int pre = trial ? INT32_MAX : it.pre, np1 = trial ? 0 : it.np1;
-            const int gap = trial ? 0 : it.gap, ta = trial ? 0 : it.ta, part = trial ? -1 : it.part;
+        ptx::griddep_wait();
+        for (int k = 0;; ++k) {
+            fail |= !wait(i_full(k), k >> 1 & 1);
+            const TreeItem &it = item(k);
+            const int nt = it.nt, n = it.n, ctx = it.base, pre = it.pre, np1 = it.np1, gap = it.gap;
+            const int ta = it.ta, part = it.part;
             auto real = [&](int v) { return v + (v >= np1 ? gap : 0); };
             const int rj = t / p.chunk, rh = t - rj * p.chunk;   // token and head of row t
-            const bool mine = !trial && key < kRows && rj < it.toks && rh < it.heads;
+            const bool mine = key < kRows && rj < it.toks && rh < it.heads;
             if (key < kRows && nt > 0) {
                 // rows that are not the item's: a reference that nothing exceeds
                 off[t] = mine ? kLift - kNone : -INFINITY;
@@ -498,12 +486,12 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                     slp[t] = mine && !fail ? __ldg(p.slopes + it.head + rh) * 1.4426950408889634f
                                            : 0.f;
             }
-            if (!trial) fail |= !wait(t_full(k), k >> 1 & 1);
+            fail |= !wait(t_full(k), k >> 1 & 1);
             if (group_any(i, fail)) break;
             if (nt == 0) break;
-            const bool bad_tree = !trial && flags[4 + (k & 1)] != 0;
+            const bool bad_tree = flags[4 + (k & 1)] != 0;
             const int *up = reinterpret_cast<const int *>(smem + M::kUp) + kParents * (k & 1);
-            const int32_t *par = p.parents + (trial ? 0 : it.start);
+            const int32_t *par = p.parents + it.start;
             auto parent = [&](int j) { return j < kParents ? up[j] : __ldg(par + j); };
             const int node = mine && !bad_tree ? it.row + rj : -1;
             int lo = 0;
@@ -513,17 +501,24 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                     for (int j = parent(node); j >= 0; j = parent(j)) ++pos;
                 lo = max(pos - p.window + 1, 0);
             }
+            // whether some rows of the group are not the item's
+            const bool ragged = it.toks < p.tokens || it.heads < p.chunk ||
+                                c0 + kRows > p.tokens * p.chunk;
+            // all rows see all keys of the tiles (of 8 pages) clean_a <= t < clean_b, which
+            // lie behind the gap, and t < clean_p, in the prefix
+            const int late = ctx + n - 1 - p.window;   // the deepest row sees what is behind
+            const int first = p.window > 0 && late >= 0 ? late / kPage + 1 - gap : 0;
+            const int clean_a = (max(first, gap ? np1 : 0) + kPagesPerTile - 1) / kPagesPerTile;
+            const int clean_b = max(ctx / kPage - gap, 0) / kPagesPerTile;
+            const int clean_p = (gap ? min(pre / kPage, np1) : pre / kPage) / kPagesPerTile;
+            const bool plain = !(p.cap > 0.f) && !p.slopes;
             bool left = false;
             float l[kRows];   // the thread's shares of the rows' sums
 #pragma unroll
             for (int e = 0; e < kRows; ++e) l[e] = 0.f;
             for (int j = 0; j < nt; ++j) {
                 const int v0 = (ta + j) * kPagesPerTile;
-                const int t0 = real(v0) * kPage;
-                const int t1 = real(v0 + kPagesPerTile - 1) * kPage + kPage - 1;
-                // whether all rows see all keys
-                const bool clean =
-                    (t1 < ctx && (p.window <= 0 || ctx + n - 1 - t0 < p.window)) || t1 < pre;
+                const bool clean = (ta + j >= clean_a && ta + j < clean_b) || ta + j < clean_p;
                 const int at = real(v0 + (key >> 4)) * kPage + (key & 15);   // the key's slot
                 if (!clean) {
                     // bits of the keys that row t sees
@@ -537,7 +532,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                                     (below(ctx - k0) & ~below(lo - k0)) | below(pre - k0);
                                 w[q >> 1] |= seen << (q & 1) * 16;
                             }
-                            if (t1 >= ctx)
+                            if (real(v0 + kPagesPerTile) * kPage > ctx)
                                 for (int a = node, far = 0;
                                      a >= 0 && (p.window <= 0 || far < p.window);
                                      a = parent(a), ++far) {
@@ -565,36 +560,8 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                     }
                     far = static_cast<float>(d);
                 }
-                // the probabilities' buffer was read by the product before
-                const uint32_t was = g - M::kPBufs;
-                if (!trial) {
-                    fail |= !wait(s_full(g), g >> 1 & 1);
-                    if (g >= M::kPBufs) fail |= !wait(pv_done(pr, was), was >> 1 & 1);
-                }
+                fail |= !wait(s_full(g), g >> 1 & 1);
                 umma::fence_after();
-                if (!clean) {
-                    // V rows of keys that no row of the tree sees may hold anything, NaN
-                    // included (and are not loaded for pages past the item's last):
-                    // zeros.  The product waits for this; the other group writes the same.
-                    const bool dead = v0 + (key >> 4) >= it.visited || at >= ctx + n ||
-                                      (at < it.lo && at >= pre);
-                    if (__any_sync(0xffffffffu, dead)) {
-                        // (the stage's element before this one must have landed: it is K
-                        // of a tile before, or V of one whose product is done)
-                        if (S == 2 && g > 0) fail |= !wait(pv_done(pr, g - 1), (g - 1) >> 1 & 1);
-                        static_assert(S % 2 ? S >= 3 : S == 2 || S / 2 >= M::kPBufs,
-                                      "phase of the stage");
-                        const uint32_t e = 2 * g + 1;
-                        fail |= !wait(full(e % S), (e / S) & 1);
-                        const uint32_t row =
-                            base + M::kRing + (e % S) * M::kTileBytes + key * 128;
-                        if (dead)
-#pragma unroll 1
-                            for (int b = 0; b < kD / 8; ++b)
-                                st_shared16(row + (b >> 3) * M::kHalfBytes + (b & 7) * 16,
-                                            make_uint4(0, 0, 0, 0));
-                    }
-                }
                 // what a product is multiplied with, log2 of the page's V scale, and
                 // the scale's reciprocal
                 float f0 = p.scale_log2;
@@ -644,13 +611,15 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                             // (unseen keys and other rows have no say in how it is
                             // evaluated)
                             if (!clean) hide(0.f);
+                            if (ragged) {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const float4 o = four(off, c0 + e);
-                                if (o.x == -INFINITY) x[e] = 0.f;
-                                if (o.y == -INFINITY) x[e + 1] = 0.f;
-                                if (o.z == -INFINITY) x[e + 2] = 0.f;
-                                if (o.w == -INFINITY) x[e + 3] = 0.f;
+                                for (int e = 0; e < kRows; e += 4) {
+                                    const float4 o = four(off, c0 + e);
+                                    if (o.x == -INFINITY) x[e] = 0.f;
+                                    if (o.y == -INFINITY) x[e + 1] = 0.f;
+                                    if (o.z == -INFINITY) x[e + 2] = 0.f;
+                                    if (o.w == -INFINITY) x[e + 3] = 0.f;
+                                }
                             }
                             tanh_all(x);
                         }
@@ -684,15 +653,16 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 // into the sums.  Returns the largest exponent.
                 auto probabilities = [&](auto simple) -> float {
                     float top = -INFINITY, x[kRows], f;
+                    uint32_t pk[kRows / 2];
                     scores(x, f, simple);
 #pragma unroll
-                    for (int e = 0; e < kRows; e += 8) {
-                        uint32_t pk[4];
+                    for (int e = 0; e < kRows; e += 4) {
+                        const float4 o = four(off, c0 + e);
 #pragma unroll
-                        for (int q = 0; q < 8; q += 2) {
-                            const float2 o = *reinterpret_cast<const float2 *>(off + c0 + e + q);
-                            const float2 z = exponents(x, f, e + q, o.x, o.y);
-                            top = fmaxf(fmaxf(top, z.x), z.y);
+                        for (int q = 0; q < 4; q += 2) {
+                            const float2 z = q == 0 ? exponents(x, f, e, o.x, o.y)
+                                                    : exponents(x, f, e + 2, o.z, o.w);
+                            top = max3(top, z.x, z.y);
                             const float2 y = make_float2(ptx::ex2(z.x), ptx::ex2(z.y));
                             const uint64_t y2 = ptx::f32x2(y.x, y.y);
                             const uint64_t l2 = ptx::f32x2(l[e + q], l[e + q + 1]);
@@ -700,11 +670,17 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                                                                      : ptx::add2(l2, y2));
                             l[e + q] = s.x;
                             l[e + q + 1] = s.y;
-                            pk[q / 2] = pack2(y.x, y.y);
+                            pk[(e + q) / 2] = pack2(y.x, y.y);
                         }
-                        put_shared16(to + (c0 + e) / 8 * (16 * kTile),
-                                     make_uint4(pk[0], pk[1], pk[2], pk[3]));
                     }
+                    // (the buffer was read by the product before)
+                    const uint32_t was = g - M::kPBufs;
+                    if (g >= M::kPBufs) fail |= !wait(pv_done(pr, was), was >> 1 & 1);
+#pragma unroll
+                    for (int e = 0; e < kRows; e += 8)
+                        put_shared16(to + (c0 + e) / 8 * (16 * kTile),
+                                     make_uint4(pk[e / 2], pk[e / 2 + 1], pk[e / 2 + 2],
+                                                pk[e / 2 + 3]));
                     return top;
                 };
                 // New references: the rows' maxima over the tile, where these are above.
@@ -761,9 +737,8 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 // probabilities hold; later an exponent too far above its reference makes
                 // the tile's be worked out once more.
                 if (j == 0) references();
-                const bool simple = clean && !(p.cap > 0.f) && !p.slopes;
-                const float top = simple ? probabilities(std::true_type())
-                                         : probabilities(std::false_type());
+                const float top = clean && plain ? probabilities(std::true_type())
+                                                 : probabilities(std::false_type());
                 if (group_any(i, fail || (j > 0 && top > kLift + kLazy))) {
                     left = group_any(i, fail);
                     if (left) break;
@@ -771,16 +746,38 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                     follow();
                     probabilities(std::false_type());
                 }
+                if (!clean) {
+                    // V rows of keys that no row of the tree sees may hold anything, NaN
+                    // included (and are not loaded for pages past the item's last):
+                    // zeros.  The product waits for this; the other group writes the same.
+                    const bool dead = v0 + (key >> 4) >= it.visited || at >= ctx + n ||
+                                      (at < it.lo && at >= pre);
+                    if (__any_sync(0xffffffffu, dead)) {
+                        // (the stage's element before this one must have landed: it is K
+                        // of a tile before, or V of one whose product is done)
+                        if (S == 2 && g > 0) fail |= !wait(pv_done(pr, g - 1), (g - 1) >> 1 & 1);
+                        static_assert(S % 2 ? S >= 3 : S == 2 || S / 2 >= M::kPBufs,
+                                      "phase of the stage");
+                        const uint32_t e = 2 * g + 1;
+                        fail |= !wait(full(e % S), (e / S) & 1);
+                        const uint32_t row =
+                            base + M::kRing + (e % S) * M::kTileBytes + key * 128;
+                        if (dead)
+#pragma unroll 1
+                            for (int b = 0; b < kD / 8; ++b)
+                                st_shared16(row + (b >> 3) * M::kHalfBytes + (b & 7) * 16,
+                                            make_uint4(0, 0, 0, 0));
+                    }
+                }
                 ptx::fence_proxy_async_smem();
                 umma::fence_before();
                 __syncwarp();
-                if (trial) break;
                 if (lane == 0) ptx::mbar_arrive(p_full(pr, g));
                 ++g;
             }
             if (left) break;
             // the rows' sums, the quarters of the keys in their order
-            if (!trial) fail |= !wait(pv_done(pr, g - 1), (g - 1) >> 1 & 1);
+            fail |= !wait(pv_done(pr, g - 1), (g - 1) >> 1 & 1);
             umma::fence_after();
             lane_sums(l, lane);
             sums[quad * kN + c0 + lane] = l[0];
@@ -823,7 +820,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
             // which come after this; its rows' places are written behind a barrier)
             umma::fence_before();
             group_sync(i);
-            if (!trial && lane == 0) ptx::mbar_arrive(i_empty(k));
+            if (lane == 0) ptx::mbar_arrive(i_empty(k));
         }
     } else if (warp < kSoftWarps + 4) {
         other_registers<kKv, kN>();
@@ -910,6 +907,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
             uint32_t tiles = 0;   // tiles of keys so far: ring elements 2 tiles (+ 1)
             int queries = 0;      // items whose queries were asked for
             bool ok = true;
+            ptx::griddep_wait();
             for (int k = 0; ok; ++k) {
                 ok = wait(i_full(k), k >> 1 & 1);
                 if (!ok) break;
@@ -956,16 +954,8 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                     scales_of(next, k_next, v_next);
                     ok = wait(eb, ((n / R) & 1) ^ 1);
                     if (!ok) break;
-                    if constexpr (kCodes)
-                        if (!is_v && lane < kPagesPerTile) {
-                            float *to = reinterpret_cast<float *>(smem + M::kScales) +
-                                        (tiles & (M::kScaleTiles - 1)) * 2 * kPagesPerTile + lane;
-                            to[0] = k_scale;
-                            to[kPagesPerTile] = v_scale;
-                        }
-                    __syncwarp();  // (the arrival is behind the flag and the scales)
                     if (umma::elect_one())
-                        ptx::mbar_arrive_expect_tx(fb, __popc(pages) * kBoxes * kBoxBytes);
+                        ptx::mbar_expect_tx(fb, __popc(pages) * kBoxes * kBoxBytes);
                     __syncwarp();
                     const uint32_t dst = ring + s * kStageBytes;
 #pragma unroll
@@ -978,7 +968,15 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                                                  b * kBox, y, fb);
                         }
                     }
-                    __syncwarp();
+                    if constexpr (kCodes)
+                        if (!is_v && lane < kPagesPerTile) {
+                            float *to = reinterpret_cast<float *>(smem + M::kScales) +
+                                        (tiles & (M::kScaleTiles - 1)) * 2 * kPagesPerTile + lane;
+                            to[0] = k_scale;
+                            to[kPagesPerTile] = v_scale;
+                        }
+                    __syncwarp();  // (the arrival is behind the flag and the scales)
+                    if (lane == 0) ptx::mbar_arrive(fb);
                     ++tiles;
                     blk = next;
                     next = after;
@@ -1013,6 +1011,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
             // ------------------------------------------------ the items of the piece
             const Waiter wait = waiter.as(kRoleItems);
             const int side = blockIdx.x % p.sides, piece = blockIdx.x / p.sides;
+            ptx::griddep_wait();
             // A sequence: its keys, and this side's items of it for a kv head's chunk of
             // heads (one tile where they only get zeros).
             struct Seq {
