@@ -550,10 +550,9 @@ PKV_API size_t pkv_prefill_workspace_size(int num_tokens, int num_seqs, int num_
  * with FP32 sums, maxima and accumulators; the probabilities (for code caches,
  * times the V scales) enter the second product rounded to fp16, as in
  * pkv_paged_prefill_*, relative to the largest such product of the row.  V
- * scales must not be negative; one that is, or is not finite, makes the rows
- * NaN that see its page.  Keys that no row of the same work item (up to 128 rows:
- * tokens times heads of a kv head) sees have no effect, whatever their slots
- * hold.  Keys and values that a row of the call sees must be finite.
+ * scales must not be negative; one that is not finite makes the rows that see its
+ * page not finite.  Keys that no row of the call sees have no effect,
+ * whatever their slots hold; those that one sees must be finite, and their values.
  *
  *   out, query  fp16 [num_tokens][num_heads][head_dim], 16-byte aligned
  *   query_starts, context_lens, num_tokens  the ragged batch;
@@ -567,7 +566,8 @@ PKV_API size_t pkv_prefill_workspace_size(int num_tokens, int num_seqs, int num_
  *               16-byte aligned; needs no initialisation
  * A sequence with a bad parent gets zeros.  A block id outside [0, num_blocks)
  * sets PKV_DEV_BAD_BLOCK; the outputs of every work item that needs the block
- * become zeros.  Two calls sharing a workspace must not overlap on the GPU.
+ * become zeros (an item is 256 rows, tokens times heads of a kv head, at most).
+ * Two calls sharing a workspace must not overlap on the GPU.
  */
 PKV_API pkv_status pkv_paged_tree_fp16(
     void *out, const void *query, const void *k_cache, const void *v_cache,
@@ -599,8 +599,8 @@ PKV_API pkv_status pkv_paged_tree_fp8(
     size_t workspace_bytes, int32_t *dev_status, void *stream);
 
 /*
- * Bytes of workspace a tree call with these sizes needs (any KV variant); 0 for
- * invalid sizes.  Not monotone: one workspace for several batches takes the
+ * Bytes of workspace a tree call with these sizes needs (any KV variant); 0 where
+ * none is, and for invalid sizes.  Not monotone: one workspace for several batches takes the
  * largest of their sizes.  Pure host arithmetic.
  */
 PKV_API size_t pkv_tree_workspace_size(int num_tokens, int num_seqs, int num_heads,

@@ -20,7 +20,8 @@ DEBUG_LIB_PATH = os.path.join(BUILD_DIR, "libpkv_debug.so")
 INCLUDE = os.path.join(os.path.dirname(PKG_DIR), "include")
 SOURCES = ("pkv_host.cu", "pkv_quantize.cu", "pkv_decode.cu", "pkv_decode_scored.cu",
            "pkv_prefill.cu", "pkv_tree.cu", "pkv_tree_fp16.cu", "pkv_tree_int8.cu",
-           "pkv_tree_fp8.cu", "pkv_accept.cu", "pkv_compact.cu", "pkv_append.cu", "pkv_rope.cu",
+           "pkv_tree_fp8.cu", "pkv_prefill_tree.cu", "pkv_accept.cu", "pkv_compact.cu",
+           "pkv_append.cu", "pkv_rope.cu",
            "pkv_evict.cu", "pkv_copy.cu", "pkv_block_manager.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -78,7 +79,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
 
 # the kernels with PKV_DEBUG checks and settings
 DEBUG_SOURCES = ("pkv_decode.cu", "pkv_decode_scored.cu", "pkv_prefill.cu", "pkv_tree.cu",
-                 "pkv_tree_fp16.cu", "pkv_tree_int8.cu", "pkv_tree_fp8.cu", "pkv_evict.cu")
+                 "pkv_tree_fp16.cu", "pkv_tree_int8.cu", "pkv_tree_fp8.cu",
+                 "pkv_prefill_tree.cu", "pkv_evict.cu")
 
 
 def build_debug() -> str:

@@ -59,6 +59,14 @@
 namespace pkv {
 namespace {
 
+// pkv_prefill_tree.cu compiles this file once more for trees of drafted tokens, whose
+// rows see the context, their ancestors and themselves.
+#ifdef PKV_PREFILL_TREES
+constexpr bool kTree = true;
+#else
+constexpr bool kTree = false;
+#endif
+
 constexpr int kRows = 256;      // query rows per item: two tiles
 constexpr int kTile = 128;      // rows per tile, keys per step
 constexpr int kPage = 16;
@@ -111,6 +119,8 @@ struct PrefillArgs {
     int tokens;         // tokens per item: 256 / chunk
     int max_blocks_per_seq, num_blocks, ctx_cap, window, splits, units;
     float scale_log2, cap, cap_inv;
+    const int32_t *parents;  // kTree: rows within the sequence, or -1
+    int max_tree_len;
 };
 
 // ------------------------------------------------------------ shared memory
@@ -161,7 +171,7 @@ struct __align__(16) Item {
     int tok, toks;              // first token (of the batch) and tokens of the item
     int head;                   // first query head
     int16_t heads, dir;         // heads; order of the tiles (see tile)
-    int pos;                    // position of the first token
+    int pos;                    // position of the first token (kTree: the context's length)
     int z;                      // split
     int lo, hi, pre;            // keys of the item: lo .. hi and below pre
     int np1, gap, visited;      // pages: np1, a gap, the rest (see the decode)
@@ -241,11 +251,11 @@ __device__ __forceinline__ int find_item(const PrefillArgs &p, int block, Item &
     it.heads = static_cast<int16_t>(min(p.chunk, p.group - c * p.chunk));
     it.dir = p.slopes ? -1 : 1;
     it.ta = it.nt = 0;
-    if (!sr.ok) return 0;
-    it.pos = sr.ctx - sr.len + static_cast<int>(t0);
-    it.hi = it.pos + it.toks - 1;
+    if (!sr.ok || (kTree && sr.len > p.max_tree_len)) return 0;
+    it.pos = sr.ctx - sr.len + (kTree ? 0 : static_cast<int>(t0));
+    it.hi = sr.ctx - sr.len + static_cast<int>(t0) + it.toks - 1;
     it.lo = p.window > 0 && it.pos >= p.window ? it.pos - p.window + 1 : 0;
-    it.pre = min(max(pre, 0), sr.ctx);
+    it.pre = min(max(pre, 0), kTree ? it.pos : sr.ctx);
     const int fp = it.lo / kPage;
     it.np1 = min((it.pre + kPage - 1) / kPage, fp);
     it.gap = fp - it.np1;
@@ -262,6 +272,11 @@ __device__ __noinline__ void check_sequences(const PrefillArgs &p, int lane)
 {
     report_bad_sequences(p.query_starts, p.context_lens, p.num_seqs, p.num_tokens, p.ctx_cap,
                          p.dev_status, lane, 32);
+    if constexpr (kTree)
+        for (int s = lane; s < p.num_seqs; s += 32)
+            if (static_cast<int64_t>(__ldg(p.query_starts + s + 1)) - __ldg(p.query_starts + s) >
+                p.max_tree_len)
+                atomicOr(p.dev_status, static_cast<int32_t>(PKV_DEV_BAD_CTX));
 }
 
 // ------------------------------------------------------------------ kernel
@@ -541,14 +556,34 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
             // begins at +inf, which nothing exceeds, and their capped scores are
             // 0 (or NaN, which a maximum leaves out).
             const bool mine = rj < it.toks && rh < it.heads;
-            const int pos = it.pos + min(rj, it.toks - 1);
-            const int lo = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
+            const int pos = kTree ? it.pos - 1 : it.pos + min(rj, it.toks - 1);
+            int lo = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
             const int pre = it.pre;
+            // kTree: the row's number in its tree, the tree's parents, and the row's depth.
+            // `pos` is the context's last position, up to which every row sees it (from
+            // `lo` on).  (A parent that is no earlier row, for which the item gets zeros,
+            // ends a walk.)
+            [[maybe_unused]] int node = 0, depth = 0;
+            [[maybe_unused]] const int32_t *parents = nullptr;
+            auto above = [&](int a) {
+                const int b = __ldg(parents + a);
+                return b < a ? b : -1;
+            };
+            if constexpr (kTree) {
+                const int row_a = it.hi - it.pos - it.toks + 1;
+                node = row_a + min(rj, it.toks - 1);
+                parents = p.parents + (it.tok - row_a);
+                if (p.window > 0 || (kMod && p.slopes)) {
+                    for (int a = above(node); a >= 0; a = above(a)) ++depth;
+                    if (p.window > 0) lo = max(it.pos + depth - p.window + 1, 0);
+                }
+            }
             // positions of the tile's first and last row; all of its rows see
             // all keys of the tiles (of 8 pages) clean_a <= t < clean_b, which
             // lie behind the gap, and t < clean_p, in the prefix
-            const int pos_a = it.pos + row0 / p.chunk;
-            const int pos_b = it.pos + (min(row0 + kTile, rows) - 1) / p.chunk;
+            // (kTree: the context's last one, and the deepest that a row can have)
+            const int pos_a = kTree ? pos : it.pos + row0 / p.chunk;
+            const int pos_b = kTree ? it.hi : it.pos + (min(row0 + kTile, rows) - 1) / p.chunk;
             const int first = p.window > 0 ? max(0, pos_b - p.window + kPage) / kPage - it.gap : 0;
             const int clean_a = (max(first, it.np1) + kPagesPerTile - 1) / kPagesPerTile;
             const int clean_b = max((pos_a + 1) / kPage - it.gap, 0) / kPagesPerTile;
@@ -573,9 +608,33 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                 // Tiles in which some row does not see some key: the rows'
                 // seen keys page by page; true if all rows see the whole page.
                 const bool clean = (tile >= clean_a && tile < clean_b) || tile < clean_p;
+                // kTree: the row's ancestors and itself among the tile's keys, within the
+                // window, and how many of them lie behind the tile.
+                [[maybe_unused]] uint32_t kin[4] = {0, 0, 0, 0};
+                [[maybe_unused]] int later = 0;
+                [[maybe_unused]] const bool drafted =
+                    kTree && !clean && it.real((tile + 1) * kPagesPerTile) * kPage > it.pos;
+                if constexpr (kTree)
+                    if (drafted)
+                        for (int a = node, far = 0; a >= 0 && (p.window <= 0 || far < p.window);
+                             a = above(a), ++far) {
+                            const int e = it.pos + a - it.gap * kPage - tile * kTile;
+                            if (e < 0) break;
+                            const uint32_t bit = 1u << (e & 31);
+                            if (e < 32) kin[0] |= bit;
+                            else if (e < 64) kin[1] |= bit;
+                            else if (e < 96) kin[2] |= bit;
+                            else if (e < kTile) kin[3] |= bit;
+                            else ++later;
+                        }
+                [[maybe_unused]] auto kin_of = [&](int q) -> uint32_t {   // of page q of 8
+                    const uint32_t w = q < 4 ? (q < 2 ? kin[0] : kin[1]) : (q < 6 ? kin[2] : kin[3]);
+                    return w >> (q & 1) * kPage & 0xffffu;
+                };
                 auto page_seen = [&](int g, uint32_t &seen) {
                     const int t0 = it.real(v0 + g) * kPage;
                     seen = (below(pos + 1 - t0) & ~below(lo - t0)) | below(pre - t0);
+                    if constexpr (kTree) seen |= kin_of(half * kColPages + g);
                     return (t0 + kPage - 1 <= pos_a && (p.window <= 0 || t0 > pos_b - p.window)) ||
                            t0 + kPage <= pre;
                 };
@@ -641,11 +700,28 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                     if (p.slopes) {
                         // - slope |pos - t|; keys ahead of a row are seen in the
                         // prefix only
-                        const bool ahead = it.real(v0) * kPage < pre;
+                        // (kTree: up to a constant of the row, - slope (pos - p(t)); of the
+                        // drafted keys those that are seen lie one step apart)
+                        const bool ahead = !kTree && it.real(v0) * kPage < pre;
+                        [[maybe_unused]] int far =
+                            later + __popc(kin[0]) + __popc(kin[1]) + __popc(kin[2]) + __popc(kin[3]);
+                        if (half) far -= __popc(kin[0]) + __popc(kin[1]);
 #pragma unroll
                         for (int g = 0; g < kColPages; ++g) {
                             const float f = static_cast<float>(pos - it.real(v0 + g) * kPage);
-                            if (ahead) {
+                            if (drafted) {
+                                uint32_t seen;
+                                page_seen(g, seen);
+#pragma unroll
+                                for (int c = 0; c < kPage; ++c) {
+                                    float d = f - c;
+                                    if (d < 0.f) {
+                                        far -= seen >> c & 1u;
+                                        d = static_cast<float>(far - depth - 1);
+                                    }
+                                    x[kPage * g + c] = fmaf(x[kPage * g + c], sl, -slope * d);
+                                }
+                            } else if (ahead) {
 #pragma unroll
                                 for (int c = 0; c < kPage; ++c)
                                     x[kPage * g + c] =
@@ -718,7 +794,10 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
 #pragma unroll 1
                                 for (int g = 0; g < kPagesPerTile; ++g) {
                                     const int t0 = it.real(tile * kPagesPerTile + g) * kPage;
-                                    if ((t0 <= pos && t0 + kPage > lo) || t0 < pre)
+                                    bool sees = (t0 <= pos && t0 + kPage > lo) || t0 < pre;
+                                    if constexpr (kTree)
+                                        sees |= kin_of(g) != 0;
+                                    if (sees)
                                         most = fmaxf(most, scales[kPagesPerTile + g]);
                                 }
                             }
@@ -1183,11 +1262,24 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                 __syncwarp();
                 Item it;
                 const int what = find_item(p, block, it);
+                [[maybe_unused]] bool wrong = false;   // kTree: a parent that is no earlier row
+                if constexpr (kTree)
+                    if (what > 0) {
+                        const int start = it.tok - (it.hi - it.pos - it.toks + 1);
+                        const int n = __ldg(p.query_starts + it.seq + 1) - start;
+                        for (int a = lane; a < n; a += 32) {
+                            const int b = __ldg(p.parents + start + a);
+                            wrong |= b < -1 || b >= a;
+                        }
+                        wrong = __any_sync(0xffffffffu, wrong);
+                        if (wrong && lane == 0 && p.dev_status)
+                            atomicOr(p.dev_status, static_cast<int32_t>(PKV_DEV_BAD_TREE));
+                    }
                 if (what > 0) {
                     ok = wait(i_empty(k), (k >> 1 & 1) ^ 1);
                     if (ok && lane == 0) {
                         item(k) = it;
-                        flags[1 + (k & 1)] = 0;
+                        flags[1 + (k & 1)] = kTree && wrong;
                         ptx::mbar_arrive(i_full(k));
                     }
                     __syncwarp();
@@ -1220,9 +1312,13 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                 if (!ok || !ptx::cancelled_block(base + M::kNext, block)) break;
                 ptx::fence_proxy_async_smem();  // read before the next answer is written
             }
-            if (kLate && first && p.dev_status)
-                report_bad_sequences(p.query_starts, p.context_lens, p.num_seqs, p.num_tokens,
-                                     p.ctx_cap, p.dev_status, lane, 32);
+            if (kLate && first && p.dev_status) {
+                if constexpr (kTree)
+                    check_sequences(p, lane);
+                else
+                    report_bad_sequences(p.query_starts, p.context_lens, p.num_seqs, p.num_tokens,
+                                         p.ctx_cap, p.dev_status, lane, 32);
+            }
             if (ok) ok = wait(i_empty(k), (k >> 1 & 1) ^ 1);
             if (ok && lane == 0) {
                 item(k).nt = 0;
@@ -1437,6 +1533,8 @@ struct PrefillCall {
     size_t workspace_bytes;
     int32_t *dev_status;
     void *stream;
+    const int32_t *parents = nullptr;   // kTree
+    int max_tree_len = 0;
 };
 
 struct Plan {
@@ -1568,6 +1666,8 @@ pkv_status launch_prefill(const PrefillCall &c, const Plan &plan)
     a.scale_log2 = c.softmax_scale * 1.4426950408889634f;
     a.cap = c.logit_cap * 1.4426950408889634f;
     a.cap_inv = c.logit_cap > 0.f ? 1.f / a.cap : 0.f;
+    a.parents = c.parents;
+    a.max_tree_len = c.max_tree_len;
 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim =
@@ -1640,6 +1740,7 @@ pkv_status prefill_entry(const PrefillCall &c, int kv)
 }  // namespace
 }  // namespace pkv
 
+#ifndef PKV_PREFILL_TREES
 extern "C" pkv_status pkv_paged_prefill_fp16(
     void *out, const void *query, const void *k_cache, const void *v_cache, int num_blocks,
     const int32_t *block_tables, int max_blocks_per_seq, const int32_t *query_starts,
@@ -1720,3 +1821,4 @@ extern "C" __attribute__((visibility("default"))) int pkv_debug_set_prefill(int 
     return 0;
 }
 #endif
+#endif  // !PKV_PREFILL_TREES

@@ -11,13 +11,9 @@ namespace pkv {
 namespace {
 
 constexpr int kPage = 16, kTile = 128;   // tokens of a page, keys of a step
-constexpr int kMostRows = 128;           // of an item
-constexpr int kSms = 152;                // GB300: pieces of the line of tiles
-constexpr int64_t kReread = 96 << 20;    // bytes that stay in L2 (129 MB)
 
-// From the sizes alone: items of 32 or 64 rows where no tree has more, else of 128.
-// Trees with more rows than an item have a CTA for every item, side by side, as many
-// as their mean length asks for.
+// From the sizes alone.  Up to 64 rows per kv head (tokens times heads) are the short
+// side of both products, keys the long one; with more the rows are.
 pkv_status tree_plan(int num_tokens, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
                      int max_context_len, int max_tree_len, TreePlan *plan)
 {
@@ -25,27 +21,21 @@ pkv_status tree_plan(int num_tokens, int num_seqs, int num_heads, int num_kv_hea
         max_context_len < 0 || max_tree_len < 0 || num_heads % num_kv_heads != 0)
         return PKV_ERR_INVALID_ARG;
     if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
-    const int group = num_heads / num_kv_heads;
-    int tree = max_tree_len < num_tokens ? max_tree_len : num_tokens;
-    if (tree < 1) tree = 1;
-    plan->chunk = group < kMostRows ? group : kMostRows;
-    plan->chunks = (group + plan->chunk - 1) / plan->chunk;
-    const int64_t rows = static_cast<int64_t>(tree) * plan->chunk;
-    plan->rows = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-    plan->tokens = plan->rows / plan->chunk;
-    const int mean = num_seqs > 0 ? (num_tokens - 1) / num_seqs + 1 : 1;
-    plan->sides = ((mean < tree ? mean : tree) - 1) / plan->tokens + 1;
-    if (plan->sides < 1) plan->sides = 1;
-    plan->pieces = plan->sides < kSms ? kSms / plan->sides : 1;
-    const size_t ctas = plan->sides < kSms ? kSms : plan->sides;   // at most
-    plan->bytes = ctas * (2 * plan->rows * (head_dim + 2) * sizeof(float) + kTreeMetaBytes);
+    const int tree = max_tree_len < num_tokens ? max_tree_len : num_tokens;
+    const int64_t rows = static_cast<int64_t>(tree) * (num_heads / num_kv_heads);
+    plan->rows = rows <= 32 ? 32 : rows <= 64 ? 64 : 0;
+    if (num_heads / num_kv_heads > 64) plan->rows = 0;
+    if (plan->rows == 0)
+        return tree_rows_workspace(num_tokens, num_seqs, num_heads, num_kv_heads, head_dim,
+                                   max_context_len, &plan->bytes);
+    plan->bytes =
+        kTreePieces * (2 * plan->rows * (head_dim + 2) * sizeof(float) + kTreeMetaBytes);
     return PKV_OK;
 }
 
-using Launch = pkv_status (*)(const TreeCall &, const TreePlan &);
-
-pkv_status tree_entry(const TreeCall &c, bool codes, Launch launch)
+pkv_status tree_entry(const TreeCall &c, TreeKind kind)
 {
+    const bool codes = kind != kTreeFp16;
     if (!c.kpool || !c.vpool || !c.query_starts) return PKV_ERR_INVALID_ARG;
     // (arrays without elements may be null)
     if (c.num_tokens != 0 && (!c.out || !c.query || !c.parents)) return PKV_ERR_INVALID_ARG;
@@ -70,23 +60,17 @@ pkv_status tree_entry(const TreeCall &c, bool codes, Launch launch)
         !aligned(c.prefix_lens, 4))
         return PKV_ERR_MISALIGNED;
     if (c.num_tokens == 0 || c.num_seqs == 0) return PKV_OK;
+    if (plan.rows == 0) return launch_tree_rows(c, kind);
     // the line of tiles is counted in 32 bits
     const int64_t cap = static_cast<int64_t>(c.max_blocks_per_seq) * kPage;
     const int64_t most = (c.max_context_len < cap ? c.max_context_len : cap) / kTile + 2;
-    const int64_t line = static_cast<int64_t>(plan.chunks) * c.num_kv_heads *
-                         (c.num_tokens / plan.tokens + static_cast<int64_t>(c.num_seqs));
+    const int64_t line = static_cast<int64_t>(c.num_seqs) * c.num_kv_heads;
     if (line > INT32_MAX || line * most > INT32_MAX) return PKV_ERR_UNSUPPORTED;
-    // Where the keys that all CTAs read for an item are likely to be in L2 still when
-    // they come to the next item of the tree, items follow one another: that fits
-    // trees of any lengths.
-    const int64_t keys = c.window > 0 && c.window < c.max_context_len ? c.window : c.max_context_len;
-    if (kSms * keys * c.head_dim * (codes ? 2 : 4) <= kReread) {
-        plan.sides = 1;
-        plan.pieces = kSms;
-    }
     if (plan.bytes > 0 && (!c.workspace || c.workspace_bytes < plan.bytes)) return PKV_ERR_WORKSPACE;
     if (!aligned(c.workspace, 16)) return PKV_ERR_MISALIGNED;
-    return launch(c, plan);
+    return kind == kTreeFp8    ? launch_tree_fp8(c, plan)
+           : kind == kTreeInt8 ? launch_tree_int8(c, plan)
+                               : launch_tree_fp16(c, plan);
 }
 
 }  // namespace
@@ -106,7 +90,7 @@ extern "C" pkv_status pkv_paged_tree_fp16(
                           max_context_len, max_tree_len, num_tokens, num_seqs, num_heads,
                           num_kv_heads, head_dim, block_size, softmax_scale, logit_cap, window,
                           slopes, prefix_lens, workspace, workspace_bytes, dev_status, stream};
-    return pkv::tree_entry(c, false, pkv::launch_tree_fp16);
+    return pkv::tree_entry(c, pkv::kTreeFp16);
 }
 
 extern "C" pkv_status pkv_paged_tree_int8(
@@ -123,7 +107,7 @@ extern "C" pkv_status pkv_paged_tree_int8(
                           max_context_len, max_tree_len, num_tokens, num_seqs, num_heads,
                           num_kv_heads, head_dim, block_size, softmax_scale, logit_cap, window,
                           slopes, prefix_lens, workspace, workspace_bytes, dev_status, stream};
-    return pkv::tree_entry(c, true, pkv::launch_tree_int8);
+    return pkv::tree_entry(c, pkv::kTreeInt8);
 }
 
 extern "C" pkv_status pkv_paged_tree_fp8(
@@ -140,7 +124,7 @@ extern "C" pkv_status pkv_paged_tree_fp8(
                           max_context_len, max_tree_len, num_tokens, num_seqs, num_heads,
                           num_kv_heads, head_dim, block_size, softmax_scale, logit_cap, window,
                           slopes, prefix_lens, workspace, workspace_bytes, dev_status, stream};
-    return pkv::tree_entry(c, true, pkv::launch_tree_fp8);
+    return pkv::tree_entry(c, pkv::kTreeFp8);
 }
 
 extern "C" size_t pkv_tree_workspace_size(int num_tokens, int num_seqs, int num_heads,
@@ -165,7 +149,8 @@ extern "C" __attribute__((visibility("default"))) int pkv_debug_set_tree(int giv
     if (give_role > 5 || slow_role > 5 || slow_ns < 0 || slow_ns > 1000000 ||
         cudaDeviceSynchronize() != cudaSuccess)
         return -1;
-    return pkv::set_tree_waits_fp16(give_role, give_at, slow_role, slow_ns) |
+    return pkv::set_tree_waits_rows(give_role, give_at, slow_role, slow_ns) |
+           pkv::set_tree_waits_fp16(give_role, give_at, slow_role, slow_ns) |
            pkv::set_tree_waits_int8(give_role, give_at, slow_role, slow_ns) |
            pkv::set_tree_waits_fp8(give_role, give_at, slow_role, slow_ns);
 }

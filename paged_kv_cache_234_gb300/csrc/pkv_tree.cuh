@@ -27,11 +27,12 @@
 // The tiles of all (sequence, kv head) pairs form one line, which is cut into as
 // many equal pieces as there are SMs: a CTA walks its piece, whatever the lengths
 // of the sequences.  Where a cut lies inside a pair, the parts are joined by a
-// second kernel.  Trees with more than N rows take a CTA for every N of them, side
-// by side on the same piece, so that they read the same pages at the same time.
+// second kernel.  (Up to 64 rows per kv head; with more the rows are the long side:
+// pkv_prefill_tree.cu.)
 //
-// Roles of the warps: 0-7 scores and rows, 8 issues the products, 9 and 11 the TMA
-// loads of K and Q, and of V (a ring of tiles, K and V in turn), 10 the items.
+// Roles of the warps: four for every 32 rows work on scores and rows; of the next four
+// one issues the products, two the TMA loads of K and Q, and of V (a ring of tiles, K
+// and V in turn), one finds the items.
 // INT8 / FP8 pages land in a second ring, and further warps widen them exactly to
 // fp16.  The K scale of a page multiplies its keys' scores.  Its V scale enters
 // the exponent, 2^(S' + log2 v - m), so that the reference is that of the largest
@@ -61,7 +62,6 @@ constexpr int kTile = 128;      // keys per step
 constexpr int kPagesPerTile = kTile / kPage;
 constexpr int kKvF16 = 0, kKvI8 = 1, kKvF8 = 2;
 constexpr int kGroup = 128;     // threads that share rows: one per key of a tile
-constexpr int kSms = 152;       // GB300: pieces of the line of tiles
 constexpr int kPieceTiles = 2;  // tiles of a piece at least
 constexpr float kLift = 6.f;    // log2 factor of the probabilities
 constexpr float kLazy = 9.f;    // log2 excess over the reference that is let be
@@ -79,27 +79,19 @@ __host__ __device__ constexpr int soft_warps(int rows)
     return 4 * (rows / kRows);
 }
 
-// Rows of one product V^T P^T, whose groups are waited for together: with fewer than 64
-// it would read V from shared memory more often than it computes.
-__host__ __device__ constexpr int product_rows(int rows)
+// Warps that widen codes.
+__host__ __device__ constexpr int widen_warps(int kv)
 {
-    return rows < 64 ? rows : 64;
-}
-
-// Warps that widen codes: 128 rows leave registers for four.
-__host__ __device__ constexpr int widen_warps(int kv, int rows)
-{
-    return kv == kKvF16 ? 0 : rows > 64 ? 4 : 8;
+    return kv == kKvF16 ? 0 : 8;
 }
 
 __host__ __device__ constexpr int tree_threads(int kv, int rows)
 {
-    return 32 * (soft_warps(rows) + 4 + widen_warps(kv, rows));
+    return 32 * (soft_warps(rows) + 4 + widen_warps(kv));
 }
 
 struct TreeMeta {               // the part of an item that a piece ends in
-    int tok, toks, head, heads, parts;
-    int unused[3];
+    int start, n, kvh, parts;
 };
 static_assert(sizeof(TreeMeta) == kTreeMetaBytes, "what the plan counts");
 
@@ -114,10 +106,7 @@ struct TreeArgs {
     TreeMeta *meta;     // [CTAs]
     int32_t *dev_status;
     int num_tokens, num_seqs, num_heads, num_kv_heads, group;
-    int chunk, chunks;  // heads of a kv head per item (the group, at most 128), chunks of them
-    int tokens;         // tokens per item
-    int sides;          // CTAs side by side on a piece, for every sides-th item of a tree
-    int pieces;
+    int tokens;         // tokens that an item's rows have room for
     int max_blocks_per_seq, num_blocks, ctx_cap, max_tree_len, window;
     float scale_log2, cap, cap_inv;
 };
@@ -131,12 +120,12 @@ struct TreeSmem {
     static constexpr int kTileBytes = kHalves * kHalfBytes;
     static constexpr int kQHalfBytes = kN * 128;               // 64 values of the rows
     static constexpr int kPBytes = kN * kTile * 2;
-    static constexpr int kPBufs = !kCodes && kN == 128 ? 1 : 2;
+    static constexpr int kPBufs = 2;
     static constexpr int kCodeBytes = kTile * kD;
     static constexpr int kMore = 128 / kD;
     static constexpr int kStages =
-        kMore * (kCodes ? (kN <= 64 ? 3 : 2) : kN <= 32 ? 6 : kN <= 64 ? 5 : 4);
-    static constexpr int kCodeStages = kCodes ? kMore * (kN <= 32 ? 6 : kN <= 64 ? 4 : 3) : 0;
+        kMore * (kCodes ? 3 : kN <= 32 ? 6 : 5);
+    static constexpr int kCodeStages = kCodes ? kMore * (kN <= 32 ? 6 : 4) : 0;
     // A waiting warp must not be two phases of a barrier off.  K and V have a producer
     // each, which has seen the element S + 2 before its next one given back and takes
     // for granted that the one 2 S before it was.  With an even number of stages these
@@ -148,9 +137,9 @@ struct TreeSmem {
     static constexpr int kRing = kP + kPBufs * kPBytes;
     static constexpr int kCodeRing = kRing + kStages * kTileBytes;
     static constexpr int kCtl = kCodeRing + kCodeStages * kCodeBytes;
-    static constexpr int kBars = 2 * kStages + 2 * kCodeStages + 19;
+    static constexpr int kBars = 2 * kStages + 2 * kCodeStages + 15;
     static constexpr int kItems = (kCtl + 8 * kBars + 15) & ~15;
-    static constexpr int kFlags = kItems + 2 * 80;
+    static constexpr int kFlags = kItems + 2 * 64;
     static constexpr int kIssued = kFlags + 32;   // see drain_copies
     // scales [kScaleTiles][K, V][8 pages], written by the K warp ahead of its
     // arrival for the tile's K codes; the scores of the tile are behind that.  The
@@ -197,39 +186,31 @@ struct SeqKeys {
 
 struct __align__(16) TreeItem {
     int seq, kvh;
-    int tok, toks;              // first token (of the batch) and tokens of the item
-    int head, heads;            // first query head, heads
-    int row;                    // row of the first token in its sequence
     int start, n;               // first token of the sequence, its tokens
     int base, lo, pre;          // see SeqKeys
-    int np1, gap, visited;      // visited: pages up to the item's last token
+    int np1, gap, visited;      // visited: pages
     int ta, nt;                 // tiles of keys: the first, how many; 0: no further item
     int part;                   // -1: the whole item; else part 0 or 1 of the CTA
-    int unused[2];
+    int unused[3];
 
     __device__ __forceinline__ int real(int v) const { return v + (v >= np1 ? gap : 0); }
 };
-static_assert(sizeof(TreeItem) == 80, "an item is 80 bytes of shared memory");
+static_assert(sizeof(TreeItem) == 64, "an item is 64 bytes of shared memory");
 
 // ------------------------------------------------------------------ kernel
 // Registers: all threads are launched with 65536 / threads, rounded down to a
-// multiple of 8 (fp16: 96 for the 640 threads of 128 rows; codes: 96 for the 640 of 64
-// rows, 80 for the 768 of 128).  The score threads, which hold 32 scores and 32 sums,
-// take what the others give back.
+// multiple of 8 (96 for the 640 threads of codes with 64 rows).  The score threads,
+// which hold 32 scores and 32 sums, take what the others give back.
 template <int kKv, int kN>
 __device__ __forceinline__ void soft_registers()
 {
-    if constexpr (kKv == kKvF16 && kN == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     if constexpr (kKv != kKvF16 && kN == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
-    if constexpr (kKv != kKvF16 && kN == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
 }
 
 template <int kKv, int kN>
 __device__ __forceinline__ void other_registers()
 {
-    if constexpr (kKv == kKvF16 && kN == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if constexpr (kKv != kKvF16 && kN == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if constexpr (kKv != kKvF16 && kN == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
 }
 
 // Barriers of a group of score warps alone.
@@ -375,8 +356,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
     constexpr bool kCodes = M::kCodes;
     constexpr int S = M::kStages;
     constexpr int kSoftWarps = soft_warps(kN);
-    constexpr int kP = product_rows(kN), kProducts = kN / kP;
-    constexpr int kWidenWarps = widen_warps(kKv, kN);
+    constexpr int kWidenWarps = widen_warps(kKv);
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = ptx::smem_addr(smem);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -389,14 +369,13 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
     };
     const uint32_t one = base + M::kCtl + 8 * (2 * S + 2 * M::kCodeStages);
     const uint32_t q_full = one, q_empty = one + 8, drain = one + 16;
-    // of tile number g of the CTA and product q: scores there, probabilities there,
-    // product done
+    // of tile number g of the CTA: scores there, probabilities there, product done
     auto s_full = [&](uint32_t g) { return one + 24 + 8 * (g & 1); };
-    auto p_full = [&](int q, uint32_t g) { return one + 40 + 8 * (2 * q + (g & 1)); };
-    auto pv_done = [&](int q, uint32_t g) { return one + 72 + 8 * (2 * q + (g & 1)); };
-    auto i_full = [&](int k) { return one + 104 + 8 * (k & 1); };
-    auto i_empty = [&](int k) { return one + 120 + 8 * (k & 1); };
-    auto t_full = [&](int k) { return one + 136 + 8 * (k & 1); };   // the item's tree is there
+    auto p_full = [&](uint32_t g) { return one + 40 + 8 * (g & 1); };
+    auto pv_done = [&](uint32_t g) { return one + 56 + 8 * (g & 1); };
+    auto i_full = [&](int k) { return one + 72 + 8 * (k & 1); };
+    auto i_empty = [&](int k) { return one + 88 + 8 * (k & 1); };
+    auto t_full = [&](int k) { return one + 104 + 8 * (k & 1); };   // the item's tree is there
     volatile int *flags = reinterpret_cast<volatile int *>(smem + M::kFlags);
     // flags: abort, bad block in item slot 0, in slot 1, TMEM address, bad tree in slots
     const Waiter waiter{flags, p.dev_status};
@@ -420,10 +399,8 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
         ptx::mbar_init(drain, 1);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(s_full(i), 1);
-            for (int h = 0; h < 2; ++h) {
-                ptx::mbar_init(p_full(h, i), 4 * (kP / kRows));
-                ptx::mbar_init(pv_done(h, i), 1);
-            }
+            ptx::mbar_init(p_full(i), kSoftWarps);
+            ptx::mbar_init(pv_done(i), 1);
             ptx::mbar_init(i_full(i), 1);
             ptx::mbar_init(t_full(i), 1);
             ptx::mbar_init(i_empty(i), kSoftWarps + 3 + (kCodes ? kWidenWarps : 0));
@@ -452,7 +429,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
         const Waiter wait = waiter.as(kRoleRows);
         const int i = warp >> 2, quad = warp & 3;       // the group; its quarter of the keys
         const int key = threadIdx.x & (kGroup - 1);     // the thread's key of a tile
-        const int c0 = i * kRows, pr = c0 / kP;         // the group's rows, their product
+        const int c0 = i * kRows;                       // the group's rows
         const uint32_t lanes = static_cast<uint32_t>(quad) << 21;   // TMEM lane 32 quad
         // the row that a thread looks after, if key < kRows
         const int t = c0 + key;
@@ -474,17 +451,17 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
             const int nt = it.nt, n = it.n, ctx = it.base, pre = it.pre, np1 = it.np1, gap = it.gap;
             const int ta = it.ta, part = it.part;
             auto real = [&](int v) { return v + (v >= np1 ? gap : 0); };
-            const int rj = t / p.chunk, rh = t - rj * p.chunk;   // token and head of row t
-            const bool mine = key < kRows && rj < it.toks && rh < it.heads;
+            const int rj = t / p.group, rh = t - rj * p.group;   // token and head of row t
+            const bool mine = key < kRows && rj < n;
+            const int head = it.kvh * p.group + rh;
             if (key < kRows && nt > 0) {
                 // rows that are not the item's: a reference that nothing exceeds
                 off[t] = mine ? kLift - kNone : -INFINITY;
                 ref[t] = kNone;
-                place[t] = mine ? static_cast<int64_t>(it.tok + rj) * p.num_heads + it.head + rh
+                place[t] = mine ? static_cast<int64_t>(it.start + rj) * p.num_heads + head
                                 : int64_t(-1);
                 if (p.slopes)
-                    slp[t] = mine && !fail ? __ldg(p.slopes + it.head + rh) * 1.4426950408889634f
-                                           : 0.f;
+                    slp[t] = mine && !fail ? __ldg(p.slopes + head) * 1.4426950408889634f : 0.f;
             }
             fail |= !wait(t_full(k), k >> 1 & 1);
             if (group_any(i, fail)) break;
@@ -493,7 +470,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
             const int *up = reinterpret_cast<const int *>(smem + M::kUp) + kParents * (k & 1);
             const int32_t *par = p.parents + it.start;
             auto parent = [&](int j) { return j < kParents ? up[j] : __ldg(par + j); };
-            const int node = mine && !bad_tree ? it.row + rj : -1;
+            const int node = mine && !bad_tree ? rj : -1;
             int lo = 0;
             if (p.window > 0) {
                 int pos = ctx;
@@ -502,8 +479,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 lo = max(pos - p.window + 1, 0);
             }
             // whether some rows of the group are not the item's
-            const bool ragged = it.toks < p.tokens || it.heads < p.chunk ||
-                                c0 + kRows > p.tokens * p.chunk;
+            const bool ragged = c0 + kRows > n * p.group;
             // all rows see all keys of the tiles (of 8 pages) clean_a <= t < clean_b, which
             // lie behind the gap, and t < clean_p, in the prefix
             const int late = ctx + n - 1 - p.window;   // the deepest row sees what is behind
@@ -675,7 +651,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                     }
                     // (the buffer was read by the product before)
                     const uint32_t was = g - M::kPBufs;
-                    if (g >= M::kPBufs) fail |= !wait(pv_done(pr, was), was >> 1 & 1);
+                    if (g >= M::kPBufs) fail |= !wait(pv_done(was), was >> 1 & 1);
 #pragma unroll
                     for (int e = 0; e < kRows; e += 8)
                         put_shared16(to + (c0 + e) / 8 * (16 * kTile),
@@ -720,7 +696,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                         l[e] = z.x > 100.f ? 0.f : a * fac[c0 + e];
                         l[e + 1] = z.y > 100.f ? 0.f : b * fac[c0 + e + 1];
                     }
-                    fail |= !wait(pv_done(pr, g - 1), (g - 1) >> 1 & 1);
+                    fail |= !wait(pv_done(g - 1), (g - 1) >> 1 & 1);
                     umma::fence_after();
 #pragma unroll 1
                     for (int c = c0; c < c0 + kRows; c += 16) {
@@ -755,7 +731,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                     if (__any_sync(0xffffffffu, dead)) {
                         // (the stage's element before this one must have landed: it is K
                         // of a tile before, or V of one whose product is done)
-                        if (S == 2 && g > 0) fail |= !wait(pv_done(pr, g - 1), (g - 1) >> 1 & 1);
+                        if (S == 2 && g > 0) fail |= !wait(pv_done(g - 1), (g - 1) >> 1 & 1);
                         static_assert(S % 2 ? S >= 3 : S == 2 || S / 2 >= M::kPBufs,
                                       "phase of the stage");
                         const uint32_t e = 2 * g + 1;
@@ -772,12 +748,12 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 ptx::fence_proxy_async_smem();
                 umma::fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(p_full(pr, g));
+                if (lane == 0) ptx::mbar_arrive(p_full(g));
                 ++g;
             }
             if (left) break;
             // the rows' sums, the quarters of the keys in their order
-            fail |= !wait(pv_done(pr, g - 1), (g - 1) >> 1 & 1);
+            fail |= !wait(pv_done(g - 1), (g - 1) >> 1 & 1);
             umma::fence_after();
             lane_sums(l, lane);
             sums[quad * kN + c0 + lane] = l[0];
@@ -829,7 +805,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
             const Waiter wait = waiter.as(kRoleProducts);
             if (umma::elect_one()) {
                 constexpr uint32_t kQk = umma::f16_idesc(kTile, kN, false);
-                constexpr uint32_t kPv = umma::f16_idesc(kD, kP, true) | umma::kAMn;
+                constexpr uint32_t kPv = umma::f16_idesc(kD, kN, true) | umma::kAMn;
                 const uint32_t q_lo = umma::desc_lo(base, 16);
                 const uint32_t k_lo = umma::desc_lo(base + M::kRing, 16);
                 const uint32_t v_lo = umma::desc_lo(base + M::kRing, M::kHalfBytes);
@@ -867,21 +843,16 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                             if (j + 2 == nt) umma::commit(q_empty);
                         }
                         const uint32_t n = 2 * g + 1, s = n % S;
-                        ok = wait.one(full(s), (n / S) & 1);
-                        const uint32_t a = v_lo + s * (M::kTileBytes >> 4);
-                        for (int q = 0; q < kProducts && ok; ++q) {
-                            ok = wait.one(p_full(q, g), g >> 1 & 1);
-                            if (!ok) break;
-                            umma::fence_after();
-                            const uint64_t b =
-                                p_at + ((g % M::kPBufs * M::kPBytes + q * (kP * 2 * kTile)) >> 4);
-#pragma unroll
-                            for (int k2 = 0; k2 < kTile / 16; ++k2)   // O^T += V^T P^T
-                                umma::mma_ss(t_o + q * kP, umma::desc(a + k2 * (2048 >> 4)),
-                                             b + k2 * (256 >> 4), kPv, j > 0 || k2 > 0);
-                            umma::commit(pv_done(q, g));
-                        }
+                        ok = wait.one(p_full(g), g >> 1 & 1) && wait.one(full(s), (n / S) & 1);
                         if (!ok) break;
+                        umma::fence_after();
+                        const uint32_t a = v_lo + s * (M::kTileBytes >> 4);
+                        const uint64_t b = p_at + (g % M::kPBufs * M::kPBytes >> 4);
+#pragma unroll
+                        for (int k2 = 0; k2 < kTile / 16; ++k2)   // O^T += V^T P^T
+                            umma::mma_ss(t_o, umma::desc(a + k2 * (2048 >> 4)), b + k2 * (256 >> 4),
+                                         kPv, j > 0 || k2 > 0);
+                        umma::commit(pv_done(g));
                         umma::commit(empty(s));
                     }
                     if (ok) ptx::mbar_arrive(i_empty(k));
@@ -989,11 +960,11 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                         ok = wait(q_empty, (k & 1) ^ 1);
                         if (!ok) break;
                         if (umma::elect_one()) {
-                            ptx::mbar_arrive_expect_tx(q_full, p.tokens * p.chunk * M::kHalves * 128);
+                            ptx::mbar_arrive_expect_tx(q_full, p.tokens * p.group * M::kHalves * 128);
     #pragma unroll
                             for (int b = 0; b < M::kHalves; ++b)
-                                ptx::tma_load_3d(base + b * M::kQHalfBytes, &tmq, b * 64, it.head,
-                                                 it.tok, q_full);
+                                ptx::tma_load_3d(base + b * M::kQHalfBytes, &tmq, b * 64,
+                                                 it.kvh * p.group, it.start, q_full);
                         }
                         __syncwarp();
                         ++queries;
@@ -1010,14 +981,11 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
         } else {
             // ------------------------------------------------ the items of the piece
             const Waiter wait = waiter.as(kRoleItems);
-            const int side = blockIdx.x % p.sides, piece = blockIdx.x / p.sides;
+            const int piece = blockIdx.x;
             ptx::griddep_wait();
-            // A sequence: its keys, and this side's items of it for a kv head's chunk of
-            // heads (one tile where they only get zeros).
             struct Seq {
                 SeqRows rows;
-                SeqKeys keys;
-                int items;
+                SeqKeys keys;   // (one tile where the rows only get zeros)
                 bool zeros;
             };
             auto sequence = [&](int s) -> Seq {
@@ -1027,20 +995,13 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 const int pre = p.prefix_lens ? __ldg(p.prefix_lens + s) : 0;
                 q.rows.set(first, last, len, p.num_tokens, p.ctx_cap);
                 q.zeros = first != last && (!q.rows.ok || q.rows.len > p.max_tree_len);
-                q.items = 0;
                 q.keys = SeqKeys{};
-                if (q.rows.len == 0) return q;
-                if (q.zeros) {
-                    q.items = side == 0;
-                    q.keys.tiles = 1;
-                } else {
-                    const int all = (q.rows.len - 1) / p.tokens + 1;
-                    q.items = all > side ? (all - 1 - side) / p.sides + 1 : 0;
+                if (q.zeros)
+                    q.keys.tiles = q.rows.len > 0;
+                else if (q.rows.len > 0)
                     q.keys.set(p, q.rows.ctx, q.rows.len, pre);
-                }
                 return q;
             };
-            const int heads = p.num_kv_heads * p.chunks;   // items of a sequence's row chunk
             // The whole line, then where the piece begins: twice over the sequences, 32
             // at a time.
             int total = 0, begin = 0, end = 0, quo = 0, rem = 0;
@@ -1053,7 +1014,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 if (s0 >= p.num_seqs) {
                     if (pass == 1 || total == 0) break;
                     // (cuts are whole tiles, pieces not below kPieceTiles where they can)
-                    const int pieces = max(min(total / kPieceTiles, p.pieces), 1);
+                    const int pieces = max(min(total / kPieceTiles, kTreePieces), 1);
                     quo = total / pieces;
                     rem = total - quo * pieces;
                     begin = piece < pieces ? cut(piece) : total;
@@ -1065,7 +1026,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 int t = 0;
                 if (s0 + lane < p.num_seqs) {
                     const Seq q = sequence(s0 + lane);
-                    t = q.keys.tiles * q.items * heads;
+                    t = q.keys.tiles * p.num_kv_heads;
                     any |= q.zeros;
                 }
                 int sum = t;
@@ -1095,7 +1056,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
             for (; at < end && ok; ++seq, rest = 0) {
                 const Seq q = sequence(seq);
                 const int tiles = q.keys.tiles;
-                const int items = q.items * heads;
+                if (tiles == 0) continue;
                 TreeItem it;
                 it.seq = seq;
                 it.start = q.rows.start;
@@ -1105,31 +1066,23 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 it.pre = q.keys.pre;
                 it.np1 = q.keys.np1;
                 it.gap = q.keys.gap;
-                // kv heads, chunks of heads, the side's rows of the tree
-                for (int i = rest > 0 ? rest / tiles : 0; i < items && at < end && ok; ++i) {
-                    it.ta = rest - i * tiles;
+                it.visited = (it.base + it.n - 1) / kPage + 1 - it.gap;
+                it.kvh = rest / tiles;
+                it.ta = rest - it.kvh * tiles;
+                for (; it.kvh < p.num_kv_heads && at < end && ok; ++it.kvh, it.ta = 0) {
                     it.nt = min(tiles - it.ta, end - at);
                     const int stop = at + (tiles - it.ta);   // the item's end on the line
                     it.part = it.ta > 0 ? 0 : it.nt < tiles ? 1 : -1;
-                    const int hc = i / q.items;
-                    it.kvh = hc / p.chunks;
-                    const int c = hc - it.kvh * p.chunks;
-                    it.head = it.kvh * p.group + c * p.chunk;
-                    it.heads = min(p.chunk, p.group - c * p.chunk);
-                    it.row = ((i - hc * q.items) * p.sides + side) * p.tokens;
-                    it.tok = it.start + it.row;
-                    it.toks = min(p.tokens, it.n - it.row);
-                    it.visited = (it.base + it.row + it.toks - 1) / kPage + 1 - it.gap;
                     at += it.nt;
-                    rest += it.nt;
                     if (q.zeros) {
                         // (all of the sequence's rows)
-                        for (int64_t e = lane;
-                             e < static_cast<int64_t>(it.n) * it.heads * (kD / 8); e += 32) {
+                        const int64_t all = static_cast<int64_t>(it.n) * p.group * (kD / 8);
+                        for (int64_t e = lane; e < all; e += 32) {
                             const int64_t r = e / (kD / 8);
-                            const int64_t tk = it.start + r / it.heads;
+                            const int64_t tk = it.start + r / p.group;
                             if (tk < 0 || tk >= p.num_tokens) continue;
-                            const int64_t row = tk * p.num_heads + it.head + r % it.heads;
+                            const int64_t row =
+                                tk * p.num_heads + it.kvh * p.group + r % p.group;
                             reinterpret_cast<uint4 *>(p.out + row * kD)[e % (kD / 8)] =
                                 make_uint4(0, 0, 0, 0);
                         }
@@ -1139,10 +1092,9 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                         // pieces that the rest of the item lies in
                         int last = piece + 1;
                         while (cut(last + 1) < stop) ++last;
-                        tail.tok = it.tok;
-                        tail.toks = it.toks;
-                        tail.head = it.head;
-                        tail.heads = it.heads;
+                        tail.start = it.start;
+                        tail.n = it.n;
+                        tail.kvh = it.kvh;
                         tail.parts = last - piece + 1;
                     }
                     ok = wait(i_empty(k), (k >> 1 & 1) ^ 1);
@@ -1256,79 +1208,88 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
 
 // Joins the parts of the items that the cuts went through, a warp a row.
 //   out = sum_z 2^(m_z - M) acc_z / sum_z 2^(m_z - M) l_z,  M = max_z m_z
-// A part with l < 0 (a bad block or tree) makes the row zeros.
+// A part with l < 0 (a bad block or tree) makes the row zeros.  Most items have two
+// parts, whose numbers are asked for at once with the question whether there are any.
 constexpr int kJoinWarps = 8;
 
 template <int kD, int kN>
 __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid_constant__ TreeArgs p)
 {
-    constexpr int kC = kD / 32, kPer = (kSms + 31) / 32;
+    constexpr int kC = kD / 32;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int owner = blockIdx.x / (kN / kJoinWarps);
-    const int r = blockIdx.x % (kN / kJoinWarps) * kJoinWarps + warp;
-    const TreeMeta meta = p.meta[owner];
-    const int rj = r / p.chunk, rh = r - rj * p.chunk;
-    if (meta.parts <= 0 || rj >= meta.toks || rh >= meta.heads) return;
+    const int owner = blockIdx.x, r = blockIdx.y * kJoinWarps + warp;
     // part 0 is the owner's last one, the others are the first of the pieces behind
     auto at = [&](int z) -> int64_t {
-        return (2 * (static_cast<int64_t>(owner) + static_cast<int64_t>(z) * p.sides) + (z == 0)) *
-                   kN + r;
+        return (2 * static_cast<int64_t>(min(owner + z, kTreePieces - 1)) + (z == 0)) * kN + r;
     };
-    float pm[kPer], pl[kPer], m = kNone;
+    constexpr int kAt = 4;      // parts at a time
+    float2 ml[kAt];
+    float v[kAt][kC];
+    auto load = [&](int z0, int z1) {
+#pragma unroll
+        for (int u = 0; u < kAt; ++u)
+            if (z0 + u < z1) {
+                ml[u] = __ldcg(p.part_ml + at(z0 + u));
+                const float *a = p.part_acc + at(z0 + u) * kD + lane * kC;
+                if constexpr (kC == 4) {
+                    const float4 w = __ldcg(reinterpret_cast<const float4 *>(a));
+                    v[u][0] = w.x;
+                    v[u][1] = w.y;
+                    v[u][2] = w.z;
+                    v[u][3] = w.w;
+                } else {
+                    const float2 w = __ldcg(reinterpret_cast<const float2 *>(a));
+                    v[u][0] = w.x;
+                    v[u][1] = w.y;
+                }
+            }
+    };
+    const int4 mw = __ldcg(reinterpret_cast<const int4 *>(p.meta) + owner);
+    load(0, 2);
+    const int parts = mw.w, rj = r / p.group, rh = r - rj * p.group;
+    if (parts <= 0 || rj >= mw.y) return;
+    float m = kNone, l = 0.f, acc[kC];
     bool bad = false;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-        const int z = lane + 32 * e;
-        const float2 ml = z < meta.parts ? __ldcg(p.part_ml + at(z)) : make_float2(kNone, 0.f);
-        pm[e] = ml.x;
-        pl[e] = ml.y;
-        m = fmaxf(m, ml.x);
-        bad |= ml.y < 0.f;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    bad = __any_sync(0xffffffffu, bad);
-    float l = 0.f, acc[kC];
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-        pm[e] = ptx::ex2(pm[e] - m);
-        l += pm[e] * pl[e];
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-#pragma unroll
     for (int c = 0; c < kC; ++c) acc[c] = 0.f;
+    int have = 2;
+    for (int z = 0;;) {
+        float top = m;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e)
-#pragma unroll 1
-        for (int z0 = 32 * e; z0 < meta.parts && z0 < 32 * e + 32; z0 += 8) {
-            float v[8][kC];
+        for (int u = 0; u < kAt; ++u)
+            if (u < have) top = fmaxf(top, ml[u].x);
+        const float f = ptx::ex2(m - top);
+        m = top;
+        l *= f;
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
+        for (int c = 0; c < kC; ++c) acc[c] *= f;
 #pragma unroll
-                for (int c = 0; c < kC; ++c) {
-                    const int z = z0 + u;
-                    v[u][c] = z < meta.parts ? __ldcg(p.part_acc + at(z) * kD + 32 * c + lane) : 0.f;
-                }
+        for (int u = 0; u < kAt; ++u)
+            if (u < have) {
+                const float w = ptx::ex2(ml[u].x - m);
+                bad |= ml[u].y < 0.f;
+                l += w * ml[u].y;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const float f = __shfl_sync(0xffffffffu, pm[e], (z0 + u) & 31);
-#pragma unroll
-                for (int c = 0; c < kC; ++c) acc[c] += f * v[u][c];
+                for (int c = 0; c < kC; ++c) acc[c] += w * v[u][c];
             }
-        }
+        z += have;
+        if (z >= parts) break;
+        have = min(kAt, parts - z);
+        load(z, parts);
+    }
     const bool zero = bad || l == 0.f;
-    const int64_t row = static_cast<int64_t>(meta.tok + rj) * p.num_heads + meta.head + rh;
+    const int64_t row = static_cast<int64_t>(mw.x + rj) * p.num_heads + mw.z * p.group + rh;
+    __half2 *o = reinterpret_cast<__half2 *>(p.out + row * kD + lane * kC);
 #pragma unroll
-    for (int c = 0; c < kC; ++c)
-        p.out[row * kD + 32 * c + lane] = __float2half_rn(zero ? 0.f : acc[c] / l);
+    for (int c = 0; c < kC; c += 2)
+        o[c / 2] = __floats2half2_rn(zero ? 0.f : acc[c] / l, zero ? 0.f : acc[c + 1] / l);
 }
 
 // -------------------------------------------------------------------- host
 template <int kKv, int kD, int kN>
-pkv_status launch_tree(const TreeCall &c, const TreePlan &plan)
+pkv_status launch_tree(const TreeCall &c)
 {
     using M = TreeSmem<kKv, kD, kN>;
     DeviceInfo di;
@@ -1349,14 +1310,15 @@ pkv_status launch_tree(const TreeCall &c, const TreePlan &plan)
         }
     }
     CUtensorMap tmq, tmk, tmv;
+    const int group = c.num_heads / c.num_kv_heads, tokens = kN / group;
     const uint64_t rows = static_cast<uint64_t>(c.num_blocks) * c.num_kv_heads * kPage;
     const int elem = M::kCodes ? 1 : 2, box = M::kCodes ? kD : 64;
-    if (!encode_tmap_3d_f16(&tmq, c.query, kD, c.num_heads, c.num_tokens, 64, plan.chunk,
-                            plan.tokens) ||
+    if (!encode_tmap_3d_f16(&tmq, c.query, kD, c.num_heads, c.num_tokens, 64, group,
+                            tokens) ||
         !encode_tmap_2d(&tmk, c.kpool, elem, kD, rows, box, kPage, box * elem) ||
         !encode_tmap_2d(&tmv, c.vpool, elem, kD, rows, box, kPage, box * elem))
         return PKV_ERR_CUDA;
-    const int64_t ctas = static_cast<int64_t>(plan.sides) * plan.pieces;
+    constexpr int64_t ctas = kTreePieces;
     TreeArgs a;
     a.out = static_cast<__half *>(c.out);
     a.block_tables = c.block_tables;
@@ -1375,12 +1337,8 @@ pkv_status launch_tree(const TreeCall &c, const TreePlan &plan)
     a.num_seqs = c.num_seqs;
     a.num_heads = c.num_heads;
     a.num_kv_heads = c.num_kv_heads;
-    a.group = c.num_heads / c.num_kv_heads;
-    a.chunk = plan.chunk;
-    a.chunks = plan.chunks;
-    a.tokens = plan.tokens;
-    a.sides = plan.sides;
-    a.pieces = plan.pieces;
+    a.group = group;
+    a.tokens = tokens;
     a.max_blocks_per_seq = c.max_blocks_per_seq;
     a.num_blocks = c.num_blocks;
     const int64_t cap_tab = static_cast<int64_t>(c.max_blocks_per_seq) * kPage;
@@ -1402,7 +1360,7 @@ pkv_status launch_tree(const TreeCall &c, const TreePlan &plan)
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, tmq, tmk, tmv);
     if (e == cudaSuccess) {
-        cfg.gridDim = dim3(static_cast<unsigned>(ctas * (kN / kJoinWarps)));
+        cfg.gridDim = dim3(static_cast<unsigned>(ctas), kN / kJoinWarps);
         cfg.blockDim = dim3(32 * kJoinWarps);
         cfg.dynamicSmemBytes = 0;
         e = cudaLaunchKernelEx(&cfg, tree_join_kernel<kD, kN>, a);
@@ -1418,12 +1376,8 @@ template <int kKv>
 pkv_status launch_tree(const TreeCall &c, const TreePlan &plan)
 {
     if (c.head_dim == 128)
-        return plan.rows == 32   ? launch_tree<kKv, 128, 32>(c, plan)
-               : plan.rows == 64 ? launch_tree<kKv, 128, 64>(c, plan)
-                                 : launch_tree<kKv, 128, 128>(c, plan);
-    return plan.rows == 32   ? launch_tree<kKv, 64, 32>(c, plan)
-           : plan.rows == 64 ? launch_tree<kKv, 64, 64>(c, plan)
-                             : launch_tree<kKv, 64, 128>(c, plan);
+        return plan.rows == 32 ? launch_tree<kKv, 128, 32>(c) : launch_tree<kKv, 128, 64>(c);
+    return plan.rows == 32 ? launch_tree<kKv, 64, 32>(c) : launch_tree<kKv, 64, 64>(c);
 }
 
 #ifdef PKV_DEBUG

@@ -29,13 +29,23 @@ struct TreeCall {
     void *stream;
 };
 
-constexpr int kTreeMetaBytes = 32;   // of a CTA in the workspace: see TreeMeta
+constexpr int kTreeMetaBytes = 16;   // of a CTA in the workspace: see TreeMeta
+
+constexpr int kTreePieces = 152;     // GB300: one for every SM
 
 struct TreePlan {
-    int rows = 0;              // of an item: 32, 64 or 128
-    int chunk = 0, chunks = 0, tokens = 0, sides = 0, pieces = 0;
-    size_t bytes = 0;
+    int rows = 0;      // of a work item: 32 or 64 (pkv_tree.cuh); 0: pkv_prefill_tree.cu
+    size_t bytes = 0;  // of workspace
 };
+
+enum TreeKind { kTreeFp16, kTreeInt8, kTreeFp8 };
+
+// Many rows per kv head.
+pkv_status launch_tree_rows(const TreeCall &c, TreeKind kind);
+pkv_status tree_rows_workspace(int num_tokens, int num_seqs, int num_heads, int num_kv_heads,
+                               int head_dim, int max_context_len, size_t *bytes);
+
+// Few of them.
 
 pkv_status launch_tree_fp16(const TreeCall &c, const TreePlan &plan);
 pkv_status launch_tree_int8(const TreeCall &c, const TreePlan &plan);
@@ -43,6 +53,7 @@ pkv_status launch_tree_fp8(const TreeCall &c, const TreePlan &plan);
 
 #ifdef PKV_DEBUG
 // Sets a unit's WaitDebug; 0, or -1 if the CUDA runtime fails.
+int set_tree_waits_rows(int give_role, int give_at, int slow_role, int slow_ns);
 int set_tree_waits_fp16(int give_role, int give_at, int slow_role, int slow_ns);
 int set_tree_waits_int8(int give_role, int give_at, int slow_role, int slow_ns);
 int set_tree_waits_fp8(int give_role, int give_at, int slow_role, int slow_ns);

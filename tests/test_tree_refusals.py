@@ -101,16 +101,19 @@ def test_compact(kind):
 
 
 def test_workspace_size():
-    # for each of the pieces' CTAs two parts of 32 or 128 rows, d values and two
-    # numbers each, and 32 bytes that say whose they are
-    def expect(ctas, rows, d):
-        return ctas * (2 * rows * (d + 2) * 4 + 32)
-    assert pkv.pkv_tree_workspace_size(64, 8, 8, 8, 128, 512, 8) == expect(152, 32, 128)
-    assert pkv.pkv_tree_workspace_size(64, 8, 32, 8, 128, 512, 8) == expect(152, 32, 128)
-    assert pkv.pkv_tree_workspace_size(64, 8, 32, 8, 128, 512, 9) == expect(152, 128, 128)
-    assert pkv.pkv_tree_workspace_size(64, 1, 32, 8, 64, 512, 64) == expect(2 * 76, 128, 64)
+    # few rows per kv head: for each of 152 pieces two parts of 32 or 64 rows, d values
+    # and two numbers each, and 16 bytes that say whose they are
+    def expect(rows, d):
+        return 152 * (2 * rows * (d + 2) * 4 + 16)
+    assert pkv.pkv_tree_workspace_size(64, 8, 8, 8, 128, 512, 8) == expect(32, 128)
+    assert pkv.pkv_tree_workspace_size(64, 8, 32, 8, 128, 512, 8) == expect(32, 128)
+    assert pkv.pkv_tree_workspace_size(64, 8, 32, 8, 64, 512, 9) == expect(64, 64)
     # a bound above the batch's tokens does not count
-    assert pkv.pkv_tree_workspace_size(4, 1, 8, 1, 64, 512, 4096) == expect(152, 32, 64)
+    assert pkv.pkv_tree_workspace_size(4, 1, 8, 1, 64, 512, 4096) == expect(32, 64)
+    # many rows: as for the prefill
+    for tree, heads in ((17, 32), (1, 80 * 8)):
+        args = (64, 8, heads, 8, 128, 20000)
+        assert pkv.pkv_tree_workspace_size(*args, tree) == pkv.pkv_prefill_workspace_size(*args)
     assert pkv.pkv_tree_workspace_size(8, 1, 4, 3, 128, 20000, 8) == 0
     assert pkv.pkv_tree_workspace_size(8, 1, 4, 1, 96, 20000, 8) == 0
     assert pkv.pkv_tree_workspace_size(-1, 1, 4, 1, 64, 20000, 8) == 0
