@@ -139,7 +139,7 @@ struct Smem {
     static constexpr int kOut = kCodeRing + kCodeStages * kCodeBytes;   // rows on their way out
     static constexpr int kOutBytes = 16 * 1024;
     static constexpr int kCtl = kOut + kOutBytes;
-    static constexpr int kBars = 3 * kStages + 2 * kCodeStages + 16;
+    static constexpr int kBars = 3 * kStages + 2 * kCodeStages + 16 + (kTree ? 1 : 0);
     // scales [kScaleTiles][K, V][8 pages].  The K warp writes both of a tile
     // before it arrives for the tile's K codes; their widening waits for that,
     // the product Q K^T for the widening and the softmax for the product, so
@@ -452,6 +452,8 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
     [[maybe_unused]] auto swapped = [&](int i) { return one + 112 + 8 * i; };
     // one per stage: rows are zeroed tiles ahead of the products
     [[maybe_unused]] auto fixed = [&](int s) { return one + 128 + 8 * s; };
+    // kTree: all K of the item was asked for
+    [[maybe_unused]] const uint32_t k_asked = one + 128 + 8 * S;
     volatile int *flags = reinterpret_cast<volatile int *>(smem + M::kFlags);
     // flags: abort, bad of item slot 0, of slot 1, TMEM address
     const Waiter waiter{flags, p.dev_status};
@@ -476,6 +478,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
         ptx::mbar_init(q_empty, 1);
         ptx::mbar_init(drain, 1);
         ptx::mbar_init(next_full, 1);
+        if (kTree) ptx::mbar_init(k_asked, 1);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(s_full(i), 1);
             ptx::mbar_init(p_full(i), kSoftWarps / 2);
@@ -1232,6 +1235,7 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                         }
                 }
                 __syncwarp();
+                if (kTree && !is_v && lane == 0) ptx::mbar_arrive(k_asked);
                 if (lane == 0) ptx::mbar_arrive(i_empty(k));
             }
             // The products have waited for every copy, unless a wait ran out:
@@ -1254,12 +1258,15 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
             // INT8 299 / 307.
             constexpr bool kLate = kMod && (kCodes || kD == 64);
             [[maybe_unused]] bool first = false;
-            for (uint32_t asked = 0; ok; ++asked) {
+            auto ask = [&]() {
                 if (umma::elect_one()) {
                     ptx::mbar_arrive_expect_tx(next_full, 16);
                     ptx::try_cancel(base + M::kNext, next_full);
                 }
                 __syncwarp();
+            };
+            for (uint32_t asked = 0; ok; ++asked) {
+                if (!kTree) ask();
                 Item it;
                 const int what = find_item(p, block, it);
                 [[maybe_unused]] bool wrong = false;   // kTree: a parent that is no earlier row
@@ -1304,6 +1311,15 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                     first |= block == 0;
                 else if (block == 0 && p.dev_status)
                     check_sequences(p, lane);
+                // Trees often have about as many items as there are SMs, and all of the same
+                // length: a CTA that asked for its next one at once would take it away from
+                // another that has none (16 x 64 over 8192: 189 us so, 105 now).  So it asks when its
+                // loads are through.
+                if constexpr (kTree) {
+                    if (what > 0 && ok) ok = wait(k_asked, (k - 1) & 1);
+                    if (!ok) break;
+                    ask();
+                }
                 // (also after a wait that ran out: the answer must have come)
                 if (!wait(next_full, asked & 1)) {
                     ptx::mbar_wait_bounded(next_full, asked & 1, kWaitLimitNs);
