@@ -69,20 +69,22 @@ constexpr float kNone = -3.0e38f;        // reference of a row that has seen not
 constexpr float kLeastV = 0x1p-60f;      // V scales below (zero) count as this
 constexpr int kParents = 512;   // parents of a sequence kept in shared memory
 
-// Score warps: a group of four, a thread per key, for every 32 rows.  A tile's chain
+// Score warps: a group of four, a thread per key, for every 16 rows.  A tile's chain
 // (scores, exponentials, reference, product) has more waits than work, which groups
-// with rows of their own and nothing to tell each other fill.
-constexpr int kRows = 32;       // of a group
+// with rows of their own and nothing to tell each other fill.  (32 rows to a group: 8
+// tokens of 4 heads over 131072 INT8 keys took 93.6 us, with 16 78.8.)
+constexpr int kRows = 16;       // of a group, and the columns of one TMEM access
 
 __host__ __device__ constexpr int soft_warps(int rows)
 {
     return 4 * (rows / kRows);
 }
 
-// Warps that widen codes.
+// Warps that widen codes: a team for K, a team for V.
+constexpr int kTeam = 4;
 __host__ __device__ constexpr int widen_warps(int kv)
 {
-    return kv == kKvF16 ? 0 : 8;
+    return kv == kKvF16 ? 0 : 2 * kTeam;
 }
 
 __host__ __device__ constexpr int tree_threads(int kv, int rows)
@@ -123,32 +125,35 @@ struct TreeSmem {
     static constexpr int kPBufs = 2;
     static constexpr int kCodeBytes = kTile * kD;
     static constexpr int kMore = 128 / kD;
+    // fp16: K and V tiles in turn; codes: widened V tiles (widened K lies in TMEM), and
+    // the codes of K and V in turn
     static constexpr int kStages =
-        kMore * (kCodes ? 3 : kN <= 32 ? 6 : 5);
-    static constexpr int kCodeStages = kCodes ? kMore * (kN <= 32 ? 6 : 4) : 0;
+        kMore * (kCodes ? 2 : kN <= 32 ? 6 : 5);
+    static constexpr int kCodeStages = kCodes ? kMore * (kN <= 32 ? 8 : 6) : 0;
+    static constexpr int kKBufs = 2;                           // widened K tiles
     // A waiting warp must not be two phases of a barrier off.  K and V have a producer
     // each, which has seen the element S + 2 before its next one given back and takes
     // for granted that the one 2 S before it was.  With an even number of stages these
     // are both K or both V.  With an odd one, V's producer has seen a K, whose product
-    // follows the one with V of two tiles before: 5 stages will do, 3 will not.  (Codes
-    // are widened in their order, by the same warps.)
+    // follows the one with V of two tiles before: 5 stages will do, 3 will not.
     static_assert(kCodes || kStages % 2 == 0 || kStages >= 5, "phases of the ring");
+    static_assert(kCodeStages % 2 == 0, "K and V codes in slots of their own");
     static constexpr int kP = kHalves * kQHalfBytes;
     static constexpr int kRing = kP + kPBufs * kPBytes;
     static constexpr int kCodeRing = kRing + kStages * kTileBytes;
     static constexpr int kCtl = kCodeRing + kCodeStages * kCodeBytes;
-    static constexpr int kBars = 2 * kStages + 2 * kCodeStages + 15;
+    static constexpr int kBars = 2 * kStages + 2 * kCodeStages + 15 + 2 * kKBufs;
     static constexpr int kItems = (kCtl + 8 * kBars + 15) & ~15;
     static constexpr int kFlags = kItems + 2 * 64;
     static constexpr int kIssued = kFlags + 32;   // see drain_copies
-    // scales [kScaleTiles][K, V][8 pages], written by the K warp ahead of its
-    // arrival for the tile's K codes; the scores of the tile are behind that.  The
-    // warp runs ahead by the elements of both rings and one that it holds, and the
-    // scores lag behind the products by two tiles.
+    // scales [kScaleTiles][3][8 pages], written by the K warp ahead of its arrival for
+    // the tile's K codes and worked out by K's widening team (scales_at); the scores of
+    // the tile are behind that.  The K warp runs ahead by the K tiles of its ring, the widened ones and one that it
+    // holds, and the scores lag behind the products by two tiles.
     static constexpr int kScaleTiles = 16;
-    static_assert((kStages + kCodeStages + 1) / 2 + 3 <= kScaleTiles, "scales overwritten");
+    static_assert(kCodeStages / 2 + kKBufs + 4 <= kScaleTiles, "scales overwritten");
     static constexpr int kScales = kIssued + 16;
-    static constexpr int kOff = kScales + (kCodes ? kScaleTiles * 2 * kPagesPerTile * 4 : 0);
+    static constexpr int kOff = kScales + (kCodes ? kScaleTiles * 3 * kPagesPerTile * 4 : 0);
     static constexpr int kMax = kOff + 4 * kN;      // a row's reference
     static constexpr int kFac = kMax + 4 * kN;      // factor of its sums; 1 / sum at the end
     static constexpr int kOld = kFac + 4 * kN;      // kOff before the last change
@@ -199,18 +204,18 @@ static_assert(sizeof(TreeItem) == 64, "an item is 64 bytes of shared memory");
 
 // ------------------------------------------------------------------ kernel
 // Registers: all threads are launched with 65536 / threads, rounded down to a
-// multiple of 8 (96 for the 640 threads of codes with 64 rows).  The score threads,
-// which hold 32 scores and 32 sums, take what the others give back.
+// multiple of 8 (72 for the 896 threads of codes with 64 rows).  The 512 score threads,
+// which hold 16 scores and 16 sums, take what the other 384 give back.
 template <int kKv, int kN>
 __device__ __forceinline__ void soft_registers()
 {
-    if constexpr (kKv != kKvF16 && kN == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    if constexpr (kKv != kKvF16 && kN == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
 }
 
 template <int kKv, int kN>
 __device__ __forceinline__ void other_registers()
 {
-    if constexpr (kKv != kKvF16 && kN == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (kKv != kKvF16 && kN == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
 }
 
 // Barriers of a group of score warps alone.
@@ -332,12 +337,13 @@ __device__ __forceinline__ void tanh_all(float (&x)[kC])
     }
 }
 
-// Sums of 32 columns over the lanes of the warp: afterwards v[0] of a lane is the
-// column of its number.
-__device__ __forceinline__ void lane_sums(float *v, int lane)
+// Sums of kC columns over the lanes of the warp: afterwards v[0] of a lane is the
+// column of its number, modulo kC.
+template <int kC>
+__device__ __forceinline__ void lane_sums(float (&v)[kC], int lane)
 {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int o = kC / 2; o > 0; o >>= 1) {
         const bool up = lane & o;
 #pragma unroll
         for (int i = 0; i < o; ++i) {
@@ -345,6 +351,8 @@ __device__ __forceinline__ void lane_sums(float *v, int lane)
             v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
         }
     }
+#pragma unroll
+    for (int o = kC; o < 32; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
 }
 
 template <int kKv, int kD, int kN>
@@ -355,6 +363,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
     using M = TreeSmem<kKv, kD, kN>;
     constexpr bool kCodes = M::kCodes;
     constexpr int S = M::kStages;
+    constexpr int kGroups = kN / kRows;
     constexpr int kSoftWarps = soft_warps(kN);
     constexpr int kWidenWarps = widen_warps(kKv);
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -376,6 +385,11 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
     auto i_full = [&](int k) { return one + 72 + 8 * (k & 1); };
     auto i_empty = [&](int k) { return one + 88 + 8 * (k & 1); };
     auto t_full = [&](int k) { return one + 104 + 8 * (k & 1); };   // the item's tree is there
+    // codes: widened K of tile number g there, read
+    [[maybe_unused]] auto k_full = [&](uint32_t g) { return one + 120 + 8 * (g % M::kKBufs); };
+    [[maybe_unused]] auto k_empty = [&](uint32_t g) {
+        return one + 120 + 8 * (M::kKBufs + g % M::kKBufs);
+    };
     volatile int *flags = reinterpret_cast<volatile int *>(smem + M::kFlags);
     // flags: abort, bad block in item slot 0, in slot 1, TMEM address, bad tree in slots
     const Waiter waiter{flags, p.dev_status};
@@ -387,12 +401,16 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            ptx::mbar_init(full(s), kCodes ? kWidenWarps : 1);
+            ptx::mbar_init(full(s), kCodes ? kTeam : 1);
             ptx::mbar_init(empty(s), 1);
         }
         for (int s = 0; s < M::kCodeStages; ++s) {
             ptx::mbar_init(cfull(s), 1);
-            ptx::mbar_init(cempty(s), kWidenWarps);
+            ptx::mbar_init(cempty(s), kTeam);
+        }
+        for (int i = 0; kCodes && i < M::kKBufs; ++i) {
+            ptx::mbar_init(k_full(i), kTeam);
+            ptx::mbar_init(k_empty(i), 1);
         }
         ptx::mbar_init(q_full, 1);
         ptx::mbar_init(q_empty, 1);
@@ -422,6 +440,17 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
 
     auto t_s = [&](uint32_t g) { return tmem + kN * (g & 1); };   // S^T of tile g
     const uint32_t t_o = tmem + 2 * kN;                           // O^T
+    [[maybe_unused]] auto t_k = [&](uint32_t g) {                 // widened K
+        return tmem + 4 * kN + kD / 2 * (g % M::kKBufs);
+    };
+    static_assert(4 * kN + kD / 2 * M::kKBufs <= 512, "columns of TMEM");
+
+    // codes: of tile number g, a page's K scale times the softmax's, its V scale's log2
+    // and reciprocal
+    [[maybe_unused]] auto scales_at = [&](uint32_t g) {
+        return reinterpret_cast<float *>(smem + M::kScales) +
+               (g & (M::kScaleTiles - 1)) * 3 * kPagesPerTile;
+    };
 
     if (warp < kSoftWarps) {
         // ------------------------------------------------ scores and rows
@@ -543,12 +572,10 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 float f0 = p.scale_log2;
                 [[maybe_unused]] float lv = 0.f, rv = 1.f;
                 if constexpr (kCodes) {
-                    const float *sc = reinterpret_cast<const float *>(smem + M::kScales) +
-                                      (g & (M::kScaleTiles - 1)) * 2 * kPagesPerTile + (key >> 4);
-                    const float vs = sc[kPagesPerTile], vc = fmaxf(vs, kLeastV);
-                    f0 *= sc[0];
-                    lv = vs >= 0.f && vs < INFINITY ? log2_of(vc) : NAN;
-                    rv = __frcp_rn(vc);
+                    const float *sc = scales_at(g) + (key >> 4);
+                    f0 = sc[0];
+                    lv = sc[kPagesPerTile];
+                    rv = sc[2 * kPagesPerTile];
                 }
                 const uint64_t rv2 = ptx::f32x2(rv, rv);
                 const uint32_t *words = mask + quad * kN;
@@ -556,13 +583,13 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 // The scores x of the tile, which times f are in log2 units.
                 auto scores = [&](float (&x)[kRows], float &f, auto simple) {
                     constexpr bool kSimple = decltype(simple)::value;
-                    umma::ld32(t_s(g) + lanes + c0, x);
+                    umma::ld16(t_s(g) + lanes + c0, x);
                     umma::wait_ld();
                     f = f0;
                     auto scale_all = [&](float by, float add) {
                         const uint64_t b2 = ptx::f32x2(by, by), a2 = ptx::f32x2(add, add);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
+                        for (int e = 0; e < kRows; e += 2) {
                             const float2 y =
                                 ptx::f32x2_parts(ptx::fma2(ptx::f32x2(x[e], x[e + 1]), b2, a2));
                             x[e] = y.x;
@@ -572,7 +599,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                     // x of the keys that a row does not see
                     auto hide = [&](float value) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
+                        for (int e = 0; e < kRows; e += 4) {
                             const uint4 w = *reinterpret_cast<const uint4 *>(words + c0 + e);
                             if (!(w.x >> lane & 1u)) x[e] = value;
                             if (!(w.y >> lane & 1u)) x[e + 1] = value;
@@ -609,7 +636,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                             // slope (p(t) - ctx): what a row's own position adds is the same
                             // for all of its keys, and the softmax does not see it
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
+                            for (int e = 0; e < kRows; e += 4) {
                                 const float4 s = four(slp, c0 + e);
                                 x[e] = fmaf(s.x, far, x[e]);
                                 x[e + 1] = fmaf(s.y, far, x[e + 1]);
@@ -698,15 +725,12 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                     }
                     fail |= !wait(pv_done(g - 1), (g - 1) >> 1 & 1);
                     umma::fence_after();
-#pragma unroll 1
-                    for (int c = c0; c < c0 + kRows; c += 16) {
-                        float o[16];
-                        umma::ld16(t_o + lanes + c, o);
-                        umma::wait_ld();
+                    float o[kRows];
+                    umma::ld16(t_o + lanes + c0, o);
+                    umma::wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] *= fac[c + e];
-                        umma::st16(t_o + lanes + c, reinterpret_cast<const uint32_t *>(o));
-                    }
+                    for (int e = 0; e < kRows; ++e) o[e] *= fac[c0 + e];
+                    umma::st16(t_o + lanes + c0, reinterpret_cast<const uint32_t *>(o));
                     umma::wait_st();
                 };
                 // In an item's first tile the references come first, so that its
@@ -725,22 +749,22 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 if (!clean) {
                     // V rows of keys that no row of the tree sees may hold anything, NaN
                     // included (and are not loaded for pages past the item's last):
-                    // zeros.  The product waits for this; the other group writes the same.
+                    // zeros.  The product waits for all groups, which take turns.
                     const bool dead = v0 + (key >> 4) >= it.visited || at >= ctx + n ||
                                       (at < it.lo && at >= pre);
                     if (__any_sync(0xffffffffu, dead)) {
                         // (the stage's element before this one must have landed: it is K
                         // of a tile before, or V of one whose product is done)
-                        if (S == 2 && g > 0) fail |= !wait(pv_done(g - 1), (g - 1) >> 1 & 1);
-                        static_assert(S % 2 ? S >= 3 : S == 2 || S / 2 >= M::kPBufs,
-                                      "phase of the stage");
-                        const uint32_t e = 2 * g + 1;
+                            static_assert(kCodes ? S >= M::kPBufs
+                                                 : S % 2 ? S >= 3 : S / 2 >= M::kPBufs,
+                                          "phase of the stage");
+                            const uint32_t e = kCodes ? g : 2 * g + 1;
                         fail |= !wait(full(e % S), (e / S) & 1);
                         const uint32_t row =
                             base + M::kRing + (e % S) * M::kTileBytes + key * 128;
                         if (dead)
 #pragma unroll 1
-                            for (int b = 0; b < kD / 8; ++b)
+                            for (int b = i; b < kD / 8; b += kGroups)
                                 st_shared16(row + (b >> 3) * M::kHalfBytes + (b & 7) * 16,
                                             make_uint4(0, 0, 0, 0));
                     }
@@ -756,7 +780,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
             fail |= !wait(pv_done(g - 1), (g - 1) >> 1 & 1);
             umma::fence_after();
             lane_sums(l, lane);
-            sums[quad * kN + c0 + lane] = l[0];
+            if (lane < kRows) sums[quad * kN + c0 + lane] = l[0];
             if (group_any(i, fail)) break;
             const bool bad = bad_tree || flags[1 + (k & 1)] != 0;
             const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + max(part, 0);
@@ -768,29 +792,26 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
             group_sync(i);
             const int dim = kD == 128 ? key : 16 * quad + lane;   // M = 64 has 16 of 32 lanes
             const bool has = kD == 128 || lane < 16, odd = lane & 1;
-#pragma unroll 1
-            for (int c = c0; c < c0 + kRows; c += 16) {
-                float o[16];
-                umma::ld16(t_o + lanes + c, o);
-                umma::wait_ld();
-                if (part < 0) {
-                    // two neighbouring values of a row to a lane: even lanes store row e,
-                    // odd ones row e + 1
+            float o[kRows];
+            umma::ld16(t_o + lanes + c0, o);
+            umma::wait_ld();
+            if (part < 0) {
+                // two neighbouring values of a row to a lane: even lanes store row e, odd
+                // ones row e + 1
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const float a = bad ? 0.f : o[e] * fac[c + e];
-                        const float b = bad ? 0.f : o[e + 1] * fac[c + e + 1];
-                        const float y = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-                        const int64_t row = place[c + e + odd];
-                        if (row >= 0 && has)
-                            *reinterpret_cast<uint32_t *>(p.out + row * kD + (dim & ~1)) =
-                                odd ? pack2(y, b) : pack2(a, y);
-                    }
-                } else if (has) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (place[c + e] >= 0) p.part_acc[(slot * kN + c + e) * kD + dim] = o[e];
+                for (int e = 0; e < kRows; e += 2) {
+                    const float a = bad ? 0.f : o[e] * fac[c0 + e];
+                    const float b = bad ? 0.f : o[e + 1] * fac[c0 + e + 1];
+                    const float y = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+                    const int64_t row = place[c0 + e + odd];
+                    if (row >= 0 && has)
+                        *reinterpret_cast<uint32_t *>(p.out + row * kD + (dim & ~1)) =
+                            odd ? pack2(y, b) : pack2(a, y);
                 }
+            } else if (has) {
+#pragma unroll
+                for (int e = 0; e < kRows; ++e)
+                    if (place[c0 + e] >= 0) p.part_acc[(slot * kN + c0 + e) * kD + dim] = o[e];
             }
             // (the next item's first product into O waits for its probabilities,
             // which come after this; its rows' places are written behind a barrier)
@@ -812,18 +833,27 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 const uint64_t p_at = umma::desc_plain(base + M::kP, 16 * kTile);
                 auto qk = [&](uint32_t g) -> bool {   // S^T = K Q^T
                     const uint32_t n = 2 * g, s = n % S;
-                    if (!wait.one(full(s), (n / S) & 1)) return false;
+                    if constexpr (kCodes) {
+                        if (!wait.one(k_full(g), (g / M::kKBufs) & 1)) return false;
+                    } else {
+                        if (!wait.one(full(s), (n / S) & 1)) return false;
+                    }
                     umma::fence_after();
-                    const uint32_t a = k_lo + s * (M::kTileBytes >> 4);
+                    [[maybe_unused]] const uint32_t a = k_lo + s * (M::kTileBytes >> 4);
 #pragma unroll
-                    for (int k = 0; k < kD / 16; ++k)
-                        umma::mma_ss(
-                            t_s(g),
-                            umma::desc(a + (((k >> 2) * M::kHalfBytes + (k & 3) * 32) >> 4)),
-                            umma::desc(q_lo + (((k >> 2) * M::kQHalfBytes + (k & 3) * 32) >> 4)),
-                            kQk, k > 0);
+                    for (int k = 0; k < kD / 16; ++k) {
+                        const uint64_t b = umma::desc(
+                            q_lo + (((k >> 2) * M::kQHalfBytes + (k & 3) * 32) >> 4));
+                        if constexpr (kCodes)
+                            umma::mma_ts(t_s(g), t_k(g) + 8 * k, b, kQk, k > 0);
+                        else
+                            umma::mma_ss(
+                                t_s(g),
+                                umma::desc(a + (((k >> 2) * M::kHalfBytes + (k & 3) * 32) >> 4)),
+                                b, kQk, k > 0);
+                    }
                     umma::commit(s_full(g));
-                    umma::commit(empty(s));
+                    umma::commit(kCodes ? k_empty(g) : empty(s));
                     return true;
                 };
                 uint32_t g = 0;
@@ -842,7 +872,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                             if (!ok) break;
                             if (j + 2 == nt) umma::commit(q_empty);
                         }
-                        const uint32_t n = 2 * g + 1, s = n % S;
+                        const uint32_t n = kCodes ? g : 2 * g + 1, s = n % S;
                         ok = wait.one(p_full(g), g >> 1 & 1) && wait.one(full(s), (n / S) & 1);
                         if (!ok) break;
                         umma::fence_after();
@@ -941,8 +971,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                     }
                     if constexpr (kCodes)
                         if (!is_v && lane < kPagesPerTile) {
-                            float *to = reinterpret_cast<float *>(smem + M::kScales) +
-                                        (tiles & (M::kScaleTiles - 1)) * 2 * kPagesPerTile + lane;
+                            float *to = scales_at(tiles) + lane;
                             to[0] = k_scale;
                             to[kPagesPerTile] = v_scale;
                         }
@@ -1139,12 +1168,38 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
             const Waiter wait = waiter.as(kRoleWiden);
             constexpr int R = M::kCodeStages;
             constexpr int kCh = kD / 16;  // 16-byte chunks of codes per key
-            constexpr int kStep = 32 * kWidenWarps / kCh;
-            constexpr int kLoads = kTile / kStep;
-            const int tid = threadIdx.x - 32 * (kSoftWarps + 4);
-            // Eight lanes take four chunks of two rows: r and r ^ 5 of eight at head_dim
+            const bool is_v = warp >= kSoftWarps + 4 + kTeam;
+            const int tid = threadIdx.x & (32 * kTeam - 1);
+            // K: a thread per key, whose codes become the key's lane of TMEM.
+            auto widen_k = [&](uint32_t g, uint32_t src) {
+                const uint32_t from = src + tid * kD;
+                const uint32_t to = t_k(g) + (static_cast<uint32_t>(tid >> 5) << 21);
+                const int sw = kD == 128 ? tid & 7 : tid >> 1 & 3;
+                uint4 w[kCh];
+#pragma unroll
+                for (int ch = 0; ch < kCh; ++ch) w[ch] = ptx::lds128(from + ((ch ^ sw) << 4));
+#pragma unroll
+                for (int ch = 0; ch < kCh; ch += 2) {
+                    uint32_t r[16];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint4 &c = w[ch + e / 2];
+                        const uint4 x = e & 1 ? widen<kKv>(c.z, c.w) : widen<kKv>(c.x, c.y);
+                        r[4 * e] = x.x;
+                        r[4 * e + 1] = x.y;
+                        r[4 * e + 2] = x.z;
+                        r[4 * e + 3] = x.w;
+                    }
+                    umma::st16(to + 8 * ch, r);
+                }
+                umma::wait_st();
+                umma::fence_before();
+            };
+            // V: eight lanes take four chunks of two rows: r and r ^ 5 of eight at head_dim
             // 128, r and r + 1 at 64, whose swizzles put the loads and both stores on
             // different banks.
+            constexpr int kStep = 32 * kTeam / kCh;
+            constexpr int kLoads = kTile / kStep;
             static_assert(kTile % kStep == 0 && kStep % 8 == 0, "whole groups of eight rows");
             int ch = tid % kCh, row0 = tid / kCh;
             if constexpr (kD == 128) {
@@ -1152,43 +1207,60 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 ch = (tid & 3) | (tid >> 1 & 4);
                 row0 = ((tid >> 4 & 3) ^ (tid & 4 ? 5 : 0)) | (tid >> 6) << 3;
             }
-            uint32_t n = 0;
+            // loads first; rows advance by whole groups of eight, so the swizzles stay
+            const uint32_t sx = kD == 128 ? (ch ^ (row0 & 7)) : (ch ^ ((row0 >> 1) & 3));
+            const int c_a = ((2 * ch) & 7) ^ (row0 & 7);
+            auto widen_v = [&](uint32_t src, uint32_t dst) {
+                const uint32_t from = src + row0 * kD + (sx << 4);
+                const uint32_t to = dst + (ch >> 2) * M::kHalfBytes + row0 * 128;
+                constexpr int kAt = kLoads < 4 ? kLoads : 4;   // registers
+#pragma unroll
+                for (int e0 = 0; e0 < kLoads; e0 += kAt) {
+                    uint4 w[kAt];
+#pragma unroll
+                    for (int e = 0; e < kAt; ++e)
+                        w[e] = ptx::lds128(from + (e0 + e) * kStep * kD);
+#pragma unroll
+                    for (int e = 0; e < kAt; ++e) {
+                        const uint32_t at = to + (e0 + e) * kStep * 128;
+                        st_shared16(at + (c_a << 4), widen<kKv>(w[e].x, w[e].y));
+                        st_shared16(at + ((c_a ^ 1) << 4), widen<kKv>(w[e].z, w[e].w));
+                    }
+                }
+                ptx::fence_proxy_async_smem();
+            };
+            uint32_t g = 0;
             bool ok = true;
             for (int k = 0; ok; ++k) {
                 ok = wait(i_full(k), k >> 1 & 1);
                 if (!ok) break;
                 const int nt = item(k).nt;
                 if (nt == 0) break;
-                for (int j = 0; j < 2 * nt; ++j, ++n) {
-                    ok = wait(cfull(n % R), (n / R) & 1) && wait(empty(n % S), ((n / S) & 1) ^ 1);
+                for (int j = 0; j < nt; ++j, ++g) {
+                    const uint32_t n = 2 * g + is_v, r = n % R;
+                    const uint32_t src = base + M::kCodeRing + r * M::kCodeBytes;
+                    const uint32_t s = g % S;
+                    ok = wait(cfull(r), (n / R) & 1) &&
+                         (is_v ? wait(empty(s), ((g / S) & 1) ^ 1)
+                               : wait(k_empty(g), ((g / M::kKBufs) & 1) ^ 1));
                     if (!ok) break;
-                    const uint32_t src = base + M::kCodeRing + (n % R) * M::kCodeBytes;
-                    const uint32_t dst = base + M::kRing + (n % S) * M::kTileBytes;
-                    // loads first; rows advance by whole groups of eight, so the swizzles
-                    // stay
-                    const uint32_t sx = kD == 128 ? (ch ^ (row0 & 7)) : (ch ^ ((row0 >> 1) & 3));
-                    const uint32_t from = src + row0 * kD + (sx << 4);
-                    const uint32_t to = dst + (ch >> 2) * M::kHalfBytes + row0 * 128;
-                    const int c_a = ((2 * ch) & 7) ^ (row0 & 7);
-                    constexpr int kAt = kLoads < 4 ? kLoads : 4;   // registers
-#pragma unroll
-                    for (int e0 = 0; e0 < kLoads; e0 += kAt) {
-                        uint4 w[kAt];
-#pragma unroll
-                        for (int e = 0; e < kAt; ++e)
-                            w[e] = ptx::lds128(from + (e0 + e) * kStep * kD);
-#pragma unroll
-                        for (int e = 0; e < kAt; ++e) {
-                            const uint32_t at = to + (e0 + e) * kStep * 128;
-                            st_shared16(at + (c_a << 4), widen<kKv>(w[e].x, w[e].y));
-                            st_shared16(at + ((c_a ^ 1) << 4), widen<kKv>(w[e].z, w[e].w));
+                    if (is_v) {
+                        widen_v(src, base + M::kRing + s * M::kTileBytes);
+                    } else {
+                        if (tid < kPagesPerTile) {
+                            float *sc = scales_at(g) + tid;
+                            const float vs = sc[kPagesPerTile], vc = fmaxf(vs, kLeastV);
+                            sc[0] *= p.scale_log2;
+                            sc[kPagesPerTile] = vs >= 0.f && vs < INFINITY ? log2_of(vc) : NAN;
+                            sc[2 * kPagesPerTile] = __frcp_rn(vc);
                         }
+                        umma::fence_after();
+                        widen_k(g, src);
                     }
-                    ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        ptx::mbar_arrive(full(n % S));
-                        ptx::mbar_arrive(cempty(n % R));
+                        ptx::mbar_arrive(is_v ? full(s) : k_full(g));
+                        ptx::mbar_arrive(cempty(r));
                     }
                 }
                 __syncwarp();
