@@ -840,7 +840,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                     }
                     umma::fence_after();
                     [[maybe_unused]] const uint32_t a = k_lo + s * (M::kTileBytes >> 4);
-#pragma unroll
+#pragma unroll 1
                     for (int k = 0; k < kD / 16; ++k) {
                         const uint64_t b = umma::desc(
                             q_lo + (((k >> 2) * M::kQHalfBytes + (k & 3) * 32) >> 4));
@@ -878,7 +878,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                         umma::fence_after();
                         const uint32_t a = v_lo + s * (M::kTileBytes >> 4);
                         const uint64_t b = p_at + (g % M::kPBufs * M::kPBytes >> 4);
-#pragma unroll
+#pragma unroll 1
                         for (int k2 = 0; k2 < kTile / 16; ++k2)   // O^T += V^T P^T
                             umma::mma_ss(t_o, umma::desc(a + k2 * (2048 >> 4)), b + k2 * (256 >> 4),
                                          kPv, j > 0 || k2 > 0);
@@ -894,8 +894,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
             __syncwarp();
         } else if (warp == kSoftWarps + 1 || warp == kSoftWarps + 3) {
             // ------------------------------------------------ loads of Q and the pages
-            // A lane per page looks its block up; one thread issues the copies, 2 KB
-            // of a page each.
+            // A lane per page looks its block up and issues its copies, 2 KB of a page each.
             constexpr int R = kCodes ? M::kCodeStages : S;
             constexpr int kBox = kCodes ? kD : 64;                       // values per box
             constexpr int kBoxes = kCodes ? 1 : M::kHalves;
@@ -959,15 +958,11 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                         ptx::mbar_expect_tx(fb, __popc(pages) * kBoxes * kBoxBytes);
                     __syncwarp();
                     const uint32_t dst = ring + s * kStageBytes;
+                    if (have) {
 #pragma unroll
-                    for (int q = 0; q < kPagesPerTile; ++q) {
-                        const int y = __shfl_sync(0xffffffffu, row, q);
-                        if ((pages >> q & 1u) && umma::elect_one()) {
-#pragma unroll
-                            for (int b = 0; b < kBoxes; ++b)
-                                ptx::tma_load_2d(dst + b * M::kHalfBytes + q * kBoxBytes, tm,
-                                                 b * kBox, y, fb);
-                        }
+                        for (int b = 0; b < kBoxes; ++b)
+                            ptx::tma_load_2d(dst + b * M::kHalfBytes + lane * kBoxBytes, tm,
+                                             b * kBox, row, fb);
                     }
                     if constexpr (kCodes)
                         if (!is_v && lane < kPagesPerTile) {
@@ -1170,20 +1165,24 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
             constexpr int kCh = kD / 16;  // 16-byte chunks of codes per key
             const bool is_v = warp >= kSoftWarps + 4 + kTeam;
             const int tid = threadIdx.x & (32 * kTeam - 1);
+            // The loops here, of the products and of the loads are left rolled: 20 to 28
+            // warps run seven programs on four schedulers, and what they wait for most is
+            // instructions.  (INT8, 64 trees of 8 tokens over 2048, 4 heads to a kv head:
+            // 111 us with all of them unrolled, 80 so.)
             // K: a thread per key, whose codes become the key's lane of TMEM.
             auto widen_k = [&](uint32_t g, uint32_t src) {
                 const uint32_t from = src + tid * kD;
                 const uint32_t to = t_k(g) + (static_cast<uint32_t>(tid >> 5) << 21);
                 const int sw = kD == 128 ? tid & 7 : tid >> 1 & 3;
-                uint4 w[kCh];
-#pragma unroll
-                for (int ch = 0; ch < kCh; ++ch) w[ch] = ptx::lds128(from + ((ch ^ sw) << 4));
-#pragma unroll
+#pragma unroll 1
                 for (int ch = 0; ch < kCh; ch += 2) {
+                    uint4 w[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) w[e] = ptx::lds128(from + (((ch + e) ^ sw) << 4));
                     uint32_t r[16];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const uint4 &c = w[ch + e / 2];
+                        const uint4 &c = w[e / 2];
                         const uint4 x = e & 1 ? widen<kKv>(c.z, c.w) : widen<kKv>(c.x, c.y);
                         r[4 * e] = x.x;
                         r[4 * e + 1] = x.y;
@@ -1207,25 +1206,18 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 ch = (tid & 3) | (tid >> 1 & 4);
                 row0 = ((tid >> 4 & 3) ^ (tid & 4 ? 5 : 0)) | (tid >> 6) << 3;
             }
-            // loads first; rows advance by whole groups of eight, so the swizzles stay
+            // (rows advance by whole groups of eight, so the swizzles stay)
             const uint32_t sx = kD == 128 ? (ch ^ (row0 & 7)) : (ch ^ ((row0 >> 1) & 3));
             const int c_a = ((2 * ch) & 7) ^ (row0 & 7);
             auto widen_v = [&](uint32_t src, uint32_t dst) {
                 const uint32_t from = src + row0 * kD + (sx << 4);
                 const uint32_t to = dst + (ch >> 2) * M::kHalfBytes + row0 * 128;
-                constexpr int kAt = kLoads < 4 ? kLoads : 4;   // registers
-#pragma unroll
-                for (int e0 = 0; e0 < kLoads; e0 += kAt) {
-                    uint4 w[kAt];
-#pragma unroll
-                    for (int e = 0; e < kAt; ++e)
-                        w[e] = ptx::lds128(from + (e0 + e) * kStep * kD);
-#pragma unroll
-                    for (int e = 0; e < kAt; ++e) {
-                        const uint32_t at = to + (e0 + e) * kStep * 128;
-                        st_shared16(at + (c_a << 4), widen<kKv>(w[e].x, w[e].y));
-                        st_shared16(at + ((c_a ^ 1) << 4), widen<kKv>(w[e].z, w[e].w));
-                    }
+#pragma unroll 1
+                for (int e = 0; e < kLoads; ++e) {
+                    const uint4 w = ptx::lds128(from + e * kStep * kD);
+                    const uint32_t at = to + e * kStep * 128;
+                    st_shared16(at + (c_a << 4), widen<kKv>(w.x, w.y));
+                    st_shared16(at + ((c_a ^ 1) << 4), widen<kKv>(w.z, w.w));
                 }
                 ptx::fence_proxy_async_smem();
             };
