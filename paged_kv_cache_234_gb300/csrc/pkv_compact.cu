@@ -20,6 +20,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "pkv_host.cuh"
 #include "pkv_ptx.cuh"
 #include "pkv_quant.cuh"
@@ -30,6 +32,7 @@ namespace {
 
 enum { kMoveF16 = 0, kMoveI8 = 1, kMoveF8 = 2 };
 constexpr int kMoveWarps = 8;
+constexpr int kBufs = 3;   // pages of a warp: the last round's, this one's, the next one's
 
 struct CompactArgs {
     __half *k_pool, *v_pool;
@@ -59,6 +62,61 @@ __device__ __forceinline__ void team_wait()
     if constexpr (!kWarp) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// The codes of eight values by x * fl(1 / scale), which is within 2 ulp of
+// fl(x / scale); false if one of them lies so close to a tie, or is NaN, that the
+// quotient itself has to say.  INT8: see quant_code.
+__device__ __forceinline__ bool near_codes_i8(const uint4 &raw, float rcp, uint2 &codes)
+{
+    const __half2 *h = reinterpret_cast<const __half2 *>(&raw);
+    const uint64_t by = ptx::f32x2(rcp, rcp), magic = ptx::f32x2(kRoundMagic, kRoundMagic);
+    const uint64_t back = ptx::f32x2(-kRoundMagic, -kRoundMagic), neg = ptx::f32x2(-1.f, -1.f);
+    float off = 0.f;
+    uint32_t c[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float2 f = __half22float2(h[w]);
+        const uint64_t y = ptx::mul2(ptx::f32x2(f.x, f.y), by);
+        const uint64_t t = ptx::add2(y, magic);
+        const float2 d = ptx::f32x2_parts(ptx::fma2(ptx::add2(t, back), neg, y));
+        off = max_nan(off, max_nan(fabsf(d.x), fabsf(d.y)));
+        const float2 i = ptx::f32x2_parts(t);
+        c[w] = ptx::prmt(__float_as_uint(i.x), __float_as_uint(i.y), 0x0040);
+    }
+    codes = make_uint2(ptx::prmt(c[0], c[1], 0x5410), ptx::prmt(c[2], c[3], 0x5410));
+    return off < 0.5f - 0.00006103515625f;   // 0.5 - 2^-14
+}
+
+// FP8: rounding is monotonic, so where the values a little below and above the
+// product (1 -+ 2^-21: more than the 2 ulp) have the same code, the quotient has it.
+__device__ __forceinline__ bool near_codes_f8(const uint4 &raw, float rcp, uint2 &codes)
+{
+    const __half2 *h = reinterpret_cast<const __half2 *>(&raw);
+    const float down = 1.f - 0x1p-21f, up = 1.f + 0x1p-21f;
+    const uint64_t by = ptx::f32x2(rcp, rcp);
+    uint32_t lo[4], hi[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float2 f = __half22float2(h[w]);
+        const uint64_t y = ptx::mul2(ptx::f32x2(f.x, f.y), by);
+        const float2 a = ptx::f32x2_parts(ptx::mul2(y, ptx::f32x2(down, down)));
+        const float2 b = ptx::f32x2_parts(ptx::mul2(y, ptx::f32x2(up, up)));
+        lo[w] = __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3);
+        hi[w] = __nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3);
+    }
+    codes = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+    const uint32_t x = hi[0] | hi[1] << 16, y = hi[2] | hi[3] << 16;
+    // (a byte of 0x7f or 0xff is NaN: none may be)
+    const uint32_t nan = ((codes.x & 0x7f7f7f7fu) + 0x01010101u) | ((codes.y & 0x7f7f7f7fu) + 0x01010101u);
+    return codes.x == x && codes.y == y && !(nan & 0x80808080u);
+}
+
 template <int kD, int kKind, bool kWarp>
 __global__ void __launch_bounds__(32 * kMoveWarps)
     compact_kernel(const __grid_constant__ CompactArgs p)
@@ -67,6 +125,7 @@ __global__ void __launch_bounds__(32 * kMoveWarps)
     constexpr int kChunks = kD / 8;           // 16-byte chunks of a row
     constexpr int kStep = 32 / kChunks;       // rows of one load of the warp
     constexpr int kLoads = 16 / kStep;        // loads of a page
+    constexpr int kPageBytes = 32 * kD;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -108,90 +167,153 @@ __global__ void __launch_bounds__(32 * kMoveWarps)
         if (p.dev_status) atomicOr(p.dev_status, static_cast<int32_t>(bit));
     };
 
-    // A page's rows, found: for lane < 16 the row of the pool that slot `lane`
-    // gets (-1: none), whether some row moves and which, and the page's tile.
-    struct Found {
-        int64_t row, tile;
-        unsigned moved;
+    // A page's rows are found in three steps, a round apart each, so that nobody waits
+    // for an index: the kept rows of its 16 slots and its own block; the blocks of the
+    // rows; where all that is.  (Every lane its slot, lanes 16 - 31 as 0 - 15.)
+    struct Kept {
+        int g, i, before, to_blk;
     };
-    auto find = [&](int g) -> Found {
-        Found f{-1, -1, 0};
-        if (g >= pages) return f;
-        const int page = page0 + g, pos = page * 16 + (lane & 15), j = pos - base;
-        int from = pos;
-        bool moves = false;
+    auto ask = [&](int g) -> Kept {
+        Kept a{g, -1, -1, -1};
+        if (g >= pages) return a;
+        const int j = (page0 + g) * 16 + (lane & 15) - base;
         if (j >= 0 && j < m) {
-            const int i = __ldg(kept + j), before = j > 0 ? __ldg(kept + j - 1) : -1;
-            if (i >= j && i > before && i < sr.len) {
-                from = base + i;
-                moves = i != j;
+            a.i = __ldg(kept + j);
+            if (j > 0) a.before = __ldg(kept + j - 1);
+        }
+        a.to_blk = __ldg(table + page0 + g);
+        return a;
+    };
+    struct From {
+        int g, from, to_blk, of_blk;
+        bool moves;
+    };
+    auto follow = [&](const Kept &a) -> From {
+        From b{a.g, -1, a.to_blk, a.to_blk, false};
+        if (a.g >= pages) return b;
+        b.from = (page0 + a.g) * 16 + (lane & 15);
+        const int j = b.from - base;
+        if (j >= 0 && j < m) {
+            if (a.i >= j && a.i > a.before && a.i < sr.len) {
+                b.from = base + a.i;
+                b.moves = a.i != j;
             } else if (lane < 16) {
                 report(PKV_DEV_BAD_KEEP);
             }
         }
-        const int to_blk = __ldg(table + page);
-        const int of_blk = moves ? __ldg(table + (from >> 4)) : to_blk;
-        const bool to_ok = to_blk >= 0 && to_blk < p.num_blocks;
-        const bool of_ok = of_blk >= 0 && of_blk < p.num_blocks;
+        if (b.moves) b.of_blk = __ldg(table + (b.from >> 4));
+        return b;
+    };
+    // For lane < 16 the row of the pool that slot `lane` gets (-1: none), which rows
+    // move, and the page's tile.
+    struct Found {
+        int64_t row, tile;
+        unsigned moved;
+    };
+    auto find = [&](const From &b) -> Found {
+        Found f{-1, -1, 0};
+        if (b.g >= pages) return f;
+        const bool to_ok = b.to_blk >= 0 && b.to_blk < p.num_blocks;
+        const bool of_ok = b.of_blk >= 0 && b.of_blk < p.num_blocks;
+        bool moves = b.moves;
         if (moves && !(to_ok && of_ok)) {
             if (lane < 16) report(PKV_DEV_BAD_BLOCK);
             moves = false;
-            from = pos;
         }
         f.moved = __ballot_sync(0xffffffffu, moves) & 0xffffu;
         if (!to_ok) return f;
-        f.tile = static_cast<int64_t>(to_blk) * p.num_kv_heads + h;
-        f.row = moves ? (static_cast<int64_t>(of_blk) * p.num_kv_heads + h) * 16 + (from & 15)
-                      : f.tile * 16 + (pos & 15);
+        f.tile = static_cast<int64_t>(b.to_blk) * p.num_kv_heads + h;
+        f.row = moves ? (static_cast<int64_t>(b.of_blk) * p.num_kv_heads + h) * 16 + (b.from & 15)
+                      : f.tile * 16 + (lane & 15);
         return f;
     };
     const int c = lane % kChunks, r0 = lane / kChunks;
-    auto load = [&](const Found &f, uint4 (&x)[kLoads]) {
-        if (!f.moved) return;
+    // Rows on their way to the warp's buffers: chunk lane + 32 e of a page by this lane,
+    // which is the one that reads it again.
+    extern __shared__ __align__(16) uint8_t smem[];
+    const uint32_t buffers = ptx::smem_addr(smem) + warp * (kBufs * kPageBytes) + lane * 16;
+    auto load = [&](const Found &f, int buf) {
+        if (f.moved) {
+            const uint32_t to = buffers + buf * kPageBytes;
+#pragma unroll
+            for (int e = 0; e < kLoads; ++e) {
+                const int r = r0 + kStep * e;
+                const int64_t row = __shfl_sync(0xffffffffu, f.row, r);
+                // (a code tile's other rows are quantized with the moved ones)
+                if (kCodes || (f.moved >> r & 1u))
+                    ptx::cp_async_16(to + 512 * e, pool + row * kChunks + c);
+            }
+        }
+        ptx::cp_async_commit();
+    };
+    // Codes and scale of a page.  Nobody reads them here: they need not wait for the team.
+    auto quantize = [&](const Found &f, uint32_t from) {
+        __half2 top = __float2half2_rn(0.f);   // (NaN left out, as the quantizer does)
 #pragma unroll
         for (int e = 0; e < kLoads; ++e) {
-            const int r = r0 + kStep * e;
-            const int64_t row = __shfl_sync(0xffffffffu, f.row, r);
-            // (a code tile's other rows are quantized with the moved ones)
-            if (kCodes || (f.moved >> r & 1u)) x[e] = pool[row * kChunks + c];
+            const uint4 v = ptx::lds128(from + 512 * e);
+            const __half2 *x = reinterpret_cast<const __half2 *>(&v);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) top = __hmax2(top, __habs2(x[w]));
         }
+        float amax = fmaxf(__low2float(top), __high2float(top));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const float scale = __fdiv_rn(amax, kKind == kMoveF8 ? 448.0f : 127.0f);
+        const float rcp = __frcp_rn(scale);
+        uint2 *codes =
+            reinterpret_cast<uint2 *>(is_v ? p.v_codes : p.k_codes) + f.tile * (16 * kChunks) + lane;
+        // (rolled: unrolled, the warps waited for instructions)
+#pragma unroll 1
+        for (int e = 0; e < kLoads; ++e) {
+            const uint4 v = ptx::lds128(from + 512 * e);
+            uint2 w;
+            if constexpr (kKind == kMoveF8) {
+                if (!near_codes_f8(v, rcp, w)) w = chunk_codes_fp8(v, scale);
+            } else {
+                if (!near_codes_i8(v, rcp, w)) w = chunk_codes(v, scale, rcp);
+            }
+            codes[32 * e] = w;
+        }
+        if (lane == 0) (is_v ? p.v_scales : p.k_scales)[f.tile] = scale;
     };
-    auto store = [&](const Found &f, const uint4 (&x)[kLoads]) {
-        if (!f.moved) return;
-        uint4 *dst = pool + f.tile * (16 * kChunks);
+    auto store = [&](const Found &f, uint32_t from) {
+        uint4 *dst = pool + f.tile * (16 * kChunks) + lane;
 #pragma unroll
         for (int e = 0; e < kLoads; ++e)
-            if (f.moved >> (r0 + kStep * e) & 1u) dst[lane + 32 * e] = x[e];
-        if constexpr (kCodes) {
-            float amax = chunks_absmax(x);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            const float scale = __fdiv_rn(amax, kKind == kMoveF8 ? 448.0f : 127.0f);
-            const float rcp = __frcp_rn(scale);
-            uint2 *codes = reinterpret_cast<uint2 *>(is_v ? p.v_codes : p.k_codes) +
-                           f.tile * (16 * kChunks);
-#pragma unroll
-            for (int e = 0; e < kLoads; ++e)
-                codes[lane + 32 * e] = kKind == kMoveF8 ? chunk_codes_fp8(x[e], scale)
-                                                        : chunk_codes(x[e], scale, rcp);
-            if (lane == 0) (is_v ? p.v_scales : p.k_scales)[f.tile] = scale;
-        }
+            if (f.moved >> (r0 + kStep * e) & 1u) dst[32 * e] = ptx::lds128(from + 512 * e);
     };
 
-    uint4 x[kLoads], y[kLoads];
-    Found f = find(rank);
-    load(f, x);
+    const Kept a0 = ask(rank), a1 = ask(rank + team), a2 = ask(rank + 2 * team);
+    Kept asked = ask(rank + 3 * team);
+    const From b0 = follow(a0), b1 = follow(a1);
+    From from = follow(a2);
+    Found f = find(b0), next = find(b1);
+    load(f, 0);
+    load(next, 1);
+    // Round k: its rows are there; the rows of round k - 1 are written, for which the
+    // team has met; its codes, which need not wait.  So a meeting has a round's work to
+    // hide behind, and so have the writes that it makes visible.
+    Found before{-1, -1, 0};
+    int buf = 0;
     for (int g = rank; g - rank < pages; g += team) {
-        const Found next = find(g + team);
+        const int free = buf == 0 ? kBufs - 1 : buf - 1;
+        ptx::cp_async_wait<1>();
         team_arrive<kWarp>();
-        load(next, y);
+        if (before.moved) store(before, buffers + free * kPageBytes);
+        const Found later = find(from);
+        load(later, free);
+        from = follow(asked);
+        asked = ask(g + 4 * team);
+        if (kCodes && f.moved) quantize(f, buffers + buf * kPageBytes);
         team_wait<kWarp>();
-        store(f, x);
+        before = f;
         f = next;
-#pragma unroll
-        for (int e = 0; e < kLoads; ++e) x[e] = y[e];
+        next = later;
+        buf = buf == kBufs - 1 ? 0 : buf + 1;
     }
+    if (before.moved) store(before, buffers + (buf == 0 ? kBufs - 1 : buf - 1) * kPageBytes);
 }
 
 struct CompactCall {
@@ -213,18 +335,35 @@ pkv_status launch_compact(const CompactCall &c, const CompactArgs &a)
     const int64_t pages = c.num_tokens / c.num_seqs / 16 + 2;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(32 * kMoveWarps);
+    cfg.dynamicSmemBytes = kMoveWarps * kBufs * 32 * kD;
     cfg.stream = static_cast<cudaStream_t>(c.stream);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
+    const auto kern = pages <= 4 ? compact_kernel<kD, kKind, true> : compact_kernel<kD, kKind, false>;
+    DeviceInfo di;
+    if (!current_device_info(&di)) return PKV_ERR_CUDA;
+    {
+        static bool ready[2][64] = {};
+        std::lock_guard<std::mutex> lock(g_cfg_mu);
+        bool &r = ready[pages <= 4][di.device & 63];
+        if (!r) {
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(cfg.dynamicSmemBytes)) != cudaSuccess) {
+                cudaGetLastError();
+                return PKV_ERR_CUDA;
+            }
+            r = true;
+        }
+    }
     cudaError_t e;
     if (pages <= 4) {
         const int64_t grid = (a.chains + kMoveWarps - 1) / kMoveWarps;
         if (grid > INT32_MAX) return PKV_ERR_UNSUPPORTED;
         cfg.gridDim = dim3(static_cast<unsigned>(grid));
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, compact_kernel<kD, kKind, true>, a);
+        e = cudaLaunchKernelEx(&cfg, kern, a);
     } else {
         int ctas = 1;
         while (ctas < 8 && ctas * kMoveWarps < pages && a.chains * ctas < 2 * 152) ctas *= 2;
@@ -234,7 +373,7 @@ pkv_status launch_compact(const CompactCall &c, const CompactArgs &a)
         attr[1].val.clusterDim.x = static_cast<unsigned>(ctas);
         attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
         cfg.numAttrs = 2;
-        e = cudaLaunchKernelEx(&cfg, compact_kernel<kD, kKind, false>, a);
+        e = cudaLaunchKernelEx(&cfg, kern, a);
     }
     if (e != cudaSuccess) {
         cudaGetLastError();

@@ -180,6 +180,19 @@ __device__ __forceinline__ void cp_async_wait_all()
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
+// The copies since the last call as a group, and the wait until at most kLeft of this
+// thread's newest groups are under way.
+__device__ __forceinline__ void cp_async_commit()
+{
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
 // Arrive on bar once every cp.async this thread issued so far has landed.
 // .noinc: the arrival counts against the count given at mbarrier.init.
 __device__ __forceinline__ void cp_async_arrive_noinc(uint32_t bar)
