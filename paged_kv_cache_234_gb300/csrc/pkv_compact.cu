@@ -8,15 +8,21 @@
 // takes its rows from pages >= p.  A page may be written as soon as every row
 // that lies in it has been read, and those go to pages <= p.  The pages of one
 // (sequence, kv head, K | V) are therefore taken in rounds by a team -- a warp, a
-// CTA or a cluster of CTAs -- one page to a warp: a round's rows are read into
-// registers, the team meets at a barrier, the round's pages are written.  Reading
-// ahead is always safe, so the next round's rows are on their way before this
-// one's are written.  No row is read twice and nothing is kept in memory.
+// CTA or a cluster of CTAs -- one page to a warp: a round's rows are fetched into
+// shared memory, the team meets at a barrier, the round's pages are written.
+// Reading ahead is always safe, so the rows of two rounds are on their way, their
+// places found two rounds ahead of that, and a page is written a round after its
+// rows came, which leaves the barrier a round to complete in.  No row is read twice.
 //
-// Bound by memory: a moved row is read once and written once; code caches write
-// the codes too.  A page's 16 rows of head_dim 128 are 4 KB, eight 16-byte loads
-// of a lane in flight, and a quantized tile's largest magnitude is found by
-// shuffles alone, since a tile is a warp's.
+// A moved row is read once and written once; code caches write the codes too.  A
+// page's 16 rows of head_dim 128 are 4 KB; a quantized tile's largest magnitude is
+// found by shuffles alone, since a tile is a warp's.
+//
+// Measured: 8 contexts of 16384 tokens to their halves, fp16, 8 kv heads: 93 us, 85 %
+// of the copy's rate; one FP8 context of 131072 tokens to its half: 299 us, half of it:
+// 16 chains keep 128 CTAs of 8 warps busy (16 warps: 348 us, 4: 478), and a page's
+// codes take a warp longer than its rows.  Paths of 16 tokens in 64 trees, which
+// is a warp's work each: 4.0 us (a launch), INT8 7.8.
 #include <cuda_fp16.h>
 #include <stdint.h>
 
@@ -69,33 +75,35 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
-// The codes of eight values by x * fl(1 / scale), which is within 2 ulp of
-// fl(x / scale); false if one of them lies so close to a tie, or is NaN, that the
-// quotient itself has to say.  INT8: see quant_code.
-__device__ __forceinline__ bool near_codes_i8(const uint4 &raw, float rcp, uint2 &codes)
+// The codes of eight values by y = x * fl(1 / scale), which is within 2 ulp of the
+// quotient q = fl(x / scale) that the quantizer rounds.  Returns a bit for every value
+// whose y lies so close to the middle M of two codes that q may be M or beyond, or is
+// NaN.  INT8: see quant_code.
+__device__ __forceinline__ uint32_t near_codes_i8(const uint4 &raw, float rcp, uint2 &codes)
 {
     const __half2 *h = reinterpret_cast<const __half2 *>(&raw);
     const uint64_t by = ptx::f32x2(rcp, rcp), magic = ptx::f32x2(kRoundMagic, kRoundMagic);
     const uint64_t back = ptx::f32x2(-kRoundMagic, -kRoundMagic), neg = ptx::f32x2(-1.f, -1.f);
-    float off = 0.f;
-    uint32_t c[4];
+    const float sure = 0.5f - 0.00006103515625f;   // 0.5 - 2^-14
+    uint32_t c[4], doubt = 0;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
         const float2 f = __half22float2(h[w]);
         const uint64_t y = ptx::mul2(ptx::f32x2(f.x, f.y), by);
         const uint64_t t = ptx::add2(y, magic);
         const float2 d = ptx::f32x2_parts(ptx::fma2(ptx::add2(t, back), neg, y));
-        off = max_nan(off, max_nan(fabsf(d.x), fabsf(d.y)));
+        if (!(fabsf(d.x) < sure)) doubt |= 1u << 2 * w;
+        if (!(fabsf(d.y) < sure)) doubt |= 2u << 2 * w;
         const float2 i = ptx::f32x2_parts(t);
         c[w] = ptx::prmt(__float_as_uint(i.x), __float_as_uint(i.y), 0x0040);
     }
     codes = make_uint2(ptx::prmt(c[0], c[1], 0x5410), ptx::prmt(c[2], c[3], 0x5410));
-    return off < 0.5f - 0.00006103515625f;   // 0.5 - 2^-14
+    return doubt;
 }
 
-// FP8: rounding is monotonic, so where the values a little below and above the
-// product (1 -+ 2^-21: more than the 2 ulp) have the same code, the quotient has it.
-__device__ __forceinline__ bool near_codes_f8(const uint4 &raw, float rcp, uint2 &codes)
+// FP8: rounding is monotonic, so where the values a little below and above y (1 -+
+// 2^-21: more than the 2 ulp) have the same code, q has it.
+__device__ __forceinline__ uint32_t near_codes_f8(const uint4 &raw, float rcp, uint2 &codes)
 {
     const __half2 *h = reinterpret_cast<const __half2 *>(&raw);
     const float down = 1.f - 0x1p-21f, up = 1.f + 0x1p-21f;
@@ -111,10 +119,60 @@ __device__ __forceinline__ bool near_codes_f8(const uint4 &raw, float rcp, uint2
         hi[w] = __nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3);
     }
     codes = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-    const uint32_t x = hi[0] | hi[1] << 16, y = hi[2] | hi[3] << 16;
-    // (a byte of 0x7f or 0xff is NaN: none may be)
-    const uint32_t nan = ((codes.x & 0x7f7f7f7fu) + 0x01010101u) | ((codes.y & 0x7f7f7f7fu) + 0x01010101u);
-    return codes.x == x && codes.y == y && !(nan & 0x80808080u);
+    // the bytes that differ, and NaN (0x7f, 0xff): their top bits
+    auto tops = [](uint32_t a, uint32_t b) {
+        const uint32_t d = a ^ b;
+        return (((d & 0x7f7f7f7fu) + 0x7f7f7f7fu) | d | ((a & 0x7f7f7f7fu) + 0x01010101u)) &
+               0x80808080u;
+    };
+    // (bits 7, 15, 23 and 31 to 0 - 3)
+    auto four = [](uint32_t t) { return (t >> 7) * 0x00204081u >> 21 & 0xfu; };
+    return four(tops(codes.x, hi[0] | hi[1] << 16)) |
+           four(tops(codes.y, hi[2] | hi[3] << 16)) << 4;
+}
+
+// The codes of the values in doubt (fp16 normal ones hit ties exactly: one of 2000 for
+// FP8), without the quotient: with a = |x| and the code L below M, e = a - M scale is
+// exact (a multiple of the lowest bit of M scale, and less than 2^12 of them), and q
+// is M -- which goes to the even code -- if e is not above half an ulp of M times the
+// scale; the ulp below a power of two is half of that above.
+// (One after the other: by divisions of all eight values a warp took a microsecond and
+// more for every doubt.)
+template <int kKind>
+__device__ __forceinline__ void settle(const uint4 &raw, float scale, float rcp, uint32_t doubt,
+                                       uint2 &codes)
+{
+#pragma unroll 1
+    for (; doubt; doubt &= doubt - 1) {
+        const int i = __ffs(doubt) - 1;
+        const uint32_t two = i & 4 ? (i & 2 ? raw.w : raw.z) : (i & 2 ? raw.y : raw.x);
+        const float x = __half2float(
+            __ushort_as_half(static_cast<unsigned short>(i & 1 ? two >> 16 : two & 0xffffu)));
+        const float a = fabsf(x), y = a * rcp;
+        uint32_t code = 0;
+        if (!isnan(y)) {
+            uint32_t low;
+            float mid;
+            if constexpr (kKind == kMoveI8) {
+                low = static_cast<uint32_t>(y);
+                mid = static_cast<float>(low) + 0.5f;
+            } else {
+                low = __nv_cvt_float_to_fp8(y * (1.f - 0x1p-21f), __NV_SATFINITE, __NV_E4M3);
+                const uint32_t both = ptx::e4m3x2_to_f16x2(low | (low + 1) << 8);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&both));
+                mid = 0.5f * (f.x + f.y);
+            }
+            const uint32_t bits = __float_as_uint(mid);
+            const float e = fmaf(-mid, scale, a);
+            const float half = scale * __uint_as_float((bits & 0x7f800000u) - (24u << 23));
+            const bool tie = e >= 0.f ? e <= half : -e <= (bits & 0x7fffffu ? half : 0.5f * half);
+            code = low + (tie ? low & 1u : e > 0.f);
+            if (x < 0.f) code = kKind == kMoveI8 ? -code & 0xffu : code | 0x80u;
+        }
+        const int at = (i & 3) * 8;
+        uint32_t &w = i & 4 ? codes.y : codes.x;
+        w = (w & ~(0xffu << at)) | code << at;
+    }
 }
 
 template <int kD, int kKind, bool kWarp>
@@ -264,16 +322,15 @@ __global__ void __launch_bounds__(32 * kMoveWarps)
         const float rcp = __frcp_rn(scale);
         uint2 *codes =
             reinterpret_cast<uint2 *>(is_v ? p.v_codes : p.k_codes) + f.tile * (16 * kChunks) + lane;
-        // (rolled: unrolled, the warps waited for instructions)
-#pragma unroll 1
+        // (paths of 64 trees over INT8: 7.8 us, 8.2 rolled, 10 and more with the tile in
+        // registers and all unrolled, when the warps waited for instructions)
+#pragma unroll 2
         for (int e = 0; e < kLoads; ++e) {
             const uint4 v = ptx::lds128(from + 512 * e);
             uint2 w;
-            if constexpr (kKind == kMoveF8) {
-                if (!near_codes_f8(v, rcp, w)) w = chunk_codes_fp8(v, scale);
-            } else {
-                if (!near_codes_i8(v, rcp, w)) w = chunk_codes(v, scale, rcp);
-            }
+            const uint32_t doubt =
+                kKind == kMoveF8 ? near_codes_f8(v, rcp, w) : near_codes_i8(v, rcp, w);
+            if (doubt) settle<kKind>(v, scale, rcp, doubt, w);
             codes[32 * e] = w;
         }
         if (lane == 0) (is_v ? p.v_scales : p.k_scales)[f.tile] = scale;
@@ -365,8 +422,10 @@ pkv_status launch_compact(const CompactCall &c, const CompactArgs &a)
         cfg.numAttrs = 1;
         e = cudaLaunchKernelEx(&cfg, kern, a);
     } else {
+        // CTAs until there is one for every SM (until there are two: the halves of 8
+        // contexts of 16384 in 94.8 against 93.0 us)
         int ctas = 1;
-        while (ctas < 8 && ctas * kMoveWarps < pages && a.chains * ctas < 2 * 152) ctas *= 2;
+        while (ctas < 8 && ctas * kMoveWarps < pages && a.chains * ctas < 152) ctas *= 2;
         if (a.chains * ctas > INT32_MAX) return PKV_ERR_UNSUPPORTED;
         cfg.gridDim = dim3(static_cast<unsigned>(a.chains * ctas));
         attr[1].id = cudaLaunchAttributeClusterDimension;
