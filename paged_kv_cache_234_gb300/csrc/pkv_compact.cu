@@ -38,7 +38,9 @@ namespace {
 
 enum { kMoveF16 = 0, kMoveI8 = 1, kMoveF8 = 2 };
 constexpr int kMoveWarps = 8;
-constexpr int kBufs = 3;   // pages of a warp: the last round's, this one's, the next one's
+// Pages of a warp: the last round's, this one's, the next one's.  (Four leave an SM one
+// CTA, and 16 clusters of 8 are not all placed at once: 479 against 299 us.)
+constexpr int kBufs = 3;
 
 struct CompactArgs {
     __half *k_pool, *v_pool;
@@ -342,13 +344,21 @@ __global__ void __launch_bounds__(32 * kMoveWarps)
             if (f.moved >> (r0 + kStep * e) & 1u) dst[32 * e] = ptx::lds128(from + 512 * e);
     };
 
-    const Kept a0 = ask(rank), a1 = ask(rank + team), a2 = ask(rank + 2 * team);
-    Kept asked = ask(rank + 3 * team);
-    const From b0 = follow(a0), b1 = follow(a1);
-    From from = follow(a2);
-    Found f = find(b0), next = find(b1);
-    load(f, 0);
-    load(next, 1);
+    // f[0]: this round's page, then those whose rows are on their way
+    constexpr int kAhead = kBufs - 1;
+    Found f[kAhead];
+    {
+        Kept a[kAhead];
+        From b[kAhead];
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) a[q] = ask(rank + q * team);
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) b[q] = follow(a[q]);
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) load(f[q] = find(b[q]), q);
+    }
+    From from = follow(ask(rank + kAhead * team));
+    Kept asked = ask(rank + (kAhead + 1) * team);
     // Round k: its rows are there; the rows of round k - 1 are written, for which the
     // team has met; its codes, which need not wait.  So a meeting has a round's work to
     // hide behind, and so have the writes that it makes visible.
@@ -356,18 +366,19 @@ __global__ void __launch_bounds__(32 * kMoveWarps)
     int buf = 0;
     for (int g = rank; g - rank < pages; g += team) {
         const int free = buf == 0 ? kBufs - 1 : buf - 1;
-        ptx::cp_async_wait<1>();
+        ptx::cp_async_wait<kAhead - 1>();
         team_arrive<kWarp>();
         if (before.moved) store(before, buffers + free * kPageBytes);
         const Found later = find(from);
         load(later, free);
         from = follow(asked);
-        asked = ask(g + 4 * team);
-        if (kCodes && f.moved) quantize(f, buffers + buf * kPageBytes);
+        asked = ask(g + (kAhead + 2) * team);
+        if (kCodes && f[0].moved) quantize(f[0], buffers + buf * kPageBytes);
         team_wait<kWarp>();
-        before = f;
-        f = next;
-        next = later;
+        before = f[0];
+#pragma unroll
+        for (int q = 0; q + 1 < kAhead; ++q) f[q] = f[q + 1];
+        f[kAhead - 1] = later;
         buf = buf == kBufs - 1 ? 0 : buf + 1;
     }
     if (before.moved) store(before, buffers + (buf == 0 ? kBufs - 1 : buf - 1) * kPageBytes);
