@@ -658,7 +658,8 @@ PKV_API pkv_status pkv_tree_accept(int32_t *kept, int32_t *kept_lens, int32_t *n
  * above the one before sets PKV_DEV_BAD_KEEP and its row is not moved; what
  * rows the others get is then not specified.  A block id outside
  * [0, num_blocks) sets PKV_DEV_BAD_BLOCK, and the row is not moved.  No written
- * block may belong to two sequences (copy it first: pkv_bm_cow).
+ * block may belong to two sequences (copy it first: pkv_bm_cow) or stand twice in
+ * a sequence's table.
  */
 PKV_API pkv_status pkv_compact_fp16(
     void *k_cache, void *v_cache, int num_blocks, const int32_t *kept, const int32_t *kept_lens,

@@ -30,13 +30,22 @@
 // second kernel.  (Up to 64 rows per kv head; with more the rows are the long side:
 // pkv_prefill_tree.cu.)
 //
-// Roles of the warps: four for every 32 rows work on scores and rows; of the next four
+// Roles of the warps: four for every 16 rows work on scores and rows; of the next four
 // one issues the products, two the TMA loads of K and Q, and of V (a ring of tiles, K
 // and V in turn), one finds the items.
-// INT8 / FP8 pages land in a second ring, and further warps widen them exactly to
-// fp16.  The K scale of a page multiplies its keys' scores.  Its V scale enters
-// the exponent, 2^(S' + log2 v - m), so that the reference is that of the largest
-// contribution p V, and the sums take the probability times 1 / v.
+// INT8 / FP8 pages land in a ring of codes, and two teams of four warps widen them
+// exactly to fp16: K, a thread per key, into TMEM, from where it is the A operand of
+// its product without passing shared memory again; V into shared memory, where it lies
+// as the pages' fp16 would.  The K scale of a page multiplies its keys' scores.  Its V
+// scale enters the exponent, 2^(S' + log2 v - m), so that the reference is that of the
+// largest contribution p V, and the sums take the probability times 1 / v.
+//
+// Measured, 64 trees of 8 tokens over 2048 keys, 32 / 8 heads, head_dim 128: fp16 96 us,
+// 85 % of the copy's rate; INT8 81, FP8 78 (51 and 53 %): there the score warps' chain
+// and the widening (40 instructions for 32 codes) share the schedulers, which issue in
+// 44 % of the cycles, and wait for instructions more than for any pipe.  One tree of 8
+// over 131072: fp16 93, INT8 71, FP8 67 us.  Eight trees of 8 over 512, one head to a kv
+// head, INT8: 13.4, latencies from the launch to the join one after the other.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -67,7 +76,6 @@ constexpr float kLift = 6.f;    // log2 factor of the probabilities
 constexpr float kLazy = 9.f;    // log2 excess over the reference that is let be
 constexpr float kNone = -3.0e38f;        // reference of a row that has seen nothing
 constexpr float kLeastV = 0x1p-60f;      // V scales below (zero) count as this
-constexpr int kParents = 512;   // parents of a sequence kept in shared memory
 
 // Score warps: a group of four, a thread per key, for every 16 rows.  A tile's chain
 // (scores, exponentials, reference, product) has more waits than work, which groups
@@ -161,8 +169,8 @@ struct TreeSmem {
     static constexpr int kAt = kSlope + 4 * kN;     // the row's place in the output, or -1
     static constexpr int kSums = kAt + 8 * kN;      // [4 quarters of the keys][kN]
     static constexpr int kMask = kSums + 16 * kN;   // [4 quarters of the keys][kN]: bits
-    static constexpr int kUp = kMask + 16 * kN;     // parents
-    static constexpr int kBytes = kUp + 2 * 4 * kParents;   // of both item slots
+    static constexpr int kUp = kMask + 16 * kN;     // [2 item slots][kN]: parents
+    static constexpr int kBytes = kUp + 8 * kN;
     // a second CTA on the SM would wait for TMEM: ask for more than half
     static constexpr int kAsk = kBytes > 120 * 1024 ? kBytes : 120 * 1024;
     static_assert(kAsk <= 227 * 1024, "shared memory of one CTA");
@@ -496,15 +504,13 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
             if (group_any(i, fail)) break;
             if (nt == 0) break;
             const bool bad_tree = flags[4 + (k & 1)] != 0;
-            const int *up = reinterpret_cast<const int *>(smem + M::kUp) + kParents * (k & 1);
-            const int32_t *par = p.parents + it.start;
-            auto parent = [&](int j) { return j < kParents ? up[j] : __ldg(par + j); };
+            const int *up = reinterpret_cast<const int *>(smem + M::kUp) + kN * (k & 1);
             const int node = mine && !bad_tree ? rj : -1;
             int lo = 0;
             if (p.window > 0) {
                 int pos = ctx;
                 if (node >= 0)
-                    for (int j = parent(node); j >= 0; j = parent(j)) ++pos;
+                    for (int j = up[node]; j >= 0; j = up[j]) ++pos;
                 lo = max(pos - p.window + 1, 0);
             }
             // whether some rows of the group are not the item's
@@ -540,7 +546,7 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                             if (real(v0 + kPagesPerTile) * kPage > ctx)
                                 for (int a = node, far = 0;
                                      a >= 0 && (p.window <= 0 || far < p.window);
-                                     a = parent(a), ++far) {
+                                     a = up[a], ++far) {
                                     const int e = ((ctx + a) >> 4 << 4) - (gap + v0) * kPage +
                                                   ((ctx + a) & 15);   // (behind the gap)
                                     if (e < 0) break;
@@ -560,8 +566,8 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                 if (p.slopes) {
                     int d = at - ctx;
                     if (d >= 0 && !bad_tree) {
-                        int b = d < n ? parent(d) : -1;
-                        for (d = 0; b >= 0; b = parent(b)) ++d;
+                        int b = d < n ? up[d] : -1;
+                        for (d = 0; b >= 0; b = up[b]) ++d;
                     }
                     far = static_cast<float>(d);
                 }
@@ -1129,12 +1135,13 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                         ptx::mbar_arrive(i_full(k));
                     }
                     // its tree: every parent an earlier row
-                    int *up = reinterpret_cast<int *>(smem + M::kUp) + kParents * (k & 1);
+                    // (a token has a row at least: kN are enough)
+                    int *up = reinterpret_cast<int *>(smem + M::kUp) + kN * (k & 1);
                     bool wrong = false;
                     for (int j = lane; j < it.n; j += 32) {
                         const int a = __ldg(p.parents + it.start + j);
                         wrong |= a < -1 || a >= j;
-                        if (j < kParents) up[j] = a;
+                        up[j] = a;
                     }
                     wrong = __any_sync(0xffffffffu, wrong);
                     if (lane == 0) {
