@@ -1544,6 +1544,78 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     }
 }
 
+// kTree: the same with a warp a row, where there are few parts: more rows at a time.
+constexpr int kFewParts = 16;
+
+template <int kD>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    join_few_kernel(const __grid_constant__ PrefillArgs p)
+{
+    constexpr int kC = kD / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t all = static_cast<int64_t>(p.num_tokens) * p.num_heads;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kJoinWarps + warp;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    if (row >= all) return;
+    const int parts = 2 * p.splits;
+    const float2 ml =
+        lane < parts ? __ldcg(p.part_ml + lane * all + row) : make_float2(-INFINITY, 0.f);
+    const int tok = static_cast<int>(row / p.num_heads);
+    const int seq = warp_search(p.num_seqs, tok, [&](int s) { return __ldg(p.query_starts + s); });
+    if (seq < 0) return;
+    SeqRows sr;
+    sr.load(p.query_starts, p.context_lens, seq, p.num_tokens, p.ctx_cap);
+    if (tok - sr.start >= sr.len) return;
+    float m = ml.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const bool bad = __any_sync(0xffffffffu, ml.y < 0.f);
+    const float f = ml.y == 0.f ? 0.f : ptx::ex2(ml.x - m);
+    float l = f * ml.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    float acc[kC];
+#pragma unroll
+    for (int c = 0; c < kC; ++c) acc[c] = 0.f;
+    const float *src = p.part_acc + row * kD + lane * kC;
+    // (the parts that have something, four at a time)
+    for (unsigned left = __ballot_sync(0xffffffffu, f != 0.f); left;) {
+        float v[4][kC], w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int z = left ? __ffs(left) - 1 : 0;
+            w[u] = left ? __shfl_sync(0xffffffffu, f, z) : 0.f;
+#pragma unroll
+            for (int c = 0; c < kC; ++c) v[u][c] = 0.f;
+            if (left) {
+                const float *a = src + z * all * kD;
+                if constexpr (kC == 4) {
+                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(a));
+                    v[u][0] = x.x;
+                    v[u][1] = x.y;
+                    v[u][2] = x.z;
+                    v[u][3] = x.w;
+                } else {
+                    const float2 x = __ldcg(reinterpret_cast<const float2 *>(a));
+                    v[u][0] = x.x;
+                    v[u][1] = x.y;
+                }
+            }
+            left &= left - 1;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int c = 0; c < kC; ++c) acc[c] += w[u] * v[u][c];
+    }
+    const bool zero = bad || l == 0.f;
+    __half2 *o = reinterpret_cast<__half2 *>(p.out + row * kD + lane * kC);
+#pragma unroll
+    for (int c = 0; c < kC; c += 2)
+        o[c / 2] = __floats2half2_rn(zero ? 0.f : acc[c] / l, zero ? 0.f : acc[c + 1] / l);
+}
+
 // -------------------------------------------------------------------- host
 struct PrefillCall {
     void *out;
@@ -1590,8 +1662,13 @@ struct Plan {
 // and 277 us, of 2048 (28 / 4) 40 and 115, 4096 tokens over 16384 650 and 756
 // (capped 1021 and 1089); the other way around, 256 over 4096: 51 and 44 (37 with
 // three), 128 over 8192: 95 and 60 (33 with six).
+//   kTree: sequences have most_tokens at most, which bounds the items better, and up to
+// 8 splits are joined by join_few_kernel: 0.25 + 0.03 splits.  32 trees of 25 over 2048
+// (14 / 2 heads, head_dim 64, biased) 43 and 32 us (42 with three), 16 of 32 over 4096
+// (28 / 4) 54 and 44 (56), 4 of 64 over 2048 (32 / 8) 31 and 26 (24 with four); the other
+// way around 16 of 64 over 8192: 106 and 127, 16 of 20 over 1024 (FP8): 22 and 32.
 pkv_status plan_of(int num_tokens, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
-                   int max_context_len, Plan *plan)
+                   int max_context_len, Plan *plan, [[maybe_unused]] int most_tokens = 0)
 {
     if (num_tokens < 0 || num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
         max_context_len < 0 || num_heads % num_kv_heads != 0)
@@ -1602,10 +1679,15 @@ pkv_status plan_of(int num_tokens, int num_seqs, int num_heads, int num_kv_heads
     plan->chunks = (group + plan->chunk - 1) / plan->chunk;
     plan->tokens = kRows / plan->chunk;
     plan->units = num_tokens / plan->tokens + static_cast<int64_t>(num_seqs);
-    const int64_t items = plan->units * num_kv_heads * plan->chunks;
+    int64_t items = plan->units * num_kv_heads * plan->chunks;
     const int64_t tiles = (static_cast<int64_t>(max_context_len) + kTile - 1) / kTile + 1;
     if (plan->units > INT32_MAX || items * kMaxSplits > INT32_MAX)
         return PKV_ERR_UNSUPPORTED;
+    if constexpr (kTree) {
+        const int64_t most = most_tokens < num_tokens ? most_tokens : num_tokens;
+        const int64_t units = num_seqs * ((most + plan->tokens - 1) / plan->tokens);
+        if (units < plan->units) items = units * num_kv_heads * plan->chunks;
+    }
     plan->splits = 1;
     if (num_seqs > 0 && items < 4 * kSms) {  // (beyond, at most a fourth of the time is idle)
         const double krows = static_cast<double>(num_tokens) * num_heads / 1000;
@@ -1620,7 +1702,9 @@ pkv_status plan_of(int num_tokens, int num_seqs, int num_heads, int num_kv_heads
             const double t = (shared ? 0.63 * tile : tile) / z;
             double us = w * ((most + least) / 2 * t + item) + (ceil(w) - w) * (least * t + item);
             if (us < most * t + item) us = most * t + item;
-            if (z > 1) us += 1.5 + (1.05 + 0.125 * z) * krows;
+            if (z > 1)
+                us += 1.5 + (kTree && 2 * z <= kFewParts ? 0.25 + 0.03 * z : 1.05 + 0.125 * z) *
+                                krows;
             if (z == 1 || us < best) {
                 best = us;
                 plan->splits = z;
@@ -1715,7 +1799,15 @@ pkv_status launch_prefill(const PrefillCall &c, const Plan &plan)
         cfg.gridDim = dim3(static_cast<unsigned>(all));
         cfg.blockDim = dim3(32 * kJoinWarps);
         cfg.dynamicSmemBytes = 0;
-        e = cudaLaunchKernelEx(&cfg, join_kernel<kD>, a);
+        bool few = false;
+        if constexpr (kTree) {
+            few = 2 * plan.splits <= kFewParts;
+            if (few) {
+                cfg.gridDim = dim3(static_cast<unsigned>((all + kJoinWarps - 1) / kJoinWarps));
+                e = cudaLaunchKernelEx(&cfg, join_few_kernel<kD>, a);
+            }
+        }
+        if (!few) e = cudaLaunchKernelEx(&cfg, join_kernel<kD>, a);
     }
     if (e != cudaSuccess) {
         cudaGetLastError();
@@ -1738,7 +1830,7 @@ pkv_status prefill_entry(const PrefillCall &c, int kv)
     if (!(fabsf(c.softmax_scale) <= 2.0e38f) || !valid_cap(c.logit_cap)) return PKV_ERR_INVALID_ARG;
     Plan plan;
     const pkv_status st = plan_of(c.num_tokens, c.num_seqs, c.num_heads, c.num_kv_heads, c.head_dim,
-                                  c.max_context_len, &plan);
+                                  c.max_context_len, &plan, c.max_tree_len);
     if (st != PKV_OK) return st;
     if (c.block_size != kPage) return PKV_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(c.num_blocks) * c.num_kv_heads * kPage > 0x7fffffffLL ||
@@ -1752,6 +1844,18 @@ pkv_status prefill_entry(const PrefillCall &c, int kv)
     if (c.num_tokens == 0 || c.num_seqs == 0) return PKV_OK;
     if (plan.bytes > 0 && (!c.workspace || c.workspace_bytes < plan.bytes)) return PKV_ERR_WORKSPACE;
     if (!aligned(c.workspace, 16)) return PKV_ERR_MISALIGNED;
+    if constexpr (kTree) {
+        // A window leaves fewer tiles to split (a prefix is taken to be short).  The
+        // workspace's size does not know of it, so the splits only become fewer.  (24
+        // trees of 21 to 60 over 5000, window 1024: 35 us, in three splits 59.)
+        const int64_t seen = static_cast<int64_t>(c.window) + c.max_tree_len + kTile;
+        if (c.window > 0 && seen < c.max_context_len) {
+            Plan fewer;
+            plan_of(c.num_tokens, c.num_seqs, c.num_heads, c.num_kv_heads, c.head_dim,
+                    static_cast<int>(seen), &fewer, c.max_tree_len);
+            if (fewer.splits < plan.splits) plan.splits = fewer.splits;
+        }
+    }
     const bool mod = c.logit_cap > 0.f || c.slopes || !(c.softmax_scale > 0.f);
     auto pick = [&](auto kind) -> pkv_status {
         constexpr int kKv = decltype(kind)::value;

@@ -21,11 +21,12 @@ PrefillCall rows_call(const TreeCall &c)
 }  // namespace
 
 pkv_status tree_rows_workspace(int num_tokens, int num_seqs, int num_heads, int num_kv_heads,
-                               int head_dim, int max_context_len, size_t *bytes)
+                               int head_dim, int max_context_len, int max_tree_len,
+                               size_t *bytes)
 {
     Plan plan;
     const pkv_status st = plan_of(num_tokens, num_seqs, num_heads, num_kv_heads, head_dim,
-                                  max_context_len, &plan);
+                                  max_context_len, &plan, max_tree_len);
     *bytes = plan.bytes;
     return st;
 }

@@ -35,7 +35,7 @@ pkv_status tree_plan(int num_tokens, int num_seqs, int num_heads, int num_kv_hea
     if (num_heads / num_kv_heads > 64) plan->rows = 0;
     if (plan->rows == 0)
         return tree_rows_workspace(num_tokens, num_seqs, num_heads, num_kv_heads, head_dim,
-                                   max_context_len, &plan->bytes);
+                                   max_context_len, max_tree_len, &plan->bytes);
     plan->bytes =
         kTreePieces * (2 * plan->rows * (head_dim + 2) * sizeof(float) + kTreeMetaBytes);
     return PKV_OK;

@@ -43,7 +43,8 @@ enum TreeKind { kTreeFp16, kTreeInt8, kTreeFp8 };
 // Many rows per kv head.
 pkv_status launch_tree_rows(const TreeCall &c, TreeKind kind);
 pkv_status tree_rows_workspace(int num_tokens, int num_seqs, int num_heads, int num_kv_heads,
-                               int head_dim, int max_context_len, size_t *bytes);
+                               int head_dim, int max_context_len, int max_tree_len,
+                               size_t *bytes);
 
 // Few of them.
 

@@ -393,3 +393,15 @@ def test_offsets_beyond_32_bits():
                             dev(parents), 200, 7, 128 ** -0.5, ws)
     got = out.cpu().numpy().astype(np.float64)
     assert np.all(np.abs(got - ref) <= T.bound(b, expand(b, "plain"), ref, mass, 128 ** -0.5))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("seqs,tree,heads,kv,dim,ctx", [(9, 30, 14, 2, 64, 700), (3, 40, 8, 2, 128, 1500),
+                                                        (2, 70, 4, 1, 128, 5000)])
+@pytest.mark.parametrize("option", ["plain", "all"])
+def test_splits_of_the_keys_joined(kind, seqs, tree, heads, kv, dim, ctx, option):
+    # many rows, split over the keys; uneven trees and lengths, so parts without keys
+    q = [1 + (tree - 1) * (i % 3) // 2 for i in range(seqs)]
+    b = R.make(60 + seqs, q, [max(n, ctx * (i + 1) // seqs) for i, n in enumerate(q)], heads, kv, dim)
+    assert pkv.pkv_tree_workspace_size(sum(q), seqs, heads, kv, dim, int(b.ctx.max()), max(q)) > 0
+    check(b, kind, option)

@@ -110,10 +110,13 @@ def test_workspace_size():
     assert pkv.pkv_tree_workspace_size(64, 8, 32, 8, 64, 512, 9) == expect(64, 64)
     # a bound above the batch's tokens does not count
     assert pkv.pkv_tree_workspace_size(4, 1, 8, 1, 64, 512, 4096) == expect(32, 64)
-    # many rows: as for the prefill
+    # many rows: two parts of every row for each split of the keys, if there are several
     for tree, heads in ((17, 32), (1, 80 * 8)):
-        args = (64, 8, heads, 8, 128, 20000)
-        assert pkv.pkv_tree_workspace_size(*args, tree) == pkv.pkv_prefill_workspace_size(*args)
+        parts = 2 * 64 * heads * (128 + 2) * 4
+        size = pkv.pkv_tree_workspace_size(64, 8, heads, 8, 128, 20000, tree)
+        assert size % parts == 0 and 2 <= size // parts <= 32
+    # 512 work items: one for every SM three times over
+    assert pkv.pkv_tree_workspace_size(64 * 64, 64, 32, 8, 128, 8192, 64) == 0
     assert pkv.pkv_tree_workspace_size(8, 1, 4, 3, 128, 20000, 8) == 0
     assert pkv.pkv_tree_workspace_size(8, 1, 4, 1, 96, 20000, 8) == 0
     assert pkv.pkv_tree_workspace_size(-1, 1, 4, 1, 64, 20000, 8) == 0
