@@ -1326,8 +1326,8 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                     check_sequences(p, lane);
                 // Trees often have about as many items as there are SMs, and all of the same
                 // length: a CTA that asked for its next one at once would take it away from
-                // another that has none (16 x 64 over 8192: 189 us so, 105 now).  So it asks when its
-                // loads are through.
+                // another that has none (16 x 64 over 8192: 189 us so, 105 now).  So it asks
+                // when its loads are through.
                 if constexpr (kTree) {
                     if (what > 0 && ok) ok = wait(k_asked, (k - 1) & 1);
                     if (!ok) break;
