@@ -139,6 +139,8 @@ def debug_lib() -> ctypes.CDLL:
             for name in ("pkv_debug_set_prefill", "pkv_debug_set_tree"):
                 getattr(L, name).restype = ctypes.c_int
                 getattr(L, name).argtypes = [ctypes.c_int] * 4
+            L.pkv_debug_set_tree_warp.restype = ctypes.c_int
+            L.pkv_debug_set_tree_warp.argtypes = [ctypes.c_int] * 2
             _debug_lib = L
         return _debug_lib
 

@@ -1947,7 +1947,7 @@ extern "C" __attribute__((visibility("default"))) int pkv_debug_set_prefill(int 
     if (give_role >= pkv::kRoles || slow_role >= pkv::kRoles || slow_ns < 0 || slow_ns > 1000000)
         return -1;
     const pkv::WaitDebug d = {give_role < 0 ? -2 : give_role, give_at,
-                                 slow_role < 0 ? -2 : slow_role, slow_ns};
+                                 slow_role < 0 ? -2 : slow_role, slow_ns, 0};
     if (cudaDeviceSynchronize() != cudaSuccess ||
         cudaMemcpyToSymbol(pkv::g_wait_debug, &d, sizeof(d)) != cudaSuccess)
         return -1;

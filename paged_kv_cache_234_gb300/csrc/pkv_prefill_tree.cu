@@ -39,10 +39,10 @@ pkv_status launch_tree_rows(const TreeCall &c, TreeKind kind)
 }
 
 #ifdef PKV_DEBUG
-int set_tree_waits_rows(int give_role, int give_at, int slow_role, int slow_ns)
+int set_tree_waits_rows(int give_role, int give_at, int slow_role, int slow_ns, int slow_warp)
 {
     const WaitDebug d = {give_role < 0 ? -2 : give_role, give_at, slow_role < 0 ? -2 : slow_role,
-                         slow_ns};
+                         slow_ns, slow_warp};
     return cudaMemcpyToSymbol(g_wait_debug, &d, sizeof(d)) == cudaSuccess ? 0 : -1;
 }
 #endif

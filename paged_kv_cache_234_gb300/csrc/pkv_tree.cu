@@ -151,15 +151,28 @@ extern "C" size_t pkv_tree_workspace_size(int num_tokens, int num_seqs, int num_
 // V loads, 4 items, 5 widening of codes).  A negative role resets its setting.
 // Synchronises with the device; returns 0, or -1 if the CUDA runtime fails or an
 // argument is out of range.
-extern "C" __attribute__((visibility("default"))) int pkv_debug_set_tree(int give_role, int give_at,
-                                                                         int slow_role, int slow_ns)
+static int set_tree(int give_role, int give_at, int slow_role, int slow_ns, int slow_warp)
 {
     if (give_role > 5 || slow_role > 5 || slow_ns < 0 || slow_ns > 1000000 ||
         cudaDeviceSynchronize() != cudaSuccess)
         return -1;
-    return pkv::set_tree_waits_rows(give_role, give_at, slow_role, slow_ns) |
-           pkv::set_tree_waits_fp16(give_role, give_at, slow_role, slow_ns) |
-           pkv::set_tree_waits_int8(give_role, give_at, slow_role, slow_ns) |
-           pkv::set_tree_waits_fp8(give_role, give_at, slow_role, slow_ns);
+    return pkv::set_tree_waits_rows(give_role, give_at, slow_role, slow_ns, slow_warp) |
+           pkv::set_tree_waits_fp16(give_role, give_at, slow_role, slow_ns, slow_warp) |
+           pkv::set_tree_waits_int8(give_role, give_at, slow_role, slow_ns, slow_warp) |
+           pkv::set_tree_waits_fp8(give_role, give_at, slow_role, slow_ns, slow_warp);
+}
+
+extern "C" __attribute__((visibility("default"))) int pkv_debug_set_tree(int give_role, int give_at,
+                                                                         int slow_role, int slow_ns)
+{
+    return set_tree(give_role, give_at, slow_role, slow_ns, 0);
+}
+
+// Warp `warp` (0 to 3) of every group of score warps alone begins its waits slow_ns
+// later; a negative one resets the setting.
+extern "C" __attribute__((visibility("default"))) int pkv_debug_set_tree_warp(int warp, int slow_ns)
+{
+    if (warp > 3) return -1;
+    return set_tree(-1, 0, warp < 0 ? -1 : 0, slow_ns, warp < 0 ? 0 : warp + 1);
 }
 #endif

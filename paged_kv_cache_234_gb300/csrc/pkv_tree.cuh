@@ -751,6 +751,9 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                     references();
                     follow();
                     probabilities(std::false_type());
+                    // (the next tile's masks are written ahead of any barrier: behind
+                    // the other warps' use of this one's)
+                    if (!clean) group_sync(i);
                 }
                 if (!clean) {
                     // V rows of keys that no row of the tree sees may hold anything, NaN
@@ -1452,10 +1455,10 @@ pkv_status launch_tree(const TreeCall &c, const TreePlan &plan)
 }
 
 #ifdef PKV_DEBUG
-inline int set_waits(int give_role, int give_at, int slow_role, int slow_ns)
+inline int set_waits(int give_role, int give_at, int slow_role, int slow_ns, int slow_warp)
 {
     const WaitDebug d = {give_role < 0 ? -2 : give_role, give_at, slow_role < 0 ? -2 : slow_role,
-                         slow_ns};
+                         slow_ns, slow_warp};
     return cudaMemcpyToSymbol(g_wait_debug, &d, sizeof(d)) == cudaSuccess ? 0 : -1;
 }
 #endif

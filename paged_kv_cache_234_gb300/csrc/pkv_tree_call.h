@@ -54,10 +54,10 @@ pkv_status launch_tree_fp8(const TreeCall &c, const TreePlan &plan);
 
 #ifdef PKV_DEBUG
 // Sets a unit's WaitDebug; 0, or -1 if the CUDA runtime fails.
-int set_tree_waits_rows(int give_role, int give_at, int slow_role, int slow_ns);
-int set_tree_waits_fp16(int give_role, int give_at, int slow_role, int slow_ns);
-int set_tree_waits_int8(int give_role, int give_at, int slow_role, int slow_ns);
-int set_tree_waits_fp8(int give_role, int give_at, int slow_role, int slow_ns);
+int set_tree_waits_rows(int give_role, int give_at, int slow_role, int slow_ns, int slow_warp);
+int set_tree_waits_fp16(int give_role, int give_at, int slow_role, int slow_ns, int slow_warp);
+int set_tree_waits_int8(int give_role, int give_at, int slow_role, int slow_ns, int slow_warp);
+int set_tree_waits_fp8(int give_role, int give_at, int slow_role, int slow_ns, int slow_warp);
 #endif
 
 }  // namespace pkv

@@ -9,9 +9,9 @@ pkv_status launch_tree_int8(const TreeCall &c, const TreePlan &plan)
 }
 
 #ifdef PKV_DEBUG
-int set_tree_waits_int8(int give_role, int give_at, int slow_role, int slow_ns)
+int set_tree_waits_int8(int give_role, int give_at, int slow_role, int slow_ns, int slow_warp)
 {
-    return set_waits(give_role, give_at, slow_role, slow_ns);
+    return set_waits(give_role, give_at, slow_role, slow_ns, slow_warp);
 }
 #endif
 

@@ -17,11 +17,12 @@ constexpr uint64_t kWaitLimitNs = 1000000000ull;  // bounded waits: 1 s
 #ifdef PKV_DEBUG
 // Settable by the debug build's entry points: wait number give_at of every warp of
 // give_role gives up, as if its limit had run out, and every wait of slow_role
-// begins slow_ns later (role -2: none; warps without a role have -1).
+// begins slow_ns later (role -2: none; warps without a role have -1), or with
+// slow_warp > 0 those of its warps number slow_warp - 1 modulo 4 alone.
 struct WaitDebug {
-    int give_role, give_at, slow_role, slow_ns;
+    int give_role, give_at, slow_role, slow_ns, slow_warp;
 };
-static __device__ WaitDebug g_wait_debug = {-2, 0, -2, 0};
+static __device__ WaitDebug g_wait_debug = {-2, 0, -2, 0, 0};
 #endif
 
 struct Waiter {
@@ -73,7 +74,9 @@ struct Waiter {
     {
 #ifdef PKV_DEBUG
         const WaitDebug d = g_wait_debug;
-        if (role == d.slow_role) __nanosleep(d.slow_ns);
+        if (role == d.slow_role &&
+            (d.slow_warp <= 0 || static_cast<int>(threadIdx.x >> 5 & 3) == d.slow_warp - 1))
+            __nanosleep(d.slow_ns);
         if (role == d.give_role && waits++ == d.give_at) {
             give_up();
             return true;
