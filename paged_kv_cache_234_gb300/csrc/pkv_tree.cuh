@@ -76,6 +76,7 @@ constexpr float kLift = 6.f;    // log2 factor of the probabilities
 constexpr float kLazy = 9.f;    // log2 excess over the reference that is let be
 constexpr float kNone = -3.0e38f;        // reference of a row that has seen nothing
 constexpr float kLeastV = 0x1p-60f;      // V scales below (zero) count as this
+constexpr float kGone = 110.f;           // log2 share beyond which older sums are nothing
 
 // Score warps: a group of four, a thread per key, for every 16 rows.  A tile's chain
 // (scores, exponentials, reference, product) has more waits than work, which groups
@@ -715,9 +716,11 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                     group_sync(i);
                 };
                 // What the probabilities added to the sums is taken off again, and sums and
-                // accumulators follow the new references.  (Beyond 2^100 the sums so far will
-                // be nothing; else the reference grows by 2^kLazy at least, and with it the
-                // rounding of a sum that held too much goes below the sum's own.)
+                // accumulators follow the new references.  What was added may be beyond fp32,
+                // as y or as y / v: where either is above 2^kGone, the sum so far is nothing
+                // beside it (2^(kLift + kLazy) / kLeastV a key at most: 2^75) and is dropped.
+                // Else both are finite, the reference grows by 2^kLazy at least, and with it
+                // the rounding of a sum that held too much goes below the sum's own.
                 auto follow = [&]() {
                     float x[kRows], f;
                     scores(x, f, std::false_type());
@@ -726,8 +729,8 @@ __global__ void __launch_bounds__(tree_threads(kKv, kN), 1)
                         const float2 z = exponents(x, f, e, old[c0 + e], old[c0 + e + 1]);
                         const float a = fmaf(-ptx::ex2(z.x), rv, l[e]);
                         const float b = fmaf(-ptx::ex2(z.y), rv, l[e + 1]);
-                        l[e] = z.x > 100.f ? 0.f : a * fac[c0 + e];
-                        l[e + 1] = z.y > 100.f ? 0.f : b * fac[c0 + e + 1];
+                        l[e] = fmaxf(z.x, z.x - lv) > kGone ? 0.f : a * fac[c0 + e];
+                        l[e + 1] = fmaxf(z.y, z.y - lv) > kGone ? 0.f : b * fac[c0 + e + 1];
                     }
                     fail |= !wait(pv_done(g - 1), (g - 1) >> 1 & 1);
                     umma::fence_after();
