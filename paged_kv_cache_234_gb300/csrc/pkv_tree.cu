@@ -29,8 +29,9 @@ pkv_status tree_plan(int num_tokens, int num_seqs, int num_heads, int num_kv_hea
         max_context_len < 0 || max_tree_len < 0 || num_heads % num_kv_heads != 0)
         return PKV_ERR_INVALID_ARG;
     if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
-    const int tree = max_tree_len < num_tokens ? max_tree_len : num_tokens;
-    const int64_t rows = static_cast<int64_t>(tree) * (num_heads / num_kv_heads);
+    // (a token at least, also where the bound allows none: an item has room for its heads)
+    const int most = max_tree_len < num_tokens ? max_tree_len : num_tokens;
+    const int64_t rows = static_cast<int64_t>(most > 0 ? most : 1) * (num_heads / num_kv_heads);
     plan->rows = rows <= 32 ? 32 : rows <= 64 ? 64 : 0;
     if (num_heads / num_kv_heads > 64) plan->rows = 0;
     if (plan->rows == 0)
