@@ -651,7 +651,8 @@ PKV_API pkv_status pkv_tree_accept(int32_t *kept, int32_t *kept_lens, int32_t *n
  *   kept        int32 [num_tokens] in device memory; entries behind a
  *               sequence's m are not read
  *   kept_lens   int32 [num_seqs] in device memory
- *   new_context_lens  int32 [num_seqs], device, or NULL; not context_lens itself
+ *   new_context_lens  int32 [num_seqs], device, or NULL; must not overlap context_lens or
+ *               another of the call's int32 inputs (PKV_ERR_INVALID_ARG)
  * A sequence that does not fit (the ragged batch; n > ctx, ctx beyond the block
  * table) sets PKV_DEV_BAD_CTX, one with m outside [0, n] PKV_DEV_BAD_KEEP:
  * nothing of it is moved and its length stays.  An entry outside [0, n) or not

@@ -452,6 +452,14 @@ pkv_status launch_compact(const CompactCall &c, const CompactArgs &a)
     return PKV_OK;
 }
 
+// Whether two arrays of so many int32 have one in common.
+bool overlap(const void *a, int64_t na, const void *b, int64_t nb)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && na > 0 && nb > 0 && x < y + 4 * static_cast<uintptr_t>(nb) &&
+           y < x + 4 * static_cast<uintptr_t>(na);
+}
+
 pkv_status compact_entry(const CompactCall &c, int kind)
 {
     if (!c.k_cache || !c.v_cache || !c.query_starts) return PKV_ERR_INVALID_ARG;
@@ -464,7 +472,6 @@ pkv_status compact_entry(const CompactCall &c, int kind)
         c.num_kv_heads <= 0 || c.head_dim <= 0 || c.block_size <= 0)
         return PKV_ERR_INVALID_ARG;
     if (!c.block_tables && c.max_blocks_per_seq > 0 && c.num_seqs > 0) return PKV_ERR_INVALID_ARG;
-    if (c.new_context_lens && c.new_context_lens == c.context_lens) return PKV_ERR_INVALID_ARG;
     if (c.block_size != 16 || (c.head_dim != 64 && c.head_dim != 128)) return PKV_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(c.max_blocks_per_seq) * 16 > INT32_MAX) return PKV_ERR_UNSUPPORTED;
     if (!aligned(c.k_cache, 16) || !aligned(c.v_cache, 16) || !aligned(c.k_codes, 16) ||
@@ -473,6 +480,15 @@ pkv_status compact_entry(const CompactCall &c, int kind)
         !aligned(c.query_starts, 4) || !aligned(c.context_lens, 4) ||
         !aligned(c.block_tables, 4) || !aligned(c.dev_status, 4))
         return PKV_ERR_MISALIGNED;
+    // The lengths are written while other warps read the call's arrays: with a sequence
+    // that changes under them the warps of a cluster would not meet equally often.
+    const int64_t n = c.num_seqs;
+    if (overlap(c.new_context_lens, n, c.context_lens, n) ||
+        overlap(c.new_context_lens, n, c.kept_lens, n) ||
+        overlap(c.new_context_lens, n, c.query_starts, n + 1) ||
+        overlap(c.new_context_lens, n, c.kept, c.num_tokens) ||
+        overlap(c.new_context_lens, n, c.block_tables, n * c.max_blocks_per_seq))
+        return PKV_ERR_INVALID_ARG;
     if (c.num_seqs == 0) return PKV_OK;
     CompactArgs a;
     a.k_pool = static_cast<__half *>(c.k_cache);
