@@ -70,13 +70,6 @@ __device__ __forceinline__ void team_wait()
     if constexpr (!kWarp) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ float max_nan(float a, float b)
-{
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
 // The codes of eight values by y = x * fl(1 / scale), which is within 2 ulp of the
 // quotient q = fl(x / scale) that the quantizer rounds.  Returns a bit for every value
 // whose y lies so close to the middle M of two codes that q may be M or beyond, or is
