@@ -548,8 +548,11 @@ PKV_API size_t pkv_prefill_workspace_size(int num_tokens, int num_seqs, int num_
  *   of the tree's, the token itself and its ancestors with  i - p(t) < window
  *   out[row][h] = sum over seen t of softmax(z'')_t * V_t
  * with FP32 sums, maxima and accumulators; the probabilities (for code caches,
- * times the V scales) enter the second product rounded to fp16, as in
- * pkv_paged_prefill_*, relative to the largest such product of the row.  V
+ * their products with the V scales) enter the second product rounded to fp16, 11
+ * bits.  With up to 64 rows (the smaller of max_tree_len and num_tokens, times the
+ * heads of a kv head) there are fewer below 2^-20 of the row's largest such product,
+ * off by 2^-31 of that at most; with more rows it is as for pkv_paged_prefill_*, by
+ * the row's largest probability times the largest V scale that it sees.  V
  * scales must not be negative; one that is not finite makes the rows that see its
  * page not finite.  Keys that no row of the call sees have no effect,
  * whatever their slots hold; those that one sees must be finite, and their values.
@@ -625,7 +628,8 @@ PKV_API size_t pkv_tree_workspace_size(int num_tokens, int num_seqs, int num_hea
  *   query_starts  int32 [num_seqs + 1] (the ragged batch)
  * kept and kept_lens are what pkv_compact_* takes.  A sequence whose rows do
  * not lie in [0, num_tokens] sets PKV_DEV_BAD_CTX, one with a bad parent
- * PKV_DEV_BAD_TREE; its path is empty (and next_tokens -1).
+ * PKV_DEV_BAD_TREE; its path is empty (and next_tokens -1).  The outputs must not
+ * overlap the inputs.
  */
 PKV_API pkv_status pkv_tree_accept(int32_t *kept, int32_t *kept_lens, int32_t *next_tokens,
                                    const int32_t *tokens, const int32_t *targets,

@@ -88,7 +88,7 @@ def build_debug() -> str:
     with PKV_DEBUG (shared-memory address and index checks, read back by
     pkv_debug_flags / pkv_debug_evict_flags) and the prefill's and the tree
     attention's with settings of their waits (pkv_debug_set_prefill,
-    pkv_debug_set_tree).  For tests; the release library is
+    pkv_debug_set_tree, pkv_debug_set_tree_warp).  For tests; the release library is
     untouched."""
     build()
     if os.path.exists(DEBUG_LIB_PATH) and all(

@@ -19,7 +19,7 @@
 // found by shuffles alone, since a tile is a warp's.
 //
 // Measured: 8 contexts of 16384 tokens to their halves, fp16, 8 kv heads: 93 us, 85 %
-// of the copy's rate; one FP8 context of 131072 tokens to its half: 299 us, half of it:
+// of the copy's rate; one FP8 context of 131072 tokens to three quarters: 300 us, half of it:
 // 16 chains keep 128 CTAs of 8 warps busy (16 warps: 348 us, 4: 478), and a page's
 // codes take a warp longer than its rows.  Paths of 16 tokens in 64 trees, which
 // is a warp's work each: 4.0 us (a launch), INT8 7.8.

@@ -1326,8 +1326,9 @@ __global__ void __launch_bounds__(prefill_threads<kKv, kMod>(), 1)
                     check_sequences(p, lane);
                 // Trees often have about as many items as there are SMs, and all of the same
                 // length: a CTA that asked for its next one at once would take it away from
-                // another that has none (16 x 64 over 8192: 189 us so, 105 now).  So it asks
-                // when its loads are through.
+                // another that has none (16 x 64 over 8192, back to back: 190 us so, 107 to
+                // 120 now; a call by itself 199 and 115).  So it asks when its loads are
+                // through.
                 if constexpr (kTree) {
                     if (what > 0 && ok) ok = wait(k_asked, (k - 1) & 1);
                     if (!ok) break;
@@ -1666,7 +1667,8 @@ struct Plan {
 // 8 splits are joined by join_few_kernel: 0.25 + 0.03 splits.  32 trees of 25 over 2048
 // (14 / 2 heads, head_dim 64, biased) 43 and 32 us (42 with three), 16 of 32 over 4096
 // (28 / 4) 54 and 44 (56), 4 of 64 over 2048 (32 / 8) 31 and 26 (24 with four); the other
-// way around 16 of 64 over 8192: 106 and 127, 16 of 20 over 1024 (FP8): 22 and 32.
+// way around 16 of 64 over 8192: 106 and 127, 16 of 20 over 1024 (FP8): 22 and 32.  (All
+// of these calls back to back.)
 pkv_status plan_of(int num_tokens, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
                    int max_context_len, Plan *plan, [[maybe_unused]] int most_tokens = 0)
 {

@@ -13,8 +13,8 @@ namespace {
 constexpr int kPage = 16, kTile = 128;   // tokens of a page, keys of a step
 
 // From the sizes alone.  Up to 64 rows per kv head (tokens times heads) are the short
-// side of both products, keys the long one; with more the rows are.  The two ways, in us
-// (32 / 8 heads, head_dim 128; a tree of 8 tokens has 32 rows, of 16 tokens 64):
+// side of both products, keys the long one; with more the rows are.  The two ways, in us,
+// back to back (32 / 8 heads, head_dim 128; a tree of 8 tokens has 32 rows, of 16 tokens 64):
 //                          fp16            INT8            FP8
 //   64 trees of 8, 2048    96.1 | 102.2    81.1 | 114.8    78.1 | 113.5
 //   64 trees of 16, 2048  102.3 | 104.3    95.0 | 117.1    90.8 | 116.3

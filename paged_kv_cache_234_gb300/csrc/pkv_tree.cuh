@@ -12,17 +12,21 @@
 // every cached key and value is read once for all of them.  So the keys are the
 // long side of both products: per tile of 128 keys (eight pages)
 //   S^T = K Q^T     (128 keys x N rows, fp32 in TMEM; K as it lies in the page)
-//   P^T = 2^(S' - m)  (a thread per key, half of the rows each; fp16, to shared
-//                    memory in the layout of a product's operand)
+//   P^T = 2^(S' - m)  (a thread per key, in a group of them for every 16 rows; fp16, to
+//                    shared memory in the layout of a product's operand)
 //   O^T += V^T P^T  (head_dim x N, fp32 in TMEM; V as it lies in the page)
 // With rows as the N of the products, 32 rows take a quarter of the time of 128,
 // and the exponentials of all rows are spread over all threads.  Since a row's
 // scores lie across threads, its maximum is not taken for every tile: the
 // exponentials are relative to a reference per row, and a tile whose scores
-// exceed it by more than 2^6 (every row's first, hardly any other) makes all
-// threads take the maxima and rescale sums and accumulators.  The probabilities
-// enter the product with a factor 2^6, so up to that much smaller ones are normal
-// fp16 numbers.  Sums, maxima and accumulators are fp32.
+// exceed it by more than 2^9 makes the group take the maxima, rescale sums and
+// accumulators and work the tile out once more.  That is every row's first tile and
+// hardly any other -- but with a bias by distance, under which the scores rise from
+// tile to tile, nearly every tile of a head whose slope is above 0.05 (9 / (128
+// log2 e)): 64 trees of 8 tokens over 2048 with the usual slopes take 132 us in fp16
+// and 174 in INT8, without them 99 and 79.  The probabilities enter the product with a
+// factor 2^6, so up to that much smaller ones are normal fp16 numbers, and the
+// largest are 2^15.  Sums, maxima and accumulators are fp32.
 //
 // The tiles of all (sequence, kv head) pairs form one line, which is cut into as
 // many equal pieces as there are SMs: a CTA walks its piece, whatever the lengths
@@ -40,8 +44,9 @@
 // scale enters the exponent, 2^(S' + log2 v - m), so that the reference is that of the
 // largest contribution p V, and the sums take the probability times 1 / v.
 //
-// Measured, 64 trees of 8 tokens over 2048 keys, 32 / 8 heads, head_dim 128: fp16 96 us,
-// 85 % of the copy's rate; INT8 81, FP8 78 (51 and 53 %): there the score warps' chain
+// Measured back to back, 64 trees of 8 tokens over 2048 keys, 32 / 8 heads, head_dim 128:
+// fp16 96 to 99 us, 81 to 84 % of the copy's rate; INT8 79 to 81, FP8 76 to 78 (51 to 54 %):
+// there the score warps' chain
 // and the widening (40 instructions for 32 codes) share the schedulers, which issue in
 // 44 % of the cycles, and wait for instructions more than for any pipe.  One tree of 8
 // over 131072: fp16 93, INT8 71, FP8 67 us.  Eight trees of 8 over 512, one head to a kv
@@ -74,8 +79,11 @@ constexpr int kGroup = 128;     // threads that share rows: one per key of a til
 constexpr int kPieceTiles = 2;  // tiles of a piece at least
 constexpr float kLift = 6.f;    // log2 factor of the probabilities
 constexpr float kLazy = 9.f;    // log2 excess over the reference that is let be
+static_assert(kLift + kLazy < 16.f, "probabilities up to 2^(kLift + kLazy) are finite in fp16");
 constexpr float kNone = -3.0e38f;        // reference of a row that has seen nothing
-constexpr float kLeastV = 0x1p-60f;      // V scales below (zero) count as this
+// V scales below (zero) count as this.  A code is 448 at most, so what such a page adds
+// to an output stays below 2^-51, nothing beside fp16's smallest number, 2^-24.
+constexpr float kLeastV = 0x1p-60f;
 constexpr float kGone = 110.f;           // log2 share beyond which older sums are nothing
 
 // Score warps: a group of four, a thread per key, for every 16 rows.  A tile's chain
